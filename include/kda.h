@@ -241,6 +241,65 @@ int kda_gdn2_bwd(const kda_problem *p, const void *q, const void *k, const void 
                  void *dk, void *dv, void *draw_g, void *draw_b, void *draw_w, float *dA_log,
                  float *ddt_bias, void *workspace, size_t workspace_bytes, void *stream);
 
+/* The recurrent form, for decoding: the same operator token by token, each
+   sequence starting from a state in the caller's pool and leaving its last
+   state there (the h0 and ht of kda_fwd_ex, fp32 [K][V] per head, so a
+   state kda_fwd_ex returned can be decoded from). Per sequence and head:
+     S~ = Diag(exp(g_t)) S,  u = S~^T (beta_t kh_t)
+     S  = S~ + kh_t (beta_t v_t - u)^T,  o_t = S^T qh_t
+   with the prologue and gate maps of kda_fwd.
+     cu_seqlens     [N+1] (int32, device) or NULL: one token per sequence,
+                    N = T. Values are clamped to [0, T]; an empty sequence
+                    leaves its state as it is. Rows of o at and after
+                    cu_seqlens[N] are not written.
+     state_indices  [N] (int32, device) or NULL: the pool slot of each
+                    sequence (NULL: slot n, n_slots >= N). A slot outside
+                    [0, n_slots) marks a padded sequence: its rows of o are
+                    zero and no state is touched. The slots inside must be
+                    distinct: of two sequences with tokens that name one
+                    slot, which one's update stays is not determined.
+     state          [n_slots, H, K, V] (fp32, device), updated in place.
+   Nothing is read on the host but the problem, so the call can be captured
+   into a graph and replayed with other cu_seqlens and slots of the same N
+   and T. It needs no workspace. T = 0 or N = 0: nothing is launched.
+   q, k, v, raw_g and raw_beta may have rows further apart than H * K, H * V
+   or H elements (the *_stride fields, in elements; 0: rows adjacent), as
+   slices of one fused projection have; strides of q, k, v and a per-channel
+   raw_g are multiples of 16 bytes. Pointers other than those of raw_beta,
+   of a per-head raw_g, cu_seqlens and state_indices are 16-byte aligned. */
+typedef struct {
+  int32_t n_seqs;          /* N >= 0 */
+  int64_t total_tokens;    /* T >= 0; N when cu_seqlens is NULL */
+  int32_t H, K, V;         /* built: K == V in {64, 128} */
+  int32_t dtype;           /* KDA_F32 or KDA_BF16 */
+  int32_t gate_mode;       /* as kda_problem */
+  float scale;             /* as kda_problem */
+  float gate_lower_bound;  /* as kda_problem */
+  float l2_eps;            /* as kda_problem */
+  int64_t n_slots;         /* states in the pool */
+  int64_t q_stride, k_stride, v_stride; /* elements between tokens; 0: H*K, H*K, H*V */
+  int64_t g_stride;        /* 0: H*K, or H under KDA_GATE_PER_HEAD */
+  int64_t beta_stride;     /* 0: H (kda_recurrent) */
+  int64_t b_stride, w_stride; /* 0: H*K, H*V (kda_gdn2_recurrent) */
+} kda_recurrent_problem;
+
+/* Errors: KDA_ERR_INVALID (negative or inconsistent sizes, a stride shorter
+   than a row or not a multiple of 16 bytes, a null pointer),
+   KDA_ERR_UNSUPPORTED (size, dtype or gate not built; N * H of 2^24 or
+   more), KDA_ERR_HIP. */
+int kda_recurrent(const kda_recurrent_problem *p, const void *q, const void *k, const void *v,
+                  const void *raw_g, const void *raw_beta, const float *A_log,
+                  const float *dt_bias, const int32_t *cu_seqlens,
+                  const int32_t *state_indices, float *state, void *o, void *stream);
+
+/* GDN-2's recurrent form (erase gate raw_b [T, H, K], write gate raw_w
+   [T, H, V]): u = S~^T (b_t * kh_t), S = S~ + kh_t (w_t * v_t - u)^T, the
+   rest as kda_recurrent. KDA_GATE_PER_HEAD is not built for GDN-2. */
+int kda_gdn2_recurrent(const kda_recurrent_problem *p, const void *q, const void *k,
+                       const void *v, const void *raw_g, const void *raw_b, const void *raw_w,
+                       const float *A_log, const float *dt_bias, const int32_t *cu_seqlens,
+                       const int32_t *state_indices, float *state, void *o, void *stream);
+
 /* For callers that cannot allocate device memory (code under HIP graph
    capture, tight serving loops, harnesses that forbid hipMalloc): kda_fwd
    with its workspace in a device array of KDA_NOALLOC_SCRATCH_BYTES that the
@@ -280,7 +339,18 @@ enum {
   KDA_KERNEL_CHUNK_LOCAL_STATE = 8, /* state operands only (checkpoint pass) */
   KDA_KERNEL_SCAN_REC = 9,          /* forward-direction scan recording h, Vn */
   KDA_KERNEL_SCAN_STATE = 10,       /* forward-direction scan, states only */
-  KDA_KERNEL_COUNT = 11
+  /* the operators around the chunked one; their units are (token, head)
+     rows, tokens, or (convolution) sequences or tokens */
+  KDA_KERNEL_RECURRENT = 11,
+  KDA_KERNEL_GATED_NORM = 12,
+  KDA_KERNEL_GATED_NORM_BWD = 13,
+  KDA_KERNEL_BLOCK_NORM = 14,
+  KDA_KERNEL_BLOCK_NORM_BWD = 15,
+  KDA_KERNEL_SHORT_CONV = 16,
+  KDA_KERNEL_SHORT_CONV_BWD = 17,
+  KDA_KERNEL_SHORT_CONV_UPDATE = 18,
+  KDA_KERNEL_PARAM_REDUCE = 19,     /* sums of per-block parameter gradients */
+  KDA_KERNEL_COUNT = 20
 };
 int kda_profile_begin(void);
 int kda_profile_end(int32_t *launches, double *total_ms, int64_t *units, int n);

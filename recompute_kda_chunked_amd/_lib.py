@@ -20,9 +20,10 @@ EXPORTS = ("kda_fwd_workspace_bytes", "kda_bwd_workspace_bytes", "kda_check_prob
            "kda_prologue_workspace_bytes", "kda_prologue", "kda_fwd", "kda_bwd",
            "kda_checkpoint_bytes", "kda_bwd_segment_chunks", "kda_fwd_ex", "kda_bwd_ex",
            "kda_profile_begin", "kda_profile_end", "kda_kernel_name", "kda_status_string",
-           "kda_fwd_noalloc", "kda_gdn2_fwd", "kda_gdn2_bwd")
+           "kda_fwd_noalloc", "kda_gdn2_fwd", "kda_gdn2_bwd", "kda_recurrent",
+           "kda_gdn2_recurrent")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES
-KERNEL_COUNT = 11
+KERNEL_COUNT = 20
 
 
 class KdaProblem(ctypes.Structure):
@@ -51,6 +52,29 @@ class KdaStateIO(ctypes.Structure):
         ("dh0", ctypes.c_void_p),
         ("ckpt", ctypes.c_void_p),
         ("ckpt_bytes", ctypes.c_size_t),
+    ]
+
+
+class KdaRecurrentProblem(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("total_tokens", ctypes.c_int64),
+        ("H", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("V", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("gate_mode", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("gate_lower_bound", ctypes.c_float),
+        ("l2_eps", ctypes.c_float),
+        ("n_slots", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("g_stride", ctypes.c_int64),
+        ("beta_stride", ctypes.c_int64),
+        ("b_stride", ctypes.c_int64),
+        ("w_stride", ctypes.c_int64),
     ]
 
 
@@ -98,6 +122,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kda_gdn2_bwd.restype = ctypes.c_int
     lib.kda_fwd_noalloc.argtypes = [pp] + [vp] * 9 + [vp]
     lib.kda_fwd_noalloc.restype = ctypes.c_int
+    rp = ctypes.POINTER(KdaRecurrentProblem)
+    lib.kda_recurrent.argtypes = [rp] + [vp] * 11 + [vp]
+    lib.kda_recurrent.restype = ctypes.c_int
+    lib.kda_gdn2_recurrent.argtypes = [rp] + [vp] * 12 + [vp]
+    lib.kda_gdn2_recurrent.restype = ctypes.c_int
     lib.kda_profile_begin.argtypes = []
     lib.kda_profile_begin.restype = ctypes.c_int
     lib.kda_profile_end.argtypes = [ctypes.POINTER(ctypes.c_int32),

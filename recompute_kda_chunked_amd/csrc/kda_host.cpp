@@ -21,13 +21,52 @@
 #include <vector>
 
 #include "kda.h"
+#include "kda_host.h"
 #include "kda_internal.h"
+
+namespace kda {
+
+static thread_local char g_msg[256];
+
+int hip_fail(hipError_t e) {
+  std::snprintf(g_msg, sizeof g_msg, "HIP launch failed: %s", hipGetErrorString(e));
+  return KDA_ERR_HIP;
+}
+
+// Per-kernel timing (kda_profile_begin / kda_profile_end): event pairs
+// recorded on the launch stream around each launch of the calling thread.
+struct ProfRec {
+  int kind;
+  int64_t units;
+  hipEvent_t a, b;
+};
+static thread_local bool g_prof_on = false;
+static thread_local std::vector<ProfRec> g_prof;
+
+ProfScope::ProfScope(int k, int64_t u, hipStream_t st) : kind(k), units(u), s(st) {
+  if (g_prof_on && hipEventCreate(&a) == hipSuccess && hipEventRecord(a, s) != hipSuccess) {
+    (void)hipEventDestroy(a);
+    a = nullptr;
+  }
+}
+
+void ProfScope::done() {
+  if (!a) return;
+  hipEvent_t b = nullptr;
+  if (hipEventCreate(&b) == hipSuccess && hipEventRecord(b, s) == hipSuccess) {
+    g_prof.push_back({kind, units, a, b});
+  } else {
+    if (b) (void)hipEventDestroy(b);
+    (void)hipEventDestroy(a);
+  }
+  a = nullptr;
+}
+
+}  // namespace kda
 
 using namespace kda;
 
 namespace {
-
-thread_local char g_msg[256];
 
 // Largest |L| (gate_lower_bound) for which every gate factor the kernels form
 // stays finite in fp32: 15 * 5.9 = 88.5 < ln(FLT_MAX) = 88.72.
@@ -373,53 +412,6 @@ bool has_empty_sequence(const kda_problem* p) {
   return false;
 }
 
-int hip_fail(hipError_t e) {
-  std::snprintf(g_msg, sizeof g_msg, "HIP launch failed: %s", hipGetErrorString(e));
-  return KDA_ERR_HIP;
-}
-
-// Per-kernel timing (kda_profile_begin / kda_profile_end): event pairs
-// recorded on the launch stream around each launch of the calling thread.
-struct ProfRec {
-  int kind;
-  int64_t units;
-  hipEvent_t a, b;
-};
-thread_local bool g_prof_on = false;
-thread_local std::vector<ProfRec> g_prof;
-
-struct ProfScope {
-  int kind;
-  int64_t units;
-  hipStream_t s;
-  hipEvent_t a = nullptr;
-  ProfScope(int k, int64_t u, hipStream_t st) : kind(k), units(u), s(st) {
-    if (g_prof_on && hipEventCreate(&a) == hipSuccess && hipEventRecord(a, s) != hipSuccess) {
-      (void)hipEventDestroy(a);
-      a = nullptr;
-    }
-  }
-  void done() {
-    if (!a) return;
-    hipEvent_t b = nullptr;
-    if (hipEventCreate(&b) == hipSuccess && hipEventRecord(b, s) == hipSuccess) {
-      g_prof.push_back({kind, units, a, b});
-    } else {
-      if (b) (void)hipEventDestroy(b);
-      (void)hipEventDestroy(a);
-    }
-    a = nullptr;
-  }
-};
-
-#define KDA_TRY(kind, units, expr)             \
-  do {                                         \
-    ProfScope ps_(kind, units, s);             \
-    const hipError_t e_ = (expr);              \
-    ps_.done();                                \
-    if (e_ != hipSuccess) return hip_fail(e_); \
-  } while (0)
-
 Dims make_dims(const kda_problem* p) {
   Dims d{};
   d.N = p->n_seqs;
@@ -733,7 +725,9 @@ const char* kda_kernel_name(int kind) {
   static const char* names[KDA_KERNEL_COUNT] = {
       "chunk_table", "prologue",        "chunk_local",       "scan_fwd",
       "scan_bwd",    "chunk_grad",      "gate_reduce",       "chunk_local_bwd",
-      "chunk_local_state", "scan_rec",  "scan_state"};
+      "chunk_local_state", "scan_rec",  "scan_state",        "recurrent",
+      "gated_norm",  "gated_norm_bwd",  "block_norm",        "block_norm_bwd",
+      "short_conv",  "short_conv_bwd",  "short_conv_update", "param_reduce"};
   return (kind >= 0 && kind < KDA_KERNEL_COUNT) ? names[kind] : "unknown";
 }
 
@@ -741,7 +735,7 @@ const char* kda_status_string(int status) {
   switch (status) {
     case KDA_OK: return "ok";
     case KDA_ERR_INVALID: return "invalid argument";
-    case KDA_ERR_UNSUPPORTED: return "unsupported K/V/chunk/dtype/gate combination";
+    case KDA_ERR_UNSUPPORTED: return "unsupported size/chunk/dtype/gate combination";
     case KDA_ERR_WORKSPACE: return "workspace too small";
     case KDA_ERR_HIP: return g_msg[0] ? g_msg : "HIP launch failed";
     default: return "unknown status";

@@ -1,0 +1,219 @@
+// The recurrent form of the gated delta rule (KDA, its per-head gate, GDN-2):
+// one token after another from a state in HBM, for decoding.
+//
+// Per (sequence, head), with the state S [K][V] in fp32:
+//   S~ = Diag(a) S,  u = S~^T e,  d = w - u
+//   S  = S~ + kh d^T,  o = S^T qh = S~^T qh + (kh . qh) d
+// where a = exp(g); e = beta kh and w = beta v (KDA), or e = b * kh and
+// w = (write gate) * v (GDN-2). Taking o from S~ puts both sums over the rows
+// of S in one pass, so a token costs one reduction across lanes.
+//
+// What bounds it: the state's bytes, 4 K V read and written once per
+// sequence and head whatever the number of tokens; the rows of a token are
+// 1-2% of that at one token per sequence. Every column of S is independent,
+// so a wave takes all K rows of 32 columns (lane = 4 columns x K/8 rows, the
+// tile in registers over all tokens), a block the D/32 waves of one (sequence,
+// head), and no wave waits for another. Each wave computes the token's
+// prologue for itself (norms, gates; K channels over 64 lanes, passed to its
+// lanes' row layout through its own 4 K floats of LDS): its rows come from
+// the caches after the first wave's, and a shared copy would need a barrier
+// per token.
+//
+// Sums, gates and the state are fp32 for either dtype; only o is rounded,
+// once.
+#include "../kda_device.h"
+#include "../kda_prologue.h"
+#include "kda_layer.h"
+
+namespace kda {
+
+namespace {
+
+// CPL consecutive channels of a row from c0 (CPL = D / 64).
+template <typename TI, int CPL>
+struct RowPart {
+  uint32_t u[CPL];
+  __device__ __forceinline__ void load(const TI* p) {
+    if constexpr (CPL == 1) {
+      u[0] = load_bits<TI>(p);
+    } else if constexpr (sizeof(TI) == 2) {
+      u[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      u[0] = x.x;
+      u[1] = x.y;
+    }
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (CPL == 2 && sizeof(TI) == 2)
+      return __uint_as_float(e ? (u[0] & 0xffff0000u) : (u[0] << 16));
+    else
+      return bits_to_f<TI>(u[e]);
+  }
+};
+
+// Sum over the eight row groups of a wave (lanes 8, 16 and 32 apart): a
+// rotation by 8 within rows of 16 lanes, then gfx950's row and half swaps of
+// a value with itself. Every lane receives the sum.
+__device__ __forceinline__ float sum_row_groups(float x) {
+  x += dpp_mov<0x128>(x);
+  const uint32_t b = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  const uint32_t c = __float_as_uint(x);
+  const auto h = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+  return __uint_as_float(h[0]) + __uint_as_float(h[1]);
+}
+// Sum over all 64 lanes.
+__device__ __forceinline__ float sum_wave(float x) { return sum_row_groups(group_sum<8>(x)); }
+
+template <typename TI, int D, bool G2>
+__global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
+  constexpr int NW = D / 32;   // waves per block, 32 columns each
+  constexpr int CPL = D / 64;  // prologue channels per lane
+  constexpr int NJ = D / 32;   // groups of 4 rows per lane
+  __shared__ __align__(16) float sm[NW][4][D];  // per wave: a, e, kh, qh
+  const int n = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int64_t t0 = n, t1 = n + 1;
+  if (a.cu) {
+    t0 = a.cu[n];
+    t1 = a.cu[n + 1];
+    t0 = t0 < 0 ? 0 : (t0 > a.T ? a.T : t0);
+    t1 = t1 > a.T ? a.T : t1;
+  }
+  if (t0 >= t1) return;
+  const int64_t slot = a.idx ? a.idx[n] : n;
+  TI* o = static_cast<TI*>(a.o) + static_cast<size_t>(h) * D;
+  const size_t os = static_cast<size_t>(a.H) * D;
+  const int cg = lane & 7, rg = lane >> 3;
+  const int col = 32 * w + 4 * cg;
+  if (slot < 0 || slot >= a.n_slots) {  // a padded sequence
+    if (rg == 0)
+      for (int64_t t = t0; t < t1; ++t) store4<TI>(o + t * os + col, zero4());
+    return;
+  }
+
+  // rows 32 j + 4 rg + r of the lane's four columns
+  float* Sp = a.state + (static_cast<size_t>(slot) * a.H + h) * (D * D) + 4 * rg * D + col;
+  f32x4 s[NJ][4];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[j][r] = *reinterpret_cast<const f32x4*>(Sp + (32 * j + r) * D);
+
+  const int c0 = CPL * lane;
+  const size_t hc = static_cast<size_t>(h) * D + c0;
+  const float ea = expf(a.A_log[h]);
+  float db[CPL];
+#pragma unroll
+  for (int e = 0; e < CPL; ++e) db[e] = a.gate_head ? a.dt_bias[h] : a.dt_bias[hc + e];
+
+  for (int64_t t = t0; t < t1; ++t) {
+    RowPart<TI, CPL> q, k, g, b;
+    q.load(static_cast<const TI*>(a.q) + t * a.qs + hc);
+    k.load(static_cast<const TI*>(a.k) + t * a.ks + hc);
+    if (a.gate_head) {
+      const uint32_t x = load_bits<TI>(static_cast<const TI*>(a.g) + t * a.gs + h);
+      g.u[0] = x;
+      if constexpr (CPL == 2 && sizeof(TI) == 2) g.u[0] = x | (x << 16);
+      else if constexpr (CPL == 2) g.u[1] = x;
+    } else {
+      g.load(static_cast<const TI*>(a.g) + t * a.gs + hc);
+    }
+    uint32_t be = 0, vr[4], wr[4];
+    if constexpr (G2) {
+      b.load(static_cast<const TI*>(a.bk) + t * a.bks + hc);
+      load4_raw<TI>(static_cast<const TI*>(a.wv) + t * a.wvs + static_cast<size_t>(h) * D + col, wr);
+    } else {
+      be = load_bits<TI>(static_cast<const TI*>(a.beta) + t * a.bes + h);
+    }
+    load4_raw<TI>(static_cast<const TI*>(a.v) + t * a.vs + static_cast<size_t>(h) * D + col, vr);
+
+    // prologue: this lane's channels, then to the row layout through LDS
+    float sq = 0.f, sk = 0.f, qk = 0.f;
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) {
+      sq += q.get(e) * q.get(e);
+      sk += k.get(e) * k.get(e);
+      qk += q.get(e) * k.get(e);
+    }
+    sq = sum_wave(sq);
+    sk = sum_wave(sk);
+    qk = sum_wave(qk);
+    const float rq = a.scale / sqrtf(sq + a.eps), rk = 1.f / sqrtf(sk + a.eps);
+    const float beta = G2 ? 0.f : sigmoidf(bits_to_f<TI>(be));
+    const float kq = qk * rq * rk;
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) {
+      const float kh = k.get(e) * rk;
+      sm[w][0][c0 + e] = expf(gate_map<float>(a.gate_mode, ea, g.get(e) + db[e], a.lb));
+      sm[w][1][c0 + e] = (G2 ? sigmoidf(b.get(e)) : beta) * kh;
+      sm[w][2][c0 + e] = kh;
+      sm[w][3][c0 + e] = q.get(e) * rq;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+
+    f32x4 u = zero4(), oo = zero4();
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int r0 = 32 * j + 4 * rg;
+      const f32x4 av = *reinterpret_cast<const f32x4*>(&sm[w][0][r0]);
+      const f32x4 ev = *reinterpret_cast<const f32x4*>(&sm[w][1][r0]);
+      const f32x4 qv = *reinterpret_cast<const f32x4*>(&sm[w][3][r0]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        s[j][r] *= av[r];
+        u += ev[r] * s[j][r];
+        oo += qv[r] * s[j][r];
+      }
+    }
+    f32x4 d = unpack4<TI>(vr);
+    if constexpr (G2) {
+      const f32x4 x = unpack4<TI>(wr);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) d[r] *= sigmoidf(x[r]);
+    } else {
+      d *= beta;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      d[r] -= sum_row_groups(u[r]);
+      oo[r] = sum_row_groups(oo[r]) + kq * d[r];
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const f32x4 kv = *reinterpret_cast<const f32x4*>(&sm[w][2][32 * j + 4 * rg]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[j][r] += kv[r] * d;
+    }
+    if (rg == 0) store4<TI>(o + t * os + col, oo);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) *reinterpret_cast<f32x4*>(Sp + (32 * j + r) * D) = s[j][r];
+}
+
+template <typename TI, int D>
+hipError_t launch_d(bool gdn2, const RecurrentArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.N) * static_cast<unsigned>(a.H)), block(2 * D);
+  if (gdn2)
+    k_recurrent<TI, D, true><<<grid, block, 0, s>>>(a);
+  else
+    k_recurrent<TI, D, false><<<grid, block, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_recurrent(int dtype, int D, bool gdn2, const RecurrentArgs& a, hipStream_t s) {
+  if (dtype == 0) return D == 64 ? launch_d<float, 64>(gdn2, a, s) : launch_d<float, 128>(gdn2, a, s);
+  return D == 64 ? launch_d<bf16, 64>(gdn2, a, s) : launch_d<bf16, 128>(gdn2, a, s);
+}
+
+}  // namespace kda

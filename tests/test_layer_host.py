@@ -1,0 +1,108 @@
+"""Refusals of the operators around the chunked one, without a GPU: the C
+entry points on made-up pointers (validation comes before any launch), and
+the binding's checks of shapes, types and placement."""
+import ctypes
+
+import pytest
+import torch
+
+from recompute_kda_chunked_amd import KdaError, _lib, gdn2_recurrent, kda_recurrent
+from test_abi import lib  # noqa: F401  (fixture)
+
+FAKE, NUL = ctypes.c_void_p(0x1000), ctypes.c_void_p(0)
+
+
+# ------------------------------------------------------------------ recurrent
+
+
+def rec(**kw):
+    d = dict(n_seqs=3, total_tokens=3, H=2, K=128, V=128, dtype=_lib.KDA_BF16, gate_mode=0,
+             scale=1.0, gate_lower_bound=-5.0, l2_eps=1e-6, n_slots=4)
+    d.update(kw)
+    return _lib.KdaRecurrentProblem(**d)
+
+
+def call_rec(lib, p, cu=NUL, idx=NUL, g2=False, **null):  # noqa: F811
+    names = ["q", "k", "v", "raw_g"] + (["raw_b", "raw_w"] if g2 else ["raw_beta"]) + ["A_log", "dt_bias"]
+    args = [NUL if n in null else FAKE for n in names]
+    tail = [NUL if n in null else FAKE for n in ("state", "o")]
+    fn = lib.kda_gdn2_recurrent if g2 else lib.kda_recurrent
+    return fn(ctypes.byref(p) if p is not None else None, *args, cu, idx, *tail, NUL)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_seqs=-1), _lib.KDA_ERR_INVALID),
+    (dict(total_tokens=-1), _lib.KDA_ERR_INVALID),
+    (dict(total_tokens=4), _lib.KDA_ERR_INVALID),           # no cu_seqlens: one token each
+    (dict(H=0), _lib.KDA_ERR_INVALID),
+    (dict(n_slots=2), _lib.KDA_ERR_INVALID),                # no indices: slot n of sequence n
+    (dict(n_slots=-1), _lib.KDA_ERR_INVALID),
+    (dict(K=96, V=96), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(K=64), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(dtype=3), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(gate_mode=2), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(gate_lower_bound=-6.0), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(gate_lower_bound=0.0), _lib.KDA_ERR_INVALID),
+    (dict(gate_lower_bound=float("nan")), _lib.KDA_ERR_INVALID),
+    (dict(l2_eps=-1.0), _lib.KDA_ERR_INVALID),
+    (dict(scale=float("inf")), _lib.KDA_ERR_INVALID),
+    (dict(q_stride=255), _lib.KDA_ERR_INVALID),             # shorter than a row
+    (dict(k_stride=260), _lib.KDA_ERR_INVALID),             # 520 bytes
+    (dict(v_stride=-256), _lib.KDA_ERR_INVALID),
+    (dict(g_stride=257), _lib.KDA_ERR_INVALID),
+    (dict(beta_stride=1), _lib.KDA_ERR_INVALID),
+    (dict(H=1 << 23, n_seqs=3), _lib.KDA_ERR_UNSUPPORTED),  # N * H of 2^24 or more
+])
+def test_recurrent_rejects(lib, kw, code):  # noqa: F811
+    assert call_rec(lib, rec(**kw)) == code
+
+
+def test_recurrent_null_pointers_and_empty_calls(lib):  # noqa: F811
+    assert call_rec(lib, None) == _lib.KDA_ERR_INVALID
+    for n in ("q", "k", "v", "raw_g", "raw_beta", "A_log", "dt_bias", "state", "o"):
+        assert call_rec(lib, rec(), **{n: 1}) == _lib.KDA_ERR_INVALID
+    for n in ("raw_b", "raw_w"):
+        assert call_rec(lib, rec(), g2=True, **{n: 1}) == _lib.KDA_ERR_INVALID
+    assert call_rec(lib, rec(gate_mode=_lib.KDA_GATE_PER_HEAD), g2=True) == _lib.KDA_ERR_UNSUPPORTED
+    assert call_rec(lib, rec(b_stride=8), g2=True) == _lib.KDA_ERR_INVALID
+    # nothing to do: no launch, whatever the pointers
+    assert call_rec(lib, rec(n_seqs=0, total_tokens=0)) == _lib.KDA_OK
+    assert call_rec(lib, rec(total_tokens=0), cu=FAKE) == _lib.KDA_OK
+    assert call_rec(lib, rec(n_seqs=0, total_tokens=5), cu=FAKE) == _lib.KDA_OK
+
+
+def rec_inputs(T=3, H=2, D=64, dtype=torch.float32):
+    g = lambda *s: torch.zeros(s, dtype=dtype)  # noqa: E731
+    return dict(q=g(T, H, D), k=g(T, H, D), v=g(T, H, D), raw_g=g(T, H, D), raw_beta=g(T, H),
+                A_log=torch.zeros(H), dt_bias=torch.zeros(H, D), state=torch.zeros(T, H, D, D))
+
+
+@pytest.mark.parametrize("name,value,match", [
+    ("q", torch.zeros(3, 128), "q, k"),
+    ("k", torch.zeros(3, 2, 32), "k: expected"),
+    ("v", torch.zeros(3, 1, 64), "v: expected"),
+    ("raw_g", torch.zeros(2, 2), "raw_g: expected"),
+    ("raw_beta", torch.zeros(3, 2, 1), "raw_beta: expected"),
+    ("raw_beta", torch.zeros(3, 2, dtype=torch.float64), "raw_beta: expected"),
+    ("A_log", torch.zeros(2, dtype=torch.bfloat16), "A_log: expected"),
+    ("dt_bias", torch.zeros(2), "dt_bias: expected"),
+    ("state", torch.zeros(3, 2, 64, 64, dtype=torch.bfloat16), "state: expected"),
+    ("state", torch.zeros(3, 2, 64), "state"),
+    ("out", torch.zeros(3, 2, 32), "out: expected"),
+    ("state", torch.zeros(3, 2, 64, 64, requires_grad=True), "not differentiable"),
+    ("q", torch.zeros(3, 2, 64, requires_grad=True), "not differentiable"),
+])
+def test_recurrent_binding_refuses(name, value, match):
+    with pytest.raises(KdaError, match=match):
+        kda_recurrent(**dict(rec_inputs(), **{name: value}))
+
+
+def test_recurrent_binding_refuses_host_tensors_and_other_types():
+    with pytest.raises(KdaError, match="GPU"):
+        kda_recurrent(**rec_inputs())
+    with pytest.raises(KdaError, match="float32 or bfloat16"):
+        kda_recurrent(**{n: t.half() for n, t in rec_inputs().items()})
+    x = rec_inputs()
+    x.pop("raw_beta")
+    with pytest.raises(KdaError, match="raw_w: expected"):
+        gdn2_recurrent(raw_b=x["q"], raw_w=x["q"][:2], **x)
