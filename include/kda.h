@@ -300,6 +300,68 @@ int kda_gdn2_recurrent(const kda_recurrent_problem *p, const void *q, const void
                        const float *A_log, const float *dt_bias, const int32_t *cu_seqlens,
                        const int32_t *state_indices, float *state, void *o, void *stream);
 
+/* Activations of the gates and of the short convolution. */
+enum { KDA_ACT_NONE = 0, KDA_ACT_SIGMOID = 1, KDA_ACT_SILU = 2 };
+
+/* The norm behind the operator, with the output gate: for each row (one
+   head of one token)
+     y = o / sqrt(mean(o^2) + eps) * weight * act(gate)
+   o, gate, y [rows, V] (dtype, rows = T * H), weight [V] (fp32, shared by
+   the heads). act is KDA_ACT_SIGMOID or KDA_ACT_SILU. The backward
+   recomputes the norm from o and writes d_o, dgate [rows, V] (dtype) and
+   dweight [V] (fp32, summed in a fixed order). Pointers are 16-byte aligned;
+   outputs must not overlap inputs. rows = 0: nothing but dweight (zero) is
+   written. Errors: KDA_ERR_INVALID, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE
+   (backward), KDA_ERR_HIP. */
+typedef struct {
+  int64_t rows;       /* >= 0 */
+  int32_t V;          /* built: 64, 128, 256 */
+  int32_t dtype;      /* KDA_F32 or KDA_BF16 */
+  int32_t activation; /* KDA_ACT_SIGMOID or KDA_ACT_SILU */
+  float eps;          /* >= 0 */
+} kda_gated_norm_problem;
+int kda_gated_norm_fwd(const kda_gated_norm_problem *p, const void *o, const void *gate,
+                       const float *weight, void *y, void *stream);
+size_t kda_gated_norm_bwd_workspace_bytes(const kda_gated_norm_problem *p);
+int kda_gated_norm_bwd(const kda_gated_norm_problem *p, const void *o, const void *gate,
+                       const float *weight, const void *dy, void *d_o, void *dgate,
+                       float *dweight, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Between two blocks: the norm after one block's output y, its gate, the
+   residual scale, the residual stream x and the norm before the next block.
+   For each token
+     z = y / sqrt(mean(y^2) + eps) * w_post     (w_post NULL: z = y)
+     x_out = x + residual_scale * sigmoid(raw_gate) * z   (no gate: factor 1)
+     h = x_out / sqrt(mean(x_out^2) + eps) * w_pre
+   x, y, x_out, h [tokens, D] (dtype); w_post, w_pre [D] (fp32); raw_gate
+   (dtype) [tokens] (KDA_BLOCK_GATE_TOKEN) or [tokens, D]
+   (KDA_BLOCK_GATE_CHANNEL), NULL with KDA_BLOCK_GATE_NONE. h is formed from
+   x_out before its rounding to the dtype. The backward recomputes x_out and
+   both norms from x, y and raw_gate, takes the gradients dx_out and dh
+   (either may be NULL: zero) and writes dx, dy, dgate (dtype) and dw_post,
+   dw_pre [D] (fp32, summed in a fixed order). Pointers are 16-byte aligned
+   (a per-token gate and its gradient: aligned to their type); outputs must
+   not overlap inputs. tokens = 0: nothing but dw_post and dw_pre (zero) is
+   written. Errors as for the gated norm. */
+enum { KDA_BLOCK_GATE_NONE = 0, KDA_BLOCK_GATE_TOKEN = 1, KDA_BLOCK_GATE_CHANNEL = 2 };
+typedef struct {
+  int64_t tokens;       /* >= 0 */
+  int32_t D;            /* built: multiples of 8 up to 8192 */
+  int32_t dtype;        /* KDA_F32 or KDA_BF16 */
+  int32_t gate;         /* KDA_BLOCK_GATE_* */
+  float residual_scale; /* finite */
+  float eps;            /* >= 0 */
+} kda_block_norm_problem;
+int kda_block_norm_fwd(const kda_block_norm_problem *p, const void *x, const void *y,
+                       const void *raw_gate, const float *w_post, const float *w_pre,
+                       void *x_out, void *h, void *stream);
+size_t kda_block_norm_bwd_workspace_bytes(const kda_block_norm_problem *p);
+int kda_block_norm_bwd(const kda_block_norm_problem *p, const void *x, const void *y,
+                       const void *raw_gate, const float *w_post, const float *w_pre,
+                       const void *dx_out, const void *dh, void *dx, void *dy, void *dgate,
+                       float *dw_post, float *dw_pre, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
 /* For callers that cannot allocate device memory (code under HIP graph
    capture, tight serving loops, harnesses that forbid hipMalloc): kda_fwd
    with its workspace in a device array of KDA_NOALLOC_SCRATCH_BYTES that the

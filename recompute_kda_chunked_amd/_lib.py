@@ -21,7 +21,11 @@ EXPORTS = ("kda_fwd_workspace_bytes", "kda_bwd_workspace_bytes", "kda_check_prob
            "kda_checkpoint_bytes", "kda_bwd_segment_chunks", "kda_fwd_ex", "kda_bwd_ex",
            "kda_profile_begin", "kda_profile_end", "kda_kernel_name", "kda_status_string",
            "kda_fwd_noalloc", "kda_gdn2_fwd", "kda_gdn2_bwd", "kda_recurrent",
-           "kda_gdn2_recurrent")
+           "kda_gdn2_recurrent", "kda_gated_norm_fwd", "kda_gated_norm_bwd_workspace_bytes",
+           "kda_gated_norm_bwd", "kda_block_norm_fwd", "kda_block_norm_bwd_workspace_bytes",
+           "kda_block_norm_bwd")
+KDA_ACT_NONE, KDA_ACT_SIGMOID, KDA_ACT_SILU = range(3)
+KDA_BLOCK_GATE_NONE, KDA_BLOCK_GATE_TOKEN, KDA_BLOCK_GATE_CHANNEL = range(3)
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES
 KERNEL_COUNT = 20
 
@@ -78,6 +82,27 @@ class KdaRecurrentProblem(ctypes.Structure):
     ]
 
 
+class KdaGatedNormProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("V", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class KdaBlockNormProblem(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("gate", ctypes.c_int32),
+        ("residual_scale", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
+
+
 _lib = None
 
 
@@ -127,6 +152,20 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kda_recurrent.restype = ctypes.c_int
     lib.kda_gdn2_recurrent.argtypes = [rp] + [vp] * 12 + [vp]
     lib.kda_gdn2_recurrent.restype = ctypes.c_int
+    gp = ctypes.POINTER(KdaGatedNormProblem)
+    lib.kda_gated_norm_fwd.argtypes = [gp] + [vp] * 4 + [vp]
+    lib.kda_gated_norm_fwd.restype = ctypes.c_int
+    lib.kda_gated_norm_bwd_workspace_bytes.argtypes = [gp]
+    lib.kda_gated_norm_bwd_workspace_bytes.restype = sz
+    lib.kda_gated_norm_bwd.argtypes = [gp] + [vp] * 7 + [vp, sz, vp]
+    lib.kda_gated_norm_bwd.restype = ctypes.c_int
+    bp = ctypes.POINTER(KdaBlockNormProblem)
+    lib.kda_block_norm_fwd.argtypes = [bp] + [vp] * 7 + [vp]
+    lib.kda_block_norm_fwd.restype = ctypes.c_int
+    lib.kda_block_norm_bwd_workspace_bytes.argtypes = [bp]
+    lib.kda_block_norm_bwd_workspace_bytes.restype = sz
+    lib.kda_block_norm_bwd.argtypes = [bp] + [vp] * 12 + [vp, sz, vp]
+    lib.kda_block_norm_bwd.restype = ctypes.c_int
     lib.kda_profile_begin.argtypes = []
     lib.kda_profile_begin.restype = ctypes.c_int
     lib.kda_profile_end.argtypes = [ctypes.POINTER(ctypes.c_int32),

@@ -22,4 +22,44 @@ struct RecurrentArgs {
 };
 hipError_t launch_recurrent(int dtype, int D, bool gdn2, const RecurrentArgs& a, hipStream_t s);
 
+// Sums of `nb` partial rows of M = n0 + n1 floats, in a fixed order: the
+// first n0 columns to out0, the rest to out1 (nb = 0: zeros).
+struct ParamReduceArgs {
+  const float* partials;
+  int64_t nb;
+  int n0, n1;
+  float *out0, *out1;
+};
+hipError_t launch_param_reduce(const ParamReduceArgs& a, hipStream_t s);
+
+// The norm behind the operator; rows of V elements. Partial sums of dweight:
+// gated_norm_blocks(...) rows of V floats.
+struct GatedNormArgs {
+  int64_t rows;
+  int act;  // KDA_ACT_*
+  float eps;
+  const void *o, *gate, *dy;
+  const float* weight;
+  void *y, *d_o, *dgate;
+  float* partials;
+};
+int gated_norm_blocks(int dtype, int V, int64_t rows);
+hipError_t launch_gated_norm_fwd(int dtype, int V, const GatedNormArgs& a, hipStream_t s);
+hipError_t launch_gated_norm_bwd(int dtype, int V, const GatedNormArgs& a, hipStream_t s);
+
+// Between two blocks; rows of D elements. Partial sums: block_norm_blocks(T)
+// rows of dw_post (when w_post) then dw_pre.
+struct BlockNormArgs {
+  int64_t T;
+  int D;
+  float scale, eps;
+  const void *x, *y, *gate, *dx_out, *dh;
+  const float *w_post, *w_pre;
+  void *x_out, *h, *dx, *dy, *dgate;
+  float* partials;
+};
+int block_norm_blocks(int64_t T);
+hipError_t launch_block_norm_fwd(int dtype, int gate, const BlockNormArgs& a, hipStream_t s);
+hipError_t launch_block_norm_bwd(int dtype, int gate, const BlockNormArgs& a, hipStream_t s);
+
 }  // namespace kda

@@ -102,6 +102,36 @@ int recurrent_common(bool g2, const kda_recurrent_problem* p, const void* q, con
   return KDA_OK;
 }
 
+bool bad_eps(float eps) { return !(eps >= 0.f) || !std::isfinite(eps); }
+
+int check_gated_norm(const kda_gated_norm_problem* p) {
+  if (!p || p->rows < 0 || p->V < 1 || bad_eps(p->eps)) return KDA_ERR_INVALID;
+  if (p->rows > (int64_t{1} << 40)) return KDA_ERR_UNSUPPORTED;
+  if (!known_dtype(p->dtype) || (p->V != 64 && p->V != 128 && p->V != 256)) return KDA_ERR_UNSUPPORTED;
+  if (p->activation != KDA_ACT_SIGMOID && p->activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+size_t gated_norm_ws(const kda_gated_norm_problem* p) {
+  return static_cast<size_t>(gated_norm_blocks(p->dtype, p->V, p->rows)) * p->V * sizeof(float);
+}
+
+int check_block_norm(const kda_block_norm_problem* p) {
+  if (!p || p->tokens < 0 || p->D < 1 || bad_eps(p->eps) || !std::isfinite(p->residual_scale))
+    return KDA_ERR_INVALID;
+  if (p->tokens > (int64_t{1} << 31)) return KDA_ERR_UNSUPPORTED;
+  if (!known_dtype(p->dtype) || p->D % 8 != 0 || p->D > 8192) return KDA_ERR_UNSUPPORTED;
+  if (p->gate != KDA_BLOCK_GATE_NONE && p->gate != KDA_BLOCK_GATE_TOKEN &&
+      p->gate != KDA_BLOCK_GATE_CHANNEL)
+    return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+// Room for both weights' partial sums, whether or not w_post is given.
+size_t block_norm_ws(const kda_block_norm_problem* p) {
+  return static_cast<size_t>(block_norm_blocks(p->tokens)) * 2 * p->D * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -120,6 +150,127 @@ int kda_gdn2_recurrent(const kda_recurrent_problem* p, const void* q, const void
                        const int32_t* state_indices, float* state, void* o, void* stream) {
   return recurrent_common(true, p, q, k, v, raw_g, nullptr, raw_b, raw_w, A_log, dt_bias,
                           cu_seqlens, state_indices, state, o, stream);
+}
+
+int kda_gated_norm_fwd(const kda_gated_norm_problem* p, const void* o, const void* gate,
+                       const float* weight, void* y, void* stream) {
+  const int st = check_gated_norm(p);
+  if (st != KDA_OK) return st;
+  if (p->rows == 0) return KDA_OK;
+  if (!o || !gate || !weight || !y) return KDA_ERR_INVALID;
+  GatedNormArgs a{};
+  a.rows = p->rows;
+  a.act = p->activation;
+  a.eps = p->eps;
+  a.o = o;
+  a.gate = gate;
+  a.weight = weight;
+  a.y = y;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  KDA_TRY(KDA_KERNEL_GATED_NORM, p->rows, launch_gated_norm_fwd(p->dtype, p->V, a, s));
+  return KDA_OK;
+}
+
+size_t kda_gated_norm_bwd_workspace_bytes(const kda_gated_norm_problem* p) {
+  return check_gated_norm(p) == KDA_OK ? gated_norm_ws(p) : 0;
+}
+
+int kda_gated_norm_bwd(const kda_gated_norm_problem* p, const void* o, const void* gate,
+                       const float* weight, const void* dy, void* d_o, void* dgate,
+                       float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_gated_norm(p);
+  if (st != KDA_OK) return st;
+  if (!dweight) return KDA_ERR_INVALID;
+  if (p->rows > 0 && (!o || !gate || !weight || !dy || !d_o || !dgate || !workspace))
+    return KDA_ERR_INVALID;
+  if (workspace_bytes < gated_norm_ws(p)) return KDA_ERR_WORKSPACE;
+  GatedNormArgs a{};
+  a.rows = p->rows;
+  a.act = p->activation;
+  a.eps = p->eps;
+  a.o = o;
+  a.gate = gate;
+  a.weight = weight;
+  a.dy = dy;
+  a.d_o = d_o;
+  a.dgate = dgate;
+  a.partials = static_cast<float*>(workspace);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (p->rows > 0)
+    KDA_TRY(KDA_KERNEL_GATED_NORM_BWD, p->rows, launch_gated_norm_bwd(p->dtype, p->V, a, s));
+  const ParamReduceArgs r{a.partials, gated_norm_blocks(p->dtype, p->V, p->rows), p->V, 0, dweight,
+                          nullptr};
+  KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r, s));
+  return KDA_OK;
+}
+
+int kda_block_norm_fwd(const kda_block_norm_problem* p, const void* x, const void* y,
+                       const void* raw_gate, const float* w_post, const float* w_pre,
+                       void* x_out, void* h, void* stream) {
+  const int st = check_block_norm(p);
+  if (st != KDA_OK) return st;
+  if (p->tokens == 0) return KDA_OK;
+  if (!x || !y || !w_pre || !x_out || !h) return KDA_ERR_INVALID;
+  if ((p->gate == KDA_BLOCK_GATE_NONE) != (raw_gate == nullptr)) return KDA_ERR_INVALID;
+  BlockNormArgs a{};
+  a.T = p->tokens;
+  a.D = p->D;
+  a.scale = p->residual_scale;
+  a.eps = p->eps;
+  a.x = x;
+  a.y = y;
+  a.gate = raw_gate;
+  a.w_post = w_post;
+  a.w_pre = w_pre;
+  a.x_out = x_out;
+  a.h = h;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  KDA_TRY(KDA_KERNEL_BLOCK_NORM, p->tokens, launch_block_norm_fwd(p->dtype, p->gate, a, s));
+  return KDA_OK;
+}
+
+size_t kda_block_norm_bwd_workspace_bytes(const kda_block_norm_problem* p) {
+  return check_block_norm(p) == KDA_OK ? block_norm_ws(p) : 0;
+}
+
+int kda_block_norm_bwd(const kda_block_norm_problem* p, const void* x, const void* y,
+                       const void* raw_gate, const float* w_post, const float* w_pre,
+                       const void* dx_out, const void* dh, void* dx, void* dy, void* dgate,
+                       float* dw_post, float* dw_pre, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  const int st = check_block_norm(p);
+  if (st != KDA_OK) return st;
+  if (!dw_pre || (w_post != nullptr && !dw_post)) return KDA_ERR_INVALID;
+  if (p->tokens > 0) {
+    if (!x || !y || !w_pre || !dx || !dy || !workspace) return KDA_ERR_INVALID;
+    if ((p->gate == KDA_BLOCK_GATE_NONE) != (raw_gate == nullptr)) return KDA_ERR_INVALID;
+    if (p->gate != KDA_BLOCK_GATE_NONE && !dgate) return KDA_ERR_INVALID;
+  }
+  if (workspace_bytes < block_norm_ws(p)) return KDA_ERR_WORKSPACE;
+  BlockNormArgs a{};
+  a.T = p->tokens;
+  a.D = p->D;
+  a.scale = p->residual_scale;
+  a.eps = p->eps;
+  a.x = x;
+  a.y = y;
+  a.gate = raw_gate;
+  a.dx_out = dx_out;
+  a.dh = dh;
+  a.w_post = w_post;
+  a.w_pre = w_pre;
+  a.dx = dx;
+  a.dy = dy;
+  a.dgate = dgate;
+  a.partials = static_cast<float*>(workspace);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (p->tokens > 0)
+    KDA_TRY(KDA_KERNEL_BLOCK_NORM_BWD, p->tokens, launch_block_norm_bwd(p->dtype, p->gate, a, s));
+  const ParamReduceArgs r = w_post
+      ? ParamReduceArgs{a.partials, block_norm_blocks(p->tokens), p->D, p->D, dw_post, dw_pre}
+      : ParamReduceArgs{a.partials, block_norm_blocks(p->tokens), p->D, 0, dw_pre, nullptr};
+  KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r, s));
+  return KDA_OK;
 }
 
 }  // extern "C"

@@ -24,6 +24,7 @@
 #include "../kda_device.h"
 #include "../kda_prologue.h"
 #include "kda_layer.h"
+#include "kda_rows.h"
 
 namespace kda {
 
@@ -51,21 +52,6 @@ struct RowPart {
       return bits_to_f<TI>(u[e]);
   }
 };
-
-// Sum over the eight row groups of a wave (lanes 8, 16 and 32 apart): a
-// rotation by 8 within rows of 16 lanes, then gfx950's row and half swaps of
-// a value with itself. Every lane receives the sum.
-__device__ __forceinline__ float sum_row_groups(float x) {
-  x += dpp_mov<0x128>(x);
-  const uint32_t b = __float_as_uint(x);
-  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  const uint32_t c = __float_as_uint(x);
-  const auto h = __builtin_amdgcn_permlane32_swap(c, c, false, false);
-  return __uint_as_float(h[0]) + __uint_as_float(h[1]);
-}
-// Sum over all 64 lanes.
-__device__ __forceinline__ float sum_wave(float x) { return sum_row_groups(group_sum<8>(x)); }
 
 template <typename TI, int D, bool G2>
 __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {

@@ -1,0 +1,74 @@
+// Device helpers of the row kernels around the chunked operator: 16-byte
+// vectors of a row, and sums over a wave.
+#pragma once
+
+#include "../kda_device.h"
+
+namespace kda {
+
+// Sum over the lanes 8, 16 and 32 apart: a rotation by 8 within rows of 16
+// lanes, then gfx950's row and half swaps of a value with itself (no LDS
+// traffic). Every lane receives the sum.
+__device__ __forceinline__ float sum_row_groups(float x) {
+  x += dpp_mov<0x128>(x);
+  const uint32_t b = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  const uint32_t c = __float_as_uint(x);
+  const auto h = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+  return __uint_as_float(h[0]) + __uint_as_float(h[1]);
+}
+// Sum over all 64 lanes.
+__device__ __forceinline__ float sum_wave(float x) { return sum_row_groups(group_sum<8>(x)); }
+
+// 16 bytes of a row: 8 bf16 or 4 fp32 values.
+template <typename TI>
+struct RowVec {
+  static constexpr int N = 16 / sizeof(TI);
+  uint4 u;
+  __device__ __forceinline__ void load(const TI* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(TI* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  __device__ __forceinline__ void get(float (&f)[N]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(TI) == 2) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        f[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+  // rounds to nearest even
+  __device__ __forceinline__ void set(const float (&f)[N]) {
+    if constexpr (sizeof(TI) == 2) {
+      bf16x8 b;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = static_cast<bf16>(f[i]);
+      u = __builtin_bit_cast(uint4, b);
+    } else {
+      u = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                     __float_as_uint(f[3]));
+    }
+  }
+};
+
+// N consecutive fp32 parameters from a 16-byte aligned address.
+template <int N>
+__device__ __forceinline__ void load_params(const float* p, float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(p + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[i + j] = v[j];
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_params(float* p, const float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    *reinterpret_cast<f32x4*>(p + i) = f32x4{f[i], f[i + 1], f[i + 2], f[i + 3]};
+}
+
+}  // namespace kda

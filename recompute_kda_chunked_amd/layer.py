@@ -8,6 +8,7 @@ import contextlib
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .ops import _DT, KdaError, _gate_flags, _raise
@@ -192,3 +193,190 @@ def gdn2_recurrent(q, k, v, raw_g, raw_b, raw_w, A_log, dt_bias, state, cu_seqle
     gate sigmoid(raw_w) [T,H,V] in place of beta (per-channel raw_g only)."""
     return _recurrent("gdn2_recurrent", (raw_b, raw_w), q, k, v, raw_g, A_log, dt_bias, state,
                       cu_seqlens, state_indices, scale, lower_bound, eps, gate_mode, out)
+
+
+# ---------------------------------------------------------------------------- gated norm
+
+_GATE_ACT = {"sigmoid": _lib.KDA_ACT_SIGMOID, "silu": _lib.KDA_ACT_SILU}
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _wants_grad(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _gated_norm_problem(o, gate, weight, eps, activation, dy=None):
+    if o.dim() < 1:
+        raise KdaError("o: expected [..., V]")
+    dt, V = o.dtype, o.shape[-1]
+    if dt not in _DT:
+        raise KdaError("dtype must be float32 or bfloat16")
+    if activation not in _GATE_ACT:
+        raise KdaError("activation must be 'sigmoid' or 'silu', got %r" % (activation,))
+    _want("gate", gate, o.shape, dt)
+    _want("weight", weight, (V,), torch.float32)
+    if dy is not None:
+        _want("dy", dy, o.shape, dt)
+    dev = _dev(o, "o")
+    for name, t in (("o", o), ("gate", gate), ("weight", weight), ("dy", dy)):
+        if t is not None:
+            _placed(name, t, dev)
+    return dev, _lib.KdaGatedNormProblem(rows=o.numel() // V if V else 0, V=V, dtype=_DT[dt],
+                                         activation=_GATE_ACT[activation], eps=eps)
+
+
+def gated_norm_forward(o, gate, weight, *, eps=1e-6, activation="sigmoid"):
+    """y = o / sqrt(mean(o^2) + eps) * weight * act(gate) over the last
+    dimension (kda_gated_norm_fwd): o, gate [..., V]; weight fp32 [V]."""
+    dev, p = _gated_norm_problem(o, gate, weight, eps, activation)
+    y = torch.empty_like(o)
+    lib = _lib.load()
+    with _on(dev):
+        st = lib.kda_gated_norm_fwd(ctypes.byref(p), o.data_ptr(), gate.data_ptr(),
+                                    weight.data_ptr(), y.data_ptr(), _stream(dev))
+    _raise(lib, st, "kda_gated_norm_fwd")
+    return y
+
+
+def gated_norm_backward(o, gate, weight, dy, *, eps=1e-6, activation="sigmoid"):
+    """(do, dgate, dweight) of sum(y * dy) (kda_gated_norm_bwd), the norm
+    recomputed from o; dweight fp32."""
+    dev, p = _gated_norm_problem(o, gate, weight, eps, activation, dy)
+    lib = _lib.load()
+    do, dgate, dw = torch.empty_like(o), torch.empty_like(gate), torch.empty_like(weight)
+    nbytes = lib.kda_gated_norm_bwd_workspace_bytes(ctypes.byref(p))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with _on(dev):
+        st = lib.kda_gated_norm_bwd(ctypes.byref(p), o.data_ptr(), gate.data_ptr(),
+                                    weight.data_ptr(), dy.data_ptr(), do.data_ptr(),
+                                    dgate.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes,
+                                    _stream(dev))
+    _raise(lib, st, "kda_gated_norm_bwd")
+    return do, dgate, dw
+
+
+class GatedNormFunction(torch.autograd.Function):
+    """Autograd wrapper: saves references to the caller's inputs only."""
+
+    @staticmethod
+    def forward(ctx, o, gate, weight, eps, activation):
+        ctx.save_for_backward(o, gate, weight)
+        ctx.opts = dict(eps=eps, activation=activation)
+        return gated_norm_forward(o, gate, weight, **ctx.opts)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        return (*gated_norm_backward(*ctx.saved_tensors, dy.contiguous(), **ctx.opts), None, None)
+
+
+def gated_norm(o, gate, weight, *, eps=1e-6, activation="sigmoid"):
+    """The norm behind the operator with the output gate, differentiable:
+    y = rmsnorm(o) * weight * act(gate) over each head's V channels. o and
+    gate [T,H,V] (any leading dimensions), weight fp32 [V] shared by the
+    heads; activation 'sigmoid' or 'silu'. V is 64, 128 or 256."""
+    if _wants_grad(o, gate, weight):
+        return GatedNormFunction.apply(o, gate, weight, eps, activation)
+    return gated_norm_forward(o, gate, weight, eps=eps, activation=activation)
+
+
+# ---------------------------------------------------------------------------- block norm
+
+
+def _block_norm_problem(x, y, w_pre, w_post, raw_gate, residual_scale, eps, dx_out=None, dh=None):
+    if x.dim() != 2:
+        raise KdaError("x: expected [T,D], got %s" % (tuple(x.shape),))
+    T, D = x.shape
+    dt = x.dtype
+    if dt not in _DT:
+        raise KdaError("dtype must be float32 or bfloat16")
+    _want("y", y, (T, D), dt)
+    _want("w_pre", w_pre, (D,), torch.float32)
+    if w_post is not None:
+        _want("w_post", w_post, (D,), torch.float32)
+    kind = _lib.KDA_BLOCK_GATE_NONE
+    if raw_gate is not None:
+        per_token = raw_gate.dim() == 1
+        kind = _lib.KDA_BLOCK_GATE_TOKEN if per_token else _lib.KDA_BLOCK_GATE_CHANNEL
+        _want("raw_gate", raw_gate, (T,) if per_token else (T, D), dt)
+    for name, t in (("dx_out", dx_out), ("dh", dh)):
+        if t is not None:
+            _want(name, t, (T, D), dt)
+    dev = _dev(x, "x")
+    for name, t in (("x", x), ("y", y), ("w_pre", w_pre), ("w_post", w_post), ("dx_out", dx_out),
+                    ("dh", dh)):
+        if t is not None:
+            _placed(name, t, dev)
+    if raw_gate is not None:
+        _placed("raw_gate", raw_gate, dev,
+                16 if kind == _lib.KDA_BLOCK_GATE_CHANNEL else raw_gate.element_size())
+    return dev, _lib.KdaBlockNormProblem(tokens=T, D=D, dtype=_DT[dt], gate=kind,
+                                         residual_scale=residual_scale, eps=eps)
+
+
+def block_norm_forward(x, y, w_pre, *, w_post=None, raw_gate=None, residual_scale=1.0, eps=1e-6):
+    """(x_out, h) of kda_block_norm_fwd; see block_norm."""
+    dev, p = _block_norm_problem(x, y, w_pre, w_post, raw_gate, residual_scale, eps)
+    x_out, h = torch.empty_like(x), torch.empty_like(x)
+    lib = _lib.load()
+    with _on(dev):
+        st = lib.kda_block_norm_fwd(ctypes.byref(p), x.data_ptr(), y.data_ptr(), _ptr(raw_gate),
+                                    _ptr(w_post), w_pre.data_ptr(), x_out.data_ptr(),
+                                    h.data_ptr(), _stream(dev))
+    _raise(lib, st, "kda_block_norm_fwd")
+    return x_out, h
+
+
+def block_norm_backward(x, y, w_pre, dx_out, dh, *, w_post=None, raw_gate=None,
+                        residual_scale=1.0, eps=1e-6):
+    """(dx, dy, dw_pre, dw_post, dgate) of sum(x_out * dx_out) + sum(h * dh)
+    (kda_block_norm_bwd); either output gradient may be None (zero). dw_post
+    and dgate are None without w_post and raw_gate."""
+    dev, p = _block_norm_problem(x, y, w_pre, w_post, raw_gate, residual_scale, eps, dx_out, dh)
+    lib = _lib.load()
+    dx, dy, dw_pre = torch.empty_like(x), torch.empty_like(y), torch.empty_like(w_pre)
+    dw_post = None if w_post is None else torch.empty_like(w_post)
+    dgate = None if raw_gate is None else torch.empty_like(raw_gate)
+    nbytes = lib.kda_block_norm_bwd_workspace_bytes(ctypes.byref(p))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with _on(dev):
+        st = lib.kda_block_norm_bwd(ctypes.byref(p), x.data_ptr(), y.data_ptr(), _ptr(raw_gate),
+                                    _ptr(w_post), w_pre.data_ptr(), _ptr(dx_out), _ptr(dh),
+                                    dx.data_ptr(), dy.data_ptr(), _ptr(dgate), _ptr(dw_post),
+                                    dw_pre.data_ptr(), ws.data_ptr(), nbytes, _stream(dev))
+    _raise(lib, st, "kda_block_norm_bwd")
+    return dx, dy, dw_pre, dw_post, dgate
+
+
+class BlockNormFunction(torch.autograd.Function):
+    """Autograd wrapper: saves references to the caller's inputs only."""
+
+    @staticmethod
+    def forward(ctx, x, y, w_pre, w_post, raw_gate, residual_scale, eps):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, y, w_pre, w_post, raw_gate)
+        ctx.opts = dict(residual_scale=residual_scale, eps=eps)
+        return block_norm_forward(x, y, w_pre, w_post=w_post, raw_gate=raw_gate, **ctx.opts)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dx_out, dh):
+        x, y, w_pre, w_post, raw_gate = ctx.saved_tensors
+        dx_out, dh = (None if t is None else t.contiguous() for t in (dx_out, dh))
+        return (*block_norm_backward(x, y, w_pre, dx_out, dh, w_post=w_post, raw_gate=raw_gate,
+                                     **ctx.opts), None, None)
+
+
+def block_norm(x, y, w_pre, *, w_post=None, raw_gate=None, residual_scale=1.0, eps=1e-6):
+    """The step between two blocks, differentiable: the residual stream x
+    [T,D] takes up the block output y [T,D], normed by w_post (fp32 [D]; None:
+    as it is), times sigmoid(raw_gate) ([T] or [T,D]; None: 1) and
+    residual_scale; returns (x_out, h), h = rmsnorm(x_out) * w_pre the next
+    block's input. D is a multiple of 8, at most 8192."""
+    if _wants_grad(x, y, w_pre, w_post, raw_gate):
+        return BlockNormFunction.apply(x, y, w_pre, w_post, raw_gate, residual_scale, eps)
+    return block_norm_forward(x, y, w_pre, w_post=w_post, raw_gate=raw_gate,
+                              residual_scale=residual_scale, eps=eps)

@@ -6,7 +6,8 @@ import ctypes
 import pytest
 import torch
 
-from recompute_kda_chunked_amd import KdaError, _lib, gdn2_recurrent, kda_recurrent
+from recompute_kda_chunked_amd import (KdaError, _lib, block_norm, gated_norm, gdn2_recurrent,
+                                       kda_recurrent)
 from test_abi import lib  # noqa: F401  (fixture)
 
 FAKE, NUL = ctypes.c_void_p(0x1000), ctypes.c_void_p(0)
@@ -106,3 +107,104 @@ def test_recurrent_binding_refuses_host_tensors_and_other_types():
     x.pop("raw_beta")
     with pytest.raises(KdaError, match="raw_w: expected"):
         gdn2_recurrent(raw_b=x["q"], raw_w=x["q"][:2], **x)
+
+
+# ------------------------------------------------------------------ norms
+
+
+def gn(**kw):
+    d = dict(rows=6, V=128, dtype=_lib.KDA_BF16, activation=_lib.KDA_ACT_SIGMOID, eps=1e-6)
+    d.update(kw)
+    return _lib.KdaGatedNormProblem(**d)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), _lib.KDA_ERR_INVALID),
+    (dict(eps=-1.0), _lib.KDA_ERR_INVALID),
+    (dict(eps=float("nan")), _lib.KDA_ERR_INVALID),
+    (dict(V=0), _lib.KDA_ERR_INVALID),
+    (dict(V=96), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(dtype=2), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(activation=_lib.KDA_ACT_NONE), _lib.KDA_ERR_UNSUPPORTED),
+])
+def test_gated_norm_rejects(lib, kw, code):  # noqa: F811
+    p = ctypes.byref(gn(**kw))
+    assert lib.kda_gated_norm_fwd(p, *[FAKE] * 4, NUL) == code
+    assert lib.kda_gated_norm_bwd(p, *[FAKE] * 7, FAKE, 1 << 30, NUL) == code
+    assert lib.kda_gated_norm_bwd_workspace_bytes(p) == 0
+
+
+def test_gated_norm_null_pointers_and_workspace(lib):  # noqa: F811
+    p = ctypes.byref(gn())
+    need = lib.kda_gated_norm_bwd_workspace_bytes(p)
+    assert need > 0
+    for i in range(4):
+        args = [FAKE] * 4
+        args[i] = NUL
+        assert lib.kda_gated_norm_fwd(p, *args, NUL) == _lib.KDA_ERR_INVALID
+    for i in range(7):
+        args = [FAKE] * 7
+        args[i] = NUL
+        assert lib.kda_gated_norm_bwd(p, *args, FAKE, need, NUL) == _lib.KDA_ERR_INVALID
+    assert lib.kda_gated_norm_bwd(p, *[FAKE] * 7, FAKE, need - 1, NUL) == _lib.KDA_ERR_WORKSPACE
+    assert lib.kda_gated_norm_fwd(ctypes.byref(gn(rows=0)), *[NUL] * 4, NUL) == _lib.KDA_OK
+
+
+def bn(**kw):
+    d = dict(tokens=5, D=256, dtype=_lib.KDA_BF16, gate=_lib.KDA_BLOCK_GATE_CHANNEL,
+             residual_scale=0.5, eps=1e-6)
+    d.update(kw)
+    return _lib.KdaBlockNormProblem(**d)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tokens=-1), _lib.KDA_ERR_INVALID),
+    (dict(eps=-1.0), _lib.KDA_ERR_INVALID),
+    (dict(residual_scale=float("inf")), _lib.KDA_ERR_INVALID),
+    (dict(D=0), _lib.KDA_ERR_INVALID),
+    (dict(D=12), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(D=8200), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(dtype=2), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(gate=3), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(gate=_lib.KDA_BLOCK_GATE_NONE), _lib.KDA_ERR_INVALID),  # a gate is given
+])
+def test_block_norm_rejects(lib, kw, code):  # noqa: F811
+    p = ctypes.byref(bn(**kw))
+    assert lib.kda_block_norm_fwd(p, *[FAKE] * 7, NUL) == code
+    assert lib.kda_block_norm_bwd(p, *[FAKE] * 12, FAKE, 1 << 30, NUL) == code
+
+
+def test_block_norm_null_pointers_and_workspace(lib):  # noqa: F811
+    p = ctypes.byref(bn())
+    need = lib.kda_block_norm_bwd_workspace_bytes(p)
+    for i, optional in enumerate((0, 0, 0, 1, 0, 0, 0)):  # w_post may be null
+        args = [FAKE] * 7
+        args[i] = NUL
+        if not optional:
+            assert lib.kda_block_norm_fwd(p, *args, NUL) == _lib.KDA_ERR_INVALID
+    for i, optional in enumerate((0, 0, 0, 1, 0, 1, 1, 0, 0, 0, 0, 0)):
+        args = [FAKE] * 12
+        args[i] = NUL
+        if not optional:
+            assert lib.kda_block_norm_bwd(p, *args, FAKE, need, NUL) == _lib.KDA_ERR_INVALID
+    assert lib.kda_block_norm_bwd(p, *[FAKE] * 12, FAKE, need - 1, NUL) == _lib.KDA_ERR_WORKSPACE
+
+
+def test_norm_bindings_refuse():
+    z, w = torch.zeros(4, 2, 64), torch.zeros(64)
+    for args, kw, match in (((z, z, w), {}, "GPU"), ((z, z[:2], w), {}, "gate: expected"),
+                            ((z, z.bfloat16(), w), {}, "gate: expected"),
+                            ((z, z, w.bfloat16()), {}, "weight: expected"),
+                            ((z.half(), z.half(), w), {}, "float32 or bfloat16"),
+                            ((z, z, w), {"activation": "gelu"}, "activation")):
+        with pytest.raises(KdaError, match=match):
+            gated_norm(*args, **kw)
+    x = torch.zeros(4, 64)
+    for args, kw, match in (((x, x, w), {}, "GPU"), ((z, z, w), {}, "x: expected"),
+                            ((x, x[:3], w), {}, "y: expected"),
+                            ((x, x, w[:8]), {}, "w_pre: expected"),
+                            ((x, x, w), {"w_post": x}, "w_post: expected"),
+                            ((x, x, w), {"raw_gate": w}, "raw_gate: expected"),
+                            ((x, x, w), {"raw_gate": x[:, :8]}, "raw_gate: expected")):
+        with pytest.raises(KdaError, match=match):
+            block_norm(*args, **kw)
