@@ -362,6 +362,54 @@ int kda_block_norm_bwd(const kda_block_norm_problem *p, const void *x, const voi
                        float *dw_post, float *dw_pre, void *workspace, size_t workspace_bytes,
                        void *stream);
 
+/* The short causal convolution in front of the operator: depthwise over the
+   channels of each packed sequence, W taps, with an activation. With the rows
+   e_0 .. e_{W-2} of the sequence's initial state followed by its tokens
+   e_{W-1+t} = x_t,
+     y_t[c] = act(bias[c] + sum_j weight[c][j] e_{t+j}[c]),  j = 0 .. W-1
+   and the final state the last W-1 rows of e (of an empty or short sequence
+   some of them rows of its initial state).
+     x, y            [T, C] (dtype); x may have rows further apart (x_stride)
+     weight, bias    [C, W], [C] (fp32); bias NULL: zero
+     cu_seqlens      [N+1] (int32, device), or NULL: one sequence, N = 1.
+                     Values are clamped to [0, T]; rows of y (and dx) that
+                     belong to no sequence are zero
+     initial_state, final_state  [N, W-1, C] (dtype); NULL: zero, not written
+   The backward recomputes the activations' inputs, takes dy and d_final_state
+   (NULL: zero), and writes dx [T, C] (rows adjacent), d_initial_state (NULL:
+   not written) and dweight, dbias (fp32, summed in a fixed order; dbias NULL:
+   not written). Pointers are 16-byte aligned (cu_seqlens: 4); outputs must
+   not overlap inputs. T = 0 is allowed. Errors: KDA_ERR_INVALID,
+   KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE (backward), KDA_ERR_HIP. */
+typedef struct {
+  int32_t n_seqs;       /* N >= 0; 1 (update: T) when cu_seqlens is NULL */
+  int64_t total_tokens; /* T >= 0 */
+  int32_t C;            /* built: multiples of 8 up to 2^20 */
+  int32_t W;            /* built: 2, 3, 4 */
+  int32_t dtype;        /* KDA_F32 or KDA_BF16 */
+  int32_t activation;   /* KDA_ACT_NONE or KDA_ACT_SILU */
+  int64_t n_slots;      /* update: states in the pool */
+  int64_t x_stride;     /* elements between tokens of x, a multiple of 16
+                           bytes; 0: C */
+} kda_short_conv_problem;
+int kda_short_conv_fwd(const kda_short_conv_problem *p, const void *x, const float *weight,
+                       const float *bias, const int32_t *cu_seqlens, const void *initial_state,
+                       void *y, void *final_state, void *stream);
+size_t kda_short_conv_bwd_workspace_bytes(const kda_short_conv_problem *p);
+int kda_short_conv_bwd(const kda_short_conv_problem *p, const void *x, const float *weight,
+                       const float *bias, const int32_t *cu_seqlens, const void *initial_state,
+                       const void *dy, const void *d_final_state, void *dx, float *dweight,
+                       float *dbias, void *d_initial_state, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* The convolution's decoding form: sequence n starts from its state in a
+   pool [n_slots, W-1, C] (dtype) and leaves its last W-1 rows there.
+   cu_seqlens, state_indices, padded sequences, rows behind the last sequence
+   and capture as for kda_recurrent. */
+int kda_short_conv_update(const kda_short_conv_problem *p, const void *x, const float *weight,
+                          const float *bias, const int32_t *cu_seqlens,
+                          const int32_t *state_indices, void *state, void *y, void *stream);
+
 /* For callers that cannot allocate device memory (code under HIP graph
    capture, tight serving loops, harnesses that forbid hipMalloc): kda_fwd
    with its workspace in a device array of KDA_NOALLOC_SCRATCH_BYTES that the

@@ -23,7 +23,8 @@ EXPORTS = ("kda_fwd_workspace_bytes", "kda_bwd_workspace_bytes", "kda_check_prob
            "kda_fwd_noalloc", "kda_gdn2_fwd", "kda_gdn2_bwd", "kda_recurrent",
            "kda_gdn2_recurrent", "kda_gated_norm_fwd", "kda_gated_norm_bwd_workspace_bytes",
            "kda_gated_norm_bwd", "kda_block_norm_fwd", "kda_block_norm_bwd_workspace_bytes",
-           "kda_block_norm_bwd")
+           "kda_block_norm_bwd", "kda_short_conv_fwd", "kda_short_conv_bwd_workspace_bytes",
+           "kda_short_conv_bwd", "kda_short_conv_update")
 KDA_ACT_NONE, KDA_ACT_SIGMOID, KDA_ACT_SILU = range(3)
 KDA_BLOCK_GATE_NONE, KDA_BLOCK_GATE_TOKEN, KDA_BLOCK_GATE_CHANNEL = range(3)
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES
@@ -103,6 +104,19 @@ class KdaBlockNormProblem(ctypes.Structure):
     ]
 
 
+class KdaShortConvProblem(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("total_tokens", ctypes.c_int64),
+        ("C", ctypes.c_int32),
+        ("W", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("n_slots", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -166,6 +180,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kda_block_norm_bwd_workspace_bytes.restype = sz
     lib.kda_block_norm_bwd.argtypes = [bp] + [vp] * 12 + [vp, sz, vp]
     lib.kda_block_norm_bwd.restype = ctypes.c_int
+    cp = ctypes.POINTER(KdaShortConvProblem)
+    lib.kda_short_conv_fwd.argtypes = [cp] + [vp] * 7 + [vp]
+    lib.kda_short_conv_fwd.restype = ctypes.c_int
+    lib.kda_short_conv_bwd_workspace_bytes.argtypes = [cp]
+    lib.kda_short_conv_bwd_workspace_bytes.restype = sz
+    lib.kda_short_conv_bwd.argtypes = [cp] + [vp] * 11 + [vp, sz, vp]
+    lib.kda_short_conv_bwd.restype = ctypes.c_int
+    lib.kda_short_conv_update.argtypes = [cp] + [vp] * 7 + [vp]
+    lib.kda_short_conv_update.restype = ctypes.c_int
     lib.kda_profile_begin.argtypes = []
     lib.kda_profile_begin.restype = ctypes.c_int
     lib.kda_profile_end.argtypes = [ctypes.POINTER(ctypes.c_int32),

@@ -23,7 +23,8 @@ struct RecurrentArgs {
 hipError_t launch_recurrent(int dtype, int D, bool gdn2, const RecurrentArgs& a, hipStream_t s);
 
 // Sums of `nb` partial rows of M = n0 + n1 floats, in a fixed order: the
-// first n0 columns to out0, the rest to out1 (nb = 0: zeros).
+// first n0 columns to out0, the rest to out1 unless it is null (nb = 0:
+// zeros).
 struct ParamReduceArgs {
   const float* partials;
   int64_t nb;
@@ -61,5 +62,22 @@ struct BlockNormArgs {
 int block_norm_blocks(int64_t T);
 hipError_t launch_block_norm_fwd(int dtype, int gate, const BlockNormArgs& a, hipStream_t s);
 hipError_t launch_block_norm_bwd(int dtype, int gate, const BlockNormArgs& a, hipStream_t s);
+
+// The short convolution. Partial sums: short_conv_blocks(...) rows of dweight
+// [C][W] then dbias [C].
+struct ShortConvArgs {
+  int N, C;
+  int64_t T, xs, n_slots;
+  int act;  // KDA_ACT_*
+  const void *x, *init, *dy, *dfinal;
+  const float *weight, *bias;
+  const int32_t *cu, *idx;
+  void *y, *final_state, *dx, *dinit, *state;
+  float* partials;
+};
+int64_t short_conv_blocks(int dtype, int C, int64_t T);
+hipError_t launch_short_conv_fwd(int dtype, int W, const ShortConvArgs& a, hipStream_t s);
+hipError_t launch_short_conv_bwd(int dtype, int W, const ShortConvArgs& a, hipStream_t s);
+hipError_t launch_short_conv_update(int dtype, int W, const ShortConvArgs& a, hipStream_t s);
 
 }  // namespace kda

@@ -132,6 +132,42 @@ size_t block_norm_ws(const kda_block_norm_problem* p) {
   return static_cast<size_t>(block_norm_blocks(p->tokens)) * 2 * p->D * sizeof(float);
 }
 
+int check_short_conv(const kda_short_conv_problem* p) {
+  if (!p || p->n_seqs < 0 || p->total_tokens < 0 || p->total_tokens > 0x7fffffffLL || p->C < 1 ||
+      p->W < 1)
+    return KDA_ERR_INVALID;
+  if (!known_dtype(p->dtype) || p->C % 8 != 0 || p->C > (1 << 20) || p->W < 2 || p->W > 4)
+    return KDA_ERR_UNSUPPORTED;
+  if (p->activation != KDA_ACT_NONE && p->activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
+  if (!stride_ok(p->x_stride, p->C, p->dtype, p->total_tokens, true)) return KDA_ERR_INVALID;
+  // one thread per 16 bytes of a state row or of up to 8 tokens, below 2^32 threads
+  if (static_cast<int64_t>(p->n_seqs) * (p->W - 1) * p->C >= (int64_t{1} << 32) ||
+      p->total_tokens / 8 * p->C >= (int64_t{1} << 32))
+    return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+size_t short_conv_ws(const kda_short_conv_problem* p) {
+  return static_cast<size_t>(short_conv_blocks(p->dtype, p->C, p->total_tokens)) * p->C *
+         (p->W + 1) * sizeof(float);
+}
+
+ShortConvArgs short_conv_args(const kda_short_conv_problem* p, const void* x, const float* weight,
+                              const float* bias, const int32_t* cu) {
+  ShortConvArgs a{};
+  a.N = p->n_seqs;
+  a.C = p->C;
+  a.T = p->total_tokens;
+  a.xs = stride_of(p->x_stride, p->C);
+  a.n_slots = p->n_slots;
+  a.act = p->activation;
+  a.x = x;
+  a.weight = weight;
+  a.bias = bias;
+  a.cu = cu;
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -270,6 +306,73 @@ int kda_block_norm_bwd(const kda_block_norm_problem* p, const void* x, const voi
       ? ParamReduceArgs{a.partials, block_norm_blocks(p->tokens), p->D, p->D, dw_post, dw_pre}
       : ParamReduceArgs{a.partials, block_norm_blocks(p->tokens), p->D, 0, dw_pre, nullptr};
   KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r, s));
+  return KDA_OK;
+}
+
+int kda_short_conv_fwd(const kda_short_conv_problem* p, const void* x, const float* weight,
+                       const float* bias, const int32_t* cu_seqlens, const void* initial_state,
+                       void* y, void* final_state, void* stream) {
+  const int st = check_short_conv(p);
+  if (st != KDA_OK) return st;
+  if (!cu_seqlens && p->n_seqs != 1) return KDA_ERR_INVALID;
+  if (p->total_tokens > 0 && (!x || !weight || !y)) return KDA_ERR_INVALID;
+  if (p->total_tokens == 0 && (p->n_seqs == 0 || !final_state)) return KDA_OK;
+  ShortConvArgs a = short_conv_args(p, x, weight, bias, cu_seqlens);
+  a.init = initial_state;
+  a.y = y;
+  a.final_state = final_state;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  KDA_TRY(KDA_KERNEL_SHORT_CONV, a.T, launch_short_conv_fwd(p->dtype, p->W, a, s));
+  return KDA_OK;
+}
+
+size_t kda_short_conv_bwd_workspace_bytes(const kda_short_conv_problem* p) {
+  return check_short_conv(p) == KDA_OK ? short_conv_ws(p) : 0;
+}
+
+int kda_short_conv_bwd(const kda_short_conv_problem* p, const void* x, const float* weight,
+                       const float* bias, const int32_t* cu_seqlens, const void* initial_state,
+                       const void* dy, const void* d_final_state, void* dx, float* dweight,
+                       float* dbias, void* d_initial_state, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  const int st = check_short_conv(p);
+  if (st != KDA_OK) return st;
+  if (!cu_seqlens && p->n_seqs != 1) return KDA_ERR_INVALID;
+  if (!dweight) return KDA_ERR_INVALID;
+  if (p->total_tokens > 0 && (!x || !weight || !dy || !dx || !workspace)) return KDA_ERR_INVALID;
+  if (workspace_bytes < short_conv_ws(p)) return KDA_ERR_WORKSPACE;
+  ShortConvArgs a = short_conv_args(p, x, weight, bias, cu_seqlens);
+  a.init = initial_state;
+  a.dy = dy;
+  a.dfinal = d_final_state;
+  a.dx = dx;
+  a.dinit = d_initial_state;
+  a.partials = static_cast<float*>(workspace);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a.T > 0 || (a.N > 0 && a.dinit))
+    KDA_TRY(KDA_KERNEL_SHORT_CONV_BWD, a.T, launch_short_conv_bwd(p->dtype, p->W, a, s));
+  const ParamReduceArgs r{a.partials, short_conv_blocks(p->dtype, p->C, a.T), p->C * p->W, p->C,
+                          dweight, dbias};
+  KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r, s));
+  return KDA_OK;
+}
+
+int kda_short_conv_update(const kda_short_conv_problem* p, const void* x, const float* weight,
+                          const float* bias, const int32_t* cu_seqlens,
+                          const int32_t* state_indices, void* state, void* y, void* stream) {
+  const int st = check_short_conv(p);
+  if (st != KDA_OK) return st;
+  if (p->n_slots < 0 || p->n_slots > 0x7fffffffLL) return KDA_ERR_INVALID;
+  if (!cu_seqlens && p->total_tokens != p->n_seqs) return KDA_ERR_INVALID;
+  if (!state_indices && p->n_slots < p->n_seqs) return KDA_ERR_INVALID;
+  if (p->n_seqs == 0 || p->total_tokens == 0) return KDA_OK;
+  if (!x || !weight || !state || !y) return KDA_ERR_INVALID;
+  ShortConvArgs a = short_conv_args(p, x, weight, bias, cu_seqlens);
+  a.idx = state_indices;
+  a.state = state;
+  a.y = y;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  KDA_TRY(KDA_KERNEL_SHORT_CONV_UPDATE, p->n_seqs, launch_short_conv_update(p->dtype, p->W, a, s));
   return KDA_OK;
 }
 

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(1024) k_param_reduce(ParamReduceArgs a) {
 #pragma unroll
     for (int r = 0; r < 64; ++r) t += sm[r][cl];
     if (c < a.n0) a.out0[c] = t;
-    else a.out1[c - a.n0] = t;
+    else if (a.out1) a.out1[c - a.n0] = t;
   }
 }
 

@@ -380,3 +380,164 @@ def block_norm(x, y, w_pre, *, w_post=None, raw_gate=None, residual_scale=1.0, e
         return BlockNormFunction.apply(x, y, w_pre, w_post, raw_gate, residual_scale, eps)
     return block_norm_forward(x, y, w_pre, w_post=w_post, raw_gate=raw_gate,
                               residual_scale=residual_scale, eps=eps)
+
+
+# ---------------------------------------------------------------------------- short convolution
+
+_CONV_ACT = {"silu": _lib.KDA_ACT_SILU, "none": _lib.KDA_ACT_NONE, None: _lib.KDA_ACT_NONE}
+
+
+def _conv_problem(x, weight, bias, activation, **tensors):
+    """(device, problem without its sequences) of a convolution over x [T,C];
+    `tensors`: further arguments, name = (tensor or None, shape)."""
+    if x.dim() != 2 or weight.dim() != 2:
+        raise KdaError("x: expected [T,C], weight: [C,W]")
+    T, C = x.shape
+    dt, W = x.dtype, weight.shape[1]
+    if dt not in _DT:
+        raise KdaError("dtype must be float32 or bfloat16")
+    if activation not in _CONV_ACT:
+        raise KdaError("activation must be 'silu' or 'none', got %r" % (activation,))
+    _want("weight", weight, (C, W), torch.float32)
+    if bias is not None:
+        _want("bias", bias, (C,), torch.float32)
+    for name, (t, shape) in tensors.items():
+        if t is not None:
+            _want(name, t, shape, dt)
+    dev = _dev(x, "x")
+    p = _lib.KdaShortConvProblem(total_tokens=T, C=C, W=W, dtype=_DT[dt],
+                                 activation=_CONV_ACT[activation],
+                                 x_stride=_rows("x", x, dev, True))
+    _placed("weight", weight, dev)
+    if bias is not None:
+        _placed("bias", bias, dev)
+    for name, (t, shape) in tensors.items():
+        if t is not None:
+            _placed(name, t, dev)
+    return dev, p
+
+
+def _conv_seqs(cu_seqlens):
+    if cu_seqlens is None:
+        return 1
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.dtype is not torch.int32:
+        raise KdaError("cu_seqlens: expected int32 [N+1], got %s %s"
+                       % (tuple(cu_seqlens.shape), cu_seqlens.dtype))
+    return cu_seqlens.shape[0] - 1
+
+
+def short_conv_forward(x, weight, bias=None, cu_seqlens=None, *, initial_state=None,
+                       output_final_state=False, activation="silu"):
+    """y, or (y, final_state), of kda_short_conv_fwd; see short_conv."""
+    N = _conv_seqs(cu_seqlens)
+    shape = (N, weight.shape[-1] - 1, x.shape[-1])
+    dev, p = _conv_problem(x, weight, bias, activation, initial_state=(initial_state, shape))
+    if cu_seqlens is not None:
+        _placed("cu_seqlens", cu_seqlens, dev, 4)
+    p.n_seqs = N
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    final = torch.empty(shape, dtype=x.dtype, device=dev) if output_final_state else None
+    lib = _lib.load()
+    with _on(dev):
+        st = lib.kda_short_conv_fwd(ctypes.byref(p), x.data_ptr(), weight.data_ptr(), _ptr(bias),
+                                    _ptr(cu_seqlens), _ptr(initial_state), y.data_ptr(),
+                                    _ptr(final), _stream(dev))
+    _raise(lib, st, "kda_short_conv_fwd")
+    return (y, final) if output_final_state else y
+
+
+def short_conv_backward(x, weight, bias, dy, cu_seqlens=None, *, initial_state=None,
+                        d_final_state=None, activation="silu"):
+    """(dx, dweight, dbias, d_initial_state) of sum(y * dy) + sum(final_state
+    * d_final_state) (kda_short_conv_bwd); dbias and d_initial_state are None
+    without bias and initial_state."""
+    N = _conv_seqs(cu_seqlens)
+    shape = (N, weight.shape[-1] - 1, x.shape[-1])
+    dev, p = _conv_problem(x, weight, bias, activation, dy=(dy, x.shape),
+                           initial_state=(initial_state, shape),
+                           d_final_state=(d_final_state, shape))
+    if cu_seqlens is not None:
+        _placed("cu_seqlens", cu_seqlens, dev, 4)
+    p.n_seqs = N
+    lib = _lib.load()
+    dx, dw = torch.empty(x.shape, dtype=x.dtype, device=dev), torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    dinit = None if initial_state is None else torch.empty_like(initial_state)
+    nbytes = lib.kda_short_conv_bwd_workspace_bytes(ctypes.byref(p))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with _on(dev):
+        st = lib.kda_short_conv_bwd(ctypes.byref(p), x.data_ptr(), weight.data_ptr(), _ptr(bias),
+                                    _ptr(cu_seqlens), _ptr(initial_state), dy.data_ptr(),
+                                    _ptr(d_final_state), dx.data_ptr(), dw.data_ptr(), _ptr(db),
+                                    _ptr(dinit), ws.data_ptr(), nbytes, _stream(dev))
+    _raise(lib, st, "kda_short_conv_bwd")
+    return dx, dw, db, dinit
+
+
+class ShortConvFunction(torch.autograd.Function):
+    """Autograd wrapper: saves references to the caller's inputs only."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, cu_seqlens, initial_state, final, activation):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, weight, bias, cu_seqlens, initial_state)
+        ctx.activation = activation
+        return short_conv_forward(x, weight, bias, cu_seqlens, initial_state=initial_state,
+                                  output_final_state=final, activation=activation)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dfinal=None):
+        x, weight, bias, cu, init = ctx.saved_tensors
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
+        dfinal = None if dfinal is None else dfinal.contiguous()
+        dx, dw, db, dinit = short_conv_backward(x, weight, bias, dy, cu, initial_state=init,
+                                                d_final_state=dfinal, activation=ctx.activation)
+        return dx, dw, db, None, dinit, None, None
+
+
+def short_conv(x, weight, bias=None, cu_seqlens=None, *, initial_state=None,
+               output_final_state=False, activation="silu"):
+    """The short causal convolution in front of the operator, differentiable:
+    y [T,C] depthwise over the channels of x [T,C] within each packed sequence
+    (cu_seqlens int32 [N+1] on the device; None: one sequence), then SiLU
+    ('none': none). weight fp32 [C,W], W 2 to 4, the last tap on the token
+    itself; bias fp32 [C] or None; C a multiple of 8. initial_state [N,W-1,C]
+    (x's dtype): the rows before each sequence (None: zero). With
+    output_final_state returns (y, final_state), final_state the last W-1 rows
+    of each sequence, from which the next call or short_conv_update goes on.
+    Rows of y behind the last sequence are zero."""
+    if _wants_grad(x, weight, bias, initial_state):
+        return ShortConvFunction.apply(x, weight, bias, cu_seqlens, initial_state,
+                                       output_final_state, activation)
+    return short_conv_forward(x, weight, bias, cu_seqlens, initial_state=initial_state,
+                              output_final_state=output_final_state, activation=activation)
+
+
+def short_conv_update(x, weight, bias, state, cu_seqlens=None, *, state_indices=None,
+                      activation="silu", out=None):
+    """The convolution's decoding form: y [T,C] with the rows before each
+    sequence in a pool `state` [slots,W-1,C] (x's dtype; short_conv's final
+    states serve as they are), which is updated in place. cu_seqlens,
+    state_indices, padded sequences and rows behind the last sequence as for
+    kda_recurrent. Not differentiable."""
+    if state.dim() != 3:
+        raise KdaError("state: expected [slots,W-1,C], got %s" % (tuple(state.shape),))
+    _no_grad("short_conv_update", "train with short_conv", (x, weight, bias, state))
+    dev, p = _conv_problem(x, weight, bias, activation,
+                           state=(state, (state.shape[0], weight.shape[-1] - 1, x.shape[-1])),
+                           out=(out, x.shape))
+    p.n_seqs = _seqs(cu_seqlens, state_indices, x.shape[0], state.shape[0], dev)
+    p.n_slots = state.shape[0]
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _apart("out", out, [t for t in (x, weight, bias, state, cu_seqlens, state_indices)
+                            if t is not None])
+    lib = _lib.load()
+    with _on(dev):
+        st = lib.kda_short_conv_update(ctypes.byref(p), x.data_ptr(), weight.data_ptr(),
+                                       _ptr(bias), _ptr(cu_seqlens), _ptr(state_indices),
+                                       state.data_ptr(), out.data_ptr(), _stream(dev))
+    _raise(lib, st, "kda_short_conv_update")
+    return out

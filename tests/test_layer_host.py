@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from recompute_kda_chunked_amd import (KdaError, _lib, block_norm, gated_norm, gdn2_recurrent,
-                                       kda_recurrent)
+                                       kda_recurrent, short_conv, short_conv_update)
 from test_abi import lib  # noqa: F401  (fixture)
 
 FAKE, NUL = ctypes.c_void_p(0x1000), ctypes.c_void_p(0)
@@ -208,3 +208,85 @@ def test_norm_bindings_refuse():
                             ((x, x, w), {"raw_gate": x[:, :8]}, "raw_gate: expected")):
         with pytest.raises(KdaError, match=match):
             block_norm(*args, **kw)
+
+
+# ------------------------------------------------------------------ short convolution
+
+
+def sc(**kw):
+    d = dict(n_seqs=2, total_tokens=9, C=64, W=4, dtype=_lib.KDA_BF16, activation=_lib.KDA_ACT_SILU,
+             n_slots=4, x_stride=0)
+    d.update(kw)
+    return _lib.KdaShortConvProblem(**d)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_seqs=-1), _lib.KDA_ERR_INVALID),
+    (dict(total_tokens=-1), _lib.KDA_ERR_INVALID),
+    (dict(C=0), _lib.KDA_ERR_INVALID),
+    (dict(C=60), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(C=(1 << 20) + 8), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(W=1), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(W=5), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(W=0), _lib.KDA_ERR_INVALID),
+    (dict(dtype=2), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(activation=_lib.KDA_ACT_SIGMOID), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(x_stride=56), _lib.KDA_ERR_INVALID),
+    (dict(x_stride=68), _lib.KDA_ERR_INVALID),
+    (dict(C=1 << 20, total_tokens=1 << 16), _lib.KDA_ERR_UNSUPPORTED),
+])
+def test_short_conv_rejects(lib, kw, code):  # noqa: F811
+    p = ctypes.byref(sc(**kw))
+    assert lib.kda_short_conv_fwd(p, *[FAKE] * 7, NUL) == code
+    assert lib.kda_short_conv_bwd(p, *[FAKE] * 11, FAKE, 1 << 40, NUL) == code
+    assert lib.kda_short_conv_update(p, *[FAKE] * 7, NUL) == code
+    assert lib.kda_short_conv_bwd_workspace_bytes(p) == 0
+
+
+def test_short_conv_null_pointers_sequences_and_workspace(lib):  # noqa: F811
+    p = ctypes.byref(sc())
+    need = lib.kda_short_conv_bwd_workspace_bytes(p)
+    for i, optional in enumerate((0, 0, 1, 0, 1, 0, 1)):  # x weight bias cu init y final
+        args = [FAKE] * 7
+        args[i] = NUL
+        if not optional:  # without cu_seqlens there is one sequence
+            assert lib.kda_short_conv_fwd(p, *args, NUL) == _lib.KDA_ERR_INVALID
+    for i, optional in enumerate((0, 0, 1, 0, 1, 0, 1, 0, 0, 1, 1)):
+        args = [FAKE] * 11
+        args[i] = NUL
+        if not optional:
+            assert lib.kda_short_conv_bwd(p, *args, FAKE, need, NUL) == _lib.KDA_ERR_INVALID
+    assert lib.kda_short_conv_bwd(p, *[FAKE] * 11, FAKE, need - 1, NUL) == _lib.KDA_ERR_WORKSPACE
+    for i, optional in enumerate((0, 0, 1, 0, 1, 0, 0)):  # x weight bias cu idx state y
+        args = [FAKE] * 7
+        args[i] = NUL
+        if not optional:  # without cu_seqlens there are as many sequences as tokens
+            assert lib.kda_short_conv_update(p, *args, NUL) == _lib.KDA_ERR_INVALID
+    few = ctypes.byref(sc(n_slots=1))
+    assert lib.kda_short_conv_update(few, FAKE, FAKE, FAKE, FAKE, NUL, FAKE, FAKE, NUL) == _lib.KDA_ERR_INVALID
+    none = ctypes.byref(sc(n_seqs=0, total_tokens=0))
+    assert lib.kda_short_conv_update(none, *[NUL] * 7, NUL) == _lib.KDA_OK
+    assert lib.kda_short_conv_fwd(none, NUL, NUL, NUL, FAKE, NUL, NUL, NUL, NUL) == _lib.KDA_OK
+
+
+def test_short_conv_binding_refuses():
+    x, w, b = torch.zeros(5, 64), torch.zeros(64, 4), torch.zeros(64)
+    cu, st = torch.zeros(3, dtype=torch.int32), torch.zeros(2, 3, 64)
+    for args, kw, match in (((x, w, b, cu), {}, "GPU"), ((x[0], w, b, cu), {}, "x: expected"),
+                            ((x, w[:8], b, cu), {}, "weight: expected"),
+                            ((x, w.bfloat16(), b, cu), {}, "weight: expected"),
+                            ((x, w, b[:8], cu), {}, "bias: expected"),
+                            ((x, w, b, cu.long()), {}, "cu_seqlens"),
+                            ((x, w, b, cu), {"initial_state": st[:1]}, "initial_state: expected"),
+                            ((x, w, b, cu), {"initial_state": st.bfloat16()}, "initial_state: expected"),
+                            ((x.half(), w, b, cu), {}, "float32 or bfloat16"),
+                            ((x, w, b, cu), {"activation": "relu"}, "activation")):
+        with pytest.raises(KdaError, match=match):
+            short_conv(*args, **kw)
+    for args, kw, match in (((x, w, b, st), {}, "GPU"), ((x, w, b, st[0]), {}, "state: expected"),
+                            ((x, w, b, st[:, :2]), {}, "state: expected"),
+                            ((x, w, b, st.bfloat16()), {}, "state: expected"),
+                            ((x, w, b, st), {"out": x[:4]}, "out: expected"),
+                            ((x.clone().requires_grad_(True), w, b, st), {}, "not differentiable")):
+        with pytest.raises(KdaError, match=match):
+            short_conv_update(*args, **kw)
