@@ -6,10 +6,13 @@
 //   p_t = bias + sum_j w_j e_{t+j},  y_t = act(p_t)
 //   dp_t = dy_t act'(p_t),  de_r = sum_j w_j dp_{r-j} (+ the final state's
 //   gradient on the last W-1 rows),  dw_j = sum_t dp_t e_{t+j}
-// All are bound by HBM (about 10 operations per element and direction). A
-// thread takes 16 bytes of channels over a run of consecutive tokens, the
-// last W-1 rows in registers, so that each row is read once and W-1 rows
-// before (and, backward, behind) the run again.
+// All are bound by HBM (about 10 operations per element and direction). In
+// the packed forms a wave takes 256 channels, four per lane, over a run of
+// consecutive tokens, the rows it still needs in registers, so that each row
+// is read once and W-1 rows before (and, backward, behind) the run again. One
+// run per wave keeps every decision about sequences in scalar registers. Four
+// channels per lane rather than eight halve the registers (the backward keeps
+// 4 W + 2 values per channel), so more waves cover the loads' latency.
 #include "../kda_internal.h"
 #include "kda.h"
 #include "kda_layer.h"
@@ -20,166 +23,161 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRuns = kThreads / 64;  // waves, and runs, per block
+constexpr int kLaneCh = 4;            // channels per lane
+constexpr int kWaveCh = 64 * kLaneCh;
+constexpr int kAhead = 4;             // tokens loaded together, one such group ahead
 
-// Threads side by side on the channels of a row (a power of two up to a
-// wave); the block's others take further runs.
-int channel_lanes(int nvec) {
-  int cl = 8;
-  while (cl < 64 && cl < nvec) cl *= 2;
-  return cl;
-}
-
-// How a launch covers [T][C]: `cl` channel lanes, runs of `R` tokens, ncb
-// blocks across the channels times nrb along the tokens.
+// How a launch covers [T][C]: runs of `R` tokens, ncb blocks across the
+// channels times nrb along the tokens.
 struct Cover {
-  int cl, R, ncb;
+  int R, ncb;
   int64_t nrb;
 };
-Cover cover(int nvec, int64_t T, int maxR, int64_t want) {
-  Cover c;
-  c.cl = channel_lanes(nvec);
-  c.ncb = (nvec + c.cl - 1) / c.cl;
-  c.R = maxR;
-  while (c.R > 8 && nvec * ((T + c.R - 1) / c.R) < want) c.R /= 2;
-  const int64_t runs = (T + c.R - 1) / c.R, rpb = kThreads / c.cl;
-  c.nrb = (runs + rpb - 1) / rpb;
-  return c;
-}
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // Bounds [s, e) of sequence n, inside [0, T] whatever cu_seqlens holds.
 struct Bounds {
-  int64_t s, e;
+  int s, e;
 };
 __device__ __forceinline__ Bounds bounds(const ShortConvArgs& a, int n) {
-  if (!a.cu) return Bounds{0, a.T};
-  int64_t s = a.cu[n], e = a.cu[n + 1];
-  s = s < 0 ? 0 : (s > a.T ? a.T : s);
-  e = e > a.T ? a.T : e;
+  const int T = static_cast<int>(a.T);
+  if (!a.cu) return Bounds{0, T};
+  int s = a.cu[n], e = a.cu[n + 1];
+  s = s < 0 ? 0 : (s > T ? T : s);
+  e = e > T ? T : e;
   return Bounds{s, e < s ? s : e};
 }
+__device__ __forceinline__ Bounds uniform_bounds(const ShortConvArgs& a, int n) {
+  const Bounds q = bounds(a, n);
+  return Bounds{uniform(q.s), uniform(q.e)};
+}
+// The sequence of token t (the one before it, if t lies in none).
+__device__ __forceinline__ int seq_of(const ShortConvArgs& a, int t) {
+  return a.cu && a.N > 0 ? uniform(find_seq(a.cu, a.N, t)) : 0;
+}
+
+// Four values of a row.
+template <typename TI>
+struct Row4 {
+  uint32_t u[4];
+  __device__ __forceinline__ void load(const TI* p) { load4_raw<TI>(p, u); }
+  __device__ __forceinline__ f32x4 get() const { return unpack4<TI>(u); }
+};
 
 // Row `tt` of the sequence n that starts at s (tt >= s - (W-1)): a token, or
 // a row of the initial state.
 template <typename TI, int W>
-__device__ __forceinline__ void load_row(const ShortConvArgs& a, int n, int64_t s, int64_t tt, int c,
-                                         RowVec<TI>& v) {
+__device__ __forceinline__ f32x4 row_at(const ShortConvArgs& a, int n, int s, int tt, int c) {
+  Row4<TI> v;
   if (tt >= s) {
     v.load(static_cast<const TI*>(a.x) + tt * a.xs + c);
   } else if (a.init) {
     v.load(static_cast<const TI*>(a.init) +
            (static_cast<size_t>(n) * (W - 1) + static_cast<size_t>(W - 1 - (s - tt))) * a.C + c);
   } else {
-    v.u = make_uint4(0, 0, 0, 0);
+    return zero4();
   }
+  return v.get();
 }
 
-// Taps [j][i] of the thread's channels (weight rows [C][W] in order).
-template <int N, int W>
-__device__ __forceinline__ void load_taps(const ShortConvArgs& a, int c, float (&w)[W][N], float (&b)[N]) {
-  float f[N * W];
-  load_params<N * W>(a.weight + static_cast<size_t>(c) * W, f);
+// Taps [j] of the lane's channels (weight rows [C][W] in order).
+template <int W>
+__device__ __forceinline__ void load_taps4(const ShortConvArgs& a, int c, f32x4 (&w)[W], f32x4& b) {
+  float f[4 * W];
+  load_params<4 * W>(a.weight + static_cast<size_t>(c) * W, f);
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = f[i * W + j];
-#pragma unroll
-  for (int i = 0; i < N; ++i) b[i] = 0.f;
-  if (a.bias) load_params<N>(a.bias + c, b);
+  for (int j = 0; j < W; ++j) w[j] = f32x4{f[j], f[W + j], f[2 * W + j], f[3 * W + j]};
+  b = a.bias ? *reinterpret_cast<const f32x4*>(a.bias + c) : zero4();
 }
 
-// p = bias + sum of the taps over the window's rows and the newest row x.
-template <typename TI, int W, int N = RowVec<TI>::N>
-__device__ __forceinline__ void taps(const RowVec<TI> (&win)[W - 1], const RowVec<TI>& x,
-                                     const float (&w)[W][N], const float (&b)[N], float (&p)[N]) {
+// p = bias + the taps over the W-1 rows of the window and the newest row.
+template <int W>
+__device__ __forceinline__ f32x4 taps4(const f32x4 (&win)[W - 1], const f32x4& x, const f32x4 (&w)[W],
+                                       const f32x4& b) {
+  f32x4 p = b;
 #pragma unroll
-  for (int i = 0; i < N; ++i) p[i] = b[i];
-#pragma unroll
-  for (int j = 0; j < W; ++j) {
-    float f[N];
-    if (j < W - 1) win[j < W - 1 ? j : 0].get(f);
-    else x.get(f);
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] += w[j][i] * f[i];
-  }
+  for (int j = 0; j < W - 1; ++j) p += w[j] * win[j];
+  return p + w[W - 1] * x;
 }
-template <typename TI, int W>
-__device__ __forceinline__ void shift(RowVec<TI> (&win)[W - 1], const RowVec<TI>& x) {
+template <int W>
+__device__ __forceinline__ void shift4(f32x4 (&win)[W - 1], const f32x4& x) {
 #pragma unroll
   for (int j = 0; j + 1 < W - 1; ++j) win[j] = win[j + 1];
   win[W - 2] = x;
 }
 
 // Row len + i of e for i in [0, W-1): the final state (threads past the runs'
-// blocks, one per 16 bytes).
+// blocks, one per four channels).
 template <typename TI, int W>
 __device__ __forceinline__ void copy_final(const ShortConvArgs& a, int64_t id) {
-  constexpr int N = RowVec<TI>::N;
-  const int nvec = a.C / N;
+  const int nvec = a.C / kLaneCh;
   const int64_t row = id / nvec;
-  const int c = static_cast<int>(id - row * nvec) * N;
-  const int n = static_cast<int>(row / (W - 1)), i = static_cast<int>(row % (W - 1));
+  const int c = static_cast<int>(id - row * nvec) * kLaneCh;
+  const int64_t n = row / (W - 1);
   if (n >= a.N) return;
-  const Bounds q = bounds(a, n);
-  RowVec<TI> v;
-  load_row<TI, W>(a, n, q.s, q.e - (W - 1) + i, c, v);
-  v.store(static_cast<TI*>(a.final_state) + static_cast<size_t>(row) * a.C + c);
+  const Bounds q = bounds(a, static_cast<int>(n));
+  const int tt = q.e - (W - 1) + static_cast<int>(row - n * (W - 1));
+  store4<TI>(static_cast<TI*>(a.final_state) + static_cast<size_t>(row) * a.C + c,
+             row_at<TI, W>(a, static_cast<int>(n), q.s, tt, c));
 }
 
 template <typename TI, int W>
 __global__ void __launch_bounds__(kThreads) k_short_conv(ShortConvArgs a, Cover g) {
-  using RV = RowVec<TI>;
-  constexpr int N = RV::N, U = 4;
+  constexpr int U = kAhead;
   const int64_t rb = blockIdx.x / g.ncb;
   if (rb >= g.nrb) {
     copy_final<TI, W>(a, (static_cast<int64_t>(blockIdx.x) - g.nrb * g.ncb) * kThreads + threadIdx.x);
     return;
   }
-  const int vec = static_cast<int>(blockIdx.x % g.ncb) * g.cl + threadIdx.x % g.cl;
-  const int64_t t0 = (rb * (kThreads / g.cl) + threadIdx.x / g.cl) * g.R;
-  const int64_t t1 = t0 + g.R < a.T ? t0 + g.R : a.T;
-  const int c = vec * N;
-  if (t0 >= t1 || c >= a.C) return;
-  float w[W][N], b[N];
-  load_taps<N, W>(a, c, w, b);
-  int n = a.cu && a.N > 0 ? find_seq(a.cu, a.N, static_cast<int>(t0)) : 0;
-  Bounds q = a.N > 0 ? bounds(a, n) : Bounds{0, 0};
-  RV win[W - 1];
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) win[j].u = make_uint4(0, 0, 0, 0);
-  if (t0 > q.s && t0 < q.e) {
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) load_row<TI, W>(a, n, q.s, t0 - (W - 1) + j, c, win[j]);
-  }
+  const int c = static_cast<int>(blockIdx.x % g.ncb) * kWaveCh + (threadIdx.x & 63) * kLaneCh;
+  const int64_t first = (rb * kRuns + uniform(threadIdx.x >> 6)) * g.R;
+  if (first >= a.T || c >= a.C) return;
+  const int T = static_cast<int>(a.T), t0 = static_cast<int>(first);
+  const int t1 = T - t0 > g.R ? t0 + g.R : T;
   const TI* x = static_cast<const TI*>(a.x) + c;
   TI* y = static_cast<TI*>(a.y) + c;
-  for (int64_t tb = t0; tb < t1; tb += U) {
-    RV xv[U];
+  Row4<TI> next[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) xv[u].load(x + (tb + u < t1 ? tb + u : t1 - 1) * a.xs);
+  for (int u = 0; u < U; ++u) next[u].load(x + (t1 - t0 > u ? t0 + u : t1 - 1) * a.xs);
+  f32x4 w[W], b;
+  load_taps4<W>(a, c, w, b);
+  int n = seq_of(a, t0);
+  Bounds q = a.N > 0 ? uniform_bounds(a, n) : Bounds{0, 0};
+  f32x4 win[W - 1];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j)
+    win[j] = t0 > q.s && t0 < q.e ? row_at<TI, W>(a, n, q.s, t0 - (W - 1) + j, c) : zero4();
+  for (int tb = t0; tb < t1; tb += U) {
+    Row4<TI> cur[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t t = tb + u;
+      cur[u] = next[u];
+      next[u].load(x + (t1 - tb > U + u ? tb + U + u : t1 - 1) * a.xs);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u;
       if (t >= t1) break;
       bool fresh = t == q.s;
       while (t >= q.e && n + 1 < a.N) {
-        q = bounds(a, ++n);
+        q = uniform_bounds(a, ++n);
         fresh = true;
       }
-      if (fresh && t >= q.s && t < q.e) {
+      const bool in = t >= q.s && t < q.e;
+      if (fresh && in) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) load_row<TI, W>(a, n, q.s, t - (W - 1) + j, c, win[j]);
+        for (int j = 0; j < W - 1; ++j) win[j] = row_at<TI, W>(a, n, q.s, t - (W - 1) + j, c);
       }
-      float p[N];
-      taps<TI, W>(win, xv[u], w, b, p);
+      const f32x4 xv = cur[u].get();
+      f32x4 p = taps4<W>(win, xv, w, b);
       if (a.act == KDA_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) p[i] *= sigmoidf(p[i]);
+        for (int i = 0; i < 4; ++i) p[i] *= sigmoidf(p[i]);
       }
-      RV out;
-      out.set(p);
-      if (t < q.s || t >= q.e) out.u = make_uint4(0, 0, 0, 0);  // a row of no sequence
-      out.store(y + static_cast<size_t>(t) * a.C);
-      shift<TI, W>(win, xv[u]);
+      store4<TI>(y + static_cast<size_t>(t) * a.C, in ? p : zero4());  // zero: a row of no sequence
+      shift4<W>(win, xv);
     }
   }
 }
@@ -194,145 +192,178 @@ __global__ void __launch_bounds__(kThreads) k_short_conv(ShortConvArgs a, Cover 
 // runs' blocks).
 template <typename TI, int W>
 __global__ void __launch_bounds__(kThreads) k_short_conv_bwd(ShortConvArgs a, Cover g) {
-  using RV = RowVec<TI>;
-  constexpr int N = RV::N;
-  __shared__ __align__(16) float sm[kThreads * N];
+  constexpr int U = kAhead;
+  __shared__ __align__(16) float sm[kRuns][kWaveCh];
   const int64_t rb = blockIdx.x / g.ncb;
   if (rb >= g.nrb) {
     const int64_t id = (static_cast<int64_t>(blockIdx.x) - g.nrb * g.ncb) * kThreads + threadIdx.x;
-    const int nvec = a.C / N;
-    const int64_t row = id / nvec;
-    const int n = static_cast<int>(row / (W - 1));
+    const int nvec = a.C / kLaneCh;
+    const int64_t row = id / nvec, n = row / (W - 1);
     if (n >= a.N) return;
-    const Bounds q = bounds(a, n);
+    const Bounds q = bounds(a, static_cast<int>(n));
     if (q.e > q.s) return;
-    const size_t at = static_cast<size_t>(row) * a.C + static_cast<size_t>(id - row * nvec) * N;
-    RV v;
-    v.u = make_uint4(0, 0, 0, 0);
-    if (a.dfinal) v.load(static_cast<const TI*>(a.dfinal) + at);
-    v.store(static_cast<TI*>(a.dinit) + at);
+    const size_t at = static_cast<size_t>(row) * a.C + static_cast<size_t>(id - row * nvec) * kLaneCh;
+    f32x4 v = zero4();
+    if (a.dfinal) {
+      Row4<TI> d;
+      d.load(static_cast<const TI*>(a.dfinal) + at);
+      v = d.get();
+    }
+    store4<TI>(static_cast<TI*>(a.dinit) + at, v);
     return;
   }
-  const int cl0 = threadIdx.x % g.cl, rsub = threadIdx.x / g.cl;
-  const int cb = static_cast<int>(blockIdx.x % g.ncb);
-  const int c = (cb * g.cl + cl0) * N;
-  const int64_t t0 = (rb * (kThreads / g.cl) + rsub) * g.R;
-  const int64_t t1 = t0 + g.R < a.T ? t0 + g.R : a.T;
-  float w[W][N], b[N], dw[W][N], db[N], acc[W][N];
+  const int cb = static_cast<int>(blockIdx.x % g.ncb), lane = threadIdx.x & 63;
+  const int run = uniform(threadIdx.x >> 6);
+  const int c = cb * kWaveCh + lane * kLaneCh;
+  const int64_t first = (rb * kRuns + run) * g.R;
+  f32x4 dw[W], db = zero4();
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    db[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) dw[j][i] = acc[j][i] = 0.f;
-  }
-  if (t0 < t1 && c < a.C) {
-    load_taps<N, W>(a, c, w, b);
-    int n = a.cu && a.N > 0 ? find_seq(a.cu, a.N, static_cast<int>(t0)) : 0;
-    Bounds q = a.N > 0 ? bounds(a, n) : Bounds{0, 0};
+  for (int j = 0; j < W; ++j) dw[j] = zero4();
+  if (first < a.T && c < a.C) {
+    const int T = static_cast<int>(a.T), t0 = static_cast<int>(first);
+    const int t1 = T - t0 > g.R ? t0 + g.R : T;
+    int n = seq_of(a, t0);
+    Bounds q = a.N > 0 ? uniform_bounds(a, n) : Bounds{0, 0};
+    // up to W-1 tokens behind the run, of the sequence its last token lies in
+    int stop = t1;
+    if (a.N > 0) {
+      const Bounds l = uniform_bounds(a, seq_of(a, t1 - 1));
+      if (l.s < t1 && l.e > t1) stop = l.e - t1 > W - 1 ? t1 + (W - 1) : l.e;
+    }
     const TI* x = static_cast<const TI*>(a.x) + c;
     const TI* dy = static_cast<const TI*>(a.dy) + c;
     TI* dx = static_cast<TI*>(a.dx) + c;
-    RV win[W - 1];
+    Row4<TI> nx[U], nd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = stop - t0 > u ? t0 + u : stop - 1;
+      nx[u].load(x + t * a.xs);
+      nd[u].load(dy + static_cast<size_t>(t) * a.C);
+    }
+    f32x4 w[W], b, acc[W], win[W - 1];
+    load_taps4<W>(a, c, w, b);
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc[j] = zero4();
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) win[j] = zero4();
     bool fresh = true;  // the window has to be read
     // the gradient of row r (counted from the sequence's state) is complete
-    auto emit = [&](int64_t r, const float (&v)[N], bool last) {
-      const int64_t tt = q.s + r - (W - 1);
+    auto emit = [&](int r, f32x4 v, bool last) {
+      const int tt = q.s + r - (W - 1);
       const bool token = r >= W - 1;
       if (token ? (tt < t0 || tt >= t1) : (!a.dinit || q.s < t0 || q.s >= t1)) return;
-      float f[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = v[i];
       if (last && a.dfinal) {
-        RV d;
-        float e[N];
+        Row4<TI> d;
         d.load(static_cast<const TI*>(a.dfinal) +
                (static_cast<size_t>(n) * (W - 1) + static_cast<size_t>(r - (q.e - q.s))) * a.C + c);
-        d.get(e);
-#pragma unroll
-        for (int i = 0; i < N; ++i) f[i] += e[i];
+        v += d.get();
       }
-      RV out;
-      out.set(f);
-      out.store(token ? dx + static_cast<size_t>(tt) * a.C
-                      : static_cast<TI*>(a.dinit) + (static_cast<size_t>(n) * (W - 1) + r) * a.C + c);
+      store4<TI>(token ? dx + static_cast<size_t>(tt) * a.C
+                       : static_cast<TI*>(a.dinit) + (static_cast<size_t>(n) * (W - 1) + r) * a.C + c, v);
     };
-    for (int64_t t = t0; t < t1 + (W - 1); ++t) {
-      if (t >= t1 && (t >= q.e || t >= a.T)) break;  // behind the run: only its last sequence
-      while (t >= q.e && n + 1 < a.N) {
-        q = bounds(a, ++n);
-        fresh = true;
-      }
-      if (t < q.s || t >= q.e) {  // a row of no sequence
-        if (t >= t1) break;
-        RV z;
-        z.u = make_uint4(0, 0, 0, 0);
-        z.store(dx + static_cast<size_t>(t) * a.C);
-        continue;
-      }
-      if (fresh) {
+    for (int tb = t0; tb < stop; tb += U) {
+      Row4<TI> cx[U], cd[U];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) load_row<TI, W>(a, n, q.s, t - (W - 1) + j, c, win[j]);
-        fresh = false;
+      for (int u = 0; u < U; ++u) {
+        const int t = stop - tb > U + u ? tb + U + u : stop - 1;
+        cx[u] = nx[u];
+        cd[u] = nd[u];
+        nx[u].load(x + t * a.xs);
+        nd[u].load(dy + static_cast<size_t>(t) * a.C);
       }
-      RV xv, dv;
-      xv.load(x + t * a.xs);
-      dv.load(dy + static_cast<size_t>(t) * a.C);
-      float p[N], d[N];
-      dv.get(d);
-      if (a.act == KDA_ACT_SILU) {
-        taps<TI, W>(win, xv, w, b, p);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float s = sigmoidf(p[i]);
-          d[i] *= s * (1.f + p[i] * (1.f - s));
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u;
+        if (t >= stop) break;
+        while (t >= q.e && n + 1 < a.N) {
+          q = uniform_bounds(a, ++n);
+          fresh = true;
         }
-      }
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        float f[N];
-        if (j < W - 1) win[j < W - 1 ? j : 0].get(f);
-        else xv.get(f);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          acc[j][i] += w[j][i] * d[i];
-          if (t < t1) dw[j][i] += f[i] * d[i];
+        if (t < q.s || t >= q.e) {  // a row of no sequence
+          if (t < t1) store4<TI>(dx + static_cast<size_t>(t) * a.C, zero4());
+          continue;
         }
-      }
-      if (t < t1) {
+        if (fresh) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) db[i] += d[i];
-      }
-      emit(t - q.s, acc[0], false);
+          for (int j = 0; j < W - 1; ++j) win[j] = row_at<TI, W>(a, n, q.s, t - (W - 1) + j, c);
+          fresh = false;
+        }
+        const f32x4 xv = cx[u].get();
+        f32x4 d = cd[u].get();
+        if (a.act == KDA_ACT_SILU) {
+          const f32x4 p = taps4<W>(win, xv, w, b);
 #pragma unroll
-      for (int j = 0; j < W; ++j)
+          for (int i = 0; i < 4; ++i) {
+            const float s = sigmoidf(p[i]);
+            d[i] *= s * (1.f + p[i] * (1.f - s));
+          }
+        }
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[j][i] = j + 1 < W ? acc[j + 1 < W ? j + 1 : 0][i] : 0.f;
-      shift<TI, W>(win, xv);
-      if (t == q.e - 1) {
+        for (int j = 0; j < W; ++j) acc[j] += w[j] * d;
+        if (t < t1) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-          emit(q.e - q.s + j, acc[j], true);
+          for (int j = 0; j < W - 1; ++j) dw[j] += win[j] * d;
+          dw[W - 1] += xv * d;
+          db += d;
+        }
+        emit(t - q.s, acc[0], false);
 #pragma unroll
-          for (int i = 0; i < N; ++i) acc[j][i] = 0.f;
+        for (int j = 0; j + 1 < W; ++j) acc[j] = acc[j + 1];
+        acc[W - 1] = zero4();
+        shift4<W>(win, xv);
+        if (t == q.e - 1) {
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) {
+            emit(q.e - q.s + j, acc[j], true);
+            acc[j] = zero4();
+          }
         }
       }
     }
   }
   // join the block's runs: one partial row of dweight [C][W], dbias [C]
-  const int cols = g.cl * N, runs = kThreads / g.cl;
   float* part = a.partials + static_cast<size_t>(rb) * a.C * (W + 1);
+  const int cc = cb * kWaveCh + threadIdx.x;  // a thread per channel
+  static_assert(kThreads == kWaveCh, "one channel per thread");
 #pragma unroll
   for (int j = 0; j <= W; ++j) {
     if (j) __syncthreads();
-    store_params<N>(sm + rsub * cols + cl0 * N, j < W ? dw[j < W ? j : 0] : db);
+    *reinterpret_cast<f32x4*>(&sm[run][lane * kLaneCh]) = j < W ? dw[j < W ? j : 0] : db;
     __syncthreads();
-    for (int k = threadIdx.x; k < cols; k += kThreads) {
-      const int cc = cb * cols + k;
-      if (cc >= a.C) break;
+    if (cc < a.C) {
       float t = 0.f;
-      for (int r = 0; r < runs; ++r) t += sm[r * cols + k];
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r) t += sm[r][threadIdx.x];
       part[j < W ? static_cast<size_t>(cc) * W + j : static_cast<size_t>(a.C) * W + cc] = t;
     }
+  }
+}
+
+// Taps [j][i] of a thread's 16 bytes of channels.
+template <int N, int W>
+__device__ __forceinline__ void load_taps(const ShortConvArgs& a, int c, float (&w)[W][N], float (&b)[N]) {
+  float f[N * W];
+  load_params<N * W>(a.weight + static_cast<size_t>(c) * W, f);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][i] = f[i * W + j];
+#pragma unroll
+  for (int i = 0; i < N; ++i) b[i] = 0.f;
+  if (a.bias) load_params<N>(a.bias + c, b);
+}
+template <typename TI, int W, int N = RowVec<TI>::N>
+__device__ __forceinline__ void taps(const RowVec<TI> (&win)[W - 1], const RowVec<TI>& x,
+                                     const float (&w)[W][N], const float (&b)[N], float (&p)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] = b[i];
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    float f[N];
+    if (j < W - 1) win[j < W - 1 ? j : 0].get(f);
+    else x.get(f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] += w[j][i] * f[i];
   }
 }
 
@@ -354,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a)
   if (slot < 0 || slot >= a.n_slots) {  // a padded sequence
     RV z;
     z.u = make_uint4(0, 0, 0, 0);
-    for (int64_t t = q.s; t < q.e; ++t) z.store(y + static_cast<size_t>(t) * a.C);
+    for (int t = q.s; t < q.e; ++t) z.store(y + static_cast<size_t>(t) * a.C);
     return;
   }
   TI* st = static_cast<TI*>(a.state) + static_cast<size_t>(slot) * (W - 1) * a.C + c;
@@ -363,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a)
   for (int j = 0; j < W - 1; ++j) win[j].load(st + static_cast<size_t>(j) * a.C);
   float w[W][N], b[N];
   load_taps<N, W>(a, c, w, b);
-  for (int64_t t = q.s; t < q.e; ++t) {
+  for (int t = q.s; t < q.e; ++t) {
     RV x, out;
     x.load(static_cast<const TI*>(a.x) + t * a.xs + c);
     float p[N];
@@ -374,7 +405,9 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a)
     }
     out.set(p);
     out.store(y + static_cast<size_t>(t) * a.C);
-    shift<TI, W>(win, x);
+#pragma unroll
+    for (int j = 0; j + 1 < W - 1; ++j) win[j] = win[j + 1];
+    win[W - 2] = x;
   }
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) win[j].store(st + static_cast<size_t>(j) * a.C);
@@ -382,23 +415,28 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a)
 
 enum { kFwd, kBwd, kUpdate };
 
-int vec_of(int dtype) { return dtype == 0 ? 4 : 8; }
-
-// Runs of up to 64 tokens, shorter while fewer than 2^17 threads (two waves
-// per SIMD) would run.
-Cover cover_of(int dtype, int C, int64_t T) { return cover(C / vec_of(dtype), T, 64, 1 << 17); }
+// Runs of up to 64 tokens, halved (to 8 at least) while fewer than 4096 waves
+// (four per SIMD) would run.
+Cover cover_of(int C, int64_t T) {
+  Cover c;
+  c.ncb = (C + kWaveCh - 1) / kWaveCh;
+  c.R = 64;
+  while (c.R > 8 && c.ncb * ((T + c.R - 1) / c.R) < 4096) c.R /= 2;
+  c.nrb = ((T + c.R - 1) / c.R + kRuns - 1) / kRuns;
+  return c;
+}
 
 template <typename TI, int W>
-hipError_t launch_w(int what, int dtype, const ShortConvArgs& a, hipStream_t s) {
-  const int64_t nvec = a.C / RowVec<TI>::N;
+hipError_t launch_w(int what, const ShortConvArgs& a, hipStream_t s) {
   if (what == kUpdate) {
-    const int64_t blocks = (a.N * nvec + kThreads - 1) / kThreads;
+    const int64_t blocks = (static_cast<int64_t>(a.N) * (a.C / RowVec<TI>::N) + kThreads - 1) / kThreads;
     k_short_conv_update<TI, W><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
     return hipGetLastError();
   }
-  const Cover g = cover_of(dtype, a.C, a.T);
+  const Cover g = cover_of(a.C, a.T);
   const bool ends = what == kFwd ? a.final_state != nullptr : a.dinit != nullptr;
-  const int64_t tail = ends ? (a.N * (W - 1) * nvec + kThreads - 1) / kThreads : 0;
+  const int64_t rows = static_cast<int64_t>(a.N) * (W - 1);
+  const int64_t tail = ends ? (rows * (a.C / kLaneCh) + kThreads - 1) / kThreads : 0;
   const unsigned grid = static_cast<unsigned>(g.nrb * g.ncb + tail);
   if (grid == 0) return hipSuccess;
   if (what == kFwd) k_short_conv<TI, W><<<grid, kThreads, 0, s>>>(a, g);
@@ -406,17 +444,17 @@ hipError_t launch_w(int what, int dtype, const ShortConvArgs& a, hipStream_t s) 
   return hipGetLastError();
 }
 template <typename TI>
-hipError_t launch_t(int what, int dtype, int W, const ShortConvArgs& a, hipStream_t s) {
-  return W == 2 ? launch_w<TI, 2>(what, dtype, a, s)
-                : W == 3 ? launch_w<TI, 3>(what, dtype, a, s) : launch_w<TI, 4>(what, dtype, a, s);
+hipError_t launch_t(int what, int W, const ShortConvArgs& a, hipStream_t s) {
+  return W == 2 ? launch_w<TI, 2>(what, a, s)
+                : W == 3 ? launch_w<TI, 3>(what, a, s) : launch_w<TI, 4>(what, a, s);
 }
 hipError_t launch(int what, int dtype, int W, const ShortConvArgs& a, hipStream_t s) {
-  return dtype == 0 ? launch_t<float>(what, dtype, W, a, s) : launch_t<bf16>(what, dtype, W, a, s);
+  return dtype == 0 ? launch_t<float>(what, W, a, s) : launch_t<bf16>(what, W, a, s);
 }
 
 }  // namespace
 
-int64_t short_conv_blocks(int dtype, int C, int64_t T) { return cover_of(dtype, C, T).nrb; }
+int64_t short_conv_blocks(int C, int64_t T) { return cover_of(C, T).nrb; }
 
 hipError_t launch_short_conv_fwd(int dtype, int W, const ShortConvArgs& a, hipStream_t s) {
   return launch(kFwd, dtype, W, a, s);

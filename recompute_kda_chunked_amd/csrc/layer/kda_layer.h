@@ -48,7 +48,7 @@ int gated_norm_blocks(int dtype, int V, int64_t rows);
 hipError_t launch_gated_norm_fwd(int dtype, int V, const GatedNormArgs& a, hipStream_t s);
 hipError_t launch_gated_norm_bwd(int dtype, int V, const GatedNormArgs& a, hipStream_t s);
 
-// Between two blocks; rows of D elements. Partial sums: block_norm_blocks(T)
+// Between two blocks; rows of D elements. Partial sums: block_norm_blocks(...)
 // rows of dw_post (when w_post) then dw_pre.
 struct BlockNormArgs {
   int64_t T;
@@ -59,7 +59,7 @@ struct BlockNormArgs {
   void *x_out, *h, *dx, *dy, *dgate;
   float* partials;
 };
-int block_norm_blocks(int64_t T);
+int block_norm_blocks(int dtype, int D, int64_t T);
 hipError_t launch_block_norm_fwd(int dtype, int gate, const BlockNormArgs& a, hipStream_t s);
 hipError_t launch_block_norm_bwd(int dtype, int gate, const BlockNormArgs& a, hipStream_t s);
 
@@ -75,7 +75,7 @@ struct ShortConvArgs {
   void *y, *final_state, *dx, *dinit, *state;
   float* partials;
 };
-int64_t short_conv_blocks(int dtype, int C, int64_t T);
+int64_t short_conv_blocks(int C, int64_t T);
 hipError_t launch_short_conv_fwd(int dtype, int W, const ShortConvArgs& a, hipStream_t s);
 hipError_t launch_short_conv_bwd(int dtype, int W, const ShortConvArgs& a, hipStream_t s);
 hipError_t launch_short_conv_update(int dtype, int W, const ShortConvArgs& a, hipStream_t s);

@@ -129,7 +129,7 @@ int check_block_norm(const kda_block_norm_problem* p) {
 
 // Room for both weights' partial sums, whether or not w_post is given.
 size_t block_norm_ws(const kda_block_norm_problem* p) {
-  return static_cast<size_t>(block_norm_blocks(p->tokens)) * 2 * p->D * sizeof(float);
+  return static_cast<size_t>(block_norm_blocks(p->dtype, p->D, p->tokens)) * 2 * p->D * sizeof(float);
 }
 
 int check_short_conv(const kda_short_conv_problem* p) {
@@ -140,15 +140,17 @@ int check_short_conv(const kda_short_conv_problem* p) {
     return KDA_ERR_UNSUPPORTED;
   if (p->activation != KDA_ACT_NONE && p->activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
   if (!stride_ok(p->x_stride, p->C, p->dtype, p->total_tokens, true)) return KDA_ERR_INVALID;
-  // one thread per 16 bytes of a state row or of up to 8 tokens, below 2^32 threads
-  if (static_cast<int64_t>(p->n_seqs) * (p->W - 1) * p->C >= (int64_t{1} << 32) ||
+  // token numbers in 32 bits with room for the tokens loaded ahead, and launches
+  // (a thread per four channels of a state row or of 8 tokens) below 2^32 threads
+  if (p->total_tokens > 0x7fffff00LL ||
+      static_cast<int64_t>(p->n_seqs) * (p->W - 1) * p->C >= (int64_t{1} << 32) ||
       p->total_tokens / 8 * p->C >= (int64_t{1} << 32))
     return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
 
 size_t short_conv_ws(const kda_short_conv_problem* p) {
-  return static_cast<size_t>(short_conv_blocks(p->dtype, p->C, p->total_tokens)) * p->C *
+  return static_cast<size_t>(short_conv_blocks(p->C, p->total_tokens)) * p->C *
          (p->W + 1) * sizeof(float);
 }
 
@@ -303,8 +305,8 @@ int kda_block_norm_bwd(const kda_block_norm_problem* p, const void* x, const voi
   if (p->tokens > 0)
     KDA_TRY(KDA_KERNEL_BLOCK_NORM_BWD, p->tokens, launch_block_norm_bwd(p->dtype, p->gate, a, s));
   const ParamReduceArgs r = w_post
-      ? ParamReduceArgs{a.partials, block_norm_blocks(p->tokens), p->D, p->D, dw_post, dw_pre}
-      : ParamReduceArgs{a.partials, block_norm_blocks(p->tokens), p->D, 0, dw_pre, nullptr};
+      ? ParamReduceArgs{a.partials, block_norm_blocks(p->dtype, p->D, p->tokens), p->D, p->D, dw_post, dw_pre}
+      : ParamReduceArgs{a.partials, block_norm_blocks(p->dtype, p->D, p->tokens), p->D, 0, dw_pre, nullptr};
   KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r, s));
   return KDA_OK;
 }
@@ -351,7 +353,7 @@ int kda_short_conv_bwd(const kda_short_conv_problem* p, const void* x, const flo
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (a.T > 0 || (a.N > 0 && a.dinit))
     KDA_TRY(KDA_KERNEL_SHORT_CONV_BWD, a.T, launch_short_conv_bwd(p->dtype, p->W, a, s));
-  const ParamReduceArgs r{a.partials, short_conv_blocks(p->dtype, p->C, a.T), p->C * p->W, p->C,
+  const ParamReduceArgs r{a.partials, short_conv_blocks(p->C, a.T), p->C * p->W, p->C,
                           dweight, dbias};
   KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r, s));
   return KDA_OK;

@@ -18,24 +18,37 @@ namespace {
 
 // ------------------------------------------------------------ parameter sums
 
-// Block: 16 columns x 64 row lanes; each lane sums every 64th partial row,
-// then the 64 sums of a column are added in row order. nb partial rows of M
-// columns are read once, 64 bytes at a time.
+// A block takes CL columns with 1024 / CL row lanes; each lane sums every
+// (1024 / CL)-th partial row, then the lanes' sums of a column are added in
+// order, first within groups of 16. Few columns take narrow blocks, so that
+// enough lanes share the rows.
+template <int CL>
 __global__ void __launch_bounds__(1024) k_param_reduce(ParamReduceArgs a) {
-  __shared__ float sm[64][17];
-  const int M = a.n0 + a.n1, cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
-  const int c = blockIdx.x * 16 + cl;
+  constexpr int RL = 1024 / CL;
+  __shared__ float sm[RL][CL + 1];
+  const int M = a.n0 + a.n1, cl = threadIdx.x % CL, rl = threadIdx.x / CL;
+  const int c = blockIdx.x * CL + cl;
   float s = 0.f;
-  if (c < M)
-    for (int64_t r = rl; r < a.nb; r += 64) s += a.partials[r * M + c];
+  if (c < M) {
+#pragma unroll 8
+    for (int64_t r = rl; r < a.nb; r += RL) s += a.partials[r * M + c];
+  }
   sm[rl][cl] = s;
   __syncthreads();
-  if (rl == 0 && c < M) {
-    float t = 0.f;
+  if (rl < RL / 16) {
+    s = 0.f;
 #pragma unroll
-    for (int r = 0; r < 64; ++r) t += sm[r][cl];
-    if (c < a.n0) a.out0[c] = t;
-    else if (a.out1) a.out1[c - a.n0] = t;
+    for (int r = 0; r < 16; ++r) s += sm[rl * 16 + r][cl];
+  }
+  __syncthreads();
+  if (rl < RL / 16) sm[rl][cl] = s;
+  __syncthreads();
+  if (rl == 0 && c < M) {
+    s = 0.f;
+#pragma unroll
+    for (int r = 0; r < RL / 16; ++r) s += sm[r][cl];
+    if (c < a.n0) a.out0[c] = s;
+    else if (a.out1) a.out1[c - a.n0] = s;
   }
 }
 
@@ -402,9 +415,19 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(BlockNormArgs a) {
   }
 }
 
+// A row as threads x values per thread: 8 values while 256 threads hold the
+// row so, else 16 (D <= 8192: up to 512 threads).
+struct RowShape {
+  int values, threads;
+  RowShape(int dtype, int D) : values(D <= 2048 ? 8 : 16) {
+    const int n = dtype == KDA_F32 ? 4 : 8, nvec = D / n, nv = values / n;
+    threads = ((nvec + nv - 1) / nv + 63) / 64 * 64;
+  }
+};
+
 template <typename TI, int NV, int GATE>
 hipError_t launch_block_g(bool bwd, int threads, const BlockNormArgs& a, hipStream_t s) {
-  const unsigned grid = bwd ? block_norm_blocks(a.T) : static_cast<unsigned>(a.T < (1 << 22) ? a.T : 1 << 22);
+  const unsigned grid = bwd ? block_norm_blocks(sizeof(TI) == 4 ? KDA_F32 : KDA_BF16, a.D, a.T) : static_cast<unsigned>(a.T < (1 << 22) ? a.T : 1 << 22);
   if (bwd) {
     if (a.w_post) k_block_norm_bwd<TI, NV, GATE, true><<<grid, threads, 0, s>>>(a);
     else k_block_norm_bwd<TI, NV, GATE, false><<<grid, threads, 0, s>>>(a);
@@ -415,19 +438,18 @@ hipError_t launch_block_g(bool bwd, int threads, const BlockNormArgs& a, hipStre
   return hipGetLastError();
 }
 template <typename TI, int NV>
-hipError_t launch_block_v(bool bwd, int gate, const BlockNormArgs& a, hipStream_t s) {
-  const int nvec = a.D / RowVec<TI>::N;
-  const int threads = ((nvec + NV - 1) / NV + 63) / 64 * 64;
+hipError_t launch_block_v(bool bwd, int gate, int threads, const BlockNormArgs& a, hipStream_t s) {
   if (gate == KDA_BLOCK_GATE_TOKEN) return launch_block_g<TI, NV, KDA_BLOCK_GATE_TOKEN>(bwd, threads, a, s);
   if (gate == KDA_BLOCK_GATE_CHANNEL) return launch_block_g<TI, NV, KDA_BLOCK_GATE_CHANNEL>(bwd, threads, a, s);
   return launch_block_g<TI, NV, KDA_BLOCK_GATE_NONE>(bwd, threads, a, s);
 }
-// Rows of up to 512 threads x NV vectors: 8 values per thread while 256
-// threads hold the row so, else 16 (D <= 8192).
 hipError_t launch_block(int dtype, int gate, bool bwd, const BlockNormArgs& a, hipStream_t s) {
+  const RowShape r(dtype, a.D);
   if (dtype == KDA_F32)
-    return a.D <= 2048 ? launch_block_v<float, 2>(bwd, gate, a, s) : launch_block_v<float, 4>(bwd, gate, a, s);
-  return a.D <= 2048 ? launch_block_v<bf16, 1>(bwd, gate, a, s) : launch_block_v<bf16, 2>(bwd, gate, a, s);
+    return r.values == 8 ? launch_block_v<float, 2>(bwd, gate, r.threads, a, s)
+                         : launch_block_v<float, 4>(bwd, gate, r.threads, a, s);
+  return r.values == 8 ? launch_block_v<bf16, 1>(bwd, gate, r.threads, a, s)
+                       : launch_block_v<bf16, 2>(bwd, gate, r.threads, a, s);
 }
 
 template <typename TI, int V>
@@ -453,7 +475,10 @@ int64_t gated_groups(int dtype, int V, int64_t rows) {
 }  // namespace
 
 hipError_t launch_param_reduce(const ParamReduceArgs& a, hipStream_t s) {
-  k_param_reduce<<<(a.n0 + a.n1 + 15) / 16, 1024, 0, s>>>(a);
+  const int M = a.n0 + a.n1;
+  if (M <= 1024) k_param_reduce<4><<<(M + 3) / 4, 1024, 0, s>>>(a);
+  else if (M <= 8192) k_param_reduce<16><<<(M + 15) / 16, 1024, 0, s>>>(a);
+  else k_param_reduce<64><<<(M + 63) / 64, 1024, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -461,9 +486,13 @@ hipError_t launch_param_reduce(const ParamReduceArgs& a, hipStream_t s) {
 // to hold several, few enough that their partial sums stay small.
 int gated_norm_blocks(int dtype, int V, int64_t rows) {
   const int64_t g = gated_groups(dtype, V, rows);
-  return static_cast<int>(g < 2048 ? g : 2048);
+  return static_cast<int>(g < 1024 ? g : 1024);
 }
-int block_norm_blocks(int64_t T) { return static_cast<int>(T < 768 ? T : 768); }
+int block_norm_blocks(int dtype, int D, int64_t T) {
+  const int values = RowShape(dtype, D).values;
+  const int64_t b = 256 * (values == 16 ? 8 : 16) / (RowShape(dtype, D).threads / 64);
+  return static_cast<int>(T < b ? T : b);
+}
 
 hipError_t launch_gated_norm_fwd(int dtype, int V, const GatedNormArgs& a, hipStream_t s) {
   const int64_t g = gated_groups(dtype, V, a.rows);
