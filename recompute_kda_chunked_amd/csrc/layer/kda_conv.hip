@@ -58,6 +58,17 @@ __device__ __forceinline__ int seq_of(const ShortConvArgs& a, int t) {
   return a.cu && a.N > 0 ? uniform(find_seq(a.cu, a.N, t)) : 0;
 }
 
+// The lane's channels, `lane_bytes` into a row the whole wave is at: a scalar
+// base and a 32-bit lane offset.
+template <typename TI>
+__device__ __forceinline__ const TI* in_row(const TI* row, uint32_t lane_bytes) {
+  return reinterpret_cast<const TI*>(reinterpret_cast<const char*>(row) + lane_bytes);
+}
+template <typename TI>
+__device__ __forceinline__ TI* in_row(TI* row, uint32_t lane_bytes) {
+  return reinterpret_cast<TI*>(reinterpret_cast<char*>(row) + lane_bytes);
+}
+
 // Four values of a row.
 template <typename TI>
 struct Row4 {
@@ -123,6 +134,29 @@ __device__ __forceinline__ void copy_final(const ShortConvArgs& a, int64_t id) {
              row_at<TI, W>(a, static_cast<int>(n), q.s, tt, c));
 }
 
+// The part of a run [t0, t1) that lies in one sequence: tokens [a0, a1) of
+// sequence n with bounds q. `next` walks the parts in order from token `pos`;
+// rows before a0 (and, when it returns false, all left) lie in no sequence.
+struct Part {
+  int n, a0, a1;
+  Bounds q;
+};
+__device__ __forceinline__ bool next_part(const ShortConvArgs& a, int t1, int pos, int& n, Part& p) {
+  for (; n < a.N; ++n) {
+    const Bounds q = uniform_bounds(a, n);
+    if (q.e <= pos) continue;
+    if (q.s >= t1) return false;
+    p = Part{n, q.s > pos ? q.s : pos, q.e < t1 ? q.e : t1, q};
+    ++n;
+    return true;
+  }
+  return false;
+}
+template <typename TI>
+__device__ __forceinline__ void zero_rows(TI* y, size_t stride, uint32_t lb, int from, int to) {
+  for (int t = from; t < to; ++t) store4<TI>(in_row(y + t * stride, lb), zero4());
+}
+
 template <typename TI, int W>
 __global__ void __launch_bounds__(kThreads) k_short_conv(ShortConvArgs a, Cover g) {
   constexpr int U = kAhead;
@@ -136,60 +170,59 @@ __global__ void __launch_bounds__(kThreads) k_short_conv(ShortConvArgs a, Cover 
   if (first >= a.T || c >= a.C) return;
   const int T = static_cast<int>(a.T), t0 = static_cast<int>(first);
   const int t1 = T - t0 > g.R ? t0 + g.R : T;
-  const TI* x = static_cast<const TI*>(a.x) + c;
-  TI* y = static_cast<TI*>(a.y) + c;
-  Row4<TI> next[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) next[u].load(x + (t1 - t0 > u ? t0 + u : t1 - 1) * a.xs);
+  const uint32_t lb = c * sizeof(TI);
+  const TI* x = static_cast<const TI*>(a.x);
+  TI* y = static_cast<TI*>(a.y);
+  const size_t xs = a.xs, ys = a.C;
   f32x4 w[W], b;
   load_taps4<W>(a, c, w, b);
-  int n = seq_of(a, t0);
-  Bounds q = a.N > 0 ? uniform_bounds(a, n) : Bounds{0, 0};
-  f32x4 win[W - 1];
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j)
-    win[j] = t0 > q.s && t0 < q.e ? row_at<TI, W>(a, n, q.s, t0 - (W - 1) + j, c) : zero4();
-  for (int tb = t0; tb < t1; tb += U) {
-    Row4<TI> cur[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      cur[u] = next[u];
-      next[u].load(x + (t1 - tb > U + u ? tb + U + u : t1 - 1) * a.xs);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = tb + u;
-      if (t >= t1) break;
-      bool fresh = t == q.s;
-      while (t >= q.e && n + 1 < a.N) {
-        q = uniform_bounds(a, ++n);
-        fresh = true;
-      }
-      const bool in = t >= q.s && t < q.e;
-      if (fresh && in) {
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) win[j] = row_at<TI, W>(a, n, q.s, t - (W - 1) + j, c);
-      }
-      const f32x4 xv = cur[u].get();
-      f32x4 p = taps4<W>(win, xv, w, b);
+  int n = seq_of(a, t0), pos = t0;
+  Part p;
+  while (pos < t1 && next_part(a, t1, pos, n, p)) {
+    zero_rows<TI>(y, ys, lb, pos, p.a0);
+    f32x4 win[W - 1];
+    auto step = [&](int t, const Row4<TI>& row) {
+      const f32x4 xv = row.get();
+      f32x4 v = taps4<W>(win, xv, w, b);
       if (a.act == KDA_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] *= sigmoidf(p[i]);
+        for (int i = 0; i < 4; ++i) v[i] *= sigmoidf(v[i]);
       }
-      store4<TI>(y + static_cast<size_t>(t) * a.C, in ? p : zero4());  // zero: a row of no sequence
+      store4<TI>(in_row(y + t * ys, lb), v);
       shift4<W>(win, xv);
+    };
+    Row4<TI> nx[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) nx[u].load(in_row(x + (p.a1 - p.a0 > u ? p.a0 + u : p.a1 - 1) * xs, lb));
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) win[j] = row_at<TI, W>(a, p.n, p.q.s, p.a0 - (W - 1) + j, c);
+    int t = p.a0;
+    for (; t + U <= p.a1; t += U) {
+      Row4<TI> cx[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        cx[u] = nx[u];
+        nx[u].load(in_row(x + (p.a1 - t > U + u ? t + U + u : p.a1 - 1) * xs, lb));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) step(t + u, cx[u]);
     }
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u)
+      if (t + u < p.a1) step(t + u, nx[u]);
+    pos = p.a1;
   }
+  zero_rows<TI>(y, ys, lb, pos, t1);
 }
 
 // Backward. A run owns its tokens' rows of dx, its share of dweight and dbias,
-// and the initial-state rows of the sequences that start in it. Walking its
-// tokens and up to W-1 behind them (of the same sequence), it keeps the W
-// rows whose gradient is still incomplete in `acc`: the token t adds
-// w_j dp_t to row t + j of e and completes row t. The last W-1 rows are
-// completed at the sequence's end, where the final state's gradient joins
-// them. An empty sequence's state gradient passes through (threads past the
-// runs' blocks).
+// and the initial-state rows of the sequences that start in it. In each
+// sequence it walks its tokens and, where the sequence goes on, W-1 behind
+// them, and keeps the W rows whose gradient is still incomplete in `acc`: the
+// token t adds w_j dp_t to row t + j of e and completes row t. The last W-1
+// rows are completed at the sequence's end, where the final state's gradient
+// joins them. An empty sequence's state gradient passes through (threads past
+// the runs' blocks).
 template <typename TI, int W>
 __global__ void __launch_bounds__(kThreads) k_short_conv_bwd(ShortConvArgs a, Cover g) {
   constexpr int U = kAhead;
@@ -222,104 +255,101 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_bwd(ShortConvArgs a, Co
   if (first < a.T && c < a.C) {
     const int T = static_cast<int>(a.T), t0 = static_cast<int>(first);
     const int t1 = T - t0 > g.R ? t0 + g.R : T;
-    int n = seq_of(a, t0);
-    Bounds q = a.N > 0 ? uniform_bounds(a, n) : Bounds{0, 0};
-    // up to W-1 tokens behind the run, of the sequence its last token lies in
-    int stop = t1;
-    if (a.N > 0) {
-      const Bounds l = uniform_bounds(a, seq_of(a, t1 - 1));
-      if (l.s < t1 && l.e > t1) stop = l.e - t1 > W - 1 ? t1 + (W - 1) : l.e;
-    }
-    const TI* x = static_cast<const TI*>(a.x) + c;
-    const TI* dy = static_cast<const TI*>(a.dy) + c;
-    TI* dx = static_cast<TI*>(a.dx) + c;
-    Row4<TI> nx[U], nd[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = stop - t0 > u ? t0 + u : stop - 1;
-      nx[u].load(x + t * a.xs);
-      nd[u].load(dy + static_cast<size_t>(t) * a.C);
-    }
-    f32x4 w[W], b, acc[W], win[W - 1];
+    const uint32_t lb = c * sizeof(TI);
+    const TI* x = static_cast<const TI*>(a.x);
+    const TI* dy = static_cast<const TI*>(a.dy);
+    TI* dx = static_cast<TI*>(a.dx);
+    const size_t xs = a.xs, ys = a.C;
+    f32x4 w[W], b;
     load_taps4<W>(a, c, w, b);
+    int n = seq_of(a, t0), pos = t0;
+    Part p;
+    while (pos < t1 && next_part(a, t1, pos, n, p)) {
+      zero_rows<TI>(dx, ys, lb, pos, p.a0);
+      // tokens [a1, stop) behind the run; the initial state's rows are this
+      // run's if the sequence starts here
+      const int stop = p.q.e - p.a1 > W - 1 ? p.a1 + (W - 1) : p.q.e;
+      TI* di = p.a0 == p.q.s && a.dinit ? static_cast<TI*>(a.dinit) + static_cast<size_t>(p.n) * (W - 1) * a.C
+                                        : nullptr;
+      f32x4 acc[W], win[W - 1];
 #pragma unroll
-    for (int j = 0; j < W; ++j) acc[j] = zero4();
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) win[j] = zero4();
-    bool fresh = true;  // the window has to be read
-    // the gradient of row r (counted from the sequence's state) is complete
-    auto emit = [&](int r, f32x4 v, bool last) {
-      const int tt = q.s + r - (W - 1);
-      const bool token = r >= W - 1;
-      if (token ? (tt < t0 || tt >= t1) : (!a.dinit || q.s < t0 || q.s >= t1)) return;
-      if (last && a.dfinal) {
-        Row4<TI> d;
-        d.load(static_cast<const TI*>(a.dfinal) +
-               (static_cast<size_t>(n) * (W - 1) + static_cast<size_t>(r - (q.e - q.s))) * a.C + c);
-        v += d.get();
-      }
-      store4<TI>(token ? dx + static_cast<size_t>(tt) * a.C
-                       : static_cast<TI*>(a.dinit) + (static_cast<size_t>(n) * (W - 1) + r) * a.C + c, v);
-    };
-    for (int tb = t0; tb < stop; tb += U) {
-      Row4<TI> cx[U], cd[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = stop - tb > U + u ? tb + U + u : stop - 1;
-        cx[u] = nx[u];
-        cd[u] = nd[u];
-        nx[u].load(x + t * a.xs);
-        nd[u].load(dy + static_cast<size_t>(t) * a.C);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u;
-        if (t >= stop) break;
-        while (t >= q.e && n + 1 < a.N) {
-          q = uniform_bounds(a, ++n);
-          fresh = true;
+      for (int j = 0; j < W; ++j) acc[j] = zero4();
+      // row t - (W-1) of the tokens, or before a0 of the initial state
+      auto put = [&](int t, const f32x4& v) {
+        const int tt = t - (W - 1);
+        if (tt >= p.a0) {
+          if (tt < p.a1) store4<TI>(in_row(dx + tt * ys, lb), v);
+        } else if (di) {
+          store4<TI>(in_row(di + (t - p.q.s) * ys, lb), v);
         }
-        if (t < q.s || t >= q.e) {  // a row of no sequence
-          if (t < t1) store4<TI>(dx + static_cast<size_t>(t) * a.C, zero4());
-          continue;
-        }
-        if (fresh) {
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) win[j] = row_at<TI, W>(a, n, q.s, t - (W - 1) + j, c);
-          fresh = false;
-        }
-        const f32x4 xv = cx[u].get();
-        f32x4 d = cd[u].get();
+      };
+      auto step = [&](int t, const Row4<TI>& xr, const Row4<TI>& dr, bool own) {
+        const f32x4 xv = xr.get();
+        f32x4 d = dr.get();
         if (a.act == KDA_ACT_SILU) {
-          const f32x4 p = taps4<W>(win, xv, w, b);
+          const f32x4 v = taps4<W>(win, xv, w, b);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float s = sigmoidf(p[i]);
-            d[i] *= s * (1.f + p[i] * (1.f - s));
+            const float s = sigmoidf(v[i]);
+            d[i] *= s * (1.f + v[i] * (1.f - s));
           }
         }
-#pragma unroll
-        for (int j = 0; j < W; ++j) acc[j] += w[j] * d;
-        if (t < t1) {
+        if (own) {
 #pragma unroll
           for (int j = 0; j < W - 1; ++j) dw[j] += win[j] * d;
           dw[W - 1] += xv * d;
           db += d;
         }
-        emit(t - q.s, acc[0], false);
+        put(t, acc[0] + w[0] * d);
 #pragma unroll
-        for (int j = 0; j + 1 < W; ++j) acc[j] = acc[j + 1];
+        for (int j = 0; j + 1 < W; ++j) acc[j] = acc[j + 1] + w[j + 1] * d;
         acc[W - 1] = zero4();
         shift4<W>(win, xv);
-        if (t == q.e - 1) {
+      };
+      Row4<TI> nx[U], nd[U];
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) {
-            emit(q.e - q.s + j, acc[j], true);
-            acc[j] = zero4();
+      for (int u = 0; u < U; ++u) {
+        const int tu = stop - p.a0 > u ? p.a0 + u : stop - 1;
+        nx[u].load(in_row(x + tu * xs, lb));
+        nd[u].load(in_row(dy + tu * ys, lb));
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) win[j] = row_at<TI, W>(a, p.n, p.q.s, p.a0 - (W - 1) + j, c);
+      int t = p.a0;
+      for (; t + U <= p.a1; t += U) {
+        Row4<TI> cx[U], cd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int tu = stop - t > U + u ? t + U + u : stop - 1;
+          cx[u] = nx[u];
+          cd[u] = nd[u];
+          nx[u].load(in_row(x + tu * xs, lb));
+          nd[u].load(in_row(dy + tu * ys, lb));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) step(t + u, cx[u], cd[u], true);
+      }
+      for (; t < stop; ++t) {
+        Row4<TI> xr, dr;
+        xr.load(in_row(x + t * xs, lb));
+        dr.load(in_row(dy + t * ys, lb));
+        step(t, xr, dr, t < p.a1);
+      }
+      if (stop == p.q.e) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+          f32x4 v = acc[j];
+          if (a.dfinal) {
+            Row4<TI> d;
+            d.load(in_row(static_cast<const TI*>(a.dfinal) + (static_cast<size_t>(p.n) * (W - 1) + j) * ys, lb));
+            v += d.get();
           }
+          put(stop + j, v);
         }
       }
+      pos = p.a1;
     }
+    zero_rows<TI>(dx, ys, lb, pos, t1);
   }
   // join the block's runs: one partial row of dweight [C][W], dbias [C]
   float* part = a.partials + static_cast<size_t>(rb) * a.C * (W + 1);
@@ -415,13 +445,16 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a)
 
 enum { kFwd, kBwd, kUpdate };
 
-// Runs of up to 64 tokens, halved (to 8 at least) while fewer than 4096 waves
-// (four per SIMD) would run.
+// Runs of up to 128 tokens, halved (to 8 at least) while fewer than 2048 waves
+// would run: the backward's registers let two waves per SIMD run at once, and
+// a second, part-filled round of waves costs more than longer runs save
+// (8192 x 8192 bf16, backward: 93 us with 2048 runs of 128, 101 us with 4096 of
+// 64; the forward takes 51 us either way).
 Cover cover_of(int C, int64_t T) {
   Cover c;
   c.ncb = (C + kWaveCh - 1) / kWaveCh;
-  c.R = 64;
-  while (c.R > 8 && c.ncb * ((T + c.R - 1) / c.R) < 4096) c.R /= 2;
+  c.R = 128;
+  while (c.R > 8 && c.ncb * ((T + c.R - 1) / c.R) < 2048) c.R /= 2;
   c.nrb = ((T + c.R - 1) / c.R + kRuns - 1) / kRuns;
   return c;
 }

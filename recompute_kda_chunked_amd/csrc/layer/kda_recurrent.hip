@@ -80,6 +80,40 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
     return;
   }
 
+  const int c0 = CPL * lane;
+  const size_t hc = static_cast<size_t>(h) * D + c0;
+  const float ea = expf(a.A_log[h]);
+  float db[CPL];
+#pragma unroll
+  for (int e = 0; e < CPL; ++e) db[e] = a.gate_head ? a.dt_bias[h] : a.dt_bias[hc + e];
+
+  // a token's rows, loaded one token ahead of their use
+  struct Token {
+    RowPart<TI, CPL> q, k, g, b;
+    uint32_t be, v[4], w[4];
+  };
+  auto load = [&](int64_t t, Token& x) {
+    x.q.load(static_cast<const TI*>(a.q) + t * a.qs + hc);
+    x.k.load(static_cast<const TI*>(a.k) + t * a.ks + hc);
+    if (a.gate_head) {
+      const uint32_t u = load_bits<TI>(static_cast<const TI*>(a.g) + t * a.gs + h);
+      if constexpr (CPL == 2 && sizeof(TI) == 2) x.g.u[0] = u | (u << 16);
+      else x.g.u[0] = x.g.u[CPL - 1] = u;
+    } else {
+      x.g.load(static_cast<const TI*>(a.g) + t * a.gs + hc);
+    }
+    const size_t vc = static_cast<size_t>(h) * D + col;
+    if constexpr (G2) {
+      x.b.load(static_cast<const TI*>(a.bk) + t * a.bks + hc);
+      load4_raw<TI>(static_cast<const TI*>(a.wv) + t * a.wvs + vc, x.w);
+    } else {
+      x.be = load_bits<TI>(static_cast<const TI*>(a.beta) + t * a.bes + h);
+    }
+    load4_raw<TI>(static_cast<const TI*>(a.v) + t * a.vs + vc, x.v);
+  };
+  Token next;
+  load(t0, next);
+
   // rows 32 j + 4 rg + r of the lane's four columns
   float* Sp = a.state + (static_cast<size_t>(slot) * a.H + h) * (D * D) + 4 * rg * D + col;
   f32x4 s[NJ][4];
@@ -88,34 +122,10 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) s[j][r] = *reinterpret_cast<const f32x4*>(Sp + (32 * j + r) * D);
 
-  const int c0 = CPL * lane;
-  const size_t hc = static_cast<size_t>(h) * D + c0;
-  const float ea = expf(a.A_log[h]);
-  float db[CPL];
-#pragma unroll
-  for (int e = 0; e < CPL; ++e) db[e] = a.gate_head ? a.dt_bias[h] : a.dt_bias[hc + e];
-
   for (int64_t t = t0; t < t1; ++t) {
-    RowPart<TI, CPL> q, k, g, b;
-    q.load(static_cast<const TI*>(a.q) + t * a.qs + hc);
-    k.load(static_cast<const TI*>(a.k) + t * a.ks + hc);
-    if (a.gate_head) {
-      const uint32_t x = load_bits<TI>(static_cast<const TI*>(a.g) + t * a.gs + h);
-      g.u[0] = x;
-      if constexpr (CPL == 2 && sizeof(TI) == 2) g.u[0] = x | (x << 16);
-      else if constexpr (CPL == 2) g.u[1] = x;
-    } else {
-      g.load(static_cast<const TI*>(a.g) + t * a.gs + hc);
-    }
-    uint32_t be = 0, vr[4], wr[4];
-    if constexpr (G2) {
-      b.load(static_cast<const TI*>(a.bk) + t * a.bks + hc);
-      load4_raw<TI>(static_cast<const TI*>(a.wv) + t * a.wvs + static_cast<size_t>(h) * D + col, wr);
-    } else {
-      be = load_bits<TI>(static_cast<const TI*>(a.beta) + t * a.bes + h);
-    }
-    load4_raw<TI>(static_cast<const TI*>(a.v) + t * a.vs + static_cast<size_t>(h) * D + col, vr);
-
+    const Token x = next;
+    if (t + 1 < t1) load(t + 1, next);
+    const RowPart<TI, CPL>&q = x.q, &k = x.k, &g = x.g, &b = x.b;
     // prologue: this lane's channels, then to the row layout through LDS
     float sq = 0.f, sk = 0.f, qk = 0.f;
 #pragma unroll
@@ -128,7 +138,7 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
     sk = sum_wave(sk);
     qk = sum_wave(qk);
     const float rq = a.scale / sqrtf(sq + a.eps), rk = 1.f / sqrtf(sk + a.eps);
-    const float beta = G2 ? 0.f : sigmoidf(bits_to_f<TI>(be));
+    const float beta = G2 ? 0.f : sigmoidf(bits_to_f<TI>(x.be));
     const float kq = qk * rq * rk;
 #pragma unroll
     for (int e = 0; e < CPL; ++e) {
@@ -155,11 +165,11 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
         oo += qv[r] * s[j][r];
       }
     }
-    f32x4 d = unpack4<TI>(vr);
+    f32x4 d = unpack4<TI>(x.v);
     if constexpr (G2) {
-      const f32x4 x = unpack4<TI>(wr);
+      const f32x4 wg = unpack4<TI>(x.w);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) d[r] *= sigmoidf(x[r]);
+      for (int r = 0; r < 4; ++r) d[r] *= sigmoidf(wg[r]);
     } else {
       d *= beta;
     }

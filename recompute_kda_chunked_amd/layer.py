@@ -4,7 +4,6 @@ marshalling only, as in ``ops``. Every step runs in the HIP kernels behind
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -20,20 +19,35 @@ def _dev(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
-def _on(dev: torch.device):
-    """The device's context where it is not the current one (a launch goes to
-    a stream of the current device)."""
+# The stream handle itself: torch.cuda.current_stream builds an object around
+# it, which costs about as much as the rest of a small call's checks.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(dev, name, problem, *tensors, workspace=None):
+    """An entry point on the current stream of the tensors' device (a launch
+    goes to a stream of the current device, so another one is made current)."""
+    lib = _lib.load()
+    fn = getattr(lib, name)
+    args = [None if t is None else t.data_ptr() for t in tensors]
+    if workspace is not None:
+        args += (workspace.data_ptr(), workspace.numel())
     if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+        st = fn(ctypes.byref(problem), *args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(ctypes.byref(problem), *args, _raw_stream(dev.index))
+    if st != _lib.KDA_OK:
+        _raise(lib, st, name)
 
 
-def _stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+def _workspace(dev, name, problem):
+    nbytes = getattr(_lib.load(), name + "_workspace_bytes")(ctypes.byref(problem))
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
 def _want(name, t, shape, dtype):
-    if not isinstance(t, torch.Tensor):
+    if t is None:
         raise KdaError("%s: expected a tensor of shape %s" % (name, tuple(shape)))
     if t.shape != shape or t.dtype is not dtype:
         raise KdaError("%s: expected shape %s dtype %s, got %s %s"
@@ -154,15 +168,8 @@ def _recurrent(name, gates, q, k, v, raw_g, A_log, dt_bias, state, cu_seqlens, s
         _placed("out", out, dev)
         _apart("out", out, [t for t in (q, k, v, raw_g, *gates, A_log, dt_bias, state, cu_seqlens,
                                         state_indices) if t is not None])
-    lib = _lib.load()
-    fn = lib.kda_gdn2_recurrent if g2 else lib.kda_recurrent
-    with _on(dev):
-        st = fn(ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(), raw_g.data_ptr(),
-                *[t.data_ptr() for t in gates], A_log.data_ptr(), dt_bias.data_ptr(),
-                None if cu_seqlens is None else cu_seqlens.data_ptr(),
-                None if state_indices is None else state_indices.data_ptr(),
-                state.data_ptr(), out.data_ptr(), _stream(dev))
-    _raise(lib, st, name)
+    _call(dev, "kda_gdn2_recurrent" if g2 else "kda_recurrent", p, q, k, v, raw_g, *gates, A_log,
+          dt_bias, cu_seqlens, state_indices, state, out)
     return out
 
 
@@ -200,10 +207,6 @@ def gdn2_recurrent(q, k, v, raw_g, raw_b, raw_w, A_log, dt_bias, state, cu_seqle
 _GATE_ACT = {"sigmoid": _lib.KDA_ACT_SIGMOID, "silu": _lib.KDA_ACT_SILU}
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _wants_grad(*tensors):
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
@@ -233,11 +236,7 @@ def gated_norm_forward(o, gate, weight, *, eps=1e-6, activation="sigmoid"):
     dimension (kda_gated_norm_fwd): o, gate [..., V]; weight fp32 [V]."""
     dev, p = _gated_norm_problem(o, gate, weight, eps, activation)
     y = torch.empty_like(o)
-    lib = _lib.load()
-    with _on(dev):
-        st = lib.kda_gated_norm_fwd(ctypes.byref(p), o.data_ptr(), gate.data_ptr(),
-                                    weight.data_ptr(), y.data_ptr(), _stream(dev))
-    _raise(lib, st, "kda_gated_norm_fwd")
+    _call(dev, "kda_gated_norm_fwd", p, o, gate, weight, y)
     return y
 
 
@@ -245,16 +244,9 @@ def gated_norm_backward(o, gate, weight, dy, *, eps=1e-6, activation="sigmoid"):
     """(do, dgate, dweight) of sum(y * dy) (kda_gated_norm_bwd), the norm
     recomputed from o; dweight fp32."""
     dev, p = _gated_norm_problem(o, gate, weight, eps, activation, dy)
-    lib = _lib.load()
     do, dgate, dw = torch.empty_like(o), torch.empty_like(gate), torch.empty_like(weight)
-    nbytes = lib.kda_gated_norm_bwd_workspace_bytes(ctypes.byref(p))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    with _on(dev):
-        st = lib.kda_gated_norm_bwd(ctypes.byref(p), o.data_ptr(), gate.data_ptr(),
-                                    weight.data_ptr(), dy.data_ptr(), do.data_ptr(),
-                                    dgate.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes,
-                                    _stream(dev))
-    _raise(lib, st, "kda_gated_norm_bwd")
+    ws = _workspace(dev, "kda_gated_norm_bwd", p)
+    _call(dev, "kda_gated_norm_bwd", p, o, gate, weight, dy, do, dgate, dw, workspace=ws)
     return do, dgate, dw
 
 
@@ -321,12 +313,7 @@ def block_norm_forward(x, y, w_pre, *, w_post=None, raw_gate=None, residual_scal
     """(x_out, h) of kda_block_norm_fwd; see block_norm."""
     dev, p = _block_norm_problem(x, y, w_pre, w_post, raw_gate, residual_scale, eps)
     x_out, h = torch.empty_like(x), torch.empty_like(x)
-    lib = _lib.load()
-    with _on(dev):
-        st = lib.kda_block_norm_fwd(ctypes.byref(p), x.data_ptr(), y.data_ptr(), _ptr(raw_gate),
-                                    _ptr(w_post), w_pre.data_ptr(), x_out.data_ptr(),
-                                    h.data_ptr(), _stream(dev))
-    _raise(lib, st, "kda_block_norm_fwd")
+    _call(dev, "kda_block_norm_fwd", p, x, y, raw_gate, w_post, w_pre, x_out, h)
     return x_out, h
 
 
@@ -336,18 +323,12 @@ def block_norm_backward(x, y, w_pre, dx_out, dh, *, w_post=None, raw_gate=None,
     (kda_block_norm_bwd); either output gradient may be None (zero). dw_post
     and dgate are None without w_post and raw_gate."""
     dev, p = _block_norm_problem(x, y, w_pre, w_post, raw_gate, residual_scale, eps, dx_out, dh)
-    lib = _lib.load()
     dx, dy, dw_pre = torch.empty_like(x), torch.empty_like(y), torch.empty_like(w_pre)
     dw_post = None if w_post is None else torch.empty_like(w_post)
     dgate = None if raw_gate is None else torch.empty_like(raw_gate)
-    nbytes = lib.kda_block_norm_bwd_workspace_bytes(ctypes.byref(p))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    with _on(dev):
-        st = lib.kda_block_norm_bwd(ctypes.byref(p), x.data_ptr(), y.data_ptr(), _ptr(raw_gate),
-                                    _ptr(w_post), w_pre.data_ptr(), _ptr(dx_out), _ptr(dh),
-                                    dx.data_ptr(), dy.data_ptr(), _ptr(dgate), _ptr(dw_post),
-                                    dw_pre.data_ptr(), ws.data_ptr(), nbytes, _stream(dev))
-    _raise(lib, st, "kda_block_norm_bwd")
+    ws = _workspace(dev, "kda_block_norm_bwd", p)
+    _call(dev, "kda_block_norm_bwd", p, x, y, raw_gate, w_post, w_pre, dx_out, dh, dx, dy, dgate,
+          dw_post, dw_pre, workspace=ws)
     return dx, dy, dw_pre, dw_post, dgate
 
 
@@ -437,12 +418,7 @@ def short_conv_forward(x, weight, bias=None, cu_seqlens=None, *, initial_state=N
     p.n_seqs = N
     y = torch.empty(x.shape, dtype=x.dtype, device=dev)
     final = torch.empty(shape, dtype=x.dtype, device=dev) if output_final_state else None
-    lib = _lib.load()
-    with _on(dev):
-        st = lib.kda_short_conv_fwd(ctypes.byref(p), x.data_ptr(), weight.data_ptr(), _ptr(bias),
-                                    _ptr(cu_seqlens), _ptr(initial_state), y.data_ptr(),
-                                    _ptr(final), _stream(dev))
-    _raise(lib, st, "kda_short_conv_fwd")
+    _call(dev, "kda_short_conv_fwd", p, x, weight, bias, cu_seqlens, initial_state, y, final)
     return (y, final) if output_final_state else y
 
 
@@ -459,18 +435,12 @@ def short_conv_backward(x, weight, bias, dy, cu_seqlens=None, *, initial_state=N
     if cu_seqlens is not None:
         _placed("cu_seqlens", cu_seqlens, dev, 4)
     p.n_seqs = N
-    lib = _lib.load()
     dx, dw = torch.empty(x.shape, dtype=x.dtype, device=dev), torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
     dinit = None if initial_state is None else torch.empty_like(initial_state)
-    nbytes = lib.kda_short_conv_bwd_workspace_bytes(ctypes.byref(p))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    with _on(dev):
-        st = lib.kda_short_conv_bwd(ctypes.byref(p), x.data_ptr(), weight.data_ptr(), _ptr(bias),
-                                    _ptr(cu_seqlens), _ptr(initial_state), dy.data_ptr(),
-                                    _ptr(d_final_state), dx.data_ptr(), dw.data_ptr(), _ptr(db),
-                                    _ptr(dinit), ws.data_ptr(), nbytes, _stream(dev))
-    _raise(lib, st, "kda_short_conv_bwd")
+    ws = _workspace(dev, "kda_short_conv_bwd", p)
+    _call(dev, "kda_short_conv_bwd", p, x, weight, bias, cu_seqlens, initial_state, dy,
+          d_final_state, dx, dw, db, dinit, workspace=ws)
     return dx, dw, db, dinit
 
 
@@ -534,10 +504,5 @@ def short_conv_update(x, weight, bias, state, cu_seqlens=None, *, state_indices=
     else:
         _apart("out", out, [t for t in (x, weight, bias, state, cu_seqlens, state_indices)
                             if t is not None])
-    lib = _lib.load()
-    with _on(dev):
-        st = lib.kda_short_conv_update(ctypes.byref(p), x.data_ptr(), weight.data_ptr(),
-                                       _ptr(bias), _ptr(cu_seqlens), _ptr(state_indices),
-                                       state.data_ptr(), out.data_ptr(), _stream(dev))
-    _raise(lib, st, "kda_short_conv_update")
+    _call(dev, "kda_short_conv_update", p, x, weight, bias, cu_seqlens, state_indices, state, out)
     return out
