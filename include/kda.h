@@ -253,11 +253,12 @@ int kda_gdn2_bwd(const kda_problem *p, const void *q, const void *k, const void 
                     leaves its state as it is. Rows of o at and after
                     cu_seqlens[N] are not written.
      state_indices  [N] (int32, device) or NULL: the pool slot of each
-                    sequence (NULL: slot n, n_slots >= N). A slot outside
-                    [0, n_slots) marks a padded sequence: its rows of o are
-                    zero and no state is touched. The slots inside must be
-                    distinct: of two sequences with tokens that name one
-                    slot, which one's update stays is not determined.
+                    sequence (NULL: slot n, n_slots >= N). A negative one
+                    marks a padded sequence: its rows of o are zero and no
+                    state is touched. A slot of n_slots or more, or one that
+                    an earlier sequence with tokens names too, is an error
+                    that the host cannot see: the sequence's rows of o are
+                    NaN and no state is touched.
      state          [n_slots, H, K, V] (fp32, device), updated in place.
    Nothing is read on the host but the problem, so the call can be captured
    into a graph and replayed with other cu_seqlens and slots of the same N

@@ -25,8 +25,8 @@ def recurrent(q, k, v, raw_g, A_log, dt_bias, state, cu, slots=None, raw_beta=No
               raw_w=None, scale=1.0, lower_bound=-5.0, eps=1e-6, gate_mode=GATE_SIGMOID_BOUND):
     """(o, state) with S_t = (I - kh e^T) Diag(exp g) S_{t-1} + kh w^T and
     o_t = S_t^T qh: e = beta kh, w = beta v (raw_beta), or e = b * kh,
-    w = wgate * v (raw_b, raw_w). Sequence n uses state slots[n]; a slot
-    outside the pool gives zero rows. Rows of o behind the last sequence are
+    w = wgate * v (raw_b, raw_w). Sequence n uses state slots[n]; a negative
+    slot gives zero rows. Rows of o behind the last sequence are
     NaN (not computed)."""
     q, k, v, raw_g, A_log, dt_bias = map(_f64, (q, k, v, raw_g, A_log, dt_bias))
     S = _f64(state).copy()
@@ -40,7 +40,7 @@ def recurrent(q, k, v, raw_g, A_log, dt_bias, state, cu, slots=None, raw_beta=No
         raw_b, raw_w = _f64(raw_b), _f64(raw_w)
     for n, sl in enumerate(slots):
         for t in range(cu[n], cu[n + 1]):
-            if not 0 <= sl < S.shape[0]:
+            if sl < 0:
                 o[t] = 0.0
                 continue
             for h in range(H):

@@ -369,78 +369,48 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_bwd(ShortConvArgs a, Co
   }
 }
 
-// Taps [j][i] of a thread's 16 bytes of channels.
-template <int N, int W>
-__device__ __forceinline__ void load_taps(const ShortConvArgs& a, int c, float (&w)[W][N], float (&b)[N]) {
-  float f[N * W];
-  load_params<N * W>(a.weight + static_cast<size_t>(c) * W, f);
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = f[i * W + j];
-#pragma unroll
-  for (int i = 0; i < N; ++i) b[i] = 0.f;
-  if (a.bias) load_params<N>(a.bias + c, b);
-}
-template <typename TI, int W, int N = RowVec<TI>::N>
-__device__ __forceinline__ void taps(const RowVec<TI> (&win)[W - 1], const RowVec<TI>& x,
-                                     const float (&w)[W][N], const float (&b)[N], float (&p)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) p[i] = b[i];
-#pragma unroll
-  for (int j = 0; j < W; ++j) {
-    float f[N];
-    if (j < W - 1) win[j < W - 1 ? j : 0].get(f);
-    else x.get(f);
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] += w[j][i] * f[i];
-  }
-}
-
-// Decoding: a thread takes 16 bytes of channels of one sequence, its state
-// rows in registers over the sequence's tokens.
+// Decoding: a block takes one sequence and 1024 channels, four per thread, the
+// state's rows in registers over the sequence's tokens.
 template <typename TI, int W>
-__global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a) {
-  using RV = RowVec<TI>;
-  constexpr int N = RV::N;
-  const int nvec = a.C / N;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int n = static_cast<int>(id / nvec), c = static_cast<int>(id - static_cast<int64_t>(n) * nvec) * N;
-  if (n >= a.N) return;
+__global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a, int ncb) {
+  const int n = blockIdx.x / ncb;
+  const int c = static_cast<int>(blockIdx.x % ncb) * kThreads * kLaneCh + threadIdx.x * kLaneCh;
   Bounds q{n, n + 1};
-  if (a.cu) q = bounds(a, n);
+  if (a.cu) q = uniform_bounds(a, n);
   if (q.s >= q.e) return;
-  const int64_t slot = a.idx ? a.idx[n] : n;
-  TI* y = static_cast<TI*>(a.y) + c;
-  if (slot < 0 || slot >= a.n_slots) {  // a padded sequence
-    RV z;
-    z.u = make_uint4(0, 0, 0, 0);
-    for (int t = q.s; t < q.e; ++t) z.store(y + static_cast<size_t>(t) * a.C);
+  const int64_t slot = find_slot(a.idx, a.cu, n, a.n_slots);
+  if (c >= a.C) return;
+  const size_t xs = a.xs, ys = a.C;
+  const uint32_t lb = c * sizeof(TI);
+  const TI* x = static_cast<const TI*>(a.x);
+  TI* y = static_cast<TI*>(a.y);
+  if (slot < 0) {  // padded: zeros; a slot it cannot have: NaN
+    const float f = slot == kPadded ? 0.f : nan_value();
+    for (int t = q.s; t < q.e; ++t) store4<TI>(in_row(y + t * ys, lb), f32x4{f, f, f, f});
     return;
   }
-  TI* st = static_cast<TI*>(a.state) + static_cast<size_t>(slot) * (W - 1) * a.C + c;
-  RV win[W - 1];
+  TI* st = static_cast<TI*>(a.state) + static_cast<size_t>(slot) * (W - 1) * a.C;
+  Row4<TI> next, old[W - 1];
+  next.load(in_row(x + q.s * xs, lb));
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) win[j].load(st + static_cast<size_t>(j) * a.C);
-  float w[W][N], b[N];
-  load_taps<N, W>(a, c, w, b);
+  for (int j = 0; j < W - 1; ++j) old[j].load(in_row(static_cast<const TI*>(st + j * ys), lb));
+  f32x4 w[W], b, win[W - 1];
+  load_taps4<W>(a, c, w, b);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) win[j] = old[j].get();
   for (int t = q.s; t < q.e; ++t) {
-    RV x, out;
-    x.load(static_cast<const TI*>(a.x) + t * a.xs + c);
-    float p[N];
-    taps<TI, W>(win, x, w, b, p);
+    const f32x4 xv = next.get();
+    if (t + 1 < q.e) next.load(in_row(x + (t + 1) * xs, lb));
+    f32x4 v = taps4<W>(win, xv, w, b);
     if (a.act == KDA_ACT_SILU) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) p[i] *= sigmoidf(p[i]);
+      for (int i = 0; i < 4; ++i) v[i] *= sigmoidf(v[i]);
     }
-    out.set(p);
-    out.store(y + static_cast<size_t>(t) * a.C);
-#pragma unroll
-    for (int j = 0; j + 1 < W - 1; ++j) win[j] = win[j + 1];
-    win[W - 2] = x;
+    store4<TI>(in_row(y + t * ys, lb), v);
+    shift4<W>(win, xv);
   }
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) win[j].store(st + static_cast<size_t>(j) * a.C);
+  for (int j = 0; j < W - 1; ++j) store4<TI>(in_row(st + j * ys, lb), win[j]);
 }
 
 enum { kFwd, kBwd, kUpdate };
@@ -462,8 +432,8 @@ Cover cover_of(int C, int64_t T) {
 template <typename TI, int W>
 hipError_t launch_w(int what, const ShortConvArgs& a, hipStream_t s) {
   if (what == kUpdate) {
-    const int64_t blocks = (static_cast<int64_t>(a.N) * (a.C / RowVec<TI>::N) + kThreads - 1) / kThreads;
-    k_short_conv_update<TI, W><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
+    const int ncb = (a.C + kThreads * kLaneCh - 1) / (kThreads * kLaneCh);
+    k_short_conv_update<TI, W><<<static_cast<unsigned>(a.N) * ncb, kThreads, 0, s>>>(a, ncb);
     return hipGetLastError();
   }
   const Cover g = cover_of(a.C, a.T);

@@ -365,6 +365,9 @@ int kda_short_conv_update(const kda_short_conv_problem* p, const void* x, const 
   const int st = check_short_conv(p);
   if (st != KDA_OK) return st;
   if (p->n_slots < 0 || p->n_slots > 0x7fffffffLL) return KDA_ERR_INVALID;
+  // a block of 256 threads per sequence and 1024 channels, below 2^32 threads
+  if (static_cast<int64_t>(p->n_seqs) * ((p->C + 1023) / 1024) >= (int64_t{1} << 24))
+    return KDA_ERR_UNSUPPORTED;
   if (!cu_seqlens && p->total_tokens != p->n_seqs) return KDA_ERR_INVALID;
   if (!state_indices && p->n_slots < p->n_seqs) return KDA_ERR_INVALID;
   if (p->n_seqs == 0 || p->total_tokens == 0) return KDA_OK;

@@ -69,14 +69,15 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
     t1 = t1 > a.T ? a.T : t1;
   }
   if (t0 >= t1) return;
-  const int64_t slot = a.idx ? a.idx[n] : n;
+  const int64_t slot = find_slot(a.idx, a.cu, n, a.n_slots);
   TI* o = static_cast<TI*>(a.o) + static_cast<size_t>(h) * D;
   const size_t os = static_cast<size_t>(a.H) * D;
   const int cg = lane & 7, rg = lane >> 3;
   const int col = 32 * w + 4 * cg;
-  if (slot < 0 || slot >= a.n_slots) {  // a padded sequence
+  if (slot < 0) {  // padded: zeros; a slot it cannot have: NaN
+    const float f = slot == kPadded ? 0.f : nan_value();
     if (rg == 0)
-      for (int64_t t = t0; t < t1; ++t) store4<TI>(o + t * os + col, zero4());
+      for (int64_t t = t0; t < t1; ++t) store4<TI>(o + t * os + col, f32x4{f, f, f, f});
     return;
   }
 
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s[j][r] = *reinterpret_cast<const f32x4*>(Sp + (32 * j + r) * D);
+    for (int r = 0; r < 4; ++r) s[j][r] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(Sp + (32 * j + r) * D));
 
   for (int64_t t = t0; t < t1; ++t) {
     const Token x = next;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
     sq = sum_wave(sq);
     sk = sum_wave(sk);
     qk = sum_wave(qk);
-    const float rq = a.scale / sqrtf(sq + a.eps), rk = 1.f / sqrtf(sk + a.eps);
+    const float rq = a.scale * rsqrtf(sq + a.eps), rk = rsqrtf(sk + a.eps);
     const float beta = G2 ? 0.f : sigmoidf(bits_to_f<TI>(x.be));
     const float kq = qk * rq * rk;
 #pragma unroll
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) *reinterpret_cast<f32x4*>(Sp + (32 * j + r) * D) = s[j][r];
+    for (int r = 0; r < 4; ++r) vstore<true>(reinterpret_cast<f32x4*>(Sp + (32 * j + r) * D), s[j][r]);
 }
 
 template <typename TI, int D>

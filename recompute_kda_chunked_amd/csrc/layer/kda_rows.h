@@ -71,4 +71,21 @@ __device__ __forceinline__ void store_params(float* p, const float (&f)[N]) {
     *reinterpret_cast<f32x4*>(p + i) = f32x4{f[i], f[i + 1], f[i + 2], f[i + 3]};
 }
 
+// The pool slot of sequence n, found by the whole wave: kPadded for a negative
+// index (a padded sequence), kBadSlot for one past the pool or one that an
+// earlier sequence with tokens names too (two writers of one state). The
+// earlier indices are read 64 at a time, together with the sequence's own.
+constexpr int64_t kPadded = -1, kBadSlot = -2;
+__device__ __forceinline__ int64_t find_slot(const int32_t* idx, const int32_t* cu, int n,
+                                             int64_t n_slots) {
+  if (!idx) return n;
+  const int32_t slot = __builtin_amdgcn_readfirstlane(idx[n]);
+  bool taken = false;
+  for (int j = threadIdx.x & 63; j < n; j += 64)
+    if (idx[j] == slot && (!cu || cu[j + 1] > cu[j])) taken = true;
+  if (slot < 0) return kPadded;
+  return slot >= n_slots || __any(taken) ? kBadSlot : slot;
+}
+__device__ __forceinline__ float nan_value() { return __uint_as_float(0x7fc00000u); }
+
 }  // namespace kda

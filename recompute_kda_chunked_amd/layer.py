@@ -183,9 +183,11 @@ def kda_recurrent(q, k, v, raw_g, raw_beta, A_log, dt_bias, state, cu_seqlens=No
     cu_seqlens: int32 [N+1] on the device, as kda_forward's (no host copy is
     needed, so the call can be captured into a graph); None: one token per
     sequence. state_indices: int32 [N] slot of each sequence (None: slot n);
-    one outside [0, slots) marks a padded sequence, whose rows of O are zero
-    and which touches no state. Sequences with tokens must name distinct
-    slots. Rows of O behind the last sequence are not written. The tokens of
+    a negative one marks a padded sequence, whose rows of O are zero and which
+    touches no state. A slot past the pool, or one that an earlier sequence
+    with tokens names too, is an error found on the device: NaN rows, no
+    state touched. Rows of O behind the last sequence are not written (those
+    of a new O hold what its memory held). The tokens of
     q, k, v, raw_g and raw_beta may be slices of wider rows. raw_g [T,H] with
     dt_bias [H] gives one gate per head. Not differentiable. Its time grows
     with the longest sequence: prompts belong to kda_forward."""

@@ -113,7 +113,7 @@ def test_padded_sequences_and_rows_behind_the_last():
     announce("padding")
     for D in (64, 128):
         x = problem([2, 1, 1, 3, 2], 2, D, torch.bfloat16, 6, slots=5)
-        x["idx"][1], x["idx"][3], x["idx"][4] = -1, 5, 2147483647
+        x["idx"][1], x["idx"][3], x["idx"][4] = -1, -7, 2147483647
         cu = [0, 2, 3, 4, 7, 7]  # the last two rows belong to no sequence
         x["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
         x["cu_seqlens_host"] = cu
@@ -128,6 +128,26 @@ def test_padded_sequences_and_rows_behind_the_last():
         y = problem([2, 1, 1, 3, 2], 2, D, torch.bfloat16, 6, slots=5)
         for s in set(range(5)) - used:
             assert torch.equal(x["state"][s], y["state"][s])
+
+
+@pytest.mark.parametrize("n", [3, 70, 200])
+def test_bad_slots_give_nan_and_touch_nothing(n):
+    announce("slots past the pool and slots named twice, %d sequences" % n)
+    lens = [1] * n
+    lens[0] = 0  # a sequence without tokens takes no slot
+    x = problem(lens, 2, 64, torch.bfloat16, 15, slots=n + 2)
+    x["idx"][0] = x["idx"][1]
+    bad = {n - 1: n + 2}
+    if n > 3:
+        bad.update({n - 2: int(x["idx"][1]), n // 2: int(x["idx"][2])})
+    y = dict(x, state=x["state"].clone(), idx=x["idx"].clone())
+    for i, s in bad.items():
+        x["idx"][i], y["idx"][i] = s, -1
+    got, want = run(x), run(y)
+    for i in range(1, n):
+        row = got[i - 1]
+        assert bool(torch.isnan(row).all()) if i in bad else torch.equal(row, want[i - 1])
+    assert torch.equal(x["state"], y["state"])
 
 
 def test_padding_hides_nan_inputs():

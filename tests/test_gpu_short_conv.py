@@ -195,20 +195,32 @@ def test_update_padding_strides_and_rows_behind():
     wide[:, C:2 * C] = v["x"]
     x = wide[:, C:2 * C]
     cu = torch.tensor([0, 2, 3, 4, 4], dtype=torch.int32, device="cuda")
-    idx = torch.tensor([1, -1, 9, 0], dtype=torch.int32, device="cuda")
+    idx = torch.tensor([1, -1, 9, 0], dtype=torch.int32, device="cuda")  # 9: past the pool
     pool = randn(71, BF16, 2, 3, C)
     start = pool.clone()
     out = torch.full((6, C), 5.0, dtype=BF16, device="cuda")
     short_conv_update(x, v["w"], v["b"], pool, cu, state_indices=idx, out=out)
     ref = layer_ref.short_conv(v["x"][:2], v["w"], v["b"], [0, 2], start[1:2])
     assert rel(to_np(out[:2]), ref["y"]) <= 2.0 ** -8
-    assert bool((out[2:4] == 0).all()) and bool((out[4:] == 5).all())
+    assert bool((out[2] == 0).all()) and bool(torch.isnan(out[3]).all()) and bool((out[4:] == 5).all())
     assert np.array_equal(to_np(pool[1]), ref["final"][0]) and torch.equal(pool[0], start[0])
     assert torch.equal(short_conv_forward(x, v["w"], v["b"], v["cud"]),
                        short_conv_forward(v["x"], v["w"], v["b"], v["cud"]))
     a = short_conv_backward(x, v["w"], v["b"], v["dy"], v["cud"])
     b = short_conv_backward(v["x"], v["w"], v["b"], v["dy"], v["cud"])
     assert all(torch.equal(s, t) for s, t in zip(a[:3], b[:3]))
+
+
+def test_update_of_a_slot_named_twice():
+    announce("short conv update, a slot named twice")
+    for C in (8, 2056):
+        v = inputs(F32, [1, 0, 1, 1], C, 3, seed=75)
+        pool = randn(76, F32, 3, 2, C)
+        idx = torch.tensor([2, 1, 1, 2], dtype=torch.int32, device="cuda")
+        other, pad = pool.clone(), torch.tensor([2, 1, 1, -1], dtype=torch.int32, device="cuda")
+        got = short_conv_update(v["x"], v["w"], v["b"], pool, v["cud"], state_indices=idx)
+        want = short_conv_update(v["x"], v["w"], v["b"], other, v["cud"], state_indices=pad)
+        assert torch.equal(got[:2], want[:2]) and bool(torch.isnan(got[2]).all()) and torch.equal(pool, other)
 
 
 def test_update_continues_forward():

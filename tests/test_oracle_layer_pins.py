@@ -50,7 +50,7 @@ def test_recurrent_slots_and_padding():
     T, H, K = 5, 1, 8
     q, k, v, g = (draw(rng, T, H, K) for _ in range(4))
     beta, A, dt, pool = draw(rng, T, H), draw(rng, H), draw(rng, H, K), draw(rng, 4, H, K, K)
-    o, S = layer_ref.recurrent(q, k, v, g, A, dt, pool, [0, 2, 3, 3, 4], [3, -1, 9, 0], raw_beta=beta)
+    o, S = layer_ref.recurrent(q, k, v, g, A, dt, pool, [0, 2, 3, 3, 4], [3, -1, 2, 0], raw_beta=beta)
     assert np.all(o[2] == 0) and np.isnan(o[4]).all()
     assert np.array_equal(S[1:3], pool[1:3])
     for sl, a, b in ((3, 0, 2), (0, 3, 4)):
