@@ -11,13 +11,21 @@
 // What bounds it: the state's bytes, 4 K V read and written once per
 // sequence and head whatever the number of tokens; the rows of a token are
 // 1-2% of that at one token per sequence. Every column of S is independent,
-// so a wave takes all K rows of 32 columns (lane = 4 columns x K/8 rows, the
-// tile in registers over all tokens), a block the D/32 waves of one (sequence,
-// head), and no wave waits for another. Each wave computes the token's
-// prologue for itself (norms, gates; K channels over 64 lanes, passed to its
-// lanes' row layout through its own 4 K floats of LDS): its rows come from
-// the caches after the first wave's, and a shared copy would need a barrier
-// per token.
+// so a wave takes all K rows of CW columns (a lane: 4 columns and every
+// (CW / 4)-lane-th group of 4 rows), the tile in registers over all tokens,
+// and no wave waits for another. Each wave computes the token's prologue for
+// itself (norms, gates; K channels over 64 lanes, passed to its lanes' row
+// layout through its own 4 K floats of LDS): its rows come from the caches
+// after the first wave's, and a shared copy would need a barrier per token.
+// The next token's rows are loaded during a token's step (9 x 12 heads of 5
+// tokens: 9.0 -> 8.2 us); computing its prologue there too gained nothing and
+// its registers cost a wave per SIMD.
+//
+// States are loaded and stored past the caches (non-temporal): a model's
+// layers together hold more states than the caches, and then 64 sequences x
+// 32 heads x D128 take 51 us instead of 57, 16 x 32 heads 14.2 instead of
+// 16.7. A single pool that would have stayed in the cache from call to call
+// takes 48.7 instead of 41.9.
 //
 // Sums, gates and the state are fp32 for either dtype; only o is rounded,
 // once.
@@ -53,13 +61,23 @@ struct RowPart {
   }
 };
 
-template <typename TI, int D, bool G2>
-__global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
-  constexpr int NW = D / 32;   // waves per block, 32 columns each
-  constexpr int CPL = D / 64;  // prologue channels per lane
-  constexpr int NJ = D / 32;   // groups of 4 rows per lane
+// Sum over the row groups of a wave: the lanes that differ in lane / (CW / 4),
+// by rotations within rows of 16 lanes and swaps of rows and halves.
+template <int CW>
+__device__ __forceinline__ float sum_rows(float x) {
+  if constexpr (CW == 16) x += dpp_mov<0x124>(x);
+  return sum_row_groups(x);
+}
+
+template <typename TI, int D, bool G2, int CW, int NW>
+__global__ void __launch_bounds__(64 * NW) k_recurrent(RecurrentArgs a) {
+  constexpr int NT = D / CW;            // waves per (sequence, head), CW columns each
+  constexpr int CPL = D / 64;           // prologue channels per lane
+  constexpr int RS = 4 * 64 / (CW / 4); // rows of one load by the wave's lanes, 4 each
+  constexpr int NJ = D / RS;            // groups of 4 rows per lane
   __shared__ __align__(16) float sm[NW][4][D];  // per wave: a, e, kh, qh
-  const int n = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int nh = blockIdx.x / (NT / NW);
+  const int n = nh / a.H, h = nh % a.H;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   int64_t t0 = n, t1 = n + 1;
   if (a.cu) {
@@ -72,8 +90,8 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
   const int64_t slot = find_slot(a.idx, a.cu, n, a.n_slots);
   TI* o = static_cast<TI*>(a.o) + static_cast<size_t>(h) * D;
   const size_t os = static_cast<size_t>(a.H) * D;
-  const int cg = lane & 7, rg = lane >> 3;
-  const int col = 32 * w + 4 * cg;
+  const int cg = lane % (CW / 4), rg = lane / (CW / 4);
+  const int col = CW * (static_cast<int>(blockIdx.x % (NT / NW)) * NW + w) + 4 * cg;
   if (slot < 0) {  // padded: zeros; a slot it cannot have: NaN
     const float f = slot == kPadded ? 0.f : nan_value();
     if (rg == 0)
@@ -115,13 +133,13 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
   Token next;
   load(t0, next);
 
-  // rows 32 j + 4 rg + r of the lane's four columns
+  // rows RS j + 4 rg + r of the lane's four columns
   float* Sp = a.state + (static_cast<size_t>(slot) * a.H + h) * (D * D) + 4 * rg * D + col;
   f32x4 s[NJ][4];
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s[j][r] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(Sp + (32 * j + r) * D));
+    for (int r = 0; r < 4; ++r) s[j][r] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(Sp + (RS * j + r) * D));
 
   for (int64_t t = t0; t < t1; ++t) {
     const Token x = next;
@@ -155,7 +173,7 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
     f32x4 u = zero4(), oo = zero4();
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int r0 = 32 * j + 4 * rg;
+      const int r0 = RS * j + 4 * rg;
       const f32x4 av = *reinterpret_cast<const f32x4*>(&sm[w][0][r0]);
       const f32x4 ev = *reinterpret_cast<const f32x4*>(&sm[w][1][r0]);
       const f32x4 qv = *reinterpret_cast<const f32x4*>(&sm[w][3][r0]);
@@ -176,12 +194,12 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      d[r] -= sum_row_groups(u[r]);
-      oo[r] = sum_row_groups(oo[r]) + kq * d[r];
+      d[r] -= sum_rows<CW>(u[r]);
+      oo[r] = sum_rows<CW>(oo[r]) + kq * d[r];
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const f32x4 kv = *reinterpret_cast<const f32x4*>(&sm[w][2][32 * j + 4 * rg]);
+      const f32x4 kv = *reinterpret_cast<const f32x4*>(&sm[w][2][RS * j + 4 * rg]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[j][r] += kv[r] * d;
     }
@@ -193,17 +211,42 @@ __global__ void __launch_bounds__(2 * D) k_recurrent(RecurrentArgs a) {
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) vstore<true>(reinterpret_cast<f32x4*>(Sp + (32 * j + r) * D), s[j][r]);
+    for (int r = 0; r < 4; ++r) vstore<true>(reinterpret_cast<f32x4*>(Sp + (RS * j + r) * D), s[j][r]);
 }
 
+// Three shapes of one kernel (microseconds per launch, bf16, D = 128, states
+// that come from HBM):
+//   wide: the waves of a (sequence, head) in one block, 32 columns each.
+//   narrow: single waves of 16 columns. A token's step is bound by one wave's
+//     instructions (about 1.1 us), and half the columns are half of them:
+//     1 sequence x 32 heads, 8 tokens 13.7 -> 11.1, 4 x 32 heads 13.8 -> 11.9.
+//     Taken while one such wave per SIMD holds the launch and cu_seqlens says
+//     that sequences may have several tokens; with one token its half lines
+//     cost more (4 x 32 heads 5.9 -> 7.8). D = 64 has half the rows: no gain
+//     (8 x 16 heads, 8 tokens fp32 10.1 either way).
+//   wide with one block (D = 128) or four (D = 64) per CU, kept apart by LDS
+//     that nothing uses: one token a sequence is a copy of the states, which
+//     runs faster with fewer reads and writes interleaved: 128 sequences x 32
+//     heads 100.2 -> 94.1, 251 x 32 heads 195.9 -> 182.5 (5.8 TB/s), 256 x 64
+//     heads 383 -> 353; D = 64, 512 x 64 heads 201.7 -> 194.4. From 4096
+//     (sequence, head) pairs: at 512 it loses (13.1 -> 14.1). Several tokens
+//     need the waves (37 x 64 heads of up to 8: 59.6 -> 84.5).
+template <typename TI, int D, bool G2>
+hipError_t launch_g(const RecurrentArgs& a, hipStream_t s) {
+  const unsigned nh = static_cast<unsigned>(a.N) * static_cast<unsigned>(a.H);
+  if constexpr (D == 128) {
+    if (a.cu && nh * (D / 16) <= 1024) {
+      k_recurrent<TI, D, G2, 16, 1><<<nh * (D / 16), 64, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  }
+  const unsigned apart = !a.cu && nh >= 4096 ? (D == 128 ? 100 : 35) * 1024 : 0;
+  k_recurrent<TI, D, G2, 32, D / 32><<<nh, 2 * D, apart, s>>>(a);
+  return hipGetLastError();
+}
 template <typename TI, int D>
 hipError_t launch_d(bool gdn2, const RecurrentArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.N) * static_cast<unsigned>(a.H)), block(2 * D);
-  if (gdn2)
-    k_recurrent<TI, D, true><<<grid, block, 0, s>>>(a);
-  else
-    k_recurrent<TI, D, false><<<grid, block, 0, s>>>(a);
-  return hipGetLastError();
+  return gdn2 ? launch_g<TI, D, true>(a, s) : launch_g<TI, D, false>(a, s);
 }
 
 }  // namespace
