@@ -241,6 +241,16 @@ int kda_gdn2_bwd(const kda_problem *p, const void *q, const void *k, const void 
                  void *dk, void *dv, void *draw_g, void *draw_b, void *draw_w, float *dA_log,
                  float *ddt_bias, void *workspace, size_t workspace_bytes, void *stream);
 
+/* kda_gdn2_fwd with the states a prompt starts from and leaves for
+   kda_gdn2_recurrent: io->h0 and io->ht as for kda_fwd_ex (io may be NULL).
+   GDN-2's backward takes no states, so there is nothing to checkpoint:
+   io->ckpt other than NULL is KDA_ERR_INVALID. */
+int kda_gdn2_fwd_ex(const kda_problem *p, const void *q, const void *k, const void *v,
+                    const void *raw_g, const void *raw_b, const void *raw_w, const float *A_log,
+                    const float *dt_bias, const int32_t *cu_seqlens, void *o,
+                    const kda_state_io *io, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
 /* The recurrent form, for decoding: the same operator token by token, each
    sequence starting from a state in the caller's pool and leaving its last
    state there (the h0 and ht of kda_fwd_ex, fp32 [K][V] per head, so a

@@ -20,7 +20,8 @@ EXPORTS = ("kda_fwd_workspace_bytes", "kda_bwd_workspace_bytes", "kda_check_prob
            "kda_prologue_workspace_bytes", "kda_prologue", "kda_fwd", "kda_bwd",
            "kda_checkpoint_bytes", "kda_bwd_segment_chunks", "kda_fwd_ex", "kda_bwd_ex",
            "kda_profile_begin", "kda_profile_end", "kda_kernel_name", "kda_status_string",
-           "kda_fwd_noalloc", "kda_gdn2_fwd", "kda_gdn2_bwd", "kda_recurrent",
+           "kda_fwd_noalloc", "kda_gdn2_fwd", "kda_gdn2_bwd", "kda_gdn2_fwd_ex",
+           "kda_recurrent",
            "kda_gdn2_recurrent", "kda_gated_norm_fwd", "kda_gated_norm_bwd_workspace_bytes",
            "kda_gated_norm_bwd", "kda_block_norm_fwd", "kda_block_norm_bwd_workspace_bytes",
            "kda_block_norm_bwd", "kda_short_conv_fwd", "kda_short_conv_bwd_workspace_bytes",
@@ -157,6 +158,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kda_bwd_ex.restype = ctypes.c_int
     lib.kda_gdn2_fwd.argtypes = [pp] + [vp] * 10 + [vp, sz, vp]
     lib.kda_gdn2_fwd.restype = ctypes.c_int
+    lib.kda_gdn2_fwd_ex.argtypes = [pp] + [vp] * 10 + [iop, vp, sz, vp]
+    lib.kda_gdn2_fwd_ex.restype = ctypes.c_int
     lib.kda_gdn2_bwd.argtypes = [pp] + [vp] * 18 + [vp, sz, vp]
     lib.kda_gdn2_bwd.restype = ctypes.c_int
     lib.kda_fwd_noalloc.argtypes = [pp] + [vp] * 9 + [vp]

@@ -542,6 +542,16 @@ int kda_fwd_ex(const kda_problem* p, const void* q, const void* k, const void* v
                     o, io, workspace, workspace_bytes, stream);
 }
 
+int kda_gdn2_fwd_ex(const kda_problem* p, const void* q, const void* k, const void* v,
+                    const void* raw_g, const void* raw_b, const void* raw_w, const float* A_log,
+                    const float* dt_bias, const int32_t* cu_seqlens, void* o,
+                    const kda_state_io* io, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  if (io && io->ckpt) return KDA_ERR_INVALID;
+  return fwd_common(true, p, q, k, v, raw_g, nullptr, raw_b, raw_w, A_log, dt_bias, cu_seqlens, o,
+                    io, workspace, workspace_bytes, stream);
+}
+
 int kda_gdn2_fwd(const kda_problem* p, const void* q, const void* k, const void* v,
                  const void* raw_g, const void* raw_b, const void* raw_w, const float* A_log,
                  const float* dt_bias, const int32_t* cu_seqlens, void* o, void* workspace,
@@ -735,7 +745,7 @@ const char* kda_status_string(int status) {
   switch (status) {
     case KDA_OK: return "ok";
     case KDA_ERR_INVALID: return "invalid argument";
-    case KDA_ERR_UNSUPPORTED: return "unsupported size/chunk/dtype/gate combination";
+    case KDA_ERR_UNSUPPORTED: return "unsupported K/V/chunk/dtype/gate combination";
     case KDA_ERR_WORKSPACE: return "workspace too small";
     case KDA_ERR_HIP: return g_msg[0] ? g_msg : "HIP launch failed";
     default: return "unknown status";

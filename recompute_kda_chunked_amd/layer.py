@@ -146,6 +146,8 @@ def _recurrent(name, gates, q, k, v, raw_g, A_log, dt_bias, state, cu_seqlens, s
     _want("state", state, (state.shape[0], H, K, V), torch.float32)
     if out is not None:
         _want("out", out, (T, H, V), dt)
+    if K != V or K not in (64, 128):
+        raise KdaError("heads of K = %d, V = %d are not built: K = V, 64 or 128" % (K, V))
     _no_grad(name, "train with the chunked form", (q, k, v, raw_g, *gates, A_log, dt_bias, state))
     dev = _dev(q, "q")
     p = _lib.KdaRecurrentProblem(
@@ -213,6 +215,15 @@ def _wants_grad(*tensors):
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
+def _grad(t):
+    """An output's gradient as the kernels take it: contiguous, at a multiple
+    of 16 bytes."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def _gated_norm_problem(o, gate, weight, eps, activation, dy=None):
     if o.dim() < 1:
         raise KdaError("o: expected [..., V]")
@@ -225,11 +236,13 @@ def _gated_norm_problem(o, gate, weight, eps, activation, dy=None):
     _want("weight", weight, (V,), torch.float32)
     if dy is not None:
         _want("dy", dy, o.shape, dt)
+    if V not in (64, 128, 256):
+        raise KdaError("a norm over V = %d is not built: 64, 128 or 256" % V)
     dev = _dev(o, "o")
     for name, t in (("o", o), ("gate", gate), ("weight", weight), ("dy", dy)):
         if t is not None:
             _placed(name, t, dev)
-    return dev, _lib.KdaGatedNormProblem(rows=o.numel() // V if V else 0, V=V, dtype=_DT[dt],
+    return dev, _lib.KdaGatedNormProblem(rows=o.numel() // V, V=V, dtype=_DT[dt],
                                          activation=_GATE_ACT[activation], eps=eps)
 
 
@@ -247,8 +260,8 @@ def gated_norm_backward(o, gate, weight, dy, *, eps=1e-6, activation="sigmoid"):
     recomputed from o; dweight fp32."""
     dev, p = _gated_norm_problem(o, gate, weight, eps, activation, dy)
     do, dgate, dw = torch.empty_like(o), torch.empty_like(gate), torch.empty_like(weight)
-    ws = _workspace(dev, "kda_gated_norm_bwd", p)
-    _call(dev, "kda_gated_norm_bwd", p, o, gate, weight, dy, do, dgate, dw, workspace=ws)
+    _call(dev, "kda_gated_norm_bwd", p, o, gate, weight, dy, do, dgate, dw,
+          workspace=_workspace(dev, "kda_gated_norm_bwd", p))
     return do, dgate, dw
 
 
@@ -264,7 +277,7 @@ class GatedNormFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        return (*gated_norm_backward(*ctx.saved_tensors, dy.contiguous(), **ctx.opts), None, None)
+        return (*gated_norm_backward(*ctx.saved_tensors, _grad(dy), **ctx.opts), None, None)
 
 
 def gated_norm(o, gate, weight, *, eps=1e-6, activation="sigmoid"):
@@ -299,6 +312,8 @@ def _block_norm_problem(x, y, w_pre, w_post, raw_gate, residual_scale, eps, dx_o
     for name, t in (("dx_out", dx_out), ("dh", dh)):
         if t is not None:
             _want(name, t, (T, D), dt)
+    if not 0 < D <= 8192 or D % 8:
+        raise KdaError("a norm over D = %d is not built: a multiple of 8, at most 8192" % D)
     dev = _dev(x, "x")
     for name, t in (("x", x), ("y", y), ("w_pre", w_pre), ("w_post", w_post), ("dx_out", dx_out),
                     ("dh", dh)):
@@ -328,9 +343,8 @@ def block_norm_backward(x, y, w_pre, dx_out, dh, *, w_post=None, raw_gate=None,
     dx, dy, dw_pre = torch.empty_like(x), torch.empty_like(y), torch.empty_like(w_pre)
     dw_post = None if w_post is None else torch.empty_like(w_post)
     dgate = None if raw_gate is None else torch.empty_like(raw_gate)
-    ws = _workspace(dev, "kda_block_norm_bwd", p)
     _call(dev, "kda_block_norm_bwd", p, x, y, raw_gate, w_post, w_pre, dx_out, dh, dx, dy, dgate,
-          dw_post, dw_pre, workspace=ws)
+          dw_post, dw_pre, workspace=_workspace(dev, "kda_block_norm_bwd", p))
     return dx, dy, dw_pre, dw_post, dgate
 
 
@@ -348,9 +362,9 @@ class BlockNormFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dx_out, dh):
         x, y, w_pre, w_post, raw_gate = ctx.saved_tensors
-        dx_out, dh = (None if t is None else t.contiguous() for t in (dx_out, dh))
-        return (*block_norm_backward(x, y, w_pre, dx_out, dh, w_post=w_post, raw_gate=raw_gate,
-                                     **ctx.opts), None, None)
+        grads = block_norm_backward(x, y, w_pre, _grad(dx_out), _grad(dh), w_post=w_post,
+                                    raw_gate=raw_gate, **ctx.opts)
+        return (*grads, None, None)
 
 
 def block_norm(x, y, w_pre, *, w_post=None, raw_gate=None, residual_scale=1.0, eps=1e-6):
@@ -387,6 +401,9 @@ def _conv_problem(x, weight, bias, activation, **tensors):
     for name, (t, shape) in tensors.items():
         if t is not None:
             _want(name, t, shape, dt)
+    if not 2 <= W <= 4 or C % 8:
+        raise KdaError("a convolution of %d taps over %d channels is not built: 2 to 4 taps, a "
+                       "multiple of 8 channels" % (W, C))
     dev = _dev(x, "x")
     p = _lib.KdaShortConvProblem(total_tokens=T, C=C, W=W, dtype=_DT[dt],
                                  activation=_CONV_ACT[activation],
@@ -400,26 +417,32 @@ def _conv_problem(x, weight, bias, activation, **tensors):
     return dev, p
 
 
-def _conv_seqs(cu_seqlens):
-    if cu_seqlens is None:
-        return 1
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.dtype is not torch.int32:
-        raise KdaError("cu_seqlens: expected int32 [N+1], got %s %s"
-                       % (tuple(cu_seqlens.shape), cu_seqlens.dtype))
-    return cu_seqlens.shape[0] - 1
+def _packed_conv_problem(x, weight, bias, cu_seqlens, activation, initial_state, dy=None,
+                         d_final_state=None):
+    N = 1
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.dtype is not torch.int32:
+            raise KdaError("cu_seqlens: expected int32 [N+1], got %s %s"
+                           % (tuple(cu_seqlens.shape), cu_seqlens.dtype))
+        N = cu_seqlens.shape[0] - 1
+    shape = (N, weight.shape[-1] - 1, x.shape[-1])
+    dev, p = _conv_problem(x, weight, bias, activation, dy=(dy, x.shape),
+                           initial_state=(initial_state, shape),
+                           d_final_state=(d_final_state, shape))
+    if cu_seqlens is not None:
+        _placed("cu_seqlens", cu_seqlens, dev, 4)
+    p.n_seqs = N
+    return dev, p
 
 
 def short_conv_forward(x, weight, bias=None, cu_seqlens=None, *, initial_state=None,
                        output_final_state=False, activation="silu"):
     """y, or (y, final_state), of kda_short_conv_fwd; see short_conv."""
-    N = _conv_seqs(cu_seqlens)
-    shape = (N, weight.shape[-1] - 1, x.shape[-1])
-    dev, p = _conv_problem(x, weight, bias, activation, initial_state=(initial_state, shape))
-    if cu_seqlens is not None:
-        _placed("cu_seqlens", cu_seqlens, dev, 4)
-    p.n_seqs = N
+    dev, p = _packed_conv_problem(x, weight, bias, cu_seqlens, activation, initial_state)
     y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    final = torch.empty(shape, dtype=x.dtype, device=dev) if output_final_state else None
+    final = None
+    if output_final_state:
+        final = torch.empty((p.n_seqs, p.W - 1, p.C), dtype=x.dtype, device=dev)
     _call(dev, "kda_short_conv_fwd", p, x, weight, bias, cu_seqlens, initial_state, y, final)
     return (y, final) if output_final_state else y
 
@@ -429,20 +452,13 @@ def short_conv_backward(x, weight, bias, dy, cu_seqlens=None, *, initial_state=N
     """(dx, dweight, dbias, d_initial_state) of sum(y * dy) + sum(final_state
     * d_final_state) (kda_short_conv_bwd); dbias and d_initial_state are None
     without bias and initial_state."""
-    N = _conv_seqs(cu_seqlens)
-    shape = (N, weight.shape[-1] - 1, x.shape[-1])
-    dev, p = _conv_problem(x, weight, bias, activation, dy=(dy, x.shape),
-                           initial_state=(initial_state, shape),
-                           d_final_state=(d_final_state, shape))
-    if cu_seqlens is not None:
-        _placed("cu_seqlens", cu_seqlens, dev, 4)
-    p.n_seqs = N
+    dev, p = _packed_conv_problem(x, weight, bias, cu_seqlens, activation, initial_state, dy,
+                                  d_final_state)
     dx, dw = torch.empty(x.shape, dtype=x.dtype, device=dev), torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
     dinit = None if initial_state is None else torch.empty_like(initial_state)
-    ws = _workspace(dev, "kda_short_conv_bwd", p)
     _call(dev, "kda_short_conv_bwd", p, x, weight, bias, cu_seqlens, initial_state, dy,
-          d_final_state, dx, dw, db, dinit, workspace=ws)
+          d_final_state, dx, dw, db, dinit, workspace=_workspace(dev, "kda_short_conv_bwd", p))
     return dx, dw, db, dinit
 
 
@@ -461,10 +477,10 @@ class ShortConvFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, dfinal=None):
         x, weight, bias, cu, init = ctx.saved_tensors
-        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
-        dfinal = None if dfinal is None else dfinal.contiguous()
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _grad(dy)
         dx, dw, db, dinit = short_conv_backward(x, weight, bias, dy, cu, initial_state=init,
-                                                d_final_state=dfinal, activation=ctx.activation)
+                                                d_final_state=_grad(dfinal),
+                                                activation=ctx.activation)
         return dx, dw, db, None, dinit, None, None
 
 

@@ -242,25 +242,36 @@ def kda_backward(q, k, v, raw_g, raw_beta, A_log, dt_bias, dO, cu_seqlens=None, 
 
 def gdn2_forward(q, k, v, raw_g, raw_b, raw_w, A_log, dt_bias, cu_seqlens=None, *,
                  cu_seqlens_host=None, scale=1.0, chunk=64, lower_bound=-5.0, eps=1e-6,
-                 seg_chunks=0, gate_mode=_lib.KDA_GATE_SIGMOID_BOUND):
+                 seg_chunks=0, gate_mode=_lib.KDA_GATE_SIGMOID_BOUND, initial_state=None,
+                 output_final_state=False):
     """O [T,H,V] of GDN-2: per-channel erase gate sigmoid(raw_b) [T,H,K] and
-    write gate sigmoid(raw_w) [T,H,V] in place of KDA's beta (kda_gdn2_fwd)."""
+    write gate sigmoid(raw_w) [T,H,V] in place of KDA's beta (kda_gdn2_fwd).
+    initial_state: fp32 [N,H,K,V] state each sequence starts from (zero when
+    None). With output_final_state the result is (O, ht), ht the fp32
+    [N,H,K,V] states to decode from with gdn2_recurrent."""
     if cu_seqlens is None:
         cu_seqlens, cu_seqlens_host = _default_cu(q.shape[0], q.device)
     T, H, K, V, dt, ph = _check_inputs(
         q, k, v, raw_g, None, A_log, dt_bias, cu_seqlens,
         extra=[("raw_b", (raw_b, tuple(k.shape), q.dtype)), ("raw_w", (raw_w, tuple(v.shape), q.dtype))])
-    prob = Problem(T, H, K, V, dt, _cu_host(cu_seqlens, cu_seqlens_host), chunk, scale,
-                   lower_bound, eps, seg_chunks, _gate_flags(gate_mode, ph))
+    cu_host = _cu_host(cu_seqlens, cu_seqlens_host)
+    N = len(cu_host) - 1
+    _check_state("initial_state", initial_state, (N, H, K, V), q.device)
+    prob = Problem(T, H, K, V, dt, cu_host, chunk, scale, lower_bound, eps, seg_chunks,
+                   _gate_flags(gate_mode, ph))
     lib = _lib.load()
     _raise(lib, prob.check(), "kda_gdn2_fwd")
     o = torch.empty((T, H, V), dtype=dt, device=q.device)
+    ht = torch.empty((N, H, K, V), dtype=torch.float32, device=q.device) \
+        if output_final_state else None
+    io = _state_io(h0=initial_state, ht=ht)
     ws = torch.empty(prob.fwd_ws(), dtype=torch.uint8, device=q.device)
-    st = lib.kda_gdn2_fwd(prob.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(raw_g), _ptr(raw_b),
-                          _ptr(raw_w), _ptr(A_log), _ptr(dt_bias), _ptr(cu_seqlens), _ptr(o),
-                          _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(q.device))
+    st = lib.kda_gdn2_fwd_ex(prob.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(raw_g), _ptr(raw_b),
+                             _ptr(raw_w), _ptr(A_log), _ptr(dt_bias), _ptr(cu_seqlens), _ptr(o),
+                             ctypes.byref(io), _ptr(ws), ctypes.c_size_t(ws.numel()),
+                             _stream(q.device))
     _raise(lib, st, "kda_gdn2_fwd")
-    return o
+    return (o, ht) if output_final_state else o
 
 
 def gdn2_backward(q, k, v, raw_g, raw_b, raw_w, A_log, dt_bias, dO, cu_seqlens=None, *,

@@ -290,3 +290,33 @@ def test_short_conv_binding_refuses():
                             ((x.clone().requires_grad_(True), w, b, st), {}, "not differentiable")):
         with pytest.raises(KdaError, match=match):
             short_conv_update(*args, **kw)
+
+
+def test_gdn2_states_take_no_checkpoints(lib):  # noqa: F811
+    from test_abi import good
+    p = good()
+    io = _lib.KdaStateIO()
+    io.ckpt, io.ckpt_bytes = 0x2000, 1 << 40
+    ws = ctypes.c_size_t(p.fwd_ws())
+    assert lib.kda_gdn2_fwd_ex(p.ref, *[FAKE] * 10, ctypes.byref(io), FAKE, ws, NUL) == _lib.KDA_ERR_INVALID
+    args = [FAKE] * 10
+    args[4] = NUL
+    assert lib.kda_gdn2_fwd_ex(p.ref, *args, None, FAKE, ws, NUL) == _lib.KDA_ERR_INVALID
+    small = ctypes.c_size_t(p.fwd_ws() - 1)
+    assert lib.kda_gdn2_fwd_ex(p.ref, *[FAKE] * 10, None, FAKE, small, NUL) == _lib.KDA_ERR_WORKSPACE
+
+
+def test_sizes_that_are_not_built_are_named():
+    x = rec_inputs(D=32)
+    with pytest.raises(KdaError, match="K = 32, V = 32 are not built"):
+        kda_recurrent(**x)
+    z = torch.zeros(2, 96)
+    with pytest.raises(KdaError, match="V = 96 is not built"):
+        gated_norm(z, z, torch.zeros(96))
+    for D in (12, 8200):
+        z = torch.zeros(2, D)
+        with pytest.raises(KdaError, match="D = %d is not built" % D):
+            block_norm(z, z, torch.zeros(D))
+    for C, W in ((12, 4), (16, 5), (16, 1)):
+        with pytest.raises(KdaError, match="not built"):
+            short_conv(torch.zeros(3, C), torch.zeros(C, W))
