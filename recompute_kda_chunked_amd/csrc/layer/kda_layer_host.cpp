@@ -141,10 +141,11 @@ int check_short_conv(const kda_short_conv_problem* p) {
   if (p->activation != KDA_ACT_NONE && p->activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
   if (!stride_ok(p->x_stride, p->C, p->dtype, p->total_tokens, true)) return KDA_ERR_INVALID;
   // token numbers in 32 bits with room for the tokens loaded ahead, and launches
-  // (a thread per four channels of a state row or of 8 tokens) below 2^32 threads
+  // (a thread per four channels of a state row, or of a run of 128 tokens) below
+  // 2^32 threads
   if (p->total_tokens > 0x7fffff00LL ||
       static_cast<int64_t>(p->n_seqs) * (p->W - 1) * p->C >= (int64_t{1} << 32) ||
-      p->total_tokens / 8 * p->C >= (int64_t{1} << 32))
+      p->total_tokens * p->C >= (int64_t{1} << 40))
     return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }

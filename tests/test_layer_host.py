@@ -233,7 +233,9 @@ def sc(**kw):
     (dict(activation=_lib.KDA_ACT_SIGMOID), _lib.KDA_ERR_UNSUPPORTED),
     (dict(x_stride=56), _lib.KDA_ERR_INVALID),
     (dict(x_stride=68), _lib.KDA_ERR_INVALID),
-    (dict(C=1 << 20, total_tokens=1 << 16), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(C=1 << 20, total_tokens=1 << 20), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(total_tokens=0x7fffffff), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(n_seqs=1 << 26), _lib.KDA_ERR_UNSUPPORTED),
 ])
 def test_short_conv_rejects(lib, kw, code):  # noqa: F811
     p = ctypes.byref(sc(**kw))
