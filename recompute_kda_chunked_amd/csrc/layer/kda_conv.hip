@@ -73,7 +73,13 @@ __device__ __forceinline__ TI* in_row(TI* row, uint32_t lane_bytes) {
 template <typename TI>
 struct Row4 {
   uint32_t u[4];
-  __device__ __forceinline__ void load(const TI* p) { load4_raw<TI>(p, u); }
+  template <bool NT = false>
+  __device__ __forceinline__ void load(const TI* p) {
+    typedef __attribute__((ext_vector_type(sizeof(TI)))) uint32_t words;
+    const words x = vload<NT>(reinterpret_cast<const words*>(p));
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(TI)); ++i) u[i] = x[i];
+  }
   __device__ __forceinline__ f32x4 get() const { return unpack4<TI>(u); }
 };
 
@@ -157,7 +163,7 @@ __device__ __forceinline__ void zero_rows(TI* y, size_t stride, uint32_t lb, int
   for (int t = from; t < to; ++t) store4<TI>(in_row(y + t * stride, lb), zero4());
 }
 
-template <typename TI, int W>
+template <typename TI, int W, bool NT>
 __global__ void __launch_bounds__(kThreads) k_short_conv(ShortConvArgs a, Cover g) {
   constexpr int U = kAhead;
   const int64_t rb = blockIdx.x / g.ncb;
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) k_short_conv(ShortConvArgs a, Cover 
     };
     Row4<TI> nx[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) nx[u].load(in_row(x + (p.a1 - p.a0 > u ? p.a0 + u : p.a1 - 1) * xs, lb));
+    for (int u = 0; u < U; ++u) nx[u].template load<NT>(in_row(x + (p.a1 - p.a0 > u ? p.a0 + u : p.a1 - 1) * xs, lb));
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) win[j] = row_at<TI, W>(a, p.n, p.q.s, p.a0 - (W - 1) + j, c);
     int t = p.a0;
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) k_short_conv(ShortConvArgs a, Cover 
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         cx[u] = nx[u];
-        nx[u].load(in_row(x + (p.a1 - t > U + u ? t + U + u : p.a1 - 1) * xs, lb));
+        nx[u].template load<NT>(in_row(x + (p.a1 - t > U + u ? t + U + u : p.a1 - 1) * xs, lb));
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) step(t + u, cx[u]);
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) k_short_conv(ShortConvArgs a, Cover 
 // rows are completed at the sequence's end, where the final state's gradient
 // joins them. An empty sequence's state gradient passes through (threads past
 // the runs' blocks).
-template <typename TI, int W>
+template <typename TI, int W, bool NT>
 __global__ void __launch_bounds__(kThreads) k_short_conv_bwd(ShortConvArgs a, Cover g) {
   constexpr int U = kAhead;
   __shared__ __align__(16) float sm[kRuns][kWaveCh];
@@ -310,8 +316,8 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_bwd(ShortConvArgs a, Co
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int tu = stop - p.a0 > u ? p.a0 + u : stop - 1;
-        nx[u].load(in_row(x + tu * xs, lb));
-        nd[u].load(in_row(dy + tu * ys, lb));
+        nx[u].template load<NT>(in_row(x + tu * xs, lb));
+        nd[u].template load<NT>(in_row(dy + tu * ys, lb));
       }
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) win[j] = row_at<TI, W>(a, p.n, p.q.s, p.a0 - (W - 1) + j, c);
@@ -323,8 +329,8 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_bwd(ShortConvArgs a, Co
           const int tu = stop - t > U + u ? t + U + u : stop - 1;
           cx[u] = nx[u];
           cd[u] = nd[u];
-          nx[u].load(in_row(x + tu * xs, lb));
-          nd[u].load(in_row(dy + tu * ys, lb));
+          nx[u].template load<NT>(in_row(x + tu * xs, lb));
+          nd[u].template load<NT>(in_row(dy + tu * ys, lb));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) step(t + u, cx[u], cd[u], true);
@@ -442,8 +448,14 @@ hipError_t launch_w(int what, const ShortConvArgs& a, hipStream_t s) {
   const int64_t tail = ends ? (rows * (a.C / kLaneCh) + kThreads - 1) / kThreads : 0;
   const unsigned grid = static_cast<unsigned>(g.nrb * g.ncb + tail);
   if (grid == 0) return hipSuccess;
-  if (what == kFwd) k_short_conv<TI, W><<<grid, kThreads, 0, s>>>(a, g);
-  else k_short_conv_bwd<TI, W><<<grid, kThreads, 0, s>>>(a, g);
+  const bool nt = streams_past_caches((what == kFwd ? 2 : 3) * a.T * a.C * static_cast<int64_t>(sizeof(TI)));
+  if (what == kFwd) {
+    if (nt) k_short_conv<TI, W, true><<<grid, kThreads, 0, s>>>(a, g);
+    else k_short_conv<TI, W, false><<<grid, kThreads, 0, s>>>(a, g);
+  } else {
+    if (nt) k_short_conv_bwd<TI, W, true><<<grid, kThreads, 0, s>>>(a, g);
+    else k_short_conv_bwd<TI, W, false><<<grid, kThreads, 0, s>>>(a, g);
+  }
   return hipGetLastError();
 }
 template <typename TI>

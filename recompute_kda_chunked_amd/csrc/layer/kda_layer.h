@@ -22,6 +22,18 @@ struct RecurrentArgs {
 };
 hipError_t launch_recurrent(int dtype, int D, bool gdn2, const RecurrentArgs& a, hipStream_t s);
 
+// Whether a launch of the row kernels that moves `bytes` loads its rows past
+// the caches (non-temporal). From about the 256 MiB that the memory-side cache
+// holds they cannot be in it and only push each other out; below, rows that
+// the kernel before wrote often are. bf16, microseconds plain / past the
+// caches, rows in the caches where they fit (in brackets: never in them):
+//   gated norm forward    275 MB 41.7 / 43.1 (42.9 / 43.5)   334 MB 55.7 / 52.5   403 MB 69.3 / 60.5
+//   gated norm backward   168 MB 33.0 / 35.9 (36.0 / 35.8)   335 MB 66.7 / 62.2   671 MB 133 / 113
+//   block norm forward    268 MB 41.2 / 48.2 (48.2 / 48.3)   335 MB 65.6 / 58.8
+//   block norm backward   268 MB 55.2 / 57.0 (56.0 / 56.3)   393 MB 82.0 / 73.4   537 MB 108 / 95
+//   convolution backward  201 MB 48.3 / 52.6 (50.6 / 53.0)   295 MB 83.2 / 82.9   403 MB 90.3 / 85.9
+inline bool streams_past_caches(int64_t bytes) { return bytes >= (int64_t{288} << 20); }
+
 // Sums of `nb` partial rows of M = n0 + n1 floats, in a fixed order: the
 // first n0 columns to out0, the rest to out1 unless it is null (nb = 0:
 // zeros).

@@ -71,7 +71,7 @@ __device__ __forceinline__ float act_slope(int act, float g, float s) {
 
 // A row lies across V / N consecutive lanes, one 16-byte vector each, so a
 // wave instruction reads 1 KB of adjacent rows.
-template <typename TI, int V>
+template <typename TI, int V, bool NT>
 __global__ void __launch_bounds__(256) k_gated_norm(GatedNormArgs a) {
   using RV = RowVec<TI>;
   constexpr int N = RV::N, LPR = V / N, RPB = 256 / LPR;
@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(256) k_gated_norm(GatedNormArgs a) {
        row += static_cast<int64_t>(gridDim.x) * RPB) {
     const size_t at = static_cast<size_t>(row) * V + c;
     RV vo, vg;
-    vo.load(static_cast<const TI*>(a.o) + at);
-    vg.load(static_cast<const TI*>(a.gate) + at);
+    vo.template load<NT>(static_cast<const TI*>(a.o) + at);
+    vg.template load<NT>(static_cast<const TI*>(a.gate) + at);
     float o[N], g[N], y[N], ss = 0.f;
     vo.get(o);
     vg.get(g);
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(256) k_gated_norm(GatedNormArgs a) {
 // mean(dn n) = r mean(dn o), so both sums of a row are taken together. A
 // lane keeps its channels over all its rows, so dweight adds up in registers;
 // the block's row groups are joined through LDS into one partial row.
-template <typename TI, int V>
+template <typename TI, int V, bool NT>
 __global__ void __launch_bounds__(256) k_gated_norm_bwd(GatedNormArgs a) {
   using RV = RowVec<TI>;
   constexpr int N = RV::N, LPR = V / N, RPB = 256 / LPR;
@@ -115,9 +115,9 @@ __global__ void __launch_bounds__(256) k_gated_norm_bwd(GatedNormArgs a) {
        row += static_cast<int64_t>(gridDim.x) * RPB) {
     const size_t at = static_cast<size_t>(row) * V + c;
     RV vo, vg, vd;
-    vo.load(static_cast<const TI*>(a.o) + at);
-    vg.load(static_cast<const TI*>(a.gate) + at);
-    vd.load(static_cast<const TI*>(a.dy) + at);
+    vo.template load<NT>(static_cast<const TI*>(a.o) + at);
+    vg.template load<NT>(static_cast<const TI*>(a.gate) + at);
+    vd.template load<NT>(static_cast<const TI*>(a.dy) + at);
     float o[N], g[N], d[N], s[N], ss = 0.f, sd = 0.f;
     vo.get(o);
     vg.get(g);
@@ -183,7 +183,7 @@ __device__ __forceinline__ void block_sum(float (&v)[K], float (&sm)[2][2][8], i
 // One block per token (a launch of 2^22 blocks takes more in turn), the row's
 // NV 16-byte vectors per thread in registers; vector j of thread t is number
 // j * threads + t of the row.
-template <typename TI, int NV, int GATE, bool POST>
+template <typename TI, int NV, int GATE, bool POST, bool NT>
 __global__ void __launch_bounds__(512) k_block_norm(BlockNormArgs a) {
   using RV = RowVec<TI>;
   constexpr int N = RV::N;
@@ -199,9 +199,9 @@ __global__ void __launch_bounds__(512) k_block_norm(BlockNormArgs a) {
       const int v = j * blockDim.x + threadIdx.x;
       vx[j].u = vy[j].u = vg[j].u = make_uint4(0, 0, 0, 0);
       if (v < nvec) {
-        vy[j].load(static_cast<const TI*>(a.y) + row + v * N);
-        vx[j].load(static_cast<const TI*>(a.x) + row + v * N);
-        if constexpr (GATE == KDA_BLOCK_GATE_CHANNEL) vg[j].load(static_cast<const TI*>(a.gate) + row + v * N);
+        vy[j].template load<NT>(static_cast<const TI*>(a.y) + row + v * N);
+        vx[j].template load<NT>(static_cast<const TI*>(a.x) + row + v * N);
+        if constexpr (GATE == KDA_BLOCK_GATE_CHANNEL) vg[j].template load<NT>(static_cast<const TI*>(a.gate) + row + v * N);
       }
     }
     float gt = 1.f;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(512) k_block_norm(BlockNormArgs a) {
 // with z dX (a per-token gate). A block takes every gridDim-th token and keeps
 // its threads' channels of dw_pre and dw_post in registers, one partial row
 // per block at the end.
-template <typename TI, int NV, int GATE, bool POST>
+template <typename TI, int NV, int GATE, bool POST, bool NT>
 __global__ void __launch_bounds__(512) k_block_norm_bwd(BlockNormArgs a) {
   using RV = RowVec<TI>;
   constexpr int N = RV::N;
@@ -294,11 +294,11 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(BlockNormArgs a) {
       const int v = j * blockDim.x + threadIdx.x;
       vx[j].u = vy[j].u = vg[j].u = vd[j].u = vh[j].u = make_uint4(0, 0, 0, 0);
       if (v < nvec) {
-        vy[j].load(static_cast<const TI*>(a.y) + row + v * N);
-        vx[j].load(static_cast<const TI*>(a.x) + row + v * N);
-        if constexpr (GATE == KDA_BLOCK_GATE_CHANNEL) vg[j].load(static_cast<const TI*>(a.gate) + row + v * N);
-        if (a.dh) vh[j].load(static_cast<const TI*>(a.dh) + row + v * N);
-        if (a.dx_out) vd[j].load(static_cast<const TI*>(a.dx_out) + row + v * N);
+        vy[j].template load<NT>(static_cast<const TI*>(a.y) + row + v * N);
+        vx[j].template load<NT>(static_cast<const TI*>(a.x) + row + v * N);
+        if constexpr (GATE == KDA_BLOCK_GATE_CHANNEL) vg[j].template load<NT>(static_cast<const TI*>(a.gate) + row + v * N);
+        if (a.dh) vh[j].template load<NT>(static_cast<const TI*>(a.dh) + row + v * N);
+        if (a.dx_out) vd[j].template load<NT>(static_cast<const TI*>(a.dx_out) + row + v * N);
       }
     }
     float gt = 1.f;
@@ -425,17 +425,26 @@ struct RowShape {
   }
 };
 
-template <typename TI, int NV, int GATE>
-hipError_t launch_block_g(bool bwd, int threads, const BlockNormArgs& a, hipStream_t s) {
+template <typename TI, int NV, int GATE, bool NT>
+hipError_t launch_block_n(bool bwd, int threads, const BlockNormArgs& a, hipStream_t s) {
   const unsigned grid = bwd ? block_norm_blocks(sizeof(TI) == 4 ? KDA_F32 : KDA_BF16, a.D, a.T) : static_cast<unsigned>(a.T < (1 << 22) ? a.T : 1 << 22);
   if (bwd) {
-    if (a.w_post) k_block_norm_bwd<TI, NV, GATE, true><<<grid, threads, 0, s>>>(a);
-    else k_block_norm_bwd<TI, NV, GATE, false><<<grid, threads, 0, s>>>(a);
+    if (a.w_post) k_block_norm_bwd<TI, NV, GATE, true, NT><<<grid, threads, 0, s>>>(a);
+    else k_block_norm_bwd<TI, NV, GATE, false, NT><<<grid, threads, 0, s>>>(a);
   } else {
-    if (a.w_post) k_block_norm<TI, NV, GATE, true><<<grid, threads, 0, s>>>(a);
-    else k_block_norm<TI, NV, GATE, false><<<grid, threads, 0, s>>>(a);
+    if (a.w_post) k_block_norm<TI, NV, GATE, true, NT><<<grid, threads, 0, s>>>(a);
+    else k_block_norm<TI, NV, GATE, false, NT><<<grid, threads, 0, s>>>(a);
   }
   return hipGetLastError();
+}
+template <typename TI, int NV, int GATE>
+hipError_t launch_block_g(bool bwd, int threads, const BlockNormArgs& a, hipStream_t s) {
+  // x, y and two gradients in; x_out and h, or dx and dy out; the gate and its gradient
+  const int64_t rows = bwd ? 4 + !!a.dx_out + !!a.dh : 4;
+  const int64_t gates = GATE == KDA_BLOCK_GATE_CHANNEL ? (bwd ? 2 : 1) : 0;
+  return streams_past_caches((rows + gates) * a.T * a.D * static_cast<int64_t>(sizeof(TI)))
+             ? launch_block_n<TI, NV, GATE, true>(bwd, threads, a, s)
+             : launch_block_n<TI, NV, GATE, false>(bwd, threads, a, s);
 }
 template <typename TI, int NV>
 hipError_t launch_block_v(bool bwd, int gate, int threads, const BlockNormArgs& a, hipStream_t s) {
@@ -452,11 +461,17 @@ hipError_t launch_block(int dtype, int gate, bool bwd, const BlockNormArgs& a, h
                        : launch_block_v<bf16, 2>(bwd, gate, r.threads, a, s);
 }
 
+template <typename TI, int V, bool NT>
+hipError_t launch_gated_n(bool bwd, const GatedNormArgs& a, int blocks, hipStream_t s) {
+  if (bwd) k_gated_norm_bwd<TI, V, NT><<<blocks, 256, 0, s>>>(a);
+  else k_gated_norm<TI, V, NT><<<blocks, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
 template <typename TI, int V>
 hipError_t launch_gated(bool bwd, const GatedNormArgs& a, int blocks, hipStream_t s) {
-  if (bwd) k_gated_norm_bwd<TI, V><<<blocks, 256, 0, s>>>(a);
-  else k_gated_norm<TI, V><<<blocks, 256, 0, s>>>(a);
-  return hipGetLastError();
+  return streams_past_caches((bwd ? 5 : 3) * a.rows * V * static_cast<int64_t>(sizeof(TI)))
+             ? launch_gated_n<TI, V, true>(bwd, a, blocks, s)
+             : launch_gated_n<TI, V, false>(bwd, a, blocks, s);
 }
 hipError_t launch_gated_t(int dtype, int V, bool bwd, const GatedNormArgs& a, int blocks, hipStream_t s) {
   if (dtype == KDA_F32)
@@ -477,7 +492,7 @@ int64_t gated_groups(int dtype, int V, int64_t rows) {
 hipError_t launch_param_reduce(const ParamReduceArgs& a, hipStream_t s) {
   const int M = a.n0 + a.n1;
   if (M <= 1024) k_param_reduce<4><<<(M + 3) / 4, 1024, 0, s>>>(a);
-  else if (M <= 8192) k_param_reduce<16><<<(M + 15) / 16, 1024, 0, s>>>(a);
+  else if (M <= 16384) k_param_reduce<32><<<(M + 31) / 32, 1024, 0, s>>>(a);
   else k_param_reduce<64><<<(M + 63) / 64, 1024, 0, s>>>(a);
   return hipGetLastError();
 }

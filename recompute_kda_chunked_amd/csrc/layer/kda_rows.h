@@ -21,12 +21,22 @@ __device__ __forceinline__ float sum_row_groups(float x) {
 // Sum over all 64 lanes.
 __device__ __forceinline__ float sum_wave(float x) { return sum_row_groups(group_sum<8>(x)); }
 
+// A load with or without the non-temporal hint (see streams_past_caches).
+template <bool NT, typename V>
+__device__ __forceinline__ V vload(const V* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+
 // 16 bytes of a row: 8 bf16 or 4 fp32 values.
 template <typename TI>
 struct RowVec {
   static constexpr int N = 16 / sizeof(TI);
   uint4 u;
-  __device__ __forceinline__ void load(const TI* p) { u = *reinterpret_cast<const uint4*>(p); }
+  template <bool NT>
+  __device__ __forceinline__ void load(const TI* p) {
+    u = __builtin_bit_cast(uint4, vload<NT>(reinterpret_cast<const f32x4*>(p)));
+  }
   __device__ __forceinline__ void store(TI* p) const { *reinterpret_cast<uint4*>(p) = u; }
   __device__ __forceinline__ void get(float (&f)[N]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};

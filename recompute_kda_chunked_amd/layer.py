@@ -65,28 +65,33 @@ def _rows(name, t, dev, vec):
     rows are contiguous; `vec`: rows start at multiples of 16 bytes."""
     if t.device != dev:
         raise KdaError("%s must be on %s" % (name, dev))
+    if vec and t.data_ptr() % 16:
+        raise KdaError("%s: tokens must start at multiples of 16 bytes" % name)
     if t.is_contiguous():
-        st = 0
-    else:
-        inner = t.stride()[1:]
-        want, n = [], 1
-        for d in reversed(t.shape[1:]):
-            want.append(n)
-            n *= d
-        if any(a != b and d > 1 for a, b, d in zip(inner, reversed(want), t.shape[1:])):
-            raise KdaError("%s: the elements of a token must be contiguous (strides %s)"
-                           % (name, tuple(t.stride())))
-        st = t.stride(0) if t.shape[0] > 1 else 0
-        if t.shape[0] > 1 and st < n:
-            raise KdaError("%s: tokens overlap (stride %d for %d elements)" % (name, st, n))
-    if vec and (t.data_ptr() % 16 or (st * t.element_size()) % 16):
+        return 0
+    inner = t.stride()[1:]
+    want, n = [], 1
+    for d in reversed(t.shape[1:]):
+        want.append(n)
+        n *= d
+    if any(a != b and d > 1 for a, b, d in zip(inner, reversed(want), t.shape[1:])):
+        raise KdaError("%s: the elements of a token must be contiguous (strides %s)"
+                       % (name, tuple(t.stride())))
+    st = t.stride(0)
+    if t.shape[0] == 1:
+        return 0
+    if st < n:
+        raise KdaError("%s: tokens overlap (stride %d for %d elements)" % (name, st, n))
+    if vec and (st * t.element_size()) % 16:
         raise KdaError("%s: tokens must start at multiples of 16 bytes" % name)
     return st
 
 
 def _no_grad(what, instead, tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise KdaError("%s is not differentiable (%s)" % (what, instead))
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise KdaError("%s is not differentiable (%s)" % (what, instead))
 
 
 def _extent(t):
@@ -166,7 +171,7 @@ def _recurrent(name, gates, q, k, v, raw_g, A_log, dt_bias, state, cu_seqlens, s
     _placed("dt_bias", dt_bias, dev)
     _placed("state", state, dev)
     if out is None:
-        out = torch.empty((T, H, V), dtype=dt, device=dev)
+        out = q.new_empty((T, H, V))
     else:
         _placed("out", out, dev)
         _apart("out", out, [t for t in (q, k, v, raw_g, *gates, A_log, dt_bias, state, cu_seqlens,
@@ -213,7 +218,11 @@ _GATE_ACT = {"sigmoid": _lib.KDA_ACT_SIGMOID, "silu": _lib.KDA_ACT_SILU}
 
 
 def _wants_grad(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 def _grad(t):

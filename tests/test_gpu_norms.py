@@ -225,3 +225,34 @@ def test_norms_on_another_stream():
         got = (gated_norm_forward(o, g, w), *gated_norm_backward(o, g, w, dy))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_larger_than_the_caches(dtype):
+    announce("norms past the caches %s" % dtype)  # 400 MB and more per launch
+    T = 8192 if dtype is BF16 else 4096
+    o, g, dy, w = randn(80, dtype, T, 64, 128), randn(81, dtype, T, 64, 128), randn(82, dtype, T, 64, 128), randn(83, F32, 128)
+    y, got = gated_norm_forward(o, g, w), gated_norm_backward(o, g, w, dy)
+    dw = torch.zeros(128, dtype=torch.float64, device="cuda")
+    for a in range(0, T, 700):  # the same rows in smaller launches
+        s = slice(a, min(a + 700, T))
+        assert torch.equal(y[s], gated_norm_forward(o[s], g[s], w))
+        part = gated_norm_backward(o[s], g[s], w, dy[s])
+        assert torch.equal(got[0][s], part[0]) and torch.equal(got[1][s], part[1])
+        dw += part[2].double()
+    assert rel(to_np(got[2]), to_np(dw)) <= 1e-5
+    del o, g, dy, y, got, part
+    for gate, post in (("channel", True), ("token", False), ("none", True)):
+        x, y, wp, wq, gt, dxo, dh = block_inputs(dtype, 2 * T, 4096, gate, post, 84)
+        kw = dict(w_post=wq, residual_scale=0.4)
+        out, got = block_norm_forward(x, y, wp, raw_gate=gt, **kw), block_norm_backward(x, y, wp, dxo, dh, raw_gate=gt, **kw)
+        dwp = torch.zeros(4096, dtype=torch.float64, device="cuda")
+        for a in range(0, 2 * T, 900):
+            s = slice(a, min(a + 900, 2 * T))
+            gs = None if gt is None else gt[s].clone()
+            assert all(torch.equal(u[s], v) for u, v in zip(out, block_norm_forward(x[s], y[s], wp, raw_gate=gs, **kw)))
+            part = block_norm_backward(x[s], y[s], wp, dxo[s], dh[s], raw_gate=gs, **kw)
+            assert torch.equal(got[0][s], part[0]) and torch.equal(got[1][s], part[1])
+            assert gt is None or torch.equal(got[4][s], part[4])
+            dwp += part[2].double()
+        assert rel(to_np(got[2]), to_np(dwp)) <= 1e-5

@@ -275,3 +275,23 @@ def test_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)) and torch.equal(pool, other), k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_rows_larger_than_the_caches(dtype, W):
+    announce("convolution past the caches %s W%d" % (dtype, W))  # 600 MB and more per launch
+    C, each = 4096, 5000 if dtype is F32 else 10001
+    v = inputs(dtype, [each, 0, 3, 2 * each - 3, each], C, W, seed=110)
+    y, final = short_conv_forward(v["x"], v["w"], v["b"], v["cud"], initial_state=v["init"], output_final_state=True)
+    got = short_conv_backward(v["x"], v["w"], v["b"], v["dy"], v["cud"], initial_state=v["init"], d_final_state=v["df"])
+    for c in range(0, C, 512):  # the same channels in smaller launches
+        s = slice(c, c + 512)
+        part = {k: v[k][..., s].contiguous() for k in ("x", "b", "init", "dy", "df")}
+        w = v["w"][s]
+        a = short_conv_forward(part["x"], w, part["b"], v["cud"], initial_state=part["init"], output_final_state=True)
+        assert torch.equal(y[:, s], a[0]) and torch.equal(final[..., s], a[1])
+        b = short_conv_backward(part["x"], w, part["b"], part["dy"], v["cud"], initial_state=part["init"],
+                                d_final_state=part["df"])
+        assert torch.equal(got[0][:, s], b[0]) and torch.equal(got[3][..., s], b[3])
+        assert rel(to_np(got[1][s]), to_np(b[1])) <= 1e-5 and rel(to_np(got[2][s]), to_np(b[2])) <= 1e-5
