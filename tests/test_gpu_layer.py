@@ -180,3 +180,78 @@ def test_gdn2_prompt_then_decoding(dtype, Dh, chunk):
     o = gdn2_recurrent(*[y[n] for n in names], ht, y["cu_seqlens"])
     assert rel(to_np(ht), rs) <= 1e-5
     assert rel(to_np(o), ro) <= 1e-5 + (0 if dtype is torch.float32 else 2.0 ** -8)
+
+
+def tiled(seed, *shape):
+    """bf16 values of a shape of more than 2^31 elements: one random block
+    repeated."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    n = int(np.prod(shape))
+    block = torch.randn(1 << 20, generator=gen, device="cuda").to(torch.bfloat16)
+    out = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    whole = n >> 20
+    out[:whole << 20].view(whole, 1 << 20).copy_(block.expand(whole, 1 << 20))
+    out[whole << 20:] = block[:n - (whole << 20)]
+    return out.view(shape)
+
+
+def test_norms_past_32_bit_offsets():
+    announce("norms of more than 2^31 elements")
+    from recompute_kda_chunked_amd import (block_norm_backward, block_norm_forward, gated_norm_backward,
+                                           gated_norm_forward)
+    rows = (1 << 24) + 77
+    o, g, dy = (tiled(s, rows, 128) for s in (1, 2, 3))
+    w = torch.linspace(0.5, 1.5, 128, device="cuda")
+    y = gated_norm_forward(o, g, w)
+    do, dg, _ = gated_norm_backward(o, g, w, dy)
+    e = slice(rows - 300, rows)
+    part = gated_norm_backward(o[e], g[e], w, dy[e])
+    assert torch.equal(y[e], gated_norm_forward(o[e], g[e], w))
+    assert torch.equal(do[e], part[0]) and torch.equal(dg[e], part[1])
+    del o, g, dy, y, do, dg
+    T, D = (1 << 18) + 9, 8192
+    x, y, d0, d1 = (tiled(s, T, D) for s in (4, 5, 6, 7))
+    w = torch.linspace(0.5, 1.5, D, device="cuda")
+    out = block_norm_forward(x, y, w, w_post=w)
+    got = block_norm_backward(x, y, w, d0, d1, w_post=w)
+    e = slice(T - 20, T)
+    assert all(torch.equal(a[e], b) for a, b in zip(out, block_norm_forward(x[e], y[e], w, w_post=w)))
+    part = block_norm_backward(x[e], y[e], w, d0[e], d1[e], w_post=w)
+    assert torch.equal(got[0][e], part[0]) and torch.equal(got[1][e], part[1])
+
+
+def test_convolution_past_32_bit_offsets():
+    announce("convolution of more than 2^31 elements")
+    from recompute_kda_chunked_amd import short_conv_backward, short_conv_forward
+    T, C = (1 << 18) + 21, 8192
+    x, dy = tiled(8, T, C), tiled(9, T, C)
+    w, b = torch.randn(C, W, device="cuda") * 0.5, torch.randn(C, device="cuda")
+    cu = torch.tensor([0, T - 50, T], dtype=torch.int32, device="cuda")
+    y, final = short_conv_forward(x, w, b, cu, output_final_state=True)
+    dx = short_conv_backward(x, w, b, dy, cu)[0]
+    e = slice(T - 50, T)
+    ye, fe = short_conv_forward(x[e], w, b, output_final_state=True)
+    assert torch.equal(y[e], ye) and torch.equal(final[1:], fe)
+    assert torch.equal(dx[e], short_conv_backward(x[e], w, b, dy[e])[0])
+
+
+def test_launches_are_timed_by_kind():
+    announce("profile kinds")
+    from recompute_kda_chunked_amd import _lib
+    o = torch.randn(5, 2, 64, device="cuda").requires_grad_(True)
+    w, x = torch.ones(64, device="cuda"), torch.randn(5, 64, device="cuda").requires_grad_(True)
+    cw, cb = torch.randn(64, W, device="cuda"), torch.randn(64, device="cuda")
+    state = torch.zeros(5, 2, 64, 64, device="cuda")
+    z = o.detach()
+    _lib.profile_begin()
+    out = (gated_norm(o, z, w), *block_norm(x, x.detach(), w), short_conv(x, cw, cb))
+    grads = torch.autograd.grad(out, (o, x), out)
+    short_conv_update(x.detach(), cw, cb, torch.zeros(5, W - 1, 64, device="cuda"))
+    kda_recurrent(z, z, z, z, z[:, :, 0].contiguous(), torch.zeros(2, device="cuda"),
+                  torch.zeros(2, 64, device="cuda"), state)
+    prof = _lib.profile_end()
+    assert len(grads) == 2
+    # the backward calls are made by autograd's own thread: their launches are not this thread's
+    for kind in ("gated_norm", "block_norm", "short_conv", "short_conv_update", "recurrent"):
+        assert prof[kind][0] == 1 and prof[kind][1] > 0, kind
+    assert prof["recurrent"][2] == 10 and prof["gated_norm"][2] == 10 and prof["block_norm"][2] == 5
