@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) k_short_conv(ShortConvArgs a, Cover 
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] *= sigmoidf(v[i]);
       }
-      store4<TI>(in_row(y + t * ys, lb), v);
+      store4<TI, NT>(in_row(y + t * ys, lb), v);
       shift4<W>(win, xv);
     };
     Row4<TI> nx[U];
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_bwd(ShortConvArgs a, Co
       auto put = [&](int t, const f32x4& v) {
         const int tt = t - (W - 1);
         if (tt >= p.a0) {
-          if (tt < p.a1) store4<TI>(in_row(dx + tt * ys, lb), v);
+          if (tt < p.a1) store4<TI, NT>(in_row(dx + tt * ys, lb), v);
         } else if (di) {
           store4<TI>(in_row(di + (t - p.q.s) * ys, lb), v);
         }
@@ -421,16 +421,20 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a,
 
 enum { kFwd, kBwd, kUpdate };
 
-// Runs of up to 128 tokens, halved (to 8 at least) while fewer than 2048 waves
-// would run: the backward's registers let two waves per SIMD run at once, and
-// a second, part-filled round of waves costs more than longer runs save
-// (8192 x 8192 bf16, backward: 93 us with 2048 runs of 128, 101 us with 4096 of
-// 64; the forward takes 51 us either way).
+// Runs of a multiple of kAhead tokens, 8 at least, such that the waves fill
+// whole rounds of 2048: the backward's registers let two waves per SIMD run at
+// once, and a part-filled round costs as much as a full one. One round while
+// its runs are at most 160 tokens (8192 x 8192 bf16, backward: 93 us with 2048
+// runs of 128, 101 us with 4096 of 64; forward and backward of 9000 x 8192: 192
+// us with 2272 runs of 128, 163 us with 2016 of 144).
 Cover cover_of(int C, int64_t T) {
+  constexpr int64_t kRound = 2048, kLongest = 160;
   Cover c;
   c.ncb = (C + kWaveCh - 1) / kWaveCh;
-  c.R = 128;
-  while (c.R > 8 && c.ncb * ((T + c.R - 1) / c.R) < 2048) c.R /= 2;
+  const int64_t work = c.ncb * T;  // tokens that one wave at a time walks
+  const int64_t rounds = work / (kRound * kLongest) + 1;
+  const int64_t run = (work + kRound * rounds - 1) / (kRound * rounds);
+  c.R = run <= 8 ? 8 : static_cast<int>((run + kAhead - 1) / kAhead * kAhead);
   c.nrb = ((T + c.R - 1) / c.R + kRuns - 1) / kRuns;
   return c;
 }

@@ -22,16 +22,23 @@ struct RecurrentArgs {
 };
 hipError_t launch_recurrent(int dtype, int D, bool gdn2, const RecurrentArgs& a, hipStream_t s);
 
-// Whether a launch of the row kernels that moves `bytes` loads its rows past
-// the caches (non-temporal). From about the 256 MiB that the memory-side cache
-// holds they cannot be in it and only push each other out; below, rows that
-// the kernel before wrote often are. bf16, microseconds plain / past the
-// caches, rows in the caches where they fit (in brackets: never in them):
+// Whether a launch of the row kernels that moves `bytes` loads and stores its
+// rows past the caches (non-temporal). From about the 256 MiB that the
+// memory-side cache holds they cannot be in it and only push each other out;
+// below, rows that the kernel before wrote often are, and the kernel behind
+// finds the ones stored. bf16, microseconds with plain loads / with loads past
+// the caches, rows in the caches where they fit (in brackets: never in them):
 //   gated norm forward    275 MB 41.7 / 43.1 (42.9 / 43.5)   334 MB 55.7 / 52.5   403 MB 69.3 / 60.5
 //   gated norm backward   168 MB 33.0 / 35.9 (36.0 / 35.8)   335 MB 66.7 / 62.2   671 MB 133 / 113
 //   block norm forward    268 MB 41.2 / 48.2 (48.2 / 48.3)   335 MB 65.6 / 58.8
 //   block norm backward   268 MB 55.2 / 57.0 (56.0 / 56.3)   393 MB 82.0 / 73.4   537 MB 108 / 95
 //   convolution backward  201 MB 48.3 / 52.6 (50.6 / 53.0)   295 MB 83.2 / 82.9   403 MB 90.3 / 85.9
+// Stores on top of that, with the outputs kept and an elementwise kernel that
+// reads them behind (in brackets: without it), plain / past the caches:
+//   gated norm forward    101 MB 29.1 / 30.7 (19.6 / 18.6)   403 MB 106.7 / 103.7 (66.8 / 63.1)
+// and for a forward with its backward behind, outputs kept: gated norm 8192 x
+// 64 x 128 199 / 186, block norm 8191 x 4096 164 / 158, convolution 8192 x 8192
+// 147 / 143.
 inline bool streams_past_caches(int64_t bytes) { return bytes >= (int64_t{288} << 20); }
 
 // Sums of `nb` partial rows of M = n0 + n1 floats, in a fixed order: the

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(256) k_gated_norm(GatedNormArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) y[i] = o[i] * r * w[i] * act_value(a.act, g[i], sigmoidf(g[i]));
     vo.set(y);
-    vo.store(static_cast<TI*>(a.y) + at);
+    vo.template store<NT>(static_cast<TI*>(a.y) + at);
   }
 }
 
@@ -139,9 +139,9 @@ __global__ void __launch_bounds__(256) k_gated_norm_bwd(GatedNormArgs a) {
       dw[i] += d[i] * n * av;
     }
     vo.set(x);
-    vo.store(static_cast<TI*>(a.d_o) + at);
+    vo.template store<NT>(static_cast<TI*>(a.d_o) + at);
     vg.set(y);
-    vg.store(static_cast<TI*>(a.dgate) + at);
+    vg.template store<NT>(static_cast<TI*>(a.dgate) + at);
   }
   store_params<N>(&sm[sub][c], dw);
   __syncthreads();
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(512) k_block_norm(BlockNormArgs a) {
       }
       if (v < nvec) {
         vx[j].set(xo[j]);
-        vx[j].store(static_cast<TI*>(a.x_out) + row + v * N);
+        vx[j].template store<NT>(static_cast<TI*>(a.x_out) + row + v * N);
       }
     }
     block_sum<1>(s, sm, phase);
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(512) k_block_norm(BlockNormArgs a) {
 #pragma unroll
         for (int i = 0; i < N; ++i) h[i] = xo[j][i] * rx * w[i];
         vx[j].set(h);
-        vx[j].store(static_cast<TI*>(a.h) + row + v * N);
+        vx[j].template store<NT>(static_cast<TI*>(a.h) + row + v * N);
       }
     }
   }
@@ -363,10 +363,10 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(BlockNormArgs a) {
       }
       if (v < nvec) {
         vd[j].set(d);
-        vd[j].store(static_cast<TI*>(a.dx) + row + v * N);
+        vd[j].template store<NT>(static_cast<TI*>(a.dx) + row + v * N);
         if constexpr (GATE == KDA_BLOCK_GATE_CHANNEL) {
           vg[j].set(dg);
-          vg[j].store(static_cast<TI*>(a.dgate) + row + v * N);
+          vg[j].template store<NT>(static_cast<TI*>(a.dgate) + row + v * N);
         }
       }
     }
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(BlockNormArgs a) {
       }
       if (v < nvec) {
         vy[j].set(y);
-        vy[j].store(static_cast<TI*>(a.dy) + row + v * N);
+        vy[j].template store<NT>(static_cast<TI*>(a.dy) + row + v * N);
       }
     }
   }

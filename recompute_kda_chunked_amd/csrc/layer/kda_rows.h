@@ -37,7 +37,10 @@ struct RowVec {
   __device__ __forceinline__ void load(const TI* p) {
     u = __builtin_bit_cast(uint4, vload<NT>(reinterpret_cast<const f32x4*>(p)));
   }
-  __device__ __forceinline__ void store(TI* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  template <bool NT>
+  __device__ __forceinline__ void store(TI* p) const {
+    vstore<NT>(reinterpret_cast<f32x4*>(p), __builtin_bit_cast(f32x4, u));
+  }
   __device__ __forceinline__ void get(float (&f)[N]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
