@@ -152,6 +152,8 @@ def _recurrent(name, gates, q, k, v, raw_g, A_log, dt_bias, state, cu_seqlens, s
     _want("state", state, (state.shape[0], H, K, V), torch.float32)
     if out is not None:
         _want("out", out, (T, H, V), dt)
+    if gate_mode & _lib.KDA_GATE_PER_HEAD and not per_head:
+        raise KdaError("KDA_GATE_PER_HEAD takes raw_g [T,H] and dt_bias [H]")
     if K != V or K not in (64, 128):
         raise KdaError("heads of K = %d, V = %d are not built: K = V, 64 or 128" % (K, V))
     _no_grad(name, "train with the chunked form", (q, k, v, raw_g, *gates, A_log, dt_bias, state))
@@ -411,9 +413,9 @@ def _conv_problem(x, weight, bias, activation, **tensors):
     for name, (t, shape) in tensors.items():
         if t is not None:
             _want(name, t, shape, dt)
-    if not 2 <= W <= 4 or C % 8:
+    if not 2 <= W <= 4 or C % 8 or not 0 < C <= 1 << 20:
         raise KdaError("a convolution of %d taps over %d channels is not built: 2 to 4 taps, a "
-                       "multiple of 8 channels" % (W, C))
+                       "multiple of 8 channels up to 2^20" % (W, C))
     dev = _dev(x, "x")
     p = _lib.KdaShortConvProblem(total_tokens=T, C=C, W=W, dtype=_DT[dt],
                                  activation=_CONV_ACT[activation],

@@ -319,6 +319,11 @@ def test_sizes_that_are_not_built_are_named():
         z = torch.zeros(2, D)
         with pytest.raises(KdaError, match="D = %d is not built" % D):
             block_norm(z, z, torch.zeros(D))
-    for C, W in ((12, 4), (16, 5), (16, 1)):
+    for C, W in ((12, 4), (16, 5), (16, 1), ((1 << 20) + 8, 2), (0, 4)):
         with pytest.raises(KdaError, match="not built"):
-            short_conv(torch.zeros(3, C), torch.zeros(C, W))
+            short_conv(torch.zeros(1, C), torch.zeros(C, W))
+
+
+def test_recurrent_refuses_a_per_head_gate_of_other_shape():
+    with pytest.raises(KdaError, match="KDA_GATE_PER_HEAD takes"):
+        kda_recurrent(**rec_inputs(), gate_mode=_lib.KDA_GATE_PER_HEAD)
