@@ -1,6 +1,9 @@
 """Python binding of the operators around the chunked one: argument checks and
 marshalling only, as in ``ops``. Every step runs in the HIP kernels behind
-``include/kda.h``.
+``include/kda.h``. Calls can be captured into graphs; a captured training step
+takes the ``*_forward`` and ``*_backward`` functions, or autograd over leaves of
+which no graph built outside the capture is alive (PyTorch's engine otherwise
+ties the capture to that graph's stream).
 """
 from __future__ import annotations
 
