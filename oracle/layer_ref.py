@@ -58,12 +58,13 @@ def recurrent(q, k, v, raw_g, A_log, dt_bias, state, cu, slots=None, raw_beta=No
 
 
 def _act(kind, x):
-    """(value, derivative) of the activation."""
-    s = sigmoid(x)
+    """(value, derivative) of the activation. 1 - s is taken as sigmoid(-x),
+    which keeps its digits where s is next to 1."""
+    s, c = sigmoid(x), sigmoid(-x)
     if kind == "sigmoid":
-        return s, s * (1 - s)
+        return s, s * c
     if kind == "silu":
-        return x * s, s * (1 + x * (1 - s))
+        return x * s, s * (1 + x * c)
     return x, np.ones_like(x)
 
 
@@ -89,10 +90,10 @@ def block_norm(x, y, w_pre, w_post=None, raw_gate=None, residual_scale=1.0, eps=
     rmsnorm(y) * w_post or y; a gate [T] or [T,D]. With dx_out and dh the
     gradients as a dict."""
     x, y, w_pre = map(_f64, (x, y, w_pre))
-    a = np.ones((1, 1))
+    a = rest = np.ones((1, 1))
     if raw_gate is not None:
-        a = sigmoid(_f64(raw_gate))
-        a = a[:, None] if a.ndim == 1 else a
+        a, rest = sigmoid(_f64(raw_gate)), sigmoid(-_f64(raw_gate))  # rest = 1 - a
+        a, rest = (t[:, None] if t.ndim == 1 else t for t in (a, rest))
     ry = 1 / np.sqrt(np.mean(y * y, -1, keepdims=True) + eps)
     z = y * ry * _f64(w_post) if w_post is not None else y
     xo = x + residual_scale * a * z
@@ -114,7 +115,7 @@ def block_norm(x, y, w_pre, w_post=None, raw_gate=None, residual_scale=1.0, eps=
         out["dy"] = ry * (dny - ny * np.mean(dny * ny, -1, keepdims=True))
         out["dw_post"] = np.sum(dz * ny, 0)
     if raw_gate is not None:
-        dg = residual_scale * z * dX * a * (1 - a)
+        dg = residual_scale * z * dX * a * rest
         out["dgate"] = dg if _f64(raw_gate).ndim == 2 else dg.sum(1)
     return out
 

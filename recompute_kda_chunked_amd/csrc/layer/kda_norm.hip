@@ -7,6 +7,8 @@
 // and each output written once (the backward recomputes the norms from the
 // inputs, so nothing is kept from the forward). Sums of squares, gate values
 // and parameter gradients are fp32; every output is rounded once.
+#include <cfloat>
+
 #include "../kda_internal.h"
 #include "kda.h"
 #include "kda_layer.h"
@@ -61,12 +63,19 @@ __device__ __forceinline__ float row_sum(float x) {
   else return group_sum<N>(x);
 }
 
+// 1 - s for s = sigmoidf(g), as e^-g s: the difference loses its digits where s
+// is next to 1 (half of them at g = 9, the last at 17). Where e^-g overflows, 1.
+__device__ __forceinline__ float sigmoid_rest(float g, float s) {
+  const float e = __expf(-g);
+  return e > FLT_MAX ? 1.f : e * s;
+}
+
 // act(g) and its derivative.
 __device__ __forceinline__ float act_value(int act, float g, float s) {
   return act == KDA_ACT_SILU ? g * s : s;
 }
 __device__ __forceinline__ float act_slope(int act, float g, float s) {
-  return act == KDA_ACT_SILU ? s * (1.f + g * (1.f - s)) : s * (1.f - s);
+  return act == KDA_ACT_SILU ? s * (1.f + g * (1.f - s)) : s * sigmoid_rest(g, s);
 }
 
 // A row lies across V / N consecutive lanes, one 16-byte vector each, so a
@@ -301,8 +310,11 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(BlockNormArgs a) {
         if (a.dx_out) vd[j].template load<NT>(static_cast<const TI*>(a.dx_out) + row + v * N);
       }
     }
-    float gt = 1.f;
-    if constexpr (GATE == KDA_BLOCK_GATE_TOKEN) gt = sigmoidf(to_f(static_cast<const TI*>(a.gate)[t]));
+    float raw = 0.f, gt = 1.f;
+    if constexpr (GATE == KDA_BLOCK_GATE_TOKEN) {
+      raw = to_f(static_cast<const TI*>(a.gate)[t]);
+      gt = sigmoidf(raw);
+    }
     float ry = 1.f;
     if constexpr (POST) {
       float s[1] = {0.f};
@@ -355,7 +367,7 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(BlockNormArgs a) {
         float e = d[i];
         if constexpr (GATE == KDA_BLOCK_GATE_CHANNEL) {
           const float s = sigmoidf(g[i]);
-          dg[i] = a.scale * z * e * s * (1.f - s);
+          dg[i] = a.scale * z * e * s * sigmoid_rest(g[i], s);
           e *= s;
         }
         dz[j][i] = e;
@@ -379,7 +391,7 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(BlockNormArgs a) {
       s3[0] = s1[0];
       if constexpr (GATE == KDA_BLOCK_GATE_TOKEN)
         if (threadIdx.x == 0)
-          static_cast<TI*>(a.dgate)[t] = from_f<TI>(a.scale * s3[0] * gt * (1.f - gt));
+          static_cast<TI*>(a.dgate)[t] = from_f<TI>(a.scale * s3[0] * gt * sigmoid_rest(raw, gt));
     }
     const float my = s3[0] * inv * cz * ry;
 #pragma unroll

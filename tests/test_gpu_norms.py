@@ -256,3 +256,58 @@ def test_rows_larger_than_the_caches(dtype):
             assert gt is None or torch.equal(got[4][s], part[4])
             dwp += part[2].double()
         assert rel(to_np(got[2]), to_np(dwp)) <= 1e-5
+
+
+# ------------------------------------------------------------------ gates far from zero
+
+
+def far_gates(seed, dtype, lo, hi, *shape):
+    """Gates of lo .. hi in magnitude, of both signs."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    g = lo + (hi - lo) * torch.rand(shape, generator=gen, device="cuda")
+    return torch.where(torch.rand(shape, generator=gen, device="cuda") < 0.5, -g, g).to(dtype)
+
+
+# The slope s(g) (1 - s(g)) of a gate of magnitude m is e^-m to within e^-m, so
+# its relative error is that of an exponential: half a step of m log2(e) (up to
+# 16: 2^-20, up to 40: 2^-19) times ln 2, and m times the constant's 1.3e-8,
+# 0.9e-6 and 1.8e-6 in all. With the 2.5e-6 of the other factors (see above):
+# 3.4e-6 and 4.3e-6 of the element's value.
+FAR = [(8.0, 16.0, 4e-6), (16.0, 40.0, 6e-6)]
+
+
+def check_products(name, got, ref, dtype, tol):
+    got, ref = to_np(got), np.asarray(ref)
+    off = np.abs(got - ref) / np.abs(ref) - HALF_STEP[dtype] * (1 + 1e-5) - tol
+    print("%s worst relative excess %.2e" % (name, off.max()), flush=True)
+    assert np.all(np.abs(ref) > 1e-30) and np.all(off <= 0), name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lo,hi,tol", FAR)
+def test_gated_norm_slope_of_far_gates(dtype, lo, hi, tol):
+    announce("gated norm, gates of %g to %g %s" % (lo, hi, dtype))
+    for V in (64, 128, 256):
+        o, dy = randn(90, dtype, 40, 3, V) + 3.0, randn(91, dtype, 40, 3, V) + 3.0
+        g, w = far_gates(92, dtype, lo, hi, 40, 3, V), torch.linspace(0.5, 1.5, V, device="cuda")
+        o, dy = torch.where(o.abs() < 1e-3, 1.0, o), torch.where(dy.abs() < 1e-3, 1.0, dy)
+        want = layer_ref.gated_norm(o, g, w, dy)[2]
+        check_products("dgate", gated_norm_backward(o, g, w, dy)[1], want, dtype, tol)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", ["token", "channel"])
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("lo,hi,tol", FAR)
+def test_block_norm_slope_of_far_gates(dtype, gate, post, lo, hi, tol):
+    announce("block norm, gates of %g to %g %s %s post %s" % (lo, hi, dtype, gate, post))
+    for D in (264, 2056):
+        x, y, wp, wq, _, dxo, _ = block_inputs(dtype, 40, D, "none", post, 93)
+        y, dxo = (torch.where(t.abs() < 1e-3, 1.0, t) for t in (y, dxo))
+        g = far_gates(99, dtype, lo, hi, *((40,) if gate == "token" else (40, D)))
+        wq = None if wq is None else torch.linspace(0.5, 1.5, D, device="cuda")
+        if gate == "token":  # terms of one sign, whose sum is of their size
+            y, dxo = y.abs(), dxo.abs()
+        want = layer_ref.block_norm(x, y, wp, wq, g, 0.3, dx_out=dxo, dh=np.zeros(x.shape))["dgate"]
+        got = block_norm_backward(x, y, wp, dxo, None, w_post=wq, raw_gate=g, residual_scale=0.3)[4]
+        check_products("dgate", got, want, dtype, tol)

@@ -130,3 +130,12 @@ def test_short_conv_in_two_parts_is_one():
     second = layer_ref.short_conv(x[5:], w, b, [0, 4], first["final"])
     np.testing.assert_allclose(np.concatenate([first["y"], second["y"]]), whole["y"], rtol=1e-13)
     assert np.array_equal(second["final"], whole["final"])
+
+
+def test_gate_slopes_keep_their_digits_far_from_zero():
+    x = np.array([-700.0, -40.0, -17.0, 17.0, 40.0, 700.0])
+    want = np.exp(-np.abs(x)) / (1 + np.exp(-np.abs(x))) ** 2
+    np.testing.assert_allclose(layer_ref._act("sigmoid", x)[1], want, rtol=1e-14)
+    one, zero = np.ones((6, 1)), np.zeros((6, 1))
+    got = layer_ref.block_norm(zero, one, np.ones(1), None, x, 1.0, dx_out=one, dh=zero)["dgate"]
+    np.testing.assert_allclose(got, want, rtol=1e-14)
