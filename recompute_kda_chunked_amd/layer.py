@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib
@@ -90,11 +91,24 @@ def _rows(name, t, dev, vec):
     return st
 
 
-def _no_grad(what, instead, tensors):
+def _has_tangent(tensors):
+    """Whether a tensor carries a forward-mode derivative (no_grad does not
+    turn those off)."""
+    return forward_ad._current_level >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
+def _wants_grad(*tensors):
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
-                raise KdaError("%s is not differentiable (%s)" % (what, instead))
+                return True
+    return _has_tangent(tensors)
+
+
+def _no_grad(what, instead, tensors):
+    if _wants_grad(*tensors):
+        raise KdaError("%s is not differentiable (%s)" % (what, instead))
 
 
 def _extent(t):
@@ -220,14 +234,6 @@ def gdn2_recurrent(q, k, v, raw_g, raw_b, raw_w, A_log, dt_bias, state, cu_seqle
 # ---------------------------------------------------------------------------- gated norm
 
 _GATE_ACT = {"sigmoid": _lib.KDA_ACT_SIGMOID, "silu": _lib.KDA_ACT_SILU}
-
-
-def _wants_grad(*tensors):
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                return True
-    return False
 
 
 def _grad(t):

@@ -1,0 +1,61 @@
+"""The binding of the operators around the chunked one as torch sees it,
+without a GPU: the launch is left out and host tensors are let through, so
+that what autograd and its neighbours make of a call can be looked at."""
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+from recompute_kda_chunked_amd import (KdaError, block_norm, gated_norm, gdn2_recurrent,
+                                       kda_recurrent, layer, short_conv, short_conv_update)
+from test_layer_host import rec_inputs
+
+
+@pytest.fixture(autouse=True)
+def no_launch(monkeypatch):
+    monkeypatch.setattr(layer, "_dev", lambda t, name: t.device)
+    monkeypatch.setattr(layer, "_call", lambda *args, **kw: None)
+
+
+def gdn2_inputs():
+    x = rec_inputs()
+    beta = x.pop("raw_beta")
+    return dict(x, raw_b=torch.zeros_like(x["k"]), raw_w=torch.zeros(*beta.shape, 64))
+
+
+def conv_update_inputs():
+    return dict(x=torch.zeros(5, 64), weight=torch.zeros(64, 4), bias=torch.zeros(64),
+                state=torch.zeros(5, 3, 64))
+
+
+DIFFERENTIABLE = [
+    (gated_norm, lambda: dict(o=torch.zeros(4, 2, 64), gate=torch.zeros(4, 2, 64), weight=torch.zeros(64))),
+    (block_norm, lambda: dict(x=torch.zeros(4, 64), y=torch.zeros(4, 64), w_pre=torch.zeros(64),
+                              w_post=torch.zeros(64), raw_gate=torch.zeros(4))),
+    (short_conv, lambda: dict(x=torch.zeros(5, 64), weight=torch.zeros(64, 4), bias=torch.zeros(64),
+                              initial_state=torch.zeros(1, 3, 64))),
+]
+IN_PLACE = [(kda_recurrent, rec_inputs), (gdn2_recurrent, gdn2_inputs), (short_conv_update, conv_update_inputs)]
+
+
+@pytest.mark.parametrize("fn,make", DIFFERENTIABLE)
+@pytest.mark.parametrize("grad", [False, True])
+def test_forward_mode_is_refused_by_the_autograd_functions(fn, make, grad):
+    for name in make():
+        with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+            x = make()
+            fn(**x)  # a level without tangents changes nothing
+            x[name] = forward_ad.make_dual(x[name], torch.ones_like(x[name]))
+            with pytest.raises(NotImplementedError, match="jvp"):
+                fn(**x)
+
+
+@pytest.mark.parametrize("fn,make", IN_PLACE)
+@pytest.mark.parametrize("grad", [False, True])
+def test_forward_mode_is_refused_by_the_decoding_forms(fn, make, grad):
+    for name in make():
+        with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+            x = make()
+            fn(**x)
+            x[name] = forward_ad.make_dual(x[name], torch.ones_like(x[name]))
+            with pytest.raises(KdaError, match="not differentiable"):
+                fn(**x)
