@@ -106,9 +106,18 @@ def _wants_grad(*tensors):
     return _has_tangent(tensors)
 
 
+def _through_autograd(*tensors):
+    """Whether a call goes through its autograd function: a gradient is wanted,
+    or torch.jit.trace records it (as a call of that function; the launch
+    itself is no torch operation and would leave nothing in the graph)."""
+    return _wants_grad(*tensors) or torch._C._get_tracing_state() is not None
+
+
 def _no_grad(what, instead, tensors):
     if _wants_grad(*tensors):
         raise KdaError("%s is not differentiable (%s)" % (what, instead))
+    if torch._C._get_tracing_state() is not None:
+        raise KdaError("%s cannot be traced: its launch is no torch operation" % what)
 
 
 def _extent(t):
@@ -306,7 +315,7 @@ def gated_norm(o, gate, weight, *, eps=1e-6, activation="sigmoid"):
     y = rmsnorm(o) * weight * act(gate) over each head's V channels. o and
     gate [T,H,V] (any leading dimensions), weight fp32 [V] shared by the
     heads; activation 'sigmoid' or 'silu'. V is 64, 128 or 256."""
-    if _wants_grad(o, gate, weight):
+    if _through_autograd(o, gate, weight):
         return GatedNormFunction.apply(o, gate, weight, eps, activation)
     return gated_norm_forward(o, gate, weight, eps=eps, activation=activation)
 
@@ -394,7 +403,7 @@ def block_norm(x, y, w_pre, *, w_post=None, raw_gate=None, residual_scale=1.0, e
     as it is), times sigmoid(raw_gate) ([T] or [T,D]; None: 1) and
     residual_scale; returns (x_out, h), h = rmsnorm(x_out) * w_pre the next
     block's input. D is a multiple of 8, at most 8192."""
-    if _wants_grad(x, y, w_pre, w_post, raw_gate):
+    if _through_autograd(x, y, w_pre, w_post, raw_gate):
         return BlockNormFunction.apply(x, y, w_pre, w_post, raw_gate, residual_scale, eps)
     return block_norm_forward(x, y, w_pre, w_post=w_post, raw_gate=raw_gate,
                               residual_scale=residual_scale, eps=eps)
@@ -516,7 +525,7 @@ def short_conv(x, weight, bias=None, cu_seqlens=None, *, initial_state=None,
     output_final_state returns (y, final_state), final_state the last W-1 rows
     of each sequence, from which the next call or short_conv_update goes on.
     Rows of y behind the last sequence are zero."""
-    if _wants_grad(x, weight, bias, initial_state):
+    if _through_autograd(x, weight, bias, initial_state):
         return ShortConvFunction.apply(x, weight, bias, cu_seqlens, initial_state,
                                        output_final_state, activation)
     return short_conv_forward(x, weight, bias, cu_seqlens, initial_state=initial_state,

@@ -59,3 +59,20 @@ def test_forward_mode_is_refused_by_the_decoding_forms(fn, make, grad):
             x[name] = forward_ad.make_dual(x[name], torch.ones_like(x[name]))
             with pytest.raises(KdaError, match="not differentiable"):
                 fn(**x)
+
+
+@pytest.mark.parametrize("fn,make", DIFFERENTIABLE)
+def test_a_trace_keeps_the_call(fn, make, monkeypatch):
+    names, calls = list(make()), []
+    monkeypatch.setattr(layer, "_call", lambda dev, name, *args, **kw: calls.append(name))
+    traced = torch.jit.trace(lambda *t: fn(**dict(zip(names, t))), tuple(make().values()), check_trace=False)
+    assert any(n.kind() == "prim::PythonOp" for n in traced.graph.nodes()) and len(calls) == 1
+    traced(*make().values())
+    assert len(calls) == 2
+
+
+@pytest.mark.parametrize("fn,make", IN_PLACE)
+def test_decoding_forms_refuse_a_trace(fn, make):
+    names = list(make())
+    with pytest.raises(KdaError, match="cannot be traced"):
+        torch.jit.trace(lambda *t: fn(**dict(zip(names, t))), tuple(make().values()), check_trace=False)
