@@ -120,6 +120,12 @@ def _no_grad(what, instead, tensors):
         raise KdaError("%s cannot be traced: its launch is no torch operation" % what)
 
 
+def _overwritten(*tensors):
+    """Tells autograd that a call has written to these tensors, so that a
+    backward that kept one of them raises instead of using the new values."""
+    torch.autograd.graph.increment_version(tensors)
+
+
 def _extent(t):
     """The address range a tensor's elements lie in."""
     if t.numel() == 0:
@@ -206,6 +212,7 @@ def _recurrent(name, gates, q, k, v, raw_g, A_log, dt_bias, state, cu_seqlens, s
                                         state_indices) if t is not None])
     _call(dev, "kda_gdn2_recurrent" if g2 else "kda_recurrent", p, q, k, v, raw_g, *gates, A_log,
           dt_bias, cu_seqlens, state_indices, state, out)
+    _overwritten(state, out)
     return out
 
 
@@ -553,4 +560,5 @@ def short_conv_update(x, weight, bias, state, cu_seqlens=None, *, state_indices=
         _apart("out", out, [t for t in (x, weight, bias, state, cu_seqlens, state_indices)
                             if t is not None])
     _call(dev, "kda_short_conv_update", p, x, weight, bias, cu_seqlens, state_indices, state, out)
+    _overwritten(state, out)
     return out

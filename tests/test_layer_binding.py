@@ -76,3 +76,30 @@ def test_decoding_forms_refuse_a_trace(fn, make):
     names = list(make())
     with pytest.raises(KdaError, match="cannot be traced"):
         torch.jit.trace(lambda *t: fn(**dict(zip(names, t))), tuple(make().values()), check_trace=False)
+
+
+@pytest.mark.parametrize("fn,make", IN_PLACE)
+def test_autograd_sees_what_a_call_overwrites(fn, make):
+    for name in ("state", "out"):
+        x = make()
+        if name == "out":
+            x["out"] = fn(**x)
+        w = torch.ones((), requires_grad=True)
+        loss = (w * x[name]).sum()  # keeps state or out for its backward
+        version = x[name]._version
+        fn(**x)
+        assert x[name]._version > version
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():  # tensors without versions
+        x = make()
+        fn(**x, out=fn(**x))
+    fn(**x)
+
+
+@pytest.mark.parametrize("fn,make", IN_PLACE)
+def test_inputs_keep_their_versions(fn, make):
+    x = make()
+    versions = {n: t._version for n, t in x.items()}
+    fn(**x)
+    assert all(t._version == versions[n] for n, t in x.items() if n != "state")
