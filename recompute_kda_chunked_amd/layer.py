@@ -188,7 +188,8 @@ def _recurrent(name, gates, q, k, v, raw_g, A_log, dt_bias, state, cu_seqlens, s
         raise KdaError("KDA_GATE_PER_HEAD takes raw_g [T,H] and dt_bias [H]")
     if K != V or K not in (64, 128):
         raise KdaError("heads of K = %d, V = %d are not built: K = V, 64 or 128" % (K, V))
-    _no_grad(name, "train with the chunked form", (q, k, v, raw_g, *gates, A_log, dt_bias, state))
+    _no_grad(name, "train with the chunked form",
+             (q, k, v, raw_g, *gates, A_log, dt_bias, state, out))
     dev = _dev(q, "q")
     p = _lib.KdaRecurrentProblem(
         n_seqs=_seqs(cu_seqlens, state_indices, T, state.shape[0], dev), total_tokens=T, H=H, K=K,
@@ -548,7 +549,7 @@ def short_conv_update(x, weight, bias, state, cu_seqlens=None, *, state_indices=
     kda_recurrent. Not differentiable."""
     if state.dim() != 3:
         raise KdaError("state: expected [slots,W-1,C], got %s" % (tuple(state.shape),))
-    _no_grad("short_conv_update", "train with short_conv", (x, weight, bias, state))
+    _no_grad("short_conv_update", "train with short_conv", (x, weight, bias, state, out))
     dev, p = _conv_problem(x, weight, bias, activation,
                            state=(state, (state.shape[0], weight.shape[-1] - 1, x.shape[-1])),
                            out=(out, x.shape))

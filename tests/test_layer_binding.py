@@ -103,3 +103,17 @@ def test_inputs_keep_their_versions(fn, make):
     versions = {n: t._version for n, t in x.items()}
     fn(**x)
     assert all(t._version == versions[n] for n, t in x.items() if n != "state")
+
+
+@pytest.mark.parametrize("fn,make", IN_PLACE)
+def test_an_out_that_requires_a_gradient_is_refused(fn, make):
+    x = make()
+    out = fn(**x).requires_grad_(True)
+    with pytest.raises(KdaError, match="not differentiable"):
+        fn(**x, out=out)
+    with pytest.raises(KdaError, match="not differentiable"):
+        fn(**x, out=out * 1)
+    with torch.no_grad():
+        assert fn(**x, out=out) is out
+    with forward_ad.dual_level(), pytest.raises(KdaError, match="not differentiable"):
+        fn(**x, out=forward_ad.make_dual(out.detach(), torch.ones_like(out)))
