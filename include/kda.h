@@ -269,7 +269,9 @@ int kda_gdn2_fwd_ex(const kda_problem *p, const void *q, const void *k, const vo
                     an earlier sequence with tokens names too, is an error
                     that the host cannot see: the sequence's rows of o are
                     NaN and no state is touched.
-     state          [n_slots, H, K, V] (fp32, device), updated in place.
+     state          [n_slots, H, K, V] (fp32, device), updated in place. Its
+                    addresses must be apart from those of every other tensor
+                    of the call (KDA_ERR_INVALID).
    Nothing is read on the host but the problem, so the call can be captured
    into a graph and replayed with other cu_seqlens and slots of the same N
    and T. It needs no workspace. T = 0 or N = 0: nothing is launched.
@@ -295,9 +297,9 @@ typedef struct {
 } kda_recurrent_problem;
 
 /* Errors: KDA_ERR_INVALID (negative or inconsistent sizes, a stride shorter
-   than a row or not a multiple of 16 bytes, a null pointer),
-   KDA_ERR_UNSUPPORTED (size, dtype or gate not built; N * H of 2^24 or
-   more), KDA_ERR_HIP. */
+   than a row or not a multiple of 16 bytes, a null pointer, a state that
+   overlaps another tensor), KDA_ERR_UNSUPPORTED (size, dtype or gate not
+   built; N * H of 2^24 or more), KDA_ERR_HIP. */
 int kda_recurrent(const kda_recurrent_problem *p, const void *q, const void *k, const void *v,
                   const void *raw_g, const void *raw_beta, const float *A_log,
                   const float *dt_bias, const int32_t *cu_seqlens,
@@ -415,8 +417,8 @@ int kda_short_conv_bwd(const kda_short_conv_problem *p, const void *x, const flo
 
 /* The convolution's decoding form: sequence n starts from its state in a
    pool [n_slots, W-1, C] (dtype) and leaves its last W-1 rows there.
-   cu_seqlens, state_indices, padded sequences, rows behind the last sequence
-   and capture as for kda_recurrent. */
+   cu_seqlens, state_indices, padded sequences, rows behind the last sequence,
+   overlap with the state and capture as for kda_recurrent. */
 int kda_short_conv_update(const kda_short_conv_problem *p, const void *x, const float *weight,
                           const float *bias, const int32_t *cu_seqlens,
                           const int32_t *state_indices, void *state, void *y, void *stream);

@@ -26,6 +26,29 @@ bool stride_ok(int64_t st, int64_t row, int dtype, int64_t T, bool vec) {
 }
 int64_t stride_of(int64_t st, int64_t row) { return st ? st : row; }
 
+// Addresses of a tensor; sizes in 128 bits, so that no problem overflows them.
+struct Range {
+  const void* at;
+  unsigned __int128 bytes;
+};
+Range dense(const void* p, int64_t a, int64_t b, size_t elem) {
+  return Range{p, static_cast<unsigned __int128>(a) * b * elem};
+}
+// T rows of `row` elements, `st` apart
+Range rows_of(const void* p, int64_t T, int64_t st, int64_t row, size_t elem) {
+  return Range{p, (static_cast<unsigned __int128>(T - 1) * st + row) * elem};
+}
+// Whether the state, which sequences write while others still read their
+// inputs, shares an address with one of `n` tensors (null ones: none).
+bool over_any(const Range& state, const Range* others, int n) {
+  const unsigned __int128 s = reinterpret_cast<uintptr_t>(state.at);
+  for (int i = 0; i < n; ++i) {
+    const unsigned __int128 x = reinterpret_cast<uintptr_t>(others[i].at);
+    if (x && x < s + state.bytes && s < x + others[i].bytes) return true;
+  }
+  return false;
+}
+
 int check_recurrent(const kda_recurrent_problem* p, bool g2, bool has_cu, bool has_idx) {
   if (!p) return KDA_ERR_INVALID;
   if (p->n_seqs < 0 || p->total_tokens < 0 || p->total_tokens > 0x7fffffffLL || p->H < 1 ||
@@ -97,6 +120,17 @@ int recurrent_common(bool g2, const kda_recurrent_problem* p, const void* q, con
   a.idx = state_indices;
   a.state = state;
   a.o = o;
+  const size_t e = p->dtype == KDA_F32 ? 4 : 2;
+  const int64_t gw = a.gate_head ? p->H : HK;
+  const Range others[] = {
+      rows_of(q, a.T, a.qs, HK, e),      rows_of(k, a.T, a.ks, HK, e),
+      rows_of(v, a.T, a.vs, HK, e),      rows_of(raw_g, a.T, a.gs, gw, e),
+      rows_of(raw_beta, a.T, a.bes, p->H, e), rows_of(raw_b, a.T, a.bks, HK, e),
+      rows_of(raw_w, a.T, a.wvs, HK, e), dense(A_log, p->H, 1, 4),
+      dense(dt_bias, gw, 1, 4),          dense(cu_seqlens, int64_t{a.N} + 1, 1, 4),
+      dense(state_indices, a.N, 1, 4),   rows_of(o, a.T, HK, HK, e)};
+  if (over_any(dense(state, a.n_slots, HK * p->V, 4), others, sizeof others / sizeof *others))
+    return KDA_ERR_INVALID;
   hipStream_t s = static_cast<hipStream_t>(stream);
   KDA_TRY(KDA_KERNEL_RECURRENT, a.T * a.H, launch_recurrent(p->dtype, p->K, g2, a, s));
   return KDA_OK;
@@ -377,6 +411,13 @@ int kda_short_conv_update(const kda_short_conv_problem* p, const void* x, const 
   a.idx = state_indices;
   a.state = state;
   a.y = y;
+  const size_t e = p->dtype == KDA_F32 ? 4 : 2;
+  const Range others[] = {rows_of(x, a.T, a.xs, a.C, e),     dense(weight, a.C, p->W, 4),
+                          dense(bias, a.C, 1, 4),            dense(cu_seqlens, int64_t{a.N} + 1, 1, 4),
+                          dense(state_indices, a.N, 1, 4),   rows_of(y, a.T, a.C, a.C, e)};
+  if (over_any(dense(state, a.n_slots, int64_t{a.C} * (p->W - 1), e), others,
+               sizeof others / sizeof *others))
+    return KDA_ERR_INVALID;
   hipStream_t s = static_cast<hipStream_t>(stream);
   KDA_TRY(KDA_KERNEL_SHORT_CONV_UPDATE, p->n_seqs, launch_short_conv_update(p->dtype, p->W, a, s));
   return KDA_OK;

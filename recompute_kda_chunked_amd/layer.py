@@ -231,7 +231,8 @@ def kda_recurrent(q, k, v, raw_g, raw_beta, A_log, dt_bias, state, cu_seqlens=No
     touches no state. A slot past the pool, or one that an earlier sequence
     with tokens names too, is an error found on the device: NaN rows, no
     state touched. Rows of O behind the last sequence are not written (those
-    of a new O hold what its memory held). The tokens of
+    of a new O hold what its memory held). `state` must not overlap any other
+    tensor of the call. The tokens of
     q, k, v, raw_g and raw_beta may be slices of wider rows. raw_g [T,H] with
     dt_bias [H] gives one gate per head. Not differentiable. Its time grows
     with the longest sequence: prompts belong to kda_forward."""

@@ -16,7 +16,7 @@ import torch
 
 import kda_inputs
 from oracle import layer_ref
-from recompute_kda_chunked_amd import gdn2_recurrent, kda_forward, kda_recurrent
+from recompute_kda_chunked_amd import KdaError, gdn2_recurrent, kda_forward, kda_recurrent
 from test_gpu_states import announce, rel, to_np
 
 pytestmark = pytest.mark.gpu
@@ -299,3 +299,27 @@ def test_no_tokens():
     x["cu_seqlens"] = torch.zeros(2, dtype=torch.int32, device="cuda")
     assert run(x).shape == (0, 2, 64)
     assert torch.equal(before, x["state"])
+
+
+def test_state_between_its_neighbours():
+    announce("a state with its inputs and its output right before and behind it")
+    x = problem([2, 1, 3], 2, 64, torch.float32, 18)
+    y = dict(x, state=x["state"].clone())
+    names = ["q", "k", "v", "raw_g", "raw_beta", "A_log", "dt_bias"]
+    sizes = {n: x[n].numel() for n in names + ["state"]}
+    order = ["q", "k", "v", "state", "raw_g", "raw_beta", "dt_bias", "A_log"]
+    buf = torch.full((sum(sizes.values()) + x["v"].numel(),), float("nan"), device="cuda")
+    at = 0
+    for n in order:
+        y[n] = buf[at:at + sizes[n]].view(x[n].shape)
+        y[n].copy_(x[n])
+        at += sizes[n]
+    assert y["state"].data_ptr() == y["v"].data_ptr() + 4 * sizes["v"]
+    assert torch.equal(run(y), run(x)) and torch.equal(x["state"], y["state"])
+    for n in ("q", "raw_g"):  # over either end
+        z = dict(y)
+        i = y["state"].data_ptr() - buf.data_ptr()
+        i = (i // 4 - sizes[n] + 4) if n == "q" else (i // 4 + sizes["state"] - 4)
+        z[n] = buf[i:i + sizes[n]].view(x[n].shape)
+        with pytest.raises(KdaError, match="kda_recurrent failed"):
+            run(z)

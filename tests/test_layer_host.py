@@ -327,3 +327,55 @@ def test_sizes_that_are_not_built_are_named():
 def test_recurrent_refuses_a_per_head_gate_of_other_shape():
     with pytest.raises(KdaError, match="KDA_GATE_PER_HEAD takes"):
         kda_recurrent(**rec_inputs(), gate_mode=_lib.KDA_GATE_PER_HEAD)
+
+
+# ------------------------------------------------------------------ overlap with the state
+
+
+def at(addr):
+    return ctypes.c_void_p(addr)
+
+
+BASE = 1 << 32  # made-up addresses: every call below is refused before a launch
+
+
+@pytest.mark.parametrize("g2", [False, True])
+@pytest.mark.parametrize("per_head", [False, True])
+def test_recurrent_refuses_a_state_over_its_other_tensors(lib, g2, per_head):  # noqa: F811
+    if g2 and per_head:
+        return
+    N, T, H, K, slots, st = 3, 7, 2, 128, 5, 512  # bf16; q's rows 1024 bytes apart
+    p = rec(total_tokens=T, n_slots=slots, q_stride=st,
+            gate_mode=_lib.KDA_GATE_PER_HEAD if per_head else 0)
+    row, head = T * H * K * 2, T * H * 2
+    size = dict(q=((T - 1) * st + H * K) * 2, k=row, v=row, raw_g=head if per_head else row)
+    size.update(dict(raw_b=row, raw_w=row) if g2 else dict(raw_beta=head))
+    size.update(A_log=H * 4, dt_bias=H * 4 if per_head else H * K * 4, cu=(N + 1) * 4, idx=N * 4)
+    state, fn = slots * H * K * K * 4, lib.kda_gdn2_recurrent if g2 else lib.kda_recurrent
+    for name, n in dict(size, o=row).items():
+        for addr in (BASE, BASE + state - 4, BASE - n + 2, BASE + 64):  # over either end, and inside
+            where = {m: at((8 + 2 * i) * BASE) for i, m in enumerate(size)}
+            o = at(6 * BASE)
+            if name == "o":
+                o = at(addr)
+            else:
+                where[name] = at(addr)
+            got = fn(ctypes.byref(p), *where.values(), at(BASE), o, NUL)
+            assert got == _lib.KDA_ERR_INVALID, (name, addr - BASE)
+
+
+def test_short_conv_update_refuses_a_state_over_its_other_tensors(lib):  # noqa: F811
+    N, T, C, W, slots, st = 3, 7, 64, 4, 5, 192
+    p = sc(n_seqs=N, total_tokens=T, n_slots=slots, x_stride=st)
+    size = dict(x=((T - 1) * st + C) * 2, weight=C * W * 4, bias=C * 4, cu=(N + 1) * 4, idx=N * 4)
+    state = slots * (W - 1) * C * 2
+    for name, n in dict(size, y=T * C * 2).items():
+        for addr in (BASE, BASE + state - 2, BASE - n + 2, BASE + 64):
+            where = {m: at((8 + 2 * i) * BASE) for i, m in enumerate(size)}
+            y = at(6 * BASE)
+            if name == "y":
+                y = at(addr)
+            else:
+                where[name] = at(addr)
+            got = lib.kda_short_conv_update(ctypes.byref(p), *where.values(), at(BASE), y, NUL)
+            assert got == _lib.KDA_ERR_INVALID, (name, addr - BASE)
