@@ -25,7 +25,8 @@ def _dev(t: torch.Tensor, name: str) -> torch.device:
 
 def _raw_stream(index):
     """The current stream's handle. torch.cuda.current_stream builds an object
-    around it first, 1.9 us of a call that takes 8 in all."""
+    around it first, 1.9 us of a call that takes 8 in all. (Here as for the
+    current device the tensors' being there means that torch.cuda is set up.)"""
     return torch._C._cuda_getCurrentRawStream(index)
 
 
@@ -37,7 +38,7 @@ def _call(dev, name, problem, *tensors, workspace=None):
     args = [None if t is None else t.data_ptr() for t in tensors]
     if workspace is not None:
         args += (workspace.data_ptr(), workspace.numel())
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         st = fn(ctypes.byref(problem), *args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
@@ -91,39 +92,38 @@ def _rows(name, t, dev, vec):
     return st
 
 
-def _has_tangent(tensors):
-    """Whether a tensor carries a forward-mode derivative (no_grad does not
-    turn those off)."""
-    return forward_ad._current_level >= 0 and any(
-        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+_tracing = torch._C._get_tracing_state
 
 
-def _wants_grad(*tensors):
+def _wants_grad(tensors):
+    """Whether a tensor wants a gradient, or carries a forward-mode derivative
+    (which no_grad does not turn off)."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 return True
-    return _has_tangent(tensors)
+    return forward_ad._current_level >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def _through_autograd(*tensors):
     """Whether a call goes through its autograd function: a gradient is wanted,
     or torch.jit.trace records it (as a call of that function; the launch
     itself is no torch operation and would leave nothing in the graph)."""
-    return _wants_grad(*tensors) or torch._C._get_tracing_state() is not None
+    return _wants_grad(tensors) or _tracing() is not None
 
 
 def _no_grad(what, instead, tensors):
-    if _wants_grad(*tensors):
+    if _wants_grad(tensors):
         raise KdaError("%s is not differentiable (%s)" % (what, instead))
-    if torch._C._get_tracing_state() is not None:
+    if _tracing() is not None:
         raise KdaError("%s cannot be traced: its launch is no torch operation" % what)
 
 
-def _overwritten(*tensors):
-    """Tells autograd that a call has written to these tensors, so that a
-    backward that kept one of them raises instead of using the new values."""
-    torch.autograd.graph.increment_version(tensors)
+# Tells autograd that a call has written to these tensors, so that a backward
+# that kept one of them raises instead of using the new values
+# (torch.autograd.graph.increment_version without its checks of types).
+_overwritten = torch._C._increment_version
 
 
 def _extent(t):
@@ -213,7 +213,7 @@ def _recurrent(name, gates, q, k, v, raw_g, A_log, dt_bias, state, cu_seqlens, s
                                         state_indices) if t is not None])
     _call(dev, "kda_gdn2_recurrent" if g2 else "kda_recurrent", p, q, k, v, raw_g, *gates, A_log,
           dt_bias, cu_seqlens, state_indices, state, out)
-    _overwritten(state, out)
+    _overwritten((state, out))
     return out
 
 
@@ -557,10 +557,10 @@ def short_conv_update(x, weight, bias, state, cu_seqlens=None, *, state_indices=
     p.n_seqs = _seqs(cu_seqlens, state_indices, x.shape[0], state.shape[0], dev)
     p.n_slots = state.shape[0]
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(x.shape)
     else:
         _apart("out", out, [t for t in (x, weight, bias, state, cu_seqlens, state_indices)
                             if t is not None])
     _call(dev, "kda_short_conv_update", p, x, weight, bias, cu_seqlens, state_indices, state, out)
-    _overwritten(state, out)
+    _overwritten((state, out))
     return out
