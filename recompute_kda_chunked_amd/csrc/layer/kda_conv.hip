@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a,
   Bounds q{n, n + 1};
   if (a.cu) q = uniform_bounds(a, n);
   if (q.s >= q.e) return;
-  const int64_t slot = find_slot(a.idx, a.cu, n, a.n_slots);
+  const int64_t slot = find_slot(a.idx, a.cu, a.T, n, a.n_slots);
   if (c >= a.C) return;
   const size_t xs = a.xs, ys = a.C;
   const uint32_t lb = c * sizeof(TI);

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(64 * NW) k_recurrent(RecurrentArgs a) {
     t1 = t1 > a.T ? a.T : t1;
   }
   if (t0 >= t1) return;
-  const int64_t slot = find_slot(a.idx, a.cu, n, a.n_slots);
+  const int64_t slot = find_slot(a.idx, a.cu, a.T, n, a.n_slots);
   TI* o = static_cast<TI*>(a.o) + static_cast<size_t>(h) * D;
   const size_t os = static_cast<size_t>(a.H) * D;
   const int cg = lane % (CW / 4), rg = lane / (CW / 4);

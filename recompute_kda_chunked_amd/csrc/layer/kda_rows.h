@@ -84,18 +84,24 @@ __device__ __forceinline__ void store_params(float* p, const float (&f)[N]) {
     *reinterpret_cast<f32x4*>(p + i) = f32x4{f[i], f[i + 1], f[i + 2], f[i + 3]};
 }
 
+// Whether sequence j has a token in [0, T), where its bounds are clamped to.
+__device__ __forceinline__ bool has_tokens(const int32_t* cu, int64_t T, int j) {
+  const int64_t s = cu[j] < 0 ? 0 : cu[j], e = cu[j + 1] > T ? T : cu[j + 1];
+  return s < e;
+}
+
 // The pool slot of sequence n, found by the whole wave: kPadded for a negative
 // index (a padded sequence), kBadSlot for one past the pool or one that an
 // earlier sequence with tokens names too (two writers of one state). The
 // earlier indices are read 64 at a time, together with the sequence's own.
 constexpr int64_t kPadded = -1, kBadSlot = -2;
-__device__ __forceinline__ int64_t find_slot(const int32_t* idx, const int32_t* cu, int n,
-                                             int64_t n_slots) {
+__device__ __forceinline__ int64_t find_slot(const int32_t* idx, const int32_t* cu, int64_t T,
+                                             int n, int64_t n_slots) {
   if (!idx) return n;
   const int32_t slot = __builtin_amdgcn_readfirstlane(idx[n]);
   bool taken = false;
   for (int j = threadIdx.x & 63; j < n; j += 64)
-    if (idx[j] == slot && (!cu || cu[j + 1] > cu[j])) taken = true;
+    if (idx[j] == slot && (!cu || has_tokens(cu, T, j))) taken = true;
   if (slot < 0) return kPadded;
   return slot >= n_slots || __any(taken) ? kBadSlot : slot;
 }

@@ -323,3 +323,12 @@ def test_state_between_its_neighbours():
         z[n] = buf[i:i + sizes[n]].view(x[n].shape)
         with pytest.raises(KdaError, match="kda_recurrent failed"):
             run(z)
+
+
+def test_sequences_that_clamping_leaves_empty_take_no_slot():
+    announce("a sequence before the first token names the slot of the next")
+    x = problem([3], 2, 64, torch.float32, 19, slots=3)
+    x["idx"] = x["idx"].repeat(2)
+    y = dict(x, state=x["state"].clone(), idx=x["idx"][:1])
+    x["cu_seqlens"] = torch.tensor([-4, -2, 3], dtype=torch.int32, device="cuda")
+    assert torch.equal(run(x), run(y)) and torch.equal(x["state"], y["state"])

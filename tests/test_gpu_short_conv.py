@@ -295,3 +295,14 @@ def test_rows_larger_than_the_caches(dtype, W):
                                 d_final_state=part["df"])
         assert torch.equal(got[0][:, s], b[0]) and torch.equal(got[3][..., s], b[3])
         assert rel(to_np(got[1][s]), to_np(b[1])) <= 1e-5 and rel(to_np(got[2][s]), to_np(b[2])) <= 1e-5
+
+
+def test_update_of_sequences_that_clamping_leaves_empty():
+    announce("short conv update, a sequence before the first token names the slot of the next")
+    v = inputs(F32, [3], 64, 4, seed=120)
+    pool, idx = randn(121, F32, 2, 3, 64), torch.tensor([1, 1], dtype=torch.int32, device="cuda")
+    other = pool.clone()
+    cu = torch.tensor([-4, -2, 3], dtype=torch.int32, device="cuda")
+    got = short_conv_update(v["x"], v["w"], v["b"], pool, cu, state_indices=idx)
+    assert torch.equal(got, short_conv_update(v["x"], v["w"], v["b"], other, v["cud"], state_indices=idx[:1]))
+    assert torch.equal(pool, other)
