@@ -263,7 +263,8 @@ int kda_gdn2_fwd_ex(const kda_problem *p, const void *q, const void *k, const vo
                     leaves its state as it is. Rows of o at and after
                     cu_seqlens[N] are not written.
      state_indices  [N] (int32, device) or NULL: the pool slot of each
-                    sequence (NULL: slot n, n_slots >= N). A negative one
+                    sequence (NULL: slot n, n_slots >= N). At most 65536
+                    sequences (KDA_ERR_UNSUPPORTED). A negative one
                     marks a padded sequence: its rows of o are zero and no
                     state is touched. A slot of n_slots or more, or one that
                     an earlier sequence with tokens names too, is an error

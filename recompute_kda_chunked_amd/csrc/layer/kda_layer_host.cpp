@@ -15,6 +15,10 @@ namespace {
 // can be decoded from with the same problem and none it refuses can.
 constexpr float kMaxGateBound = 5.9f;
 
+// Most sequences named by state_indices: every block compares its index with
+// all earlier ones (kda_rows.h), about 1 ms at this many.
+constexpr int32_t kMaxIndexed = 65536;
+
 bool known_dtype(int dtype) { return dtype == KDA_F32 || dtype == KDA_BF16; }
 
 // A token stride in elements: `row` when 0; otherwise at least a row and,
@@ -76,6 +80,7 @@ int check_recurrent(const kda_recurrent_problem* p, bool g2, bool has_cu, bool h
     return KDA_ERR_INVALID;
   // one block of 256 threads per (sequence, head), below 2^32 threads
   if (static_cast<int64_t>(p->n_seqs) * p->H >= (int64_t{1} << 24)) return KDA_ERR_UNSUPPORTED;
+  if (has_idx && p->n_seqs > kMaxIndexed) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
 
@@ -403,6 +408,7 @@ int kda_short_conv_update(const kda_short_conv_problem* p, const void* x, const 
   // a block of 256 threads per sequence and 1024 channels, below 2^32 threads
   if (static_cast<int64_t>(p->n_seqs) * ((p->C + 1023) / 1024) >= (int64_t{1} << 24))
     return KDA_ERR_UNSUPPORTED;
+  if (state_indices && p->n_seqs > kMaxIndexed) return KDA_ERR_UNSUPPORTED;
   if (!cu_seqlens && p->total_tokens != p->n_seqs) return KDA_ERR_INVALID;
   if (!state_indices && p->n_slots < p->n_seqs) return KDA_ERR_INVALID;
   if (p->n_seqs == 0 || p->total_tokens == 0) return KDA_OK;

@@ -90,20 +90,40 @@ __device__ __forceinline__ bool has_tokens(const int32_t* cu, int64_t T, int j) 
   return s < e;
 }
 
-// The pool slot of sequence n, found by the whole wave: kPadded for a negative
+// The pool slot of sequence n, found by the whole block: kPadded for a negative
 // index (a padded sequence), kBadSlot for one past the pool or one that an
-// earlier sequence with tokens names too (two writers of one state). The
-// earlier indices are read 64 at a time, together with the sequence's own.
+// earlier sequence with tokens names too (two writers of one state). Every
+// block looks through all earlier indices, so a launch's reads grow with the
+// square of their number, and the host refuses more than 65536: each wave on
+// its own up to kScanAlone (four loads at once), the block's waves together
+// above. Microseconds without indices / with them:
+//   recurrent, 1 head, D = 64   256 6.5 / 6.9   1024 10.0 / 12.0   4096 27 / 33   16384 90 / 159   65536 345 / 1252
+//   update, 2048 channels       256 6.6 / 6.7   1024 10.2 / 12.2   4096 24 / 30   16384 110 / 183  65536 433 / 1119
+// (each wave on its own one load at a time: 4096 49 and 54, 16384 375 and 512).
 constexpr int64_t kPadded = -1, kBadSlot = -2;
+constexpr int kScanAlone = 1024;
 __device__ __forceinline__ int64_t find_slot(const int32_t* idx, const int32_t* cu, int64_t T,
                                              int n, int64_t n_slots) {
   if (!idx) return n;
   const int32_t slot = __builtin_amdgcn_readfirstlane(idx[n]);
+  const bool together = n > kScanAlone;
+  const int step = together ? blockDim.x : 64;
+  int j = together ? threadIdx.x : threadIdx.x & 63;
   bool taken = false;
-  for (int j = threadIdx.x & 63; j < n; j += 64)
-    if (idx[j] == slot && (!cu || has_tokens(cu, T, j))) taken = true;
+  auto look = [&](int i, int32_t x) {
+    if (x == slot && (!cu || has_tokens(cu, T, i))) taken = true;
+  };
+  for (; j + 3 * step < n; j += 4 * step) {
+    int32_t x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[u] = idx[j + u * step];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) look(j + u * step, x[u]);
+  }
+  for (; j < n; j += step) look(j, idx[j]);
+  const bool twice = together ? __syncthreads_or(taken) != 0 : __any(taken) != 0;
   if (slot < 0) return kPadded;
-  return slot >= n_slots || __any(taken) ? kBadSlot : slot;
+  return slot >= n_slots || twice ? kBadSlot : slot;
 }
 __device__ __forceinline__ float nan_value() { return __uint_as_float(0x7fc00000u); }
 

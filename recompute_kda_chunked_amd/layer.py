@@ -155,6 +155,8 @@ def _seqs(cu_seqlens, state_indices, T, slots, dev):
     if state_indices is not None:
         _want("state_indices", state_indices, (N,), torch.int32)
         _placed("state_indices", state_indices, dev, 4)
+        if N > 65536:
+            raise KdaError("state_indices of %d sequences: not built for more than 65536" % N)
     elif slots < N:
         raise KdaError("the state pool has %d slots for %d sequences" % (slots, N))
     return N
@@ -226,7 +228,8 @@ def kda_recurrent(q, k, v, raw_g, raw_beta, A_log, dt_bias, state, cu_seqlens=No
 
     cu_seqlens: int32 [N+1] on the device, as kda_forward's (no host copy is
     needed, so the call can be captured into a graph); None: one token per
-    sequence. state_indices: int32 [N] slot of each sequence (None: slot n);
+    sequence. state_indices: int32 [N] slot of each sequence (None: slot n;
+    at most 65536);
     a negative one marks a padded sequence, whose rows of O are zero and which
     touches no state. A slot past the pool, or one that an earlier sequence
     with tokens names too, is an error found on the device: NaN rows, no

@@ -332,3 +332,19 @@ def test_sequences_that_clamping_leaves_empty_take_no_slot():
     y = dict(x, state=x["state"].clone(), idx=x["idx"][:1])
     x["cu_seqlens"] = torch.tensor([-4, -2, 3], dtype=torch.int32, device="cuda")
     assert torch.equal(run(x), run(y)) and torch.equal(x["state"], y["state"])
+
+
+@pytest.mark.parametrize("n", [1026, 1200, 5000])
+@pytest.mark.parametrize("cu", [False, True])
+def test_bad_slots_among_many_sequences(n, cu):
+    announce("slots named twice among %d sequences" % n)
+    x = problem([1] * n, 1, 64, torch.float32, 21, slots=n + 2)
+    first = {1023: 0, 1024: 1022, 1025: 7, n // 2 + 300: n // 2, n - 2: 1, n - 1: n - 3}  # sequence: the earlier one
+    y = dict(x, state=x["state"].clone(), idx=x["idx"].clone())
+    for i, j in first.items():
+        x["idx"][i], y["idx"][i] = x["idx"][j], -1
+    got, want = run(x, cu=cu), run(y, cu=cu)
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[list(first)] = True
+    assert bool(torch.isnan(got[bad]).all()) and torch.equal(got[~bad], want[~bad])
+    assert torch.equal(x["state"], y["state"])

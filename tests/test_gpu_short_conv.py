@@ -306,3 +306,28 @@ def test_update_of_sequences_that_clamping_leaves_empty():
     got = short_conv_update(v["x"], v["w"], v["b"], pool, cu, state_indices=idx)
     assert torch.equal(got, short_conv_update(v["x"], v["w"], v["b"], other, v["cud"], state_indices=idx[:1]))
     assert torch.equal(pool, other)
+
+
+@pytest.mark.parametrize("n,C", [(1026, 8), (3000, 1032)])
+def test_update_of_slots_named_twice_among_many(n, C):
+    announce("short conv update, slots named twice among %d sequences" % n)
+    v = inputs(F32, [1] * n, C, 3, seed=130)
+    pool = randn(131, F32, n + 1, 2, C)
+    other = pool.clone()
+    idx = torch.randperm(n + 1, generator=torch.Generator().manual_seed(2))[:n].to(torch.int32).cuda()
+    pad, bad = idx.clone(), torch.zeros(n, dtype=torch.bool, device="cuda")
+    for i, j in ((1025, 1024), (n - 1, 0), (700, 699)):
+        idx[i], pad[i], bad[i] = idx[j], -1, True
+    got = short_conv_update(v["x"], v["w"], v["b"], pool, state_indices=idx)
+    want = short_conv_update(v["x"], v["w"], v["b"], other, state_indices=pad)
+    assert bool(torch.isnan(got[bad]).all()) and torch.equal(got[~bad], want[~bad]) and torch.equal(pool, other)
+
+
+def test_update_of_many_sequences_without_indices():
+    announce("70000 sequences without indices")
+    v = inputs(F32, [1] * 70000, 8, 2, seed=140)
+    pool = v["init"].clone()
+    y = short_conv_update(v["x"], v["w"], v["b"], pool)
+    some = slice(65530, 65550)
+    ref = layer_ref.short_conv(v["x"][some], v["w"], v["b"], range(21), v["init"][some])
+    assert rel(to_np(y[some]), ref["y"]) <= 1e-6 and torch.equal(pool[:, 0], v["x"])

@@ -117,3 +117,12 @@ def test_an_out_that_requires_a_gradient_is_refused(fn, make):
         assert fn(**x, out=out) is out
     with forward_ad.dual_level(), pytest.raises(KdaError, match="not differentiable"):
         fn(**x, out=forward_ad.make_dual(out.detach(), torch.ones_like(out)))
+
+
+def test_too_many_indexed_sequences_are_named():
+    n = 65537
+    idx, cu = torch.zeros(n, dtype=torch.int32), torch.zeros(n + 1, dtype=torch.int32)
+    for fn, make in IN_PLACE:
+        with pytest.raises(KdaError, match="more than 65536"):
+            fn(**make(), cu_seqlens=cu, state_indices=idx)
+        fn(**make(), cu_seqlens=cu[:n], state_indices=idx[:n - 1])

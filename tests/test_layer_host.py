@@ -379,3 +379,11 @@ def test_short_conv_update_refuses_a_state_over_its_other_tensors(lib):  # noqa:
                 where[name] = at(addr)
             got = lib.kda_short_conv_update(ctypes.byref(p), *where.values(), at(BASE), y, NUL)
             assert got == _lib.KDA_ERR_INVALID, (name, addr - BASE)
+
+
+def test_more_indexed_sequences_than_the_slot_check_is_built_for(lib):  # noqa: F811
+    # the check of slots named twice reads all earlier indices for every sequence
+    n, cu = 65537, at(BASE)
+    assert call_rec(lib, rec(n_seqs=n, total_tokens=9, H=1, n_slots=n), cu=cu, idx=FAKE) == _lib.KDA_ERR_UNSUPPORTED
+    p = ctypes.byref(sc(n_seqs=n, total_tokens=9, n_slots=n))
+    assert lib.kda_short_conv_update(p, FAKE, FAKE, FAKE, cu, FAKE, FAKE, FAKE, NUL) == _lib.KDA_ERR_UNSUPPORTED
