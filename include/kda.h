@@ -260,8 +260,9 @@ int kda_gdn2_fwd_ex(const kda_problem *p, const void *q, const void *k, const vo
    with the prologue and gate maps of kda_fwd.
      cu_seqlens     [N+1] (int32, device) or NULL: one token per sequence,
                     N = T. Values are clamped to [0, T]; an empty sequence
-                    leaves its state as it is. Rows of o at and after
-                    cu_seqlens[N] are not written.
+                    leaves its state as it is. Rows of o that belong to no
+                    sequence (before cu_seqlens[0], from cu_seqlens[N] on)
+                    are not written, or zero with zero_rest.
      state_indices  [N] (int32, device) or NULL: the pool slot of each
                     sequence (NULL: slot n, n_slots >= N). At most 65536
                     sequences (KDA_ERR_UNSUPPORTED). A negative one
@@ -295,6 +296,7 @@ typedef struct {
   int64_t g_stride;        /* 0: H*K, or H under KDA_GATE_PER_HEAD */
   int64_t beta_stride;     /* 0: H (kda_recurrent) */
   int64_t b_stride, w_stride; /* 0: H*K, H*V (kda_gdn2_recurrent) */
+  int32_t zero_rest;       /* not 0: zero the rows of o that belong to no sequence */
 } kda_recurrent_problem;
 
 /* Errors: KDA_ERR_INVALID (negative or inconsistent sizes, a stride shorter
@@ -405,6 +407,8 @@ typedef struct {
   int64_t n_slots;      /* update: states in the pool */
   int64_t x_stride;     /* elements between tokens of x, a multiple of 16
                            bytes; 0: C */
+  int32_t zero_rest;    /* update, not 0: zero the rows of y that belong to no
+                           sequence (the packed form always does) */
 } kda_short_conv_problem;
 int kda_short_conv_fwd(const kda_short_conv_problem *p, const void *x, const float *weight,
                        const float *bias, const int32_t *cu_seqlens, const void *initial_state,

@@ -81,6 +81,7 @@ class KdaRecurrentProblem(ctypes.Structure):
         ("beta_stride", ctypes.c_int64),
         ("b_stride", ctypes.c_int64),
         ("w_stride", ctypes.c_int64),
+        ("zero_rest", ctypes.c_int32),
     ]
 
 
@@ -115,6 +116,7 @@ class KdaShortConvProblem(ctypes.Structure):
         ("activation", ctypes.c_int32),
         ("n_slots", ctypes.c_int64),
         ("x_stride", ctypes.c_int64),
+        ("zero_rest", ctypes.c_int32),
     ]
 
 

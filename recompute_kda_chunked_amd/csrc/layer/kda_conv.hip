@@ -381,15 +381,19 @@ template <typename TI, int W>
 __global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a, int ncb) {
   const int n = blockIdx.x / ncb;
   const int c = static_cast<int>(blockIdx.x % ncb) * kThreads * kLaneCh + threadIdx.x * kLaneCh;
+  const size_t xs = a.xs, ys = a.C;
+  const uint32_t lb = c * sizeof(TI);
+  TI* y = static_cast<TI*>(a.y);
+  if (a.zero_rest && c < a.C) {  // the sequences' blocks share these rows
+    const Rest r(a.cu, a.N, a.T);
+    for (int64_t i = n; i < r.rows(); i += a.N) store4<TI>(in_row(y + r.row(i) * ys, lb), zero4());
+  }
   Bounds q{n, n + 1};
   if (a.cu) q = uniform_bounds(a, n);
   if (q.s >= q.e) return;
   const int64_t slot = find_slot(a.idx, a.cu, a.T, n, a.n_slots);
   if (c >= a.C) return;
-  const size_t xs = a.xs, ys = a.C;
-  const uint32_t lb = c * sizeof(TI);
   const TI* x = static_cast<const TI*>(a.x);
-  TI* y = static_cast<TI*>(a.y);
   if (slot < 0) {  // padded: zeros; a slot it cannot have: NaN
     const float f = slot == kPadded ? 0.f : nan_value();
     for (int t = q.s; t < q.e; ++t) store4<TI>(in_row(y + t * ys, lb), f32x4{f, f, f, f});

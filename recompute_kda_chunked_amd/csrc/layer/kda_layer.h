@@ -19,6 +19,7 @@ struct RecurrentArgs {
   const int32_t *cu, *idx;
   float* state;
   void* o;
+  bool zero_rest;  // zero the rows of o that belong to no sequence (with cu)
 };
 hipError_t launch_recurrent(int dtype, int D, bool gdn2, const RecurrentArgs& a, hipStream_t s);
 
@@ -93,6 +94,7 @@ struct ShortConvArgs {
   const int32_t *cu, *idx;
   void *y, *final_state, *dx, *dinit, *state;
   float* partials;
+  bool zero_rest;  // update: zero the rows of y that belong to no sequence (with cu)
 };
 int64_t short_conv_blocks(int C, int64_t T);
 hipError_t launch_short_conv_fwd(int dtype, int W, const ShortConvArgs& a, hipStream_t s);

@@ -125,6 +125,7 @@ int recurrent_common(bool g2, const kda_recurrent_problem* p, const void* q, con
   a.idx = state_indices;
   a.state = state;
   a.o = o;
+  a.zero_rest = p->zero_rest != 0 && cu_seqlens;
   const size_t e = p->dtype == KDA_F32 ? 4 : 2;
   const int64_t gw = a.gate_head ? p->H : HK;
   const Range others[] = {
@@ -417,6 +418,7 @@ int kda_short_conv_update(const kda_short_conv_problem* p, const void* x, const 
   a.idx = state_indices;
   a.state = state;
   a.y = y;
+  a.zero_rest = p->zero_rest != 0 && cu_seqlens;
   const size_t e = p->dtype == KDA_F32 ? 4 : 2;
   const Range others[] = {rows_of(x, a.T, a.xs, a.C, e),     dense(weight, a.C, p->W, 4),
                           dense(bias, a.C, 1, 4),            dense(cu_seqlens, int64_t{a.N} + 1, 1, 4),

@@ -79,6 +79,16 @@ __global__ void __launch_bounds__(64 * NW) k_recurrent(RecurrentArgs a) {
   const int nh = blockIdx.x / (NT / NW);
   const int n = nh / a.H, h = nh % a.H;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int cg = lane % (CW / 4), rg = lane / (CW / 4);
+  const int col = CW * (static_cast<int>(blockIdx.x % (NT / NW)) * NW + w) + 4 * cg;
+  TI* o = static_cast<TI*>(a.o) + static_cast<size_t>(h) * D;
+  const size_t os = static_cast<size_t>(a.H) * D;
+  if (a.zero_rest) {  // the sequences' blocks share these rows, and a wave's row groups
+    const Rest r(a.cu, a.N, a.T);
+    const int64_t step = static_cast<int64_t>(a.N) * (256 / CW);
+    for (int64_t i = n + static_cast<int64_t>(a.N) * rg; i < r.rows(); i += step)
+      store4<TI>(o + r.row(i) * os + col, zero4());
+  }
   int64_t t0 = n, t1 = n + 1;
   if (a.cu) {
     t0 = a.cu[n];
@@ -88,10 +98,6 @@ __global__ void __launch_bounds__(64 * NW) k_recurrent(RecurrentArgs a) {
   }
   if (t0 >= t1) return;
   const int64_t slot = find_slot(a.idx, a.cu, a.T, n, a.n_slots);
-  TI* o = static_cast<TI*>(a.o) + static_cast<size_t>(h) * D;
-  const size_t os = static_cast<size_t>(a.H) * D;
-  const int cg = lane % (CW / 4), rg = lane / (CW / 4);
-  const int col = CW * (static_cast<int>(blockIdx.x % (NT / NW)) * NW + w) + 4 * cg;
   if (slot < 0) {  // padded: zeros; a slot it cannot have: NaN
     const float f = slot == kPadded ? 0.f : nan_value();
     if (rg == 0)

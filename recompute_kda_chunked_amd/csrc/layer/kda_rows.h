@@ -125,6 +125,17 @@ __device__ __forceinline__ int64_t find_slot(const int32_t* idx, const int32_t* 
   if (slot < 0) return kPadded;
   return slot >= n_slots || twice ? kBadSlot : slot;
 }
+// The rows in [0, T) that belong to no sequence: those before the first one and
+// those from the end of the last one on.
+struct Rest {
+  int64_t before, behind, T;
+  __device__ __forceinline__ Rest(const int32_t* cu, int N, int64_t t) : before(cu[0]), behind(cu[N]), T(t) {
+    before = before < 0 ? 0 : (before > T ? T : before);
+    behind = behind < before ? before : (behind > T ? T : behind);
+  }
+  __device__ __forceinline__ int64_t rows() const { return before + T - behind; }
+  __device__ __forceinline__ int64_t row(int64_t i) const { return i < before ? i : behind + (i - before); }
+};
 __device__ __forceinline__ float nan_value() { return __uint_as_float(0x7fc00000u); }
 
 }  // namespace kda

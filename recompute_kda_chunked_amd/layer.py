@@ -162,6 +162,15 @@ def _seqs(cu_seqlens, state_indices, T, slots, dev):
     return N
 
 
+def _new_rows(like, shape, p, cu_seqlens):
+    """A decoding call's own output: rows that belong to no sequence are zero,
+    written by the call itself (by a fill where no sequence launches one)."""
+    if cu_seqlens is None:
+        return like.new_empty(shape)
+    p.zero_rest = 1
+    return like.new_empty(shape) if p.n_seqs else like.new_zeros(shape)
+
+
 def _recurrent(name, gates, q, k, v, raw_g, A_log, dt_bias, state, cu_seqlens, state_indices,
                scale, lower_bound, eps, gate_mode, out):
     g2 = len(gates) == 2
@@ -208,7 +217,7 @@ def _recurrent(name, gates, q, k, v, raw_g, A_log, dt_bias, state, cu_seqlens, s
     _placed("dt_bias", dt_bias, dev)
     _placed("state", state, dev)
     if out is None:
-        out = q.new_empty((T, H, V))
+        out = _new_rows(q, (T, H, V), p, cu_seqlens)
     else:
         _placed("out", out, dev)
         _apart("out", out, [t for t in (q, k, v, raw_g, *gates, A_log, dt_bias, state, cu_seqlens,
@@ -560,7 +569,7 @@ def short_conv_update(x, weight, bias, state, cu_seqlens=None, *, state_indices=
     p.n_seqs = _seqs(cu_seqlens, state_indices, x.shape[0], state.shape[0], dev)
     p.n_slots = state.shape[0]
     if out is None:
-        out = x.new_empty(x.shape)
+        out = _new_rows(x, x.shape, p, cu_seqlens)
     else:
         _apart("out", out, [t for t in (x, weight, bias, state, cu_seqlens, state_indices)
                             if t is not None])

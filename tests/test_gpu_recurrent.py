@@ -348,3 +348,50 @@ def test_bad_slots_among_many_sequences(n, cu):
     bad[list(first)] = True
     assert bool(torch.isnan(got[bad]).all()) and torch.equal(got[~bad], want[~bad])
     assert torch.equal(x["state"], y["state"])
+
+
+def leave_nan(shape, dtype):
+    """NaN in the memory that the next tensor of this size is given."""
+    for _ in range(3):
+        torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D,H", [(64, 3), (128, 2), (128, 40)])  # the last: the wide launch
+@pytest.mark.parametrize("gdn2", [False, True])
+def test_new_rows_of_no_sequence_are_zero(dtype, D, H, gdn2):
+    announce("rows of no sequence in a new O, %s D%d H%d gdn2 %s" % (dtype, D, H, gdn2))
+    for cu in ([0, 2, 3, 3, 5], [1, 2, 2, 4, 4], [0, 0, 0, 0, 0], [23, 23, 23, 23, 23], [9, 9, 12, 12, 12]):
+        x = problem([5, 6, 7, 5], H, D, dtype, 22, gdn2=gdn2, slots=6)
+        x["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        y = dict(x, state=x["state"].clone())
+        leave_nan(x["v"].shape, dtype)
+        got = run(x)
+        kept = torch.full_like(x["v"], 7.0)
+        run(y, out=kept)
+        assert bool((kept[:cu[0]] == 7).all()) and bool((kept[cu[-1]:] == 7).all())
+        assert bool((got[:cu[0]] == 0).all()) and bool((got[cu[-1]:] == 0).all())
+        assert torch.equal(got[cu[0]:cu[-1]], kept[cu[0]:cu[-1]]) and torch.equal(x["state"], y["state"])
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    leave_nan(x["v"].shape, dtype)
+    assert bool((run(dict(x, cu_seqlens=none, idx=None)) == 0).all())
+
+
+def test_replay_with_fewer_tokens_leaves_no_old_rows():
+    announce("a captured call replayed with shorter sequences")
+    x = problem([3, 4, 2], 2, 128, torch.bfloat16, 23, slots=5)
+    y = dict(x, state=x["state"].clone())
+    start = x["state"].clone()
+    run(dict(x, state=start.clone()))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(x)
+    x["state"].copy_(start)
+    for cu in ([0, 3, 7, 9], [0, 1, 3, 4], [0, 0, 0, 1], [2, 4, 4, 5], [0, 3, 7, 9]):
+        x["cu_seqlens"].copy_(torch.tensor(cu, dtype=torch.int32))
+        want = run(y)  # the same lengths: y holds the same cu_seqlens
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(x["state"], y["state"])
+        assert bool((out[:cu[0]] == 0).all()) and bool((out[cu[-1]:] == 0).all())

@@ -331,3 +331,34 @@ def test_update_of_many_sequences_without_indices():
     some = slice(65530, 65550)
     ref = layer_ref.short_conv(v["x"][some], v["w"], v["b"], range(21), v["init"][some])
     assert rel(to_np(y[some]), ref["y"]) <= 1e-6 and torch.equal(pool[:, 0], v["x"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("C", [8, 2056])
+def test_update_zeroes_new_rows_of_no_sequence(dtype, C):
+    announce("short conv update, rows of no sequence in a new y %s C%d" % (dtype, C))
+    v = inputs(dtype, [5, 6, 7, 5], C, 4, seed=150)
+    pool, start = randn(151, dtype, 4, 3, C), randn(151, dtype, 4, 3, C)
+    cud = torch.empty(5, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    cud.copy_(v["cud"])
+    short_conv_update(v["x"], v["w"], v["b"], pool.clone(), cud)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = short_conv_update(v["x"], v["w"], v["b"], pool, cud)
+    for cu in ([0, 5, 11, 18, 23], [0, 2, 3, 3, 5], [1, 2, 2, 4, 4], [0] * 5, [23] * 5):
+        cud.copy_(torch.tensor(cu, dtype=torch.int32))
+        pool.copy_(start)
+        a, b = start.clone(), start.clone()
+        kept = short_conv_update(v["x"], v["w"], v["b"], a, cud, out=torch.full_like(v["x"], 7.0))
+        for _ in range(3):
+            torch.full_like(v["x"], float("nan"))
+        got = short_conv_update(v["x"], v["w"], v["b"], b, cud)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bool((kept[:cu[0]] == 7).all()) and bool((kept[cu[-1]:] == 7).all())
+        assert bool((got[:cu[0]] == 0).all()) and bool((got[cu[-1]:] == 0).all())
+        assert torch.equal(got[cu[0]:cu[-1]], kept[cu[0]:cu[-1]]) and torch.equal(out, got)
+        assert torch.equal(a, b) and torch.equal(a, pool)
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert bool((short_conv_update(v["x"], v["w"], v["b"], start, none) == 0).all())
