@@ -395,3 +395,42 @@ def test_replay_with_fewer_tokens_leaves_no_old_rows():
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(x["state"], y["state"])
         assert bool((out[:cu[0]] == 0).all()) and bool((out[cu[-1]:] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["channel", "head", "gdn2"])
+@pytest.mark.parametrize("D,H", [(128, 32), (64, 33)])
+def test_ragged_tokens_of_many_heads(dtype, kind, D, H):
+    announce("ragged tokens, %s %s D%d H%d" % (dtype, kind, D, H))  # more than 128 (sequence, head) pairs
+    compare(problem([4, 1, 0, 8, 2], H, D, dtype, 24, per_head=kind == "head", gdn2=kind == "gdn2", slots=7))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_gdn2_without_cu_seqlens(dtype, D):
+    announce("GDN-2, one token each, %s D%d" % (dtype, D))
+    x = problem([1] * 5, 3, D, dtype, 25, gdn2=True, slots=9)
+    o_ref, s_ref = reference(x)
+    check_rows(run(x, cu=False), o_ref, dtype)
+    assert rel(to_np(x["state"]), s_ref) <= 1e-5
+
+
+@pytest.mark.parametrize("dtype,D,n,H,kind", [(torch.bfloat16, 128, 130, 32, "gdn2"), (torch.float32, 128, 130, 32, "gdn2"),
+                                              (torch.float32, 64, 65, 64, "gdn2"), (torch.bfloat16, 64, 65, 64, "gdn2"),
+                                              (torch.float32, 128, 129, 32, "channel"),
+                                              (torch.bfloat16, 128, 130, 32, "head")])
+def test_large_decoding_batches_of_every_form(dtype, D, n, H, kind):
+    announce("%d sequences x %d heads D%d %s %s" % (n, H, D, kind, dtype))
+    x = problem([1] * n, H, D, dtype, 26, per_head=kind == "head", gdn2=kind == "gdn2", slots=n + 3)
+    gates = ("raw_b", "raw_w") if kind == "gdn2" else ("raw_beta",)
+    some = [0, 2, n // 2, n - 1]
+    part = {k: x[k][some].clone() for k in ("q", "k", "v", "raw_g", *gates)}
+    part.update(A_log=x["A_log"], dt_bias=x["dt_bias"], state=x["state"].clone(), idx=x["idx"][some],
+                cu_seqlens_host=[0, 1, 2, 3, 4])
+    o_ref, s_ref = reference(part)
+    o = run(x, cu=False)
+    check_rows(o[some], o_ref, dtype)
+    at = x["idx"][some].long()
+    assert rel(to_np(x["state"][at]), s_ref[at.cpu().numpy()]) <= 1e-5
+    rest = sorted(set(range(n + 3)) - set(x["idx"].tolist()))
+    assert torch.equal(x["state"][rest], part["state"][rest])
