@@ -311,3 +311,33 @@ def test_block_norm_slope_of_far_gates(dtype, gate, post, lo, hi, tol):
         want = layer_ref.block_norm(x, y, wp, wq, g, 0.3, dx_out=dxo, dh=np.zeros(x.shape))["dgate"]
         got = block_norm_backward(x, y, wp, dxo, None, w_post=wq, raw_gate=g, residual_scale=0.3)[4]
         check_products("dgate", got, want, dtype, tol)
+
+
+# ------------------------------------------------------------------ several tokens per block
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", ["none", "token", "channel"])
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("T,D", [(2100, 2048), (700, 8192), (9000, 72)])
+def test_block_norm_with_several_tokens_per_block(dtype, gate, post, T, D):
+    # the backward's blocks: 1024, 256 and 4096, so each takes two or three tokens
+    announce("block norm %s gate %s post %s T%d D%d" % (dtype, gate, post, T, D))
+    block_check(dtype, *block_inputs(dtype, T, D, gate, post, 110))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", ["none", "channel"])
+def test_post_norm_weights_of_rows_larger_than_the_caches(dtype, gate):
+    announce("block norm past the caches, dw_post %s %s" % (dtype, gate))
+    T, D = (12000 if dtype is BF16 else 6000), 4096
+    x, y, wp, wq, gt, dxo, dh = block_inputs(dtype, T, D, gate, True, 120)
+    kw = dict(w_post=wq, residual_scale=0.4)
+    got = block_norm_backward(x, y, wp, dxo, dh, raw_gate=gt, **kw)
+    sums = [torch.zeros(D, dtype=torch.float64, device="cuda") for _ in range(2)]
+    for a in range(0, T, 500):  # one token per block
+        s = slice(a, min(a + 500, T))
+        part = block_norm_backward(x[s], y[s], wp, dxo[s], dh[s], raw_gate=None if gt is None else gt[s], **kw)
+        for total, p in zip(sums, part[2:4]):
+            total += p.double()
+    assert rel(to_np(got[2]), to_np(sums[0])) <= 1e-5 and rel(to_np(got[3]), to_np(sums[1])) <= 1e-5
