@@ -98,6 +98,15 @@ def _cu_host(cu_seqlens, cu_seqlens_host):
     return [int(x) for x in cu_seqlens.tolist()]  # device-to-host copy (synchronises)
 
 
+def _check_out(out, T, H, V, dt, dev):
+    """An output that the kernels write T*H*V elements to."""
+    if out.numel() != T * H * V or out.dtype != dt:
+        raise KdaError("out: expected shape %s dtype %s, got %s %s"
+                       % ((T, H, V), dt, tuple(out.shape), out.dtype))
+    if out.device != dev or not out.is_contiguous() or out.data_ptr() % 16:
+        raise KdaError("out must be contiguous, 16-byte aligned and on %s" % dev)
+
+
 def _default_cu(T, device):
     return torch.tensor([0, T], dtype=torch.int32, device=device), [0, T]
 
@@ -148,6 +157,8 @@ def kda_forward(q, k, v, raw_g, raw_beta, A_log, dt_bias, cu_seqlens=None, *,
     if cu_seqlens is None:
         cu_seqlens, cu_seqlens_host = _default_cu(q.shape[0], q.device)
     T, H, K, V, dt, ph = _check_inputs(q, k, v, raw_g, raw_beta, A_log, dt_bias, cu_seqlens)
+    if out is not None:
+        _check_out(out, T, H, V, dt, q.device)
     cu_host = _cu_host(cu_seqlens, cu_seqlens_host)
     N = len(cu_host) - 1
     _check_state("initial_state", initial_state, (N, H, K, V), q.device)

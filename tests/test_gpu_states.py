@@ -13,7 +13,7 @@ import torch
 
 import kda_inputs
 import oracle
-from recompute_kda_chunked_amd import kda, kda_backward, kda_forward
+from recompute_kda_chunked_amd import KdaError, kda, kda_backward, kda_forward
 
 pytestmark = pytest.mark.gpu
 
@@ -246,3 +246,17 @@ def test_head_gate_with_states_and_checkpoints(chunk, seg):
     got.update({g: leaves[n].grad for n, g in zip(NAMES, GRADS)})
     assert got["draw_g"].shape == x["raw_g"].shape and got["ddt_bias"].shape == (3,)
     check(got, ref, torch.float32, label="head autograd")
+
+
+def test_forward_refuses_an_out_it_cannot_fill():
+    announce("kda_forward, out of other sizes")
+    x = kda_inputs.make_inputs([20, 13], 2, 64, 64, torch.float32, 3, "cuda")
+    args = [x[n] for n in ("q", "k", "v", "raw_g", "raw_beta", "A_log", "dt_bias", "cu_seqlens")]
+    kw = dict(cu_seqlens_host=x["cu_seqlens_host"], chunk=32)
+    want = kda_forward(*args, **kw)
+    for bad in (torch.empty(32, 2, 64, device="cuda"), torch.empty(33, 2, 64, device="cuda", dtype=torch.bfloat16),
+                torch.empty(33, 2, 128, device="cuda")[..., :64], torch.empty(33, 2, 64)):
+        with pytest.raises(KdaError, match="out"):
+            kda_forward(*args, out=bad, **kw)
+    out = torch.empty(33, 2, 64, device="cuda")
+    assert kda_forward(*args, out=out, **kw) is out and torch.equal(out, want)

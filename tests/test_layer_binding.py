@@ -6,7 +6,7 @@ import torch
 from torch.autograd import forward_ad
 
 from recompute_kda_chunked_amd import (KdaError, block_norm, gated_norm, gdn2_recurrent,
-                                       kda_recurrent, layer, short_conv, short_conv_update)
+                                       kda_recurrent, layer, ops, short_conv, short_conv_update)
 from test_layer_host import rec_inputs
 
 
@@ -126,3 +126,15 @@ def test_too_many_indexed_sequences_are_named():
         with pytest.raises(KdaError, match="more than 65536"):
             fn(**make(), cu_seqlens=cu, state_indices=idx)
         fn(**make(), cu_seqlens=cu[:n], state_indices=idx[:n - 1])
+
+
+def test_an_out_that_the_chunked_forward_cannot_fill_is_refused():
+    good = torch.empty(6, 2, 64)
+    ops._check_out(good, 6, 2, 64, torch.float32, good.device)
+    ops._check_out(good.view(6, 128), 6, 2, 64, torch.float32, good.device)
+    for bad, match in ((good[:5], "out: expected"), (good.bfloat16(), "out: expected"),
+                       (torch.empty(6, 2, 128), "out: expected"), (torch.empty(6, 2, 128)[..., :64], "contiguous"),
+                       (torch.empty(6 * 128 + 1)[1:].view(6, 2, 64), "aligned"),
+                       (good.to("meta"), "on cpu")):
+        with pytest.raises(KdaError, match=match):
+            ops._check_out(bad, 6, 2, 64, torch.float32, good.device)
