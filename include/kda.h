@@ -302,7 +302,7 @@ typedef struct {
 /* Errors: KDA_ERR_INVALID (negative or inconsistent sizes, a stride shorter
    than a row or not a multiple of 16 bytes, a null pointer, a state that
    overlaps another tensor), KDA_ERR_UNSUPPORTED (size, dtype or gate not
-   built; N * H of 2^24 or more), KDA_ERR_HIP. */
+   built; N * H of 2^24 or more, of 2^24 - 1 with zero_rest), KDA_ERR_HIP. */
 int kda_recurrent(const kda_recurrent_problem *p, const void *q, const void *k, const void *v,
                   const void *raw_g, const void *raw_beta, const float *A_log,
                   const float *dt_bias, const int32_t *cu_seqlens,
@@ -422,8 +422,8 @@ int kda_short_conv_bwd(const kda_short_conv_problem *p, const void *x, const flo
 
 /* The convolution's decoding form: sequence n starts from its state in a
    pool [n_slots, W-1, C] (dtype) and leaves its last W-1 rows there.
-   cu_seqlens, state_indices, padded sequences, rows behind the last sequence,
-   overlap with the state and capture as for kda_recurrent. */
+   cu_seqlens, state_indices, padded sequences, rows that belong to no
+   sequence, overlap with the state and capture as for kda_recurrent. */
 int kda_short_conv_update(const kda_short_conv_problem *p, const void *x, const float *weight,
                           const float *bias, const int32_t *cu_seqlens,
                           const int32_t *state_indices, void *state, void *y, void *stream);

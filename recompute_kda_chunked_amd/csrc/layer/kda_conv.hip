@@ -377,23 +377,24 @@ __global__ void __launch_bounds__(kThreads) k_short_conv_bwd(ShortConvArgs a, Co
 
 // Decoding: a block takes one sequence and 1024 channels, four per thread, the
 // state's rows in registers over the sequence's tokens.
-template <typename TI, int W>
+template <typename TI, int W, bool MANY>
 __global__ void __launch_bounds__(kThreads) k_short_conv_update(ShortConvArgs a, int ncb) {
   const int n = blockIdx.x / ncb;
-  const int c = static_cast<int>(blockIdx.x % ncb) * kThreads * kLaneCh + threadIdx.x * kLaneCh;
-  const size_t xs = a.xs, ys = a.C;
-  const uint32_t lb = c * sizeof(TI);
-  TI* y = static_cast<TI*>(a.y);
-  if (a.zero_rest && c < a.C) {  // the sequences' blocks share these rows
-    const Rest r(a.cu, a.N, a.T);
-    for (int64_t i = n; i < r.rows(); i += a.N) store4<TI>(in_row(y + r.row(i) * ys, lb), zero4());
+  if (n >= a.N) {
+    const unsigned own = static_cast<unsigned>(a.N) * ncb;
+    zero_rest(a.y, static_cast<size_t>(a.C) * sizeof(TI), a.cu, a.N, a.T, blockIdx.x - own, gridDim.x - own);
+    return;
   }
+  const int c = static_cast<int>(blockIdx.x % ncb) * kThreads * kLaneCh + threadIdx.x * kLaneCh;
   Bounds q{n, n + 1};
   if (a.cu) q = uniform_bounds(a, n);
   if (q.s >= q.e) return;
-  const int64_t slot = find_slot(a.idx, a.cu, a.T, n, a.n_slots);
+  const int64_t slot = find_slot<MANY>(a.idx, a.cu, a.T, n, a.n_slots);
   if (c >= a.C) return;
+  const size_t xs = a.xs, ys = a.C;
+  const uint32_t lb = c * sizeof(TI);
   const TI* x = static_cast<const TI*>(a.x);
+  TI* y = static_cast<TI*>(a.y);
   if (slot < 0) {  // padded: zeros; a slot it cannot have: NaN
     const float f = slot == kPadded ? 0.f : nan_value();
     for (int t = q.s; t < q.e; ++t) store4<TI>(in_row(y + t * ys, lb), f32x4{f, f, f, f});
@@ -427,10 +428,18 @@ enum { kFwd, kBwd, kUpdate };
 
 // Runs of a multiple of kAhead tokens, 8 at least, such that the waves fill
 // whole rounds of 2048: the backward's registers let two waves per SIMD run at
-// once, and a part-filled round costs as much as a full one. One round while
-// its runs are at most 160 tokens (8192 x 8192 bf16, backward: 93 us with 2048
-// runs of 128, 101 us with 4096 of 64; forward and backward of 9000 x 8192: 192
-// us with 2272 runs of 128, 163 us with 2016 of 144).
+// once, and a part-filled round costs as much as a full one (forward and
+// backward of 9000 x 8192: 192 us with 2272 runs of 128, 163 us with 2016 of
+// 144). The forward's registers would let more waves run, which gains nothing:
+// a step of 8192 x 8192 takes 144 us, with forwards of 4096 or 8192 waves 148 or
+// 157. One round while its runs are at most 160 tokens; from there on longer
+// ones change little. Longest run, bf16, microseconds forward / backward:
+//                    64           96           128          160          192          320
+//   4096 x 8192      30.3 / 61.9  29.2 / 50.2  29.3 / 49.8  29.4 / 50.2  29.3 / 50.2  29.3 / 50.4
+//   8192 x 8192      51.4 / 96.2  51.7 / 96.9  51.8 / 96.7  50.2 / 82.7  49.5 / 81.9  49.3 / 82.3
+//   9000 x 8192      55.8 / 103   53.8 / 96.3  53.8 / 95.5  50.4 / 91.5  50.2 / 91.2  50.2 / 90.8
+//   16384 x 8192     103 / 176    107 / 167    105 / 168    97.2 / 154   97.4 / 154   101 / 147
+//   20000 x 4096     70.2 / 114   68.9 / 106   68.6 / 105   67.4 / 103   66.9 / 100   67.1 / 102
 Cover cover_of(int C, int64_t T) {
   constexpr int64_t kRound = 2048, kLongest = 160;
   Cover c;
@@ -447,7 +456,10 @@ template <typename TI, int W>
 hipError_t launch_w(int what, const ShortConvArgs& a, hipStream_t s) {
   if (what == kUpdate) {
     const int ncb = (a.C + kThreads * kLaneCh - 1) / (kThreads * kLaneCh);
-    k_short_conv_update<TI, W><<<static_cast<unsigned>(a.N) * ncb, kThreads, 0, s>>>(a, ncb);
+    const unsigned own = static_cast<unsigned>(a.N) * ncb;  // below 2^24 with the rest's
+    const unsigned grid = own + rest_blocks(a.zero_rest, a.T * a.C * static_cast<int64_t>(sizeof(TI)), (1 << 24) - 1 - own);
+    if (a.idx && a.N > kScanAlone) k_short_conv_update<TI, W, true><<<grid, kThreads, 0, s>>>(a, ncb);
+    else k_short_conv_update<TI, W, false><<<grid, kThreads, 0, s>>>(a, ncb);
     return hipGetLastError();
   }
   const Cover g = cover_of(a.C, a.T);

@@ -16,7 +16,7 @@ namespace {
 constexpr float kMaxGateBound = 5.9f;
 
 // Most sequences named by state_indices: every block compares its index with
-// all earlier ones (kda_rows.h), about 1 ms at this many.
+// all earlier ones (find_slot in kda_rows.h), about 1 ms a head at this many.
 constexpr int32_t kMaxIndexed = 65536;
 
 bool known_dtype(int dtype) { return dtype == KDA_F32 || dtype == KDA_BF16; }
@@ -79,7 +79,9 @@ int check_recurrent(const kda_recurrent_problem* p, bool g2, bool has_cu, bool h
          : !stride_ok(p->beta_stride, p->H, p->dtype, T, false))
     return KDA_ERR_INVALID;
   // one block of 256 threads per (sequence, head), below 2^32 threads
-  if (static_cast<int64_t>(p->n_seqs) * p->H >= (int64_t{1} << 24)) return KDA_ERR_UNSUPPORTED;
+  // in all, at least one of them for the rows that belong to no sequence
+  if (static_cast<int64_t>(p->n_seqs) * p->H + (p->zero_rest && has_cu) >= (int64_t{1} << 24))
+    return KDA_ERR_UNSUPPORTED;
   if (has_idx && p->n_seqs > kMaxIndexed) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
@@ -181,8 +183,9 @@ int check_short_conv(const kda_short_conv_problem* p) {
   if (p->activation != KDA_ACT_NONE && p->activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
   if (!stride_ok(p->x_stride, p->C, p->dtype, p->total_tokens, true)) return KDA_ERR_INVALID;
   // token numbers in 32 bits with room for the tokens loaded ahead, and launches
-  // (a thread per four channels of a state row, or of a run of 128 tokens) below
-  // 2^32 threads
+  // below 2^32 threads: a thread per four channels of a state row, 2^30 of them,
+  // and a wave per 256 channels of a run; runs of such sizes are of 160 tokens
+  // (cover_of), so T * (C / 256 + 1) < 2^32 + 2^31 makes 0.4 * 2^32.6 threads
   if (p->total_tokens > 0x7fffff00LL ||
       static_cast<int64_t>(p->n_seqs) * (p->W - 1) * p->C >= (int64_t{1} << 32) ||
       p->total_tokens * p->C >= (int64_t{1} << 40))
@@ -407,7 +410,9 @@ int kda_short_conv_update(const kda_short_conv_problem* p, const void* x, const 
   if (st != KDA_OK) return st;
   if (p->n_slots < 0 || p->n_slots > 0x7fffffffLL) return KDA_ERR_INVALID;
   // a block of 256 threads per sequence and 1024 channels, below 2^32 threads
-  if (static_cast<int64_t>(p->n_seqs) * ((p->C + 1023) / 1024) >= (int64_t{1} << 24))
+  // in all, at least one of them for the rows that belong to no sequence
+  if (static_cast<int64_t>(p->n_seqs) * ((p->C + 1023) / 1024) + (p->zero_rest && cu_seqlens) >=
+      (int64_t{1} << 24))
     return KDA_ERR_UNSUPPORTED;
   if (state_indices && p->n_seqs > kMaxIndexed) return KDA_ERR_UNSUPPORTED;
   if (!cu_seqlens && p->total_tokens != p->n_seqs) return KDA_ERR_INVALID;

@@ -28,7 +28,9 @@
 // takes 48.7 instead of 41.9.
 //
 // Sums, gates and the state are fp32 for either dtype; only o is rounded,
-// once.
+// once. The chunked form keeps an fp32 problem's gate in fp64 because it adds
+// it up over a chunk; here a gate is used alone, from the fp32 exponential and
+// reciprocal (fp32 states after up to 8 tokens: 2.2e-8 of fp64, normalised L2).
 #include "../kda_device.h"
 #include "../kda_prologue.h"
 #include "kda_layer.h"
@@ -69,7 +71,7 @@ __device__ __forceinline__ float sum_rows(float x) {
   return sum_row_groups(x);
 }
 
-template <typename TI, int D, bool G2, int CW, int NW>
+template <typename TI, int D, bool G2, int CW, int NW, bool MANY>
 __global__ void __launch_bounds__(64 * NW) k_recurrent(RecurrentArgs a) {
   constexpr int NT = D / CW;            // waves per (sequence, head), CW columns each
   constexpr int CPL = D / 64;           // prologue channels per lane
@@ -78,17 +80,12 @@ __global__ void __launch_bounds__(64 * NW) k_recurrent(RecurrentArgs a) {
   __shared__ __align__(16) float sm[NW][4][D];  // per wave: a, e, kh, qh
   const int nh = blockIdx.x / (NT / NW);
   const int n = nh / a.H, h = nh % a.H;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int cg = lane % (CW / 4), rg = lane / (CW / 4);
-  const int col = CW * (static_cast<int>(blockIdx.x % (NT / NW)) * NW + w) + 4 * cg;
-  TI* o = static_cast<TI*>(a.o) + static_cast<size_t>(h) * D;
-  const size_t os = static_cast<size_t>(a.H) * D;
-  if (a.zero_rest) {  // the sequences' blocks share these rows, and a wave's row groups
-    const Rest r(a.cu, a.N, a.T);
-    const int64_t step = static_cast<int64_t>(a.N) * (256 / CW);
-    for (int64_t i = n + static_cast<int64_t>(a.N) * rg; i < r.rows(); i += step)
-      store4<TI>(o + r.row(i) * os + col, zero4());
+  if (n >= a.N) {
+    const unsigned own = static_cast<unsigned>(a.N) * a.H * (NT / NW);
+    zero_rest(a.o, static_cast<size_t>(a.H) * D * sizeof(TI), a.cu, a.N, a.T, blockIdx.x - own, gridDim.x - own);
+    return;
   }
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   int64_t t0 = n, t1 = n + 1;
   if (a.cu) {
     t0 = a.cu[n];
@@ -97,7 +94,11 @@ __global__ void __launch_bounds__(64 * NW) k_recurrent(RecurrentArgs a) {
     t1 = t1 > a.T ? a.T : t1;
   }
   if (t0 >= t1) return;
-  const int64_t slot = find_slot(a.idx, a.cu, a.T, n, a.n_slots);
+  const int64_t slot = find_slot<MANY>(a.idx, a.cu, a.T, n, a.n_slots);
+  TI* o = static_cast<TI*>(a.o) + static_cast<size_t>(h) * D;
+  const size_t os = static_cast<size_t>(a.H) * D;
+  const int cg = lane % (CW / 4), rg = lane / (CW / 4);
+  const int col = CW * (static_cast<int>(blockIdx.x % (NT / NW)) * NW + w) + 4 * cg;
   if (slot < 0) {  // padded: zeros; a slot it cannot have: NaN
     const float f = slot == kPadded ? 0.f : nan_value();
     if (rg == 0)
@@ -235,19 +236,25 @@ __global__ void __launch_bounds__(64 * NW) k_recurrent(RecurrentArgs a) {
 //     runs faster with fewer reads and writes interleaved: 128 sequences x 32
 //     heads 100.2 -> 94.1, 251 x 32 heads 195.9 -> 182.5 (5.8 TB/s), 256 x 64
 //     heads 383 -> 353; D = 64, 512 x 64 heads 201.7 -> 194.4. From 4096
-//     (sequence, head) pairs: at 512 it loses (13.1 -> 14.1). Several tokens
-//     need the waves (37 x 64 heads of up to 8: 59.6 -> 84.5).
+//     (sequence, head) pairs, where every type gains (pairs: apart not / apart):
+//       D = 128 bf16  512 16.0 / 16.8  1024 29.1 / 28.9  2048 52.7 / 50.8  4096 101.8 / 95.4  8192 201.7 / 187.0
+//       D = 128 fp32  512 14.4 / 17.2  1024 29.0 / 30.9  2048 53.2 / 54.6  4096 103.1 / 101.7  8192 201.1 / 195.2
+//       D = 64 bf16   512 7.8 / 7.7  1024 9.1 / 9.1  2048 17.3 / 17.1  4096 29.0 / 28.6  8192 56.1 / 53.7
+//     Several tokens need the waves (37 x 64 heads of up to 8: 59.6 -> 84.5).
 template <typename TI, int D, bool G2>
 hipError_t launch_g(const RecurrentArgs& a, hipStream_t s) {
   const unsigned nh = static_cast<unsigned>(a.N) * static_cast<unsigned>(a.H);
+  // blocks of 256 threads, below 2^32 in all
+  const unsigned rest = rest_blocks(a.zero_rest, a.T * a.H * D * static_cast<int64_t>(sizeof(TI)), (1 << 24) - 1 - nh);
   if constexpr (D == 128) {
     if (a.cu && nh * (D / 16) <= 1024) {
-      k_recurrent<TI, D, G2, 16, 1><<<nh * (D / 16), 64, 0, s>>>(a);
+      k_recurrent<TI, D, G2, 16, 1, false><<<nh * (D / 16) + rest, 64, 0, s>>>(a);
       return hipGetLastError();
     }
   }
   const unsigned apart = !a.cu && nh >= 4096 ? (D == 128 ? 100 : 35) * 1024 : 0;
-  k_recurrent<TI, D, G2, 32, D / 32><<<nh, 2 * D, apart, s>>>(a);
+  if (a.idx && a.N > kScanAlone) k_recurrent<TI, D, G2, 32, D / 32, true><<<nh + rest, 2 * D, apart, s>>>(a);
+  else k_recurrent<TI, D, G2, 32, D / 32, false><<<nh + rest, 2 * D, apart, s>>>(a);
   return hipGetLastError();
 }
 template <typename TI, int D>

@@ -93,49 +93,66 @@ __device__ __forceinline__ bool has_tokens(const int32_t* cu, int64_t T, int j) 
 // The pool slot of sequence n, found by the whole block: kPadded for a negative
 // index (a padded sequence), kBadSlot for one past the pool or one that an
 // earlier sequence with tokens names too (two writers of one state). Every
-// block looks through all earlier indices, so a launch's reads grow with the
-// square of their number, and the host refuses more than 65536: each wave on
-// its own up to kScanAlone (four loads at once), the block's waves together
-// above. Microseconds without indices / with them:
-//   recurrent, 1 head, D = 64   256 6.5 / 6.9   1024 10.0 / 12.0   4096 27 / 33   16384 90 / 159   65536 345 / 1252
-//   update, 2048 channels       256 6.6 / 6.7   1024 10.2 / 12.2   4096 24 / 30   16384 110 / 183  65536 433 / 1119
-// (each wave on its own one load at a time: 4096 49 and 54, 16384 375 and 512).
+// block looks through all earlier indices, the first of them read together with
+// its own, so a launch's reads grow with the square of their number, and the
+// host refuses more than 65536. MANY, for more than kScanAlone sequences: the
+// block's waves share the search (it costs 37 x 64 heads of drafts 0.4 of 59 us,
+// so fewer sequences go without). Microseconds without indices / with them:
+//   recurrent, 1 head, D = 64   256 6.6 / 6.7   1024 9.8 / 12.8   4096 27 / 35   16384 89 / 165   65536 344 / 1283
+//   update, 2048 channels       256 6.6 / 6.5   1024 9.9 / 13.0   4096 24 / 32   16384 109 / 191  65536 437 / 1149
+// (each wave on its own, as for fewer: 4096 49 and 54, 16384 375 and 512).
 constexpr int64_t kPadded = -1, kBadSlot = -2;
 constexpr int kScanAlone = 1024;
+template <bool MANY>
 __device__ __forceinline__ int64_t find_slot(const int32_t* idx, const int32_t* cu, int64_t T,
                                              int n, int64_t n_slots) {
   if (!idx) return n;
-  const int32_t slot = __builtin_amdgcn_readfirstlane(idx[n]);
-  const bool together = n > kScanAlone;
-  const int step = together ? blockDim.x : 64;
-  int j = together ? threadIdx.x : threadIdx.x & 63;
+  const int step = MANY ? blockDim.x : 64;
+  int j = MANY ? threadIdx.x : threadIdx.x & 63;
+  const int32_t own = idx[n], first = idx[j < n ? j : n];
+  const int32_t slot = __builtin_amdgcn_readfirstlane(own);
   bool taken = false;
   auto look = [&](int i, int32_t x) {
     if (x == slot && (!cu || has_tokens(cu, T, i))) taken = true;
   };
-  for (; j + 3 * step < n; j += 4 * step) {
-    int32_t x[4];
+  if (j < n) look(j, first);
+  j += step;
+  if constexpr (MANY) {
+    for (; j + 3 * step < n; j += 4 * step) {
+      int32_t x[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) x[u] = idx[j + u * step];
+      for (int u = 0; u < 4; ++u) x[u] = idx[j + u * step];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) look(j + u * step, x[u]);
+      for (int u = 0; u < 4; ++u) look(j + u * step, x[u]);
+    }
   }
   for (; j < n; j += step) look(j, idx[j]);
-  const bool twice = together ? __syncthreads_or(taken) != 0 : __any(taken) != 0;
+  const bool twice = MANY ? __syncthreads_or(taken) != 0 : __any(taken) != 0;
   if (slot < 0) return kPadded;
   return slot >= n_slots || twice ? kBadSlot : slot;
 }
-// The rows in [0, T) that belong to no sequence: those before the first one and
-// those from the end of the last one on.
-struct Rest {
-  int64_t before, behind, T;
-  __device__ __forceinline__ Rest(const int32_t* cu, int N, int64_t t) : before(cu[0]), behind(cu[N]), T(t) {
-    before = before < 0 ? 0 : (before > T ? T : before);
-    behind = behind < before ? before : (behind > T ? T : behind);
-  }
-  __device__ __forceinline__ int64_t rows() const { return before + T - behind; }
-  __device__ __forceinline__ int64_t row(int64_t i) const { return i < before ? i : behind + (i - before); }
-};
+
+// Zeroes the rows of o [T][row_bytes] that belong to no sequence, those before
+// the first one and those from the end of the last one on: the work of block
+// `b` of the `nb` that a launch has for it behind the sequences' own. (In those
+// it cost the drafts above 0.7 us, their two loads more than the rows.)
+__device__ __forceinline__ void zero_rest(void* o, size_t row_bytes, const int32_t* cu, int N,
+                                          int64_t T, unsigned b, unsigned nb) {
+  int64_t before = cu[0], behind = cu[N];
+  before = before < 0 ? 0 : (before > T ? T : before);
+  behind = behind < before ? before : (behind > T ? T : behind);
+  const int64_t row = static_cast<int64_t>(row_bytes / 16);
+  f32x4* p = static_cast<f32x4*>(o);
+  const int64_t step = static_cast<int64_t>(nb) * blockDim.x, at = static_cast<int64_t>(b) * blockDim.x + threadIdx.x;
+  for (int64_t i = at; i < before * row; i += step) p[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int64_t i = behind * row + at; i < T * row; i += step) p[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+// Blocks for it: one per 64 KB of o, at most 1024 and at most `room`.
+inline unsigned rest_blocks(bool zero, int64_t bytes, int64_t room) {
+  if (!zero) return 0;
+  const int64_t want = (bytes + 65535) / 65536, most = room < 1024 ? room : 1024;
+  return static_cast<unsigned>(want < most ? want : most);
+}
 __device__ __forceinline__ float nan_value() { return __uint_as_float(0x7fc00000u); }
 
 }  // namespace kda

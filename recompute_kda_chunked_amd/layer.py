@@ -237,17 +237,16 @@ def kda_recurrent(q, k, v, raw_g, raw_beta, A_log, dt_bias, state, cu_seqlens=No
 
     cu_seqlens: int32 [N+1] on the device, as kda_forward's (no host copy is
     needed, so the call can be captured into a graph); None: one token per
-    sequence. state_indices: int32 [N] slot of each sequence (None: slot n;
-    at most 65536);
-    a negative one marks a padded sequence, whose rows of O are zero and which
-    touches no state. A slot past the pool, or one that an earlier sequence
-    with tokens names too, is an error found on the device: NaN rows, no
-    state touched. Rows of O behind the last sequence are not written (those
-    of a new O hold what its memory held). `state` must not overlap any other
-    tensor of the call. The tokens of
-    q, k, v, raw_g and raw_beta may be slices of wider rows. raw_g [T,H] with
-    dt_bias [H] gives one gate per head. Not differentiable. Its time grows
-    with the longest sequence: prompts belong to kda_forward."""
+    sequence. state_indices: int32 [N] slot of each sequence (None: slot n),
+    N at most 65536; a negative one marks a padded sequence, whose rows of O
+    are zero and which touches no state. A slot past the pool, or one that an
+    earlier sequence with tokens names too, is an error found on the device:
+    NaN rows, no state touched. Rows of O that belong to no sequence are zero
+    in a new O and left as they were in `out`. `state` must not overlap any
+    other tensor of the call. The tokens of q, k, v, raw_g and raw_beta may be
+    slices of wider rows. raw_g [T,H] with dt_bias [H] gives one gate per
+    head. Not differentiable. Its time grows with the longest sequence:
+    prompts belong to kda_forward."""
     return _recurrent("kda_recurrent", (raw_beta,), q, k, v, raw_g, A_log, dt_bias, state,
                       cu_seqlens, state_indices, scale, lower_bound, eps, gate_mode, out)
 
@@ -558,8 +557,8 @@ def short_conv_update(x, weight, bias, state, cu_seqlens=None, *, state_indices=
     """The convolution's decoding form: y [T,C] with the rows before each
     sequence in a pool `state` [slots,W-1,C] (x's dtype; short_conv's final
     states serve as they are), which is updated in place. cu_seqlens,
-    state_indices, padded sequences and rows behind the last sequence as for
-    kda_recurrent. Not differentiable."""
+    state_indices, padded sequences, rows that belong to no sequence and
+    overlap as for kda_recurrent. Not differentiable."""
     if state.dim() != 3:
         raise KdaError("state: expected [slots,W-1,C], got %s" % (tuple(state.shape),))
     _no_grad("short_conv_update", "train with short_conv", (x, weight, bias, state, out))

@@ -362,3 +362,14 @@ def test_update_zeroes_new_rows_of_no_sequence(dtype, C):
         assert torch.equal(a, b) and torch.equal(a, pool)
     none = torch.zeros(1, dtype=torch.int32, device="cuda")
     assert bool((short_conv_update(v["x"], v["w"], v["b"], start, none) == 0).all())
+
+
+def test_update_zeroes_many_new_rows():
+    announce("short conv update, 110 MB of rows that belong to no sequence")
+    T, C = 7000, 4096
+    x, w, pool = randn(160, F32, T, C), randn(161, F32, C, 4), randn(162, F32, 3, 3, C)
+    for cu in ([0, 2, 2, 5], [6900, 6902, 6902, 6905], [3000, 3002, 3002, 3005]):
+        torch.full_like(x, float("nan"))
+        got = short_conv_update(x, w, None, pool, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        assert bool((got[:cu[0]] == 0).all()) and bool((got[cu[-1]:] == 0).all())
+        assert bool((got[cu[0]:cu[-1]] != 0).any(1).all())

@@ -387,3 +387,11 @@ def test_more_indexed_sequences_than_the_slot_check_is_built_for(lib):  # noqa: 
     assert call_rec(lib, rec(n_seqs=n, total_tokens=9, H=1, n_slots=n), cu=cu, idx=FAKE) == _lib.KDA_ERR_UNSUPPORTED
     p = ctypes.byref(sc(n_seqs=n, total_tokens=9, n_slots=n))
     assert lib.kda_short_conv_update(p, FAKE, FAKE, FAKE, cu, FAKE, FAKE, FAKE, NUL) == _lib.KDA_ERR_UNSUPPORTED
+
+
+def test_largest_launches_leave_room_for_the_rows_of_no_sequence(lib):  # noqa: F811
+    n = (1 << 24) - 1
+    p = rec(n_seqs=n, total_tokens=9, H=1, n_slots=n, zero_rest=1)
+    assert call_rec(lib, p, cu=FAKE) == _lib.KDA_ERR_UNSUPPORTED
+    p = ctypes.byref(sc(n_seqs=n, total_tokens=9, n_slots=n, zero_rest=1))
+    assert lib.kda_short_conv_update(p, FAKE, FAKE, FAKE, FAKE, NUL, FAKE, FAKE, NUL) == _lib.KDA_ERR_UNSUPPORTED
