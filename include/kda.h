@@ -428,6 +428,96 @@ int kda_short_conv_update(const kda_short_conv_problem *p, const void *x, const 
                           const float *bias, const int32_t *cu_seqlens,
                           const int32_t *state_indices, void *state, void *y, void *stream);
 
+/* A state-space layer's scan: the selective recurrence of a state S [N][P] per
+   head with a scalar decay, the state's rows written by B and read by C, which
+   the heads of a group share (head h: group h / (H / G)). Per packed sequence
+   and head
+     dt_t = clamp(softplus(raw_dt[t,h] + dt_bias[h]), dt_min, dt_max)
+     S_t = exp(-exp(A_log[h]) dt_t) S_{t-1} + dt_t B_t x_t^T
+     y_t = S_t^T C_t + D[h] x_t
+     x, y            [T, H, P] (dtype)
+     raw_dt          [T, H] (dtype); dt_bias [H] (fp32) or NULL: zero
+     A_log           [H] (fp32); D [H] (fp32) or NULL: zero
+     B, C            [T, G, N] (dtype)
+     cu_seqlens      [n_seqs+1] (int32, device), or NULL: one sequence,
+                     n_seqs = 1. Values are clamped to [0, T] and should not
+                     decrease; rows of the outputs that belong to no sequence
+                     are zero
+     initial_state, final_state  [n_seqs, H, N, P] (fp32); NULL: zero, not
+                     written. An empty sequence passes its state through
+   Nothing is read on the host but the problem, so a call can be captured into
+   a graph and replayed with other cu_seqlens of the same n_seqs and T. x,
+   raw_dt, B and C may have rows further apart than H * P, H or G * N elements
+   (the *_stride fields, 0: adjacent), as slices of the convolution's output
+   have; strides of x, B and C are multiples of 16 bytes. Pointers other than
+   raw_dt's and cu_seqlens are 16-byte aligned; outputs must not overlap inputs.
+   T = 0 is allowed. States, decays and sums are fp32; a bf16 problem rounds
+   what the matrix cores multiply (once, or to a pair of bf16 where an fp32
+   output depends on it). The backward recomputes what it needs from the
+   inputs, takes dy and d_final_state (NULL: zero) and writes dx [T, H, P],
+   draw_dt [T, H], dB, dC [T, G, N] (dtype, rows adjacent), dA_log, dD and
+   ddt_bias [H] (fp32, summed in a fixed order; dD and ddt_bias may be NULL:
+   not written) and d_initial_state (NULL: not written). No gradient reaches
+   raw_dt where a limit holds. Errors: KDA_ERR_INVALID, KDA_ERR_UNSUPPORTED,
+   KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
+typedef struct {
+  int32_t n_seqs;       /* >= 0 */
+  int64_t total_tokens; /* T >= 0 */
+  int32_t H, G;         /* G divides H */
+  int32_t N, P;         /* built: 64 or 128 each */
+  int32_t dtype;        /* KDA_F32 or KDA_BF16 */
+  float dt_min, dt_max; /* 0 <= dt_min <= dt_max; dt_max may be infinite */
+  int64_t x_stride, dt_stride, B_stride, C_stride; /* elements between tokens */
+  int64_t n_slots;      /* recurrent: states in the pool */
+  int32_t zero_rest;    /* recurrent, not 0: zero the rows of y that belong to
+                           no sequence (the scan always does) */
+} kda_ssm_problem;
+
+/* The scan's decoding form: sequence n starts from its state in a pool
+   [n_slots, H, N, P] (fp32; the scan's final states serve as they are) and
+   leaves its last state there. cu_seqlens (NULL: one token a sequence),
+   state_indices, padded sequences, slots named twice, rows that belong to no
+   sequence, overlap with the state and capture as for kda_recurrent. */
+int kda_ssm_recurrent(const kda_ssm_problem *p, const void *x, const void *raw_dt,
+                      const float *A_log, const void *B, const void *C, const float *D,
+                      const float *dt_bias, const int32_t *cu_seqlens,
+                      const int32_t *state_indices, float *state, void *y, void *stream);
+
+/* Group norm over the channels of each token (channels last, C in groups of
+   C / groups), with an activation or an activated gate:
+     z = x, or x * act(gate) with KDA_GROUP_GATE_FIRST
+     n = (z - m) / sqrt(mean((z - m)^2) + eps) over each group, m the group's
+         mean, or 0 without `center`
+     p = n * weight + bias
+     y = act(p) (KDA_GROUP_GATE_NONE), p * act(gate) (KDA_GROUP_GATE_AFTER),
+         or p (KDA_GROUP_GATE_FIRST)
+   x, gate, y [rows, C] (dtype; x and gate may have rows further apart,
+   multiples of 16 bytes); weight, bias [C] (fp32; bias NULL: zero); act is
+   KDA_ACT_SIGMOID, KDA_ACT_SILU or, without a gate, KDA_ACT_NONE. The backward
+   recomputes the norm from x and gate and writes dx, dgate [rows, C] (dtype,
+   rows adjacent) and dweight, dbias [C] (fp32, summed in a fixed order; dbias
+   NULL: not written). Pointers are 16-byte aligned; outputs must not overlap
+   inputs. rows = 0: nothing but dweight and dbias (zero) is written. Errors as
+   for the gated norm. */
+enum { KDA_GROUP_GATE_NONE = 0, KDA_GROUP_GATE_AFTER = 1, KDA_GROUP_GATE_FIRST = 2 };
+typedef struct {
+  int64_t rows;       /* >= 0 */
+  int32_t C, groups;  /* built: C / groups a multiple of 8 up to 8192, C up to 2^20 */
+  int32_t dtype;      /* KDA_F32 or KDA_BF16 */
+  int32_t gate;       /* KDA_GROUP_GATE_* */
+  int32_t activation; /* KDA_ACT_* */
+  int32_t center;     /* not 0: the groups' means are taken off */
+  float eps;          /* >= 0 */
+  int64_t x_stride, gate_stride; /* elements between rows; 0: C */
+} kda_group_norm_problem;
+int kda_group_norm_fwd(const kda_group_norm_problem *p, const void *x, const void *gate,
+                       const float *weight, const float *bias, void *y, void *stream);
+size_t kda_group_norm_bwd_workspace_bytes(const kda_group_norm_problem *p);
+int kda_group_norm_bwd(const kda_group_norm_problem *p, const void *x, const void *gate,
+                       const float *weight, const float *bias, const void *dy, void *dx,
+                       void *dgate, float *dweight, float *dbias, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
 /* For callers that cannot allocate device memory (code under HIP graph
    capture, tight serving loops, harnesses that forbid hipMalloc): kda_fwd
    with its workspace in a device array of KDA_NOALLOC_SCRATCH_BYTES that the
@@ -478,7 +568,15 @@ enum {
   KDA_KERNEL_SHORT_CONV_BWD = 17,
   KDA_KERNEL_SHORT_CONV_UPDATE = 18,
   KDA_KERNEL_PARAM_REDUCE = 19,     /* sums of per-block parameter gradients */
-  KDA_KERNEL_COUNT = 20
+  KDA_KERNEL_SSM_STEPS = 20,        /* step sizes and decays of the scan's chunks */
+  KDA_KERNEL_SSM_STATE = 21,        /* states entering (and gradients leaving) chunks */
+  KDA_KERNEL_SSM_OUT = 22,
+  KDA_KERNEL_SSM_GRAD = 23,
+  KDA_KERNEL_SSM_REDUCE = 24,       /* sums of dB and dC over heads */
+  KDA_KERNEL_SSM_RECURRENT = 25,
+  KDA_KERNEL_GROUP_NORM = 26,
+  KDA_KERNEL_GROUP_NORM_BWD = 27,
+  KDA_KERNEL_COUNT = 28
 };
 int kda_profile_begin(void);
 int kda_profile_end(int32_t *launches, double *total_ms, int64_t *units, int n);

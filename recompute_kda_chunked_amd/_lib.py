@@ -25,11 +25,13 @@ EXPORTS = ("kda_fwd_workspace_bytes", "kda_bwd_workspace_bytes", "kda_check_prob
            "kda_gdn2_recurrent", "kda_gated_norm_fwd", "kda_gated_norm_bwd_workspace_bytes",
            "kda_gated_norm_bwd", "kda_block_norm_fwd", "kda_block_norm_bwd_workspace_bytes",
            "kda_block_norm_bwd", "kda_short_conv_fwd", "kda_short_conv_bwd_workspace_bytes",
-           "kda_short_conv_bwd", "kda_short_conv_update")
+           "kda_short_conv_bwd", "kda_short_conv_update", "kda_ssm_recurrent",
+           "kda_group_norm_fwd", "kda_group_norm_bwd_workspace_bytes", "kda_group_norm_bwd")
 KDA_ACT_NONE, KDA_ACT_SIGMOID, KDA_ACT_SILU = range(3)
 KDA_BLOCK_GATE_NONE, KDA_BLOCK_GATE_TOKEN, KDA_BLOCK_GATE_CHANNEL = range(3)
+KDA_GROUP_GATE_NONE, KDA_GROUP_GATE_AFTER, KDA_GROUP_GATE_FIRST = range(3)
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES
-KERNEL_COUNT = 20
+KERNEL_COUNT = 28
 
 
 class KdaProblem(ctypes.Structure):
@@ -120,6 +122,41 @@ class KdaShortConvProblem(ctypes.Structure):
     ]
 
 
+class KdaSsmProblem(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("total_tokens", ctypes.c_int64),
+        ("H", ctypes.c_int32),
+        ("G", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("P", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("dt_min", ctypes.c_float),
+        ("dt_max", ctypes.c_float),
+        ("x_stride", ctypes.c_int64),
+        ("dt_stride", ctypes.c_int64),
+        ("B_stride", ctypes.c_int64),
+        ("C_stride", ctypes.c_int64),
+        ("n_slots", ctypes.c_int64),
+        ("zero_rest", ctypes.c_int32),
+    ]
+
+
+class KdaGroupNormProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("C", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("gate", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("center", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("x_stride", ctypes.c_int64),
+        ("gate_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -194,6 +231,16 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kda_short_conv_bwd.restype = ctypes.c_int
     lib.kda_short_conv_update.argtypes = [cp] + [vp] * 7 + [vp]
     lib.kda_short_conv_update.restype = ctypes.c_int
+    sp = ctypes.POINTER(KdaSsmProblem)
+    lib.kda_ssm_recurrent.argtypes = [sp] + [vp] * 11 + [vp]
+    lib.kda_ssm_recurrent.restype = ctypes.c_int
+    np_ = ctypes.POINTER(KdaGroupNormProblem)
+    lib.kda_group_norm_fwd.argtypes = [np_] + [vp] * 5 + [vp]
+    lib.kda_group_norm_fwd.restype = ctypes.c_int
+    lib.kda_group_norm_bwd_workspace_bytes.argtypes = [np_]
+    lib.kda_group_norm_bwd_workspace_bytes.restype = sz
+    lib.kda_group_norm_bwd.argtypes = [np_] + [vp] * 9 + [vp, sz, vp]
+    lib.kda_group_norm_bwd.restype = ctypes.c_int
     lib.kda_profile_begin.argtypes = []
     lib.kda_profile_begin.restype = ctypes.c_int
     lib.kda_profile_end.argtypes = [ctypes.POINTER(ctypes.c_int32),

@@ -737,7 +737,9 @@ const char* kda_kernel_name(int kind) {
       "scan_bwd",    "chunk_grad",      "gate_reduce",       "chunk_local_bwd",
       "chunk_local_state", "scan_rec",  "scan_state",        "recurrent",
       "gated_norm",  "gated_norm_bwd",  "block_norm",        "block_norm_bwd",
-      "short_conv",  "short_conv_bwd",  "short_conv_update", "param_reduce"};
+      "short_conv",  "short_conv_bwd",  "short_conv_update", "param_reduce",
+      "ssm_steps",   "ssm_state",       "ssm_out",           "ssm_grad",
+      "ssm_reduce",  "ssm_recurrent",   "group_norm",        "group_norm_bwd"};
   return (kind >= 0 && kind < KDA_KERNEL_COUNT) ? names[kind] : "unknown";
 }
 

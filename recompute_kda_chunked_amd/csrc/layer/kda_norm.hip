@@ -7,8 +7,6 @@
 // and each output written once (the backward recomputes the norms from the
 // inputs, so nothing is kept from the forward). Sums of squares, gate values
 // and parameter gradients are fp32; every output is rounded once.
-#include <cfloat>
-
 #include "../kda_internal.h"
 #include "kda.h"
 #include "kda_layer.h"
@@ -61,21 +59,6 @@ template <int N>
 __device__ __forceinline__ float row_sum(float x) {
   if constexpr (N == 64) return sum_wave(x);
   else return group_sum<N>(x);
-}
-
-// 1 - s for s = sigmoidf(g), as e^-g s: the difference loses its digits where s
-// is next to 1 (half of them at g = 9, the last at 17). Where e^-g overflows, 1.
-__device__ __forceinline__ float sigmoid_rest(float g, float s) {
-  const float e = __expf(-g);
-  return e > FLT_MAX ? 1.f : e * s;
-}
-
-// act(g) and its derivative.
-__device__ __forceinline__ float act_value(int act, float g, float s) {
-  return act == KDA_ACT_SILU ? g * s : s;
-}
-__device__ __forceinline__ float act_slope(int act, float g, float s) {
-  return act == KDA_ACT_SILU ? s * (1.f + g * (1.f - s)) : s * sigmoid_rest(g, s);
 }
 
 // A row lies across V / N consecutive lanes, one 16-byte vector each, so a

@@ -2,7 +2,10 @@
 // vectors of a row, and sums over a wave.
 #pragma once
 
+#include <cfloat>
+
 #include "../kda_device.h"
+#include "kda.h"
 
 namespace kda {
 
@@ -82,6 +85,21 @@ __device__ __forceinline__ void store_params(float* p, const float (&f)[N]) {
 #pragma unroll
   for (int i = 0; i < N; i += 4)
     *reinterpret_cast<f32x4*>(p + i) = f32x4{f[i], f[i + 1], f[i + 2], f[i + 3]};
+}
+
+// 1 - s for s = sigmoidf(g), as e^-g s: the difference loses its digits where s
+// is next to 1 (half of them at g = 9, the last at 17). Where e^-g overflows, 1.
+__device__ __forceinline__ float sigmoid_rest(float g, float s) {
+  const float e = __expf(-g);
+  return e > FLT_MAX ? 1.f : e * s;
+}
+
+// act(g) and its derivative.
+__device__ __forceinline__ float act_value(int act, float g, float s) {
+  return act == KDA_ACT_SILU ? g * s : s;
+}
+__device__ __forceinline__ float act_slope(int act, float g, float s) {
+  return act == KDA_ACT_SILU ? s * (1.f + g * (1.f - s)) : s * sigmoid_rest(g, s);
 }
 
 // Whether sequence j has a token in [0, T), where its bounds are clamped to.

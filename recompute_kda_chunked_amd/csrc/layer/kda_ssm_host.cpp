@@ -1,0 +1,175 @@
+// Entry points of a state-space layer's operators (include/kda.h): validation
+// on the host, then the launches.
+#include <cmath>
+
+#include "../kda_host.h"
+#include "kda.h"
+#include "kda_checks.h"
+#include "kda_layer.h"
+#include "kda_ssm.h"
+
+using namespace kda;
+
+namespace {
+
+int check_ssm(const kda_ssm_problem* p) {
+  if (!p || p->n_seqs < 0 || p->total_tokens < 0 || p->total_tokens > 0x7fffffffLL || p->H < 1 ||
+      p->G < 1 || p->N < 1 || p->P < 1 || p->H % p->G != 0)
+    return KDA_ERR_INVALID;
+  if (!(p->dt_min >= 0.f) || !(p->dt_max >= p->dt_min) || !std::isfinite(p->dt_min)) return KDA_ERR_INVALID;
+  if (!known_dtype(p->dtype) || (p->N != 64 && p->N != 128) || (p->P != 64 && p->P != 128))
+    return KDA_ERR_UNSUPPORTED;
+  const int64_t T = p->total_tokens, HP = static_cast<int64_t>(p->H) * p->P, GN = static_cast<int64_t>(p->G) * p->N;
+  if (!stride_ok(p->x_stride, HP, p->dtype, T, true) || !stride_ok(p->dt_stride, p->H, p->dtype, T, false) ||
+      !stride_ok(p->B_stride, GN, p->dtype, T, true) || !stride_ok(p->C_stride, GN, p->dtype, T, true))
+    return KDA_ERR_INVALID;
+  return KDA_OK;
+}
+
+int check_group_norm(const kda_group_norm_problem* p) {
+  if (!p || p->rows < 0 || p->C < 1 || p->groups < 1 || p->C % p->groups != 0 || bad_eps(p->eps))
+    return KDA_ERR_INVALID;
+  if (p->rows > (int64_t{1} << 31) || p->C > (1 << 20)) return KDA_ERR_UNSUPPORTED;
+  const int W = p->C / p->groups;
+  if (!known_dtype(p->dtype) || W % 8 != 0 || W > 8192) return KDA_ERR_UNSUPPORTED;
+  if (p->gate != KDA_GROUP_GATE_NONE && p->gate != KDA_GROUP_GATE_AFTER && p->gate != KDA_GROUP_GATE_FIRST)
+    return KDA_ERR_UNSUPPORTED;
+  if (p->activation != KDA_ACT_SIGMOID && p->activation != KDA_ACT_SILU &&
+      !(p->activation == KDA_ACT_NONE && p->gate == KDA_GROUP_GATE_NONE))
+    return KDA_ERR_UNSUPPORTED;
+  if (!stride_ok(p->x_stride, p->C, p->dtype, p->rows, true) ||
+      !stride_ok(p->gate_stride, p->C, p->dtype, p->rows, true))
+    return KDA_ERR_INVALID;
+  return KDA_OK;
+}
+
+// Room for both parameters' partial sums, whether or not there is a bias.
+size_t group_norm_ws(const kda_group_norm_problem* p) {
+  return static_cast<size_t>(group_norm_partials(p->dtype, p->C, p->groups, p->rows)) * 2 * p->C * sizeof(float);
+}
+
+GroupNormArgs group_norm_args(const kda_group_norm_problem* p, const void* x, const void* gate,
+                              const float* weight, const float* bias) {
+  GroupNormArgs a{};
+  a.rows = p->rows;
+  a.xs = stride_of(p->x_stride, p->C);
+  a.gs = stride_of(p->gate_stride, p->C);
+  a.C = p->C;
+  a.groups = p->groups;
+  a.W = p->C / p->groups;
+  a.act = p->activation;
+  a.center = p->center != 0;
+  a.eps = p->eps;
+  a.x = x;
+  a.gate = gate;
+  a.weight = weight;
+  a.bias = bias;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_ssm_recurrent(const kda_ssm_problem* p, const void* x, const void* raw_dt,
+                      const float* A_log, const void* B, const void* C, const float* D,
+                      const float* dt_bias, const int32_t* cu_seqlens,
+                      const int32_t* state_indices, float* state, void* y, void* stream) {
+  const int st = check_ssm(p);
+  if (st != KDA_OK) return st;
+  if (p->n_slots < 0 || p->n_slots > 0x7fffffffLL) return KDA_ERR_INVALID;
+  if (!cu_seqlens && p->total_tokens != p->n_seqs) return KDA_ERR_INVALID;
+  if (!state_indices && p->n_slots < p->n_seqs) return KDA_ERR_INVALID;
+  // one block of 256 threads per (sequence, head), below 2^32 threads
+  // in all, at least one of them for the rows that belong to no sequence
+  if (static_cast<int64_t>(p->n_seqs) * p->H + (p->zero_rest && cu_seqlens) >= (int64_t{1} << 24))
+    return KDA_ERR_UNSUPPORTED;
+  if (state_indices && p->n_seqs > kMaxIndexed) return KDA_ERR_UNSUPPORTED;
+  if (p->n_seqs == 0 || p->total_tokens == 0) return KDA_OK;
+  if (!x || !raw_dt || !A_log || !B || !C || !state || !y) return KDA_ERR_INVALID;
+  const int64_t HP = static_cast<int64_t>(p->H) * p->P, GN = static_cast<int64_t>(p->G) * p->N;
+  SsmStepArgs a{};
+  a.n_seqs = p->n_seqs;
+  a.H = p->H;
+  a.G = p->G;
+  a.T = p->total_tokens;
+  a.n_slots = p->n_slots;
+  a.dt_min = p->dt_min;
+  a.dt_max = p->dt_max;
+  a.x = x;
+  a.dt = raw_dt;
+  a.B = B;
+  a.C = C;
+  a.xs = stride_of(p->x_stride, HP);
+  a.dts = stride_of(p->dt_stride, p->H);
+  a.Bs = stride_of(p->B_stride, GN);
+  a.Cs = stride_of(p->C_stride, GN);
+  a.A_log = A_log;
+  a.D = D;
+  a.dt_bias = dt_bias;
+  a.cu = cu_seqlens;
+  a.idx = state_indices;
+  a.state = state;
+  a.y = y;
+  a.zero_rest = p->zero_rest != 0 && cu_seqlens;
+  const size_t e = p->dtype == KDA_F32 ? 4 : 2;
+  const Range others[] = {
+      rows_of(x, a.T, a.xs, HP, e),        rows_of(raw_dt, a.T, a.dts, p->H, e),
+      rows_of(B, a.T, a.Bs, GN, e),        rows_of(C, a.T, a.Cs, GN, e),
+      dense(A_log, p->H, 1, 4),            dense(D, p->H, 1, 4),
+      dense(dt_bias, p->H, 1, 4),          dense(cu_seqlens, int64_t{a.n_seqs} + 1, 1, 4),
+      dense(state_indices, a.n_seqs, 1, 4), rows_of(y, a.T, HP, HP, e)};
+  if (over_any(dense(state, a.n_slots, HP * p->N, 4), others, sizeof others / sizeof *others))
+    return KDA_ERR_INVALID;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  KDA_TRY(KDA_KERNEL_SSM_RECURRENT, a.T * a.H, launch_ssm_recurrent(p->dtype, p->N, p->P, a, s));
+  return KDA_OK;
+}
+
+int kda_group_norm_fwd(const kda_group_norm_problem* p, const void* x, const void* gate,
+                       const float* weight, const float* bias, void* y, void* stream) {
+  const int st = check_group_norm(p);
+  if (st != KDA_OK) return st;
+  if (p->rows == 0) return KDA_OK;
+  if (!x || !weight || !y) return KDA_ERR_INVALID;
+  if ((p->gate == KDA_GROUP_GATE_NONE) != (gate == nullptr)) return KDA_ERR_INVALID;
+  GroupNormArgs a = group_norm_args(p, x, gate, weight, bias);
+  a.y = y;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  KDA_TRY(KDA_KERNEL_GROUP_NORM, p->rows, launch_group_norm_fwd(p->dtype, p->gate, a, s));
+  return KDA_OK;
+}
+
+size_t kda_group_norm_bwd_workspace_bytes(const kda_group_norm_problem* p) {
+  return check_group_norm(p) == KDA_OK ? group_norm_ws(p) : 0;
+}
+
+int kda_group_norm_bwd(const kda_group_norm_problem* p, const void* x, const void* gate,
+                       const float* weight, const float* bias, const void* dy, void* dx,
+                       void* dgate, float* dweight, float* dbias, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  const int st = check_group_norm(p);
+  if (st != KDA_OK) return st;
+  if (!dweight) return KDA_ERR_INVALID;
+  if (p->rows > 0) {
+    if (!x || !weight || !dy || !dx || !workspace) return KDA_ERR_INVALID;
+    if ((p->gate == KDA_GROUP_GATE_NONE) != (gate == nullptr)) return KDA_ERR_INVALID;
+    if (gate && !dgate) return KDA_ERR_INVALID;
+  }
+  if (workspace_bytes < group_norm_ws(p)) return KDA_ERR_WORKSPACE;
+  GroupNormArgs a = group_norm_args(p, x, gate, weight, bias);
+  a.dy = dy;
+  a.dx = dx;
+  a.dgate = dgate;
+  a.partials = static_cast<float*>(workspace);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (p->rows > 0)
+    KDA_TRY(KDA_KERNEL_GROUP_NORM_BWD, p->rows, launch_group_norm_bwd(p->dtype, p->gate, a, s));
+  const int64_t nb = group_norm_partials(p->dtype, p->C, p->groups, p->rows);
+  const bool two = bias != nullptr || (p->rows == 0 && dbias);  // no rows: zeros for both
+  const ParamReduceArgs r{a.partials, nb, p->C, two ? p->C : 0, dweight, dbias};
+  KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r, s));
+  return KDA_OK;
+}
+
+}  // extern "C"
