@@ -473,6 +473,19 @@ typedef struct {
                            no sequence (the scan always does) */
 } kda_ssm_problem;
 
+size_t kda_ssm_fwd_workspace_bytes(const kda_ssm_problem *p);
+int kda_ssm_fwd(const kda_ssm_problem *p, const void *x, const void *raw_dt, const float *A_log,
+                const void *B, const void *C, const float *D, const float *dt_bias,
+                const int32_t *cu_seqlens, const float *initial_state, void *y,
+                float *final_state, void *workspace, size_t workspace_bytes, void *stream);
+size_t kda_ssm_bwd_workspace_bytes(const kda_ssm_problem *p);
+int kda_ssm_bwd(const kda_ssm_problem *p, const void *x, const void *raw_dt, const float *A_log,
+                const void *B, const void *C, const float *D, const float *dt_bias,
+                const int32_t *cu_seqlens, const float *initial_state, const void *dy,
+                const float *d_final_state, void *dx, void *draw_dt, float *dA_log, void *dB,
+                void *dC, float *dD, float *ddt_bias, float *d_initial_state, void *workspace,
+                size_t workspace_bytes, void *stream);
+
 /* The scan's decoding form: sequence n starts from its state in a pool
    [n_slots, H, N, P] (fp32; the scan's final states serve as they are) and
    leaves its last state there. cu_seqlens (NULL: one token a sequence),

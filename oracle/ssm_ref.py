@@ -25,7 +25,9 @@ def scan(x, raw_dt, A_log, B, C, D, dt_bias, cu, state=None, slots=None, limit=(
     """y and the states left behind: S = exp(-exp(A_log) dt) S + dt B x^T,
     y = S^T C + D x, sequence n from state[slots[n]] (slots None: n; state None:
     zeros; a negative slot: zero rows). Rows of no sequence are zero. With dy
-    (and dfinal) a dict of the gradients of sum(y dy) + sum(final dfinal)."""
+    (and dfinal) a dict of the gradients of sum(y dy) + sum(final dfinal), and
+    `tall`, the step sizes' gradient with its two terms added up instead of
+    taken off each other (of inputs without signs: their size)."""
     x, A, B, C = _f64(x), np.exp(_f64(A_log)), _f64(B), _f64(C)
     T, H, P = x.shape
     per, N = H // B.shape[1], B.shape[2]
@@ -52,7 +54,7 @@ def scan(x, raw_dt, A_log, B, C, D, dt_bias, cu, state=None, slots=None, limit=(
     dy = _f64(dy)
     dS = np.zeros_like(S) if dfinal is None else _f64(dfinal).copy()
     g = {k: np.zeros_like(v) for k, v in dict(x=x, B=Bh, C=Ch, dt=dt).items()}
-    dA, dD = np.zeros(H), np.zeros(H)
+    dA, dD, tdt = np.zeros(H), np.zeros(H), np.zeros((T, H))
     for n in range(len(cu) - 1):
         for t in reversed(range(cu[n], cu[n + 1])):
             decayed, after = states[t]
@@ -63,13 +65,14 @@ def scan(x, raw_dt, A_log, B, C, D, dt_bias, cu, state=None, slots=None, limit=(
             g["x"][t] = dt[t][:, None] * np.einsum("hnp,hn->hp", dS[n], Bh[t]) + Dv[:, None] * dy[t]
             g["B"][t] = dt[t][:, None] * np.einsum("hnp,hp->hn", dS[n], x[t])
             g["dt"][t] = Bx - A * dl
+            tdt[t] = Bx + A * dl
             dA += -A * dt[t] * dl
             dD += np.sum(x[t] * dy[t], 1)
             dS[n] = a[t][:, None, None] * dS[n]
     draw = g["dt"] * slope
     G = B.shape[1]
     return y, S, dict(dx=g["x"], draw_dt=draw, dA_log=dA, dB=g["B"].reshape(T, G, per, N).sum(2),
-                      dC=g["C"].reshape(T, G, per, N).sum(2), dD=dD, ddt_bias=draw.sum(0), dinit=dS)
+                      dC=g["C"].reshape(T, G, per, N).sum(2), dD=dD, ddt_bias=draw.sum(0), dinit=dS, tall=tdt)
 
 
 def group_norm(x, weight, bias=None, gate=None, groups=1, eps=1e-6, activation="silu", center=True,

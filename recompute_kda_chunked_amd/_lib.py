@@ -25,7 +25,9 @@ EXPORTS = ("kda_fwd_workspace_bytes", "kda_bwd_workspace_bytes", "kda_check_prob
            "kda_gdn2_recurrent", "kda_gated_norm_fwd", "kda_gated_norm_bwd_workspace_bytes",
            "kda_gated_norm_bwd", "kda_block_norm_fwd", "kda_block_norm_bwd_workspace_bytes",
            "kda_block_norm_bwd", "kda_short_conv_fwd", "kda_short_conv_bwd_workspace_bytes",
-           "kda_short_conv_bwd", "kda_short_conv_update", "kda_ssm_recurrent",
+           "kda_short_conv_bwd", "kda_short_conv_update",
+           "kda_ssm_fwd_workspace_bytes", "kda_ssm_fwd", "kda_ssm_bwd_workspace_bytes",
+           "kda_ssm_bwd", "kda_ssm_recurrent",
            "kda_group_norm_fwd", "kda_group_norm_bwd_workspace_bytes", "kda_group_norm_bwd")
 KDA_ACT_NONE, KDA_ACT_SIGMOID, KDA_ACT_SILU = range(3)
 KDA_BLOCK_GATE_NONE, KDA_BLOCK_GATE_TOKEN, KDA_BLOCK_GATE_CHANNEL = range(3)
@@ -232,6 +234,14 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kda_short_conv_update.argtypes = [cp] + [vp] * 7 + [vp]
     lib.kda_short_conv_update.restype = ctypes.c_int
     sp = ctypes.POINTER(KdaSsmProblem)
+    lib.kda_ssm_fwd_workspace_bytes.argtypes = [sp]
+    lib.kda_ssm_fwd_workspace_bytes.restype = sz
+    lib.kda_ssm_fwd.argtypes = [sp] + [vp] * 11 + [vp, sz, vp]
+    lib.kda_ssm_fwd.restype = ctypes.c_int
+    lib.kda_ssm_bwd_workspace_bytes.argtypes = [sp]
+    lib.kda_ssm_bwd_workspace_bytes.restype = sz
+    lib.kda_ssm_bwd.argtypes = [sp] + [vp] * 19 + [vp, sz, vp]
+    lib.kda_ssm_bwd.restype = ctypes.c_int
     lib.kda_ssm_recurrent.argtypes = [sp] + [vp] * 11 + [vp]
     lib.kda_ssm_recurrent.restype = ctypes.c_int
     np_ = ctypes.POINTER(KdaGroupNormProblem)

@@ -21,7 +21,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["kda_host.cpp", "kda_prologue.hip", "kda_chunk_local.hip", "kda_scan.hip",
            "kda_chunk_grad.hip", "kda_noalloc.hip", "layer/kda_layer_host.cpp",
            "layer/kda_recurrent.hip", "layer/kda_norm.hip", "layer/kda_conv.hip",
-           "layer/kda_ssm_host.cpp", "layer/kda_ssm_step.hip", "layer/kda_group_norm.hip"]
+           "layer/kda_ssm_host.cpp", "layer/kda_ssm_scan.hip", "layer/kda_ssm_step.hip",
+           "layer/kda_group_norm.hip"]
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]

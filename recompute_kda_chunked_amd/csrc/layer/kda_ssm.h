@@ -22,6 +22,39 @@ struct SsmStepArgs {
 };
 hipError_t launch_ssm_recurrent(int dtype, int N, int P, const SsmStepArgs& a, hipStream_t s);
 
+// The scan over packed sequences, in chunks of ssm_chunk(dtype) tokens of one
+// sequence. A chunk has a slot: sequence n's first is cu[n] / Q + n, which
+// leaves room for every sequence's chunks in T / Q + n_seqs slots and needs no
+// table; a slot without a chunk is passed over.
+constexpr int ssm_chunk(int dtype) { return dtype == 0 ? 64 : 128; }
+struct SsmArgs {
+  int n_seqs, H, G, P;
+  int64_t T, slots;
+  float dt_min, dt_max;
+  const void *x, *dt, *B, *C, *dy;
+  int64_t xs, dts, Bs, Cs;
+  const float *A_log, *D, *dt_bias, *init, *dfinal;
+  const int32_t* cu;
+  void *y, *dx, *ddt, *dB, *dC;
+  float *final_state, *dA, *dD, *dbias, *dinit;
+  // Workspace. steps [slots][H][Q]: {dt, high and low part of the chunk's
+  // running sum of log2 decays, d dt / d raw_dt}. S and dS: the states
+  // entering each chunk and the gradients of those leaving it, [slots][H]
+  // [P / 64][N][64] in the problem's dtype; for bf16 the second planes hold
+  // what the first ones' rounding left (null: not needed).
+  float* steps;
+  void *S, *S_lo, *dS, *dS_lo;
+  float *pB, *pC;  // partial dB and dC [sets][T][G][N] where sets > 1
+  float *part2, *part1;  // per slot {dA, ddt_bias} [2 H] and dD [H]
+  int hb, sets;    // heads of a group a block takes in turn, blocks a group
+};
+hipError_t launch_ssm_steps(int dtype, const SsmArgs& a, hipStream_t s);
+// States in sequence order (reverse: gradients, from the last chunk back).
+hipError_t launch_ssm_state(int dtype, int N, bool reverse, const SsmArgs& a, hipStream_t s);
+hipError_t launch_ssm_out(int dtype, int N, const SsmArgs& a, hipStream_t s);
+hipError_t launch_ssm_grad(int dtype, int N, const SsmArgs& a, hipStream_t s);
+hipError_t launch_ssm_reduce(int dtype, int N, const SsmArgs& a, hipStream_t s);
+
 // Group norm. Partial sums: group_norm_partials(...) rows of dweight [C] then
 // (with a bias) dbias [C].
 struct GroupNormArgs {

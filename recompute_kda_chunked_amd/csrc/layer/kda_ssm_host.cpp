@@ -26,6 +26,85 @@ int check_ssm(const kda_ssm_problem* p) {
   return KDA_OK;
 }
 
+// Workspace of the scan, in parts that start at multiples of 256 bytes.
+struct ScanPlan {
+  int Q, fwd_hb, fwd_sets, bwd_hb, bwd_sets;
+  int64_t slots;
+  size_t steps, state, partial, part2, part1;
+  explicit ScanPlan(const kda_ssm_problem* p) {
+    Q = ssm_chunk(p->dtype);
+    slots = p->total_tokens / Q + p->n_seqs;
+    const int per = p->H / p->G;
+    // heads a block takes: as many of a group as leave the launch enough blocks
+    auto heads = [&](int64_t blocks) {
+      int hb = per;
+      while (hb > 1 && slots * p->G * ((per + hb - 1) / hb) < blocks) hb = (hb + 1) / 2;
+      return hb;
+    };
+    fwd_hb = heads(1024);
+    fwd_sets = (per + fwd_hb - 1) / fwd_hb;
+    bwd_hb = heads(512);
+    bwd_sets = (per + bwd_hb - 1) / bwd_hb;
+    auto part = [](int64_t n, size_t size) { return (static_cast<size_t>(n) * size + 255) / 256 * 256; };
+    steps = part(slots * p->H * Q, 16);
+    state = part(slots * p->H * p->P * p->N, p->dtype == KDA_F32 ? 4 : 2);
+    partial = bwd_sets > 1 ? part(p->total_tokens * p->G * p->N * bwd_sets, 4) : 0;
+    part2 = part(slots * p->H * 2, 4);
+    part1 = part(slots * p->H, 4);
+  }
+  size_t fwd() const { return steps + state; }
+  size_t bwd(int dtype) const {
+    return steps + (dtype == KDA_F32 ? 2 : 4) * state + 2 * partial + part2 + part1;
+  }
+};
+
+// What the scan's launches can hold: blocks of 512 threads (256 of a state pass),
+// below 2^32 threads, some of them for the rows of no sequence; elements of a
+// workspace part below 2^40.
+int check_scan(const kda_ssm_problem* p, bool has_cu) {
+  const int st = check_ssm(p);
+  if (st != KDA_OK) return st;
+  if (!has_cu && p->n_seqs != 1) return KDA_ERR_INVALID;
+  const int64_t T = p->total_tokens, slots = T / 64 + p->n_seqs, H = p->H;
+  if (H > (1 << 20) || slots * H >= (int64_t{1} << 26) || slots * H * p->N * p->P >= (int64_t{1} << 40))
+    return KDA_ERR_UNSUPPORTED;
+  if (slots * H >= (1 << 23) - 1024 || slots * ((H + 3) / 4) >= (1 << 24) ||
+      p->n_seqs * H * (p->P / 64) * (p->N / 32) >= (1 << 24))
+    return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+SsmArgs scan_args(const kda_ssm_problem* p, const ScanPlan& plan, const void* x, const void* raw_dt,
+                  const float* A_log, const void* B, const void* C, const float* D,
+                  const float* dt_bias, const int32_t* cu, const float* init, void* workspace) {
+  SsmArgs a{};
+  a.n_seqs = p->n_seqs;
+  a.H = p->H;
+  a.G = p->G;
+  a.P = p->P;
+  a.T = p->total_tokens;
+  a.slots = plan.slots;
+  a.dt_min = p->dt_min;
+  a.dt_max = p->dt_max;
+  a.x = x;
+  a.dt = raw_dt;
+  a.B = B;
+  a.C = C;
+  a.xs = stride_of(p->x_stride, static_cast<int64_t>(p->H) * p->P);
+  a.dts = stride_of(p->dt_stride, p->H);
+  a.Bs = stride_of(p->B_stride, static_cast<int64_t>(p->G) * p->N);
+  a.Cs = stride_of(p->C_stride, static_cast<int64_t>(p->G) * p->N);
+  a.A_log = A_log;
+  a.D = D;
+  a.dt_bias = dt_bias;
+  a.cu = cu;
+  a.init = init;
+  char* w = static_cast<char*>(workspace);
+  a.steps = reinterpret_cast<float*>(w);
+  a.S = w + plan.steps;
+  return a;
+}
+
 int check_group_norm(const kda_group_norm_problem* p) {
   if (!p || p->rows < 0 || p->C < 1 || p->groups < 1 || p->C % p->groups != 0 || bad_eps(p->eps))
     return KDA_ERR_INVALID;
@@ -70,6 +149,92 @@ GroupNormArgs group_norm_args(const kda_group_norm_problem* p, const void* x, co
 }  // namespace
 
 extern "C" {
+
+size_t kda_ssm_fwd_workspace_bytes(const kda_ssm_problem* p) {
+  return check_scan(p, true) == KDA_OK ? ScanPlan(p).fwd() : 0;
+}
+
+int kda_ssm_fwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, const float* A_log,
+                const void* B, const void* C, const float* D, const float* dt_bias,
+                const int32_t* cu_seqlens, const float* initial_state, void* y,
+                float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_scan(p, cu_seqlens != nullptr);
+  if (st != KDA_OK) return st;
+  if (p->total_tokens > 0 && (!x || !raw_dt || !A_log || !B || !C || !y)) return KDA_ERR_INVALID;
+  const ScanPlan plan(p);
+  if (plan.fwd() > 0 && !workspace) return KDA_ERR_INVALID;
+  if (workspace_bytes < plan.fwd()) return KDA_ERR_WORKSPACE;
+  SsmArgs a = scan_args(p, plan, x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, initial_state, workspace);
+  a.y = y;
+  a.final_state = final_state;
+  a.hb = plan.fwd_hb;
+  a.sets = plan.fwd_sets;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t units = a.T * a.H;
+  if (a.T > 0 && a.n_seqs > 0) KDA_TRY(KDA_KERNEL_SSM_STEPS, units, launch_ssm_steps(p->dtype, a, s));
+  if (a.n_seqs > 0 && (a.T > 0 || final_state))
+    KDA_TRY(KDA_KERNEL_SSM_STATE, units, launch_ssm_state(p->dtype, p->N, false, a, s));
+  if (a.T > 0) KDA_TRY(KDA_KERNEL_SSM_OUT, units, launch_ssm_out(p->dtype, p->N, a, s));
+  return KDA_OK;
+}
+
+size_t kda_ssm_bwd_workspace_bytes(const kda_ssm_problem* p) {
+  return check_scan(p, true) == KDA_OK ? ScanPlan(p).bwd(p->dtype) : 0;
+}
+
+int kda_ssm_bwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, const float* A_log,
+                const void* B, const void* C, const float* D, const float* dt_bias,
+                const int32_t* cu_seqlens, const float* initial_state, const void* dy,
+                const float* d_final_state, void* dx, void* draw_dt, float* dA_log, void* dB,
+                void* dC, float* dD, float* ddt_bias, float* d_initial_state, void* workspace,
+                size_t workspace_bytes, void* stream) {
+  const int st = check_scan(p, cu_seqlens != nullptr);
+  if (st != KDA_OK) return st;
+  if (!dA_log) return KDA_ERR_INVALID;
+  if (p->total_tokens > 0 && (!x || !raw_dt || !A_log || !B || !C || !dy || !dx || !draw_dt || !dB || !dC))
+    return KDA_ERR_INVALID;
+  const ScanPlan plan(p);
+  if (plan.bwd(p->dtype) > 0 && !workspace) return KDA_ERR_INVALID;
+  if (workspace_bytes < plan.bwd(p->dtype)) return KDA_ERR_WORKSPACE;
+  SsmArgs a = scan_args(p, plan, x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, initial_state, workspace);
+  a.dy = dy;
+  a.dfinal = d_final_state;
+  a.dx = dx;
+  a.ddt = draw_dt;
+  a.dB = dB;
+  a.dC = dC;
+  a.dinit = d_initial_state;
+  a.hb = plan.bwd_hb;
+  a.sets = plan.bwd_sets;
+  char* w = static_cast<char*>(a.S) + plan.state;
+  a.dS = w;
+  w += plan.state;
+  if (p->dtype == KDA_BF16) {
+    a.S_lo = w;
+    a.dS_lo = w + plan.state;
+    w += 2 * plan.state;
+  }
+  a.pB = reinterpret_cast<float*>(w);
+  a.pC = reinterpret_cast<float*>(w + plan.partial);
+  a.part2 = reinterpret_cast<float*>(w + 2 * plan.partial);
+  a.part1 = reinterpret_cast<float*>(w + 2 * plan.partial + plan.part2);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t units = a.T * a.H;
+  if (a.T > 0 && a.n_seqs > 0) {
+    KDA_TRY(KDA_KERNEL_SSM_STEPS, units, launch_ssm_steps(p->dtype, a, s));
+    KDA_TRY(KDA_KERNEL_SSM_STATE, units, launch_ssm_state(p->dtype, p->N, false, a, s));
+  }
+  if (a.n_seqs > 0 && (a.T > 0 || d_initial_state))
+    KDA_TRY(KDA_KERNEL_SSM_STATE, units, launch_ssm_state(p->dtype, p->N, true, a, s));
+  if (a.T > 0) KDA_TRY(KDA_KERNEL_SSM_GRAD, units, launch_ssm_grad(p->dtype, p->N, a, s));
+  if (a.T > 0 && a.sets > 1) KDA_TRY(KDA_KERNEL_SSM_REDUCE, a.T, launch_ssm_reduce(p->dtype, p->N, a, s));
+  // without tokens the sums are empty
+  const int64_t nb = a.T > 0 ? a.slots : 0;
+  const ParamReduceArgs r2{a.part2, nb, p->H, p->H, dA_log, ddt_bias}, r1{a.part1, nb, p->H, 0, dD, nullptr};
+  KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r2, s));
+  if (dD) KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r1, s));
+  return KDA_OK;
+}
 
 int kda_ssm_recurrent(const kda_ssm_problem* p, const void* x, const void* raw_dt,
                       const float* A_log, const void* B, const void* C, const float* D,

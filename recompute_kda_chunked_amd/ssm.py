@@ -1,5 +1,5 @@
-"""Python binding of a state-space layer's operators: the decoding form of the
-selective scan and the group norm behind it. Argument checks and marshalling
+"""Python binding of a state-space layer's operators: the selective scan, its
+decoding form and the group norm behind it. Argument checks and marshalling
 only, as in ``layer``; every step runs in the HIP kernels behind
 ``include/kda.h``.
 """
@@ -50,11 +50,110 @@ def _ssm_problem(x, raw_dt, A_log, B, C, D, dt_bias, dt_limit):
     return dev, p
 
 
+def _scan_problem(x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, dt_limit, **tensors):
+    """(device, problem) of a packed scan; `tensors`: further arguments, name =
+    (tensor or None, True for a state, False for rows like x's)."""
+    dev, p = _ssm_problem(x, raw_dt, A_log, B, C, D, dt_bias, dt_limit)
+    p.n_seqs = 1
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.dtype is not torch.int32:
+            raise KdaError("cu_seqlens: expected int32 [N+1], got %s %s"
+                           % (tuple(cu_seqlens.shape), cu_seqlens.dtype))
+        _placed("cu_seqlens", cu_seqlens, dev, 4)
+        p.n_seqs = cu_seqlens.shape[0] - 1
+    for name, (t, is_state) in tensors.items():
+        if t is not None:
+            if is_state:
+                _want(name, t, (p.n_seqs, p.H, p.N, p.P), torch.float32)
+            else:
+                _want(name, t, x.shape, x.dtype)
+            _placed(name, t, dev)
+    return dev, p
+
+
+def ssm_scan_forward(x, raw_dt, A_log, B, C, D=None, dt_bias=None, cu_seqlens=None, *,
+                     initial_state=None, output_final_state=False, dt_limit=(0.0, _INF)):
+    """y, or (y, final_state), of kda_ssm_fwd; see ssm_scan."""
+    dev, p = _scan_problem(x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, dt_limit,
+                           initial_state=(initial_state, True))
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    final = None
+    if output_final_state:
+        final = torch.empty((p.n_seqs, p.H, p.N, p.P), dtype=torch.float32, device=dev)
+    _call(dev, "kda_ssm_fwd", p, x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, initial_state, y,
+          final, workspace=_workspace(dev, "kda_ssm_fwd", p))
+    return (y, final) if output_final_state else y
+
+
+def ssm_scan_backward(x, raw_dt, A_log, B, C, D, dt_bias, dy, cu_seqlens=None, *,
+                      initial_state=None, d_final_state=None, dt_limit=(0.0, _INF)):
+    """(dx, draw_dt, dA_log, dB, dC, dD, ddt_bias, d_initial_state) of
+    sum(y * dy) + sum(final_state * d_final_state) (kda_ssm_bwd), everything
+    else recomputed from the inputs; dD, ddt_bias and d_initial_state are None
+    without D, dt_bias and initial_state."""
+    dev, p = _scan_problem(x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, dt_limit, dy=(dy, False),
+                           initial_state=(initial_state, True), d_final_state=(d_final_state, True))
+    dx, ddt, dB, dC = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (x, raw_dt, B, C))
+    dA = torch.empty_like(A_log)
+    dD, dbias, dinit = (None if t is None else torch.empty_like(t) for t in (D, dt_bias, initial_state))
+    _call(dev, "kda_ssm_bwd", p, x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, initial_state, dy,
+          d_final_state, dx, ddt, dA, dB, dC, dD, dbias, dinit,
+          workspace=_workspace(dev, "kda_ssm_bwd", p))
+    return dx, ddt, dA, dB, dC, dD, dbias, dinit
+
+
+class SsmScanFunction(torch.autograd.Function):
+    """Autograd wrapper: saves references to the caller's inputs only."""
+
+    @staticmethod
+    def forward(ctx, x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, initial_state, final, dt_limit):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, initial_state)
+        ctx.dt_limit = dt_limit
+        return ssm_scan_forward(x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens,
+                                initial_state=initial_state, output_final_state=final,
+                                dt_limit=dt_limit)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dfinal=None):
+        x, raw_dt, A_log, B, C, D, dt_bias, cu, init = ctx.saved_tensors
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _grad(dy)
+        *grads, dinit = ssm_scan_backward(x, raw_dt, A_log, B, C, D, dt_bias, dy, cu,
+                                          initial_state=init, d_final_state=_grad(dfinal),
+                                          dt_limit=ctx.dt_limit)
+        return (*grads, None, dinit, None, None)
+
+
+def ssm_scan(x, raw_dt, A_log, B, C, D=None, dt_bias=None, cu_seqlens=None, *, initial_state=None,
+             output_final_state=False, dt_limit=(0.0, _INF)):
+    """The selective scan of a state-space layer over packed sequences, for
+    prompts and training, differentiable: y [T,H,P] with, per sequence and
+    head h, of group h // (H // G),
+      dt = clamp(softplus(raw_dt + dt_bias), *dt_limit)
+      S = exp(-exp(A_log) dt) S + dt B x^T,  y = S^T C + D x.
+    x [T,H,P], raw_dt [T,H], B and C [T,G,N] may have tokens that are slices
+    of wider rows, as short_conv's output has them; A_log, D and dt_bias fp32
+    [H], the last two None for zero; N and P 64 or 128; cu_seqlens int32 [n+1]
+    on the device (None: one sequence; no host copy is needed, so the call can
+    be captured into a graph). initial_state fp32 [n,H,N,P] (None: zero). With
+    output_final_state returns (y, final_state), from which the next call or
+    ssm_recurrent goes on. Rows of y that belong to no sequence are zero. No
+    gradient reaches raw_dt where a limit holds. The workspace is about the
+    states' size every 128 tokens (64 for fp32), four times that backward."""
+    if _through_autograd(x, raw_dt, A_log, B, C, D, dt_bias, initial_state):
+        return SsmScanFunction.apply(x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, initial_state,
+                                     output_final_state, dt_limit)
+    return ssm_scan_forward(x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens,
+                            initial_state=initial_state, output_final_state=output_final_state,
+                            dt_limit=dt_limit)
+
+
 def ssm_recurrent(x, raw_dt, A_log, B, C, D, dt_bias, state, cu_seqlens=None, *,
                   state_indices=None, dt_limit=(0.0, _INF), out=None):
     """The selective scan token by token, for decoding: y [T,H,P], sequence n
-    starting from its state in `state` (fp32 [slots,H,N,P]) and leaving its
-    last state there. Per head h, of group h // (H // G), with dt =
+    starting from its state in `state` (fp32 [slots,H,N,P]; ssm_scan's final
+    states serve as they are) and leaving its last state there. Per head h, of group h // (H // G), with dt =
     clamp(softplus(raw_dt + dt_bias), *dt_limit):
     S = exp(-exp(A_log) dt) S + dt B x^T, y = S^T C + D x. x [T,H,P], raw_dt
     [T,H], B and C [T,G,N] may have tokens that are slices of wider rows;
@@ -63,7 +162,7 @@ def ssm_recurrent(x, raw_dt, A_log, B, C, D, dt_bias, state, cu_seqlens=None, *,
     sequence and overlap as for kda_recurrent. Not differentiable."""
     if state.dim() != 4:
         raise KdaError("state: expected [slots,H,N,P], got %s" % (tuple(state.shape),))
-    _no_grad("ssm_recurrent", "decode under no_grad", (x, raw_dt, A_log, B, C, D, dt_bias, state, out))
+    _no_grad("ssm_recurrent", "train with ssm_scan", (x, raw_dt, A_log, B, C, D, dt_bias, state, out))
     dev, p = _ssm_problem(x, raw_dt, A_log, B, C, D, dt_bias, dt_limit)
     _want("state", state, (state.shape[0], p.H, p.N, p.P), torch.float32)
     _placed("state", state, dev)

@@ -1,0 +1,346 @@
+"""GPU parity of the selective scan, forward and backward, against the FP64
+reference (needs an MI355X).
+
+Tolerances. Decays and step sizes are positive, so the reference run on the
+inputs' absolute values gives the sum of the sizes of the terms of every
+output, and each element is held to its own:
+  y, dx, dB, dC   half a step of the dtype of the value, plus of the terms: in
+                  bf16 one rounding of a score or a state, 2^-8, and 1e-5 for
+                  fp32's roundings (sums of at most 128 + 128 terms in serial
+                  runs of 32, the scores, decays and step sizes: below 100
+                  roundings of 2^-24 = 6e-6); in fp32 1e-5
+  draw_dt         half a step, plus of the terms of its chunk, over which the
+                  decay's gradient is summed up and differs: 1e-5, and in
+                  bf16 2^-16 for the pairs of bf16 that states are (what a
+                  second rounding leaves, twice: 2 * 2^-17)
+  states and their gradients  (fp32) 2^-16 of their terms in bf16, 1e-5 in fp32
+  dA_log, ddt_bias, dD  fp32 sums of the above before their rounding: the same
+                  parts of their terms' sizes
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ssm_ref
+from recompute_kda_chunked_amd import (group_norm, short_conv, short_conv_update, ssm_recurrent, ssm_scan,
+                                       ssm_scan_backward, ssm_scan_forward)
+from test_gpu_recurrent import leave_nan
+from test_gpu_ssm_recurrent import ssm_inputs
+from test_gpu_states import announce, rel, to_np
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+HALF_STEP = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+NAMES = ("x", "raw_dt", "A_log", "B", "C", "D", "dt_bias")
+
+
+def make(lens, H, G, N, P, dtype, seed, init=True, fused=False, **kw):
+    x = dict(ssm_inputs(lens, H, G, N, P, dtype, seed, fused=fused, pool=False), **kw)
+    gen = torch.Generator(device="cuda").manual_seed(seed + 1000)
+    n = len(lens)
+    x["init"] = torch.randn((n, H, N, P), generator=gen, device="cuda") if init else None
+    x["dy"] = torch.randn(x["x"].shape, generator=gen, device="cuda").to(dtype)
+    x["dfinal"] = torch.randn((n, H, N, P), generator=gen, device="cuda") if init else None
+    return x
+
+
+def forward(x, **kw):
+    return ssm_scan_forward(*[x[k] for k in NAMES], x["cu"], initial_state=x["init"], dt_limit=x["limit"],
+                            output_final_state=True, **kw)
+
+
+def backward(x):
+    return ssm_scan_backward(*[x[k] for k in NAMES], x["dy"], x["cu"], initial_state=x["init"],
+                             d_final_state=x["dfinal"], dt_limit=x["limit"])
+
+
+def reference(x, absolute=False):
+    f = (lambda t: None if t is None else np.abs(to_np(t))) if absolute else (lambda t: None if t is None else to_np(t))
+    args = [f(x[k]) if k in ("x", "B", "C", "D") else (None if x[k] is None else to_np(x[k])) for k in NAMES]
+    return ssm_ref.scan(*args, x["cu_host"], f(x["init"]), limit=x["limit"], dy=f(x["dy"]), dfinal=f(x["dfinal"]))
+
+
+def held(name, got, ref, bound):
+    got, ref = to_np(got), np.asarray(ref)
+    off = np.abs(got - ref) - bound - 2.0 ** -126  # below fp32's normal numbers: may be zero
+    print("%s worst excess %.2e of %.2e, L2 %.2e" % (name, off.max() if off.size else 0, np.max(bound, initial=0), rel(got, ref)), flush=True)
+    assert np.isfinite(got).all() and np.all(off <= 0), name
+
+
+def chunk_sums(t, cu, Q):
+    """Of each token, the sum over its chunk."""
+    out = np.zeros_like(t)
+    for a, b in zip(cu, cu[1:]):
+        for s in range(a, b, Q):
+            e = min(s + Q, b)
+            out[s:e] = t[s:e].sum(0)
+    return out
+
+
+def parity(x):
+    dtype = x["x"].dtype
+    half, Q = HALF_STEP[dtype], 128 if dtype is BF16 else 64
+    one, two = (1e-5, 1e-5) if dtype is F32 else (2.0 ** -8 + 1e-5, 2.0 ** -16 + 1e-5)
+    state = 1e-5 if dtype is F32 else 2.0 ** -16
+    y_ref, s_ref, g = reference(x)
+    y_abs, s_abs, t = reference(x, absolute=True)
+    y, final = forward(x)
+    held("y", y, y_ref, half * np.abs(y_ref) + one * y_abs)
+    held("final", final, s_ref, state * s_abs)
+    dx, ddt, dA, dB, dC, dD, dbias, dinit = backward(x)
+    held("dx", dx, g["dx"], half * np.abs(g["dx"]) + one * t["dx"])
+    held("dB", dB, g["dB"], half * np.abs(g["dB"]) + one * t["dB"])
+    held("dC", dC, g["dC"], half * np.abs(g["dC"]) + one * t["dC"])
+    # a token's decay collects its chunk's terms, weighted with its own slope; A_log's with its step
+    dt, slope = ssm_ref.step_sizes(to_np(x["raw_dt"]), None if x["dt_bias"] is None else to_np(x["dt_bias"]), x["limit"])
+    terms = chunk_sums(t["tall"], x["cu_host"], Q) * slope
+    held("draw_dt", ddt, g["draw_dt"], half * np.abs(g["draw_dt"]) + two * terms)
+    held("dA_log", dA, g["dA_log"], two * np.sum(dt * chunk_sums(t["tall"], x["cu_host"], Q), 0))
+    if x["D"] is not None:
+        held("dD", dD, g["dD"], 1e-5 * t["dD"])
+    if x["dt_bias"] is not None:
+        held("ddt_bias", dbias, g["ddt_bias"], two * terms.sum(0))
+    assert (dD is None) == (x["D"] is None) and (dbias is None) == (x["dt_bias"] is None)
+    if x["init"] is not None:
+        held("dinit", dinit, g["dinit"], state * t["dinit"])
+    else:
+        assert dinit is None
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,P", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("lens,H,G", [([1], 1, 1), ([37], 4, 2), ([130, 0, 1, 64, 65], 2, 1)])
+def test_scan(dtype, N, P, lens, H, G):
+    announce("scan %s N%d P%d %s H%d G%d" % (dtype, N, P, lens, H, G))
+    parity(make(lens, H, G, N, P, dtype, 1))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lens,H,G", [([300], 3, 1), ([63, 127, 128, 129, 0, 2], 6, 3), ([1] * 20, 5, 5), ([257, 64], 8, 1)])
+def test_scan_lengths_and_groups(dtype, lens, H, G):
+    announce("scan lengths %s %s H%d G%d" % (dtype, lens, H, G))
+    parity(make(lens, H, G, 64, 64, dtype, 2))
+    parity(make(lens, H, G, 64, 64, dtype, 3, init=False))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scan_limits_and_missing_parameters(dtype):
+    announce("scan with limits, without D and bias %s" % dtype)
+    parity(make([70, 5], 4, 2, 64, 64, dtype, 4, limit=(0.05, 0.11)))
+    parity(make([70, 5], 4, 2, 64, 64, dtype, 5, D=None))
+    parity(make([70, 5], 4, 2, 64, 64, dtype, 6, dt_bias=None))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scan_of_large_and_vanishing_steps(dtype):
+    announce("scan with steps from 1e-30 to 90 %s" % dtype)
+    x = make([150], 4, 1, 64, 64, dtype, 7)
+    x["dt_bias"].zero_()
+    x["raw_dt"][:, 0], x["raw_dt"][:, 1] = -70.0, 90.0  # nothing written; only the own token seen
+    x["raw_dt"][::9, 2], x["raw_dt"][4::9, 3] = 60.0, -60.0
+    parity(x)
+
+
+def make_single(dtype):
+    x = make([200], 2, 1, 64, 64, dtype, 8)
+    return x, dict(x, cu=None)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scan_without_cu_seqlens_and_of_slices(dtype):
+    announce("scan without cu_seqlens; of slices of wider rows %s" % dtype)
+    x, y = make_single(dtype)
+    for a, b in zip((*forward(x), *backward(x)), (*forward(y), *backward(y))):
+        assert torch.equal(a, b)
+    x, y = (make([33, 140], 4, 2, 128, 64, dtype, 9, fused=f) for f in (False, True))
+    assert not y["x"].is_contiguous()
+    wide = torch.full((173, 12), float("nan"), dtype=dtype, device="cuda")
+    wide[:, 3:7] = y["raw_dt"]
+    y["raw_dt"] = wide[:, 3:7]
+    for a, b in zip((*forward(x), *backward(x)), (*forward(y), *backward(y))):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,G", [(2, 2), (6, 1)])
+def test_rows_of_no_sequence(dtype, H, G):
+    announce("scan: rows of no sequence, clamped cu_seqlens %s" % dtype)
+    x = make([3, 140, 0, 60, 7], H, G, 64, 64, dtype, 10)  # the first and the last tokens in no sequence
+    cu = [3, 143, 143, 203]
+    x.update(cu=torch.tensor(cu, dtype=torch.int32, device="cuda"), cu_host=cu, init=x["init"][:3].contiguous(),
+             dfinal=x["dfinal"][:3].contiguous())
+    for name in ("x", "raw_dt", "B", "C", "dy"):
+        x[name][:3] = x[name][203:] = float("nan")
+    leave_nan(x["x"].shape, dtype)
+    y, final = forward(x)
+    got = backward(x)
+    for t in (y, got[0], got[1], got[3], got[4]):
+        assert bool((t[:3] == 0).all()) and bool((t[203:] == 0).all())
+    part = dict(x, **{k: x[k][3:203].contiguous() for k in ("x", "raw_dt", "B", "C", "dy")}, cu=x["cu"] - 3)
+    want = (*forward(part), *backward(part))
+    for i, (a, b) in enumerate(zip((y, final, *got), want)):
+        assert torch.equal(a[3:203] if a.shape[0] == 210 else a, b), i
+    none = dict(x, cu=torch.zeros(1, dtype=torch.int32, device="cuda"), init=None, dfinal=None)
+    leave_nan(x["x"].shape, dtype)
+    y, final = forward(none)
+    got = backward(none)
+    assert final.shape[0] == 0
+    for t in (y, *got[:7]):
+        assert bool((t == 0).all())
+    far = dict(part, cu=torch.tensor([-7, 140, 140, 100000], dtype=torch.int32, device="cuda"))
+    for a, b in zip((*forward(far), *backward(far)), want):
+        assert torch.equal(a, b)
+
+
+def test_no_tokens():
+    announce("scan of no tokens")
+    x = make([0, 0], 2, 1, 64, 64, BF16, 11)
+    y, final = forward(x)
+    assert y.shape == (0, 2, 64) and torch.equal(final, x["init"])
+    got = backward(x)
+    assert torch.equal(got[-1], x["dfinal"])
+    assert all(bool((got[i] == 0).all()) for i in (2, 5, 6)) and got[0].shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_autograd_repeats_and_partial_gradients(dtype):
+    announce("scan autograd %s" % dtype)
+    x = make([40, 100], 4, 2, 64, 64, dtype, 12)
+    want = backward(x)
+    leaves = [x[k].detach().requires_grad_(True) for k in (*NAMES, "init")]
+    y, final = ssm_scan(*leaves[:7], x["cu"], initial_state=leaves[7], output_final_state=True)
+    wide = x["dy"].transpose(0, 1).contiguous().transpose(0, 1)  # not contiguous
+    got = torch.autograd.grad((y, final), leaves, (wide, x["dfinal"]))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    y, final = ssm_scan(*leaves[:7], x["cu"], initial_state=leaves[7], output_final_state=True)
+    only = torch.autograd.grad(final, leaves, x["dfinal"], allow_unused=True)
+    ref = backward(dict(x, dy=torch.zeros_like(x["dy"])))
+    for a, b in zip(only, ref):
+        assert torch.equal(a, b)
+    y = ssm_scan(leaves[0], x["raw_dt"], x["A_log"], x["B"], x["C"], None, None, x["cu"])
+    g, = torch.autograd.grad(y, leaves[0], x["dy"])
+    assert torch.equal(g, backward(dict(x, D=None, dt_bias=None, init=None, dfinal=None))[0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_pieces_of_a_sequence_and_decoding_continue_it(dtype):
+    announce("scan in pieces, then token by token %s" % dtype)
+    x = make([300, 41], 4, 2, 128, 64, dtype, 13)
+    y, final = forward(x)
+    # rounding points move with the pieces' chunks: each is held to the reference
+    y_ref, s_ref, _ = reference(x)
+    y_abs, s_abs, _ = reference(x, absolute=True)
+    one, state = (1e-5, 1e-5) if dtype is F32 else (2.0 ** -8 + 1e-5, 2.0 ** -16 + 1e-5)
+    lens, at, pool, rows = [300, 41], [0, 300], x["init"], []
+    got = np.zeros_like(y_ref)
+    for cut in ([100, 20], [97, 19]):
+        r = torch.cat([torch.arange(a, a + m) for a, m in zip(at, cut)]).cuda()
+        part = dict(x, **{k: x[k][r].contiguous() for k in ("x", "raw_dt", "B", "C")}, init=pool,
+                    cu=torch.tensor([0, cut[0], sum(cut)], dtype=torch.int32, device="cuda"))
+        yp, pool = forward(part)
+        got[r.cpu().numpy()] = to_np(yp)
+        at = [a + m for a, m in zip(at, cut)]
+        rows.append(r)
+    r = torch.cat([torch.arange(at[0], 300), torch.arange(at[1], 341)]).cuda()
+    cu = torch.tensor([0, 300 - at[0], len(r)], dtype=torch.int32, device="cuda")
+    yp = ssm_recurrent(*[x[k][r].contiguous() if k in ("x", "raw_dt", "B", "C") else x[k] for k in NAMES], pool, cu)
+    got[r.cpu().numpy()] = to_np(yp)
+    off = np.abs(got - y_ref) - HALF_STEP[dtype] * np.abs(y_ref) - one * y_abs
+    assert np.all(off <= 0)
+    assert np.all(np.abs(to_np(pool) - s_ref) <= 2 * state * s_abs)
+
+
+def test_streams_and_graph_replay():
+    announce("scan on two streams; captured with other lengths and replayed")
+    xs = [make([150, 30, 80], 4, 2, 128, 64, BF16, s) for s in (14, 15)]
+    want = [(*forward(x), *backward(x)) for x in xs]
+    torch.cuda.synchronize()
+    got = []
+    for x in xs:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got.append((*forward(x), *backward(x)))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
+    x = xs[0]
+    graphs, outs = [], []
+    for _ in range(2):  # two graphs of the same call: each has its own workspace
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((*forward(x), *backward(x)))
+        graphs.append(g)
+    for cu in ([0, 150, 180, 260], [0, 10, 20, 30], [5, 5, 5, 260], [0, 0, 129, 258]):
+        x["cu"].copy_(torch.tensor(cu, dtype=torch.int32))
+        x["x"].mul_(0.5)
+        ref = (*forward(x), *backward(x))
+        for g, out in zip(graphs, outs):
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(s, t) for s, t in zip(out, ref))
+
+
+def test_a_layer_in_training_and_decoding():
+    announce("convolution, scan and norm together")
+    H, G, N, P, lens = 8, 2, 64, 64, [90, 1, 150]
+    T, C, inner = sum(lens), H * P + 2 * G * N, H * P
+    gen = torch.Generator(device="cuda").manual_seed(16)
+
+    def randn(*shape, scale=1.0):
+        return torch.randn(shape, generator=gen, device="cuda") * scale
+
+    cu = torch.tensor([0, 90, 91, 241], dtype=torch.int32, device="cuda")
+    wide = randn(T, inner + C + 8)
+    par = dict(cw=randn(C, 4, scale=0.4), cb=randn(C, scale=0.2), A=torch.rand(H, generator=gen, device="cuda"),
+               D=randn(H), tb=randn(H) - 2.5, w=1 + randn(inner, scale=0.2))
+
+    def layer(wide, par, cu=None, pools=None):
+        gate, xbc, dt = wide[:, :inner], wide[:, inner:inner + C], wide[:, inner + C:]
+        if pools is None:
+            xbc = short_conv(xbc, par["cw"], par["cb"], cu, output_final_state=cu is not None)
+            xbc, conv_state = xbc
+        else:
+            xbc = short_conv_update(xbc, par["cw"], par["cb"], pools[0])
+        x, B, Cm = xbc.split([inner, G * N, G * N], 1)
+        args = (x.view(-1, H, P), dt, par["A"], B.view(-1, G, N), Cm.view(-1, G, N), par["D"], par["tb"])
+        if pools is None:
+            y, state = ssm_scan(*args, cu, output_final_state=True)
+        else:
+            y = ssm_recurrent(*args, pools[1])
+        y = group_norm(y.reshape(-1, inner), par["w"], None, gate, groups=G, center=False, gate_first=True)
+        return (y, conv_state, state) if pools is None else y
+
+    # training: gradients against differences along random directions
+    leaves = {k: v.clone().requires_grad_(True) for k, v in par.items()}
+    wl = wide.clone().requires_grad_(True)
+    dy = randn(T, inner)
+    y, conv_state, state = layer(wl, leaves, cu)
+    y.backward(dy)
+    with torch.no_grad():
+        for name, t in (("wide", wl), *leaves.items()):
+            d = torch.randn(t.shape, generator=gen, device="cuda")
+            h = 1e-2 * t.norm() / d.norm() / 10
+
+            def at(s):
+                moved = {k: (v + s * h * d if k == name else v) for k, v in par.items()}
+                out = layer(wide + s * h * d if name == "wide" else wide, moved, cu)[0]
+                return (out.double() * dy.double()).sum()
+
+            num = float((8 * (at(1) - at(-1)) - (at(2) - at(-2))) / (12 * h))  # fourth order
+            ana = float((t.grad.double() * d.double()).sum())
+            size = float((t.grad.double() * d.double()).abs().sum())
+            print("layer d%s %.5e by differences %.5e" % (name, ana, num), flush=True)
+            # differences: fp32 outputs' roundings over the step (4e-6 of the loss's terms / h) and h^4
+            loss = float((y.detach().double() * dy.double()).norm())
+            assert abs(num - ana) <= 1e-3 * max(abs(ana), size / 30) + 4e-6 * loss / float(h)
+        # decoding continues the sequences
+        more = randn(3, 4, wide.shape[1])
+        pools = (conv_state, state)
+        full = torch.cat([torch.cat([wide[a:b], more[i]]) for i, (a, b) in enumerate(zip([0, 90, 91], [90, 91, 241]))])
+        want = layer(full, par, torch.tensor([0, 94, 99, 253], dtype=torch.int32, device="cuda"))
+        for j in range(4):
+            got = layer(more[:, j].contiguous(), par, pools=pools)
+            assert rel(to_np(got), to_np(want[0][[90 + j, 95 + j, 249 + j]])) <= 1e-5
+        assert rel(to_np(pools[1]), to_np(want[2])) <= 1e-5
+        assert rel(to_np(pools[0]), to_np(want[1])) <= 1e-6
