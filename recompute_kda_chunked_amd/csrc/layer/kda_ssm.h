@@ -46,6 +46,7 @@ struct SsmArgs {
   void *S, *S_lo, *dS, *dS_lo;
   float *pB, *pC;  // partial dB and dC [sets][T][G][N] where sets > 1
   float *part2, *part1;  // per slot {dA, ddt_bias} [2 H] and dD [H]
+  float* ddt_half;       // P = 128: draw_dt of a head's first half [slots][H][Q]
   int hb, sets;    // heads of a group a block takes in turn, blocks a group
 };
 hipError_t launch_ssm_steps(int dtype, const SsmArgs& a, hipStream_t s);

@@ -30,7 +30,7 @@ int check_ssm(const kda_ssm_problem* p) {
 struct ScanPlan {
   int Q, fwd_hb, fwd_sets, bwd_hb, bwd_sets;
   int64_t slots;
-  size_t steps, state, partial, part2, part1;
+  size_t steps, state, partial, part2, part1, ddt_half;
   explicit ScanPlan(const kda_ssm_problem* p) {
     Q = ssm_chunk(p->dtype);
     slots = p->total_tokens / Q + p->n_seqs;
@@ -51,10 +51,11 @@ struct ScanPlan {
     partial = bwd_sets > 1 ? part(p->total_tokens * p->G * p->N * bwd_sets, 4) : 0;
     part2 = part(slots * p->H * 2, 4);
     part1 = part(slots * p->H, 4);
+    ddt_half = p->P > 64 ? part(slots * p->H * Q, 4) : 0;
   }
   size_t fwd() const { return steps + state; }
   size_t bwd(int dtype) const {
-    return steps + (dtype == KDA_F32 ? 2 : 4) * state + 2 * partial + part2 + part1;
+    return steps + (dtype == KDA_F32 ? 2 : 4) * state + 2 * partial + part2 + part1 + ddt_half;
   }
 };
 
@@ -218,6 +219,7 @@ int kda_ssm_bwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, con
   a.pC = reinterpret_cast<float*>(w + plan.partial);
   a.part2 = reinterpret_cast<float*>(w + 2 * plan.partial);
   a.part1 = reinterpret_cast<float*>(w + 2 * plan.partial + plan.part2);
+  a.ddt_half = reinterpret_cast<float*>(w + 2 * plan.partial + plan.part2 + plan.part1);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t units = a.T * a.H;
   if (a.T > 0 && a.n_seqs > 0) {

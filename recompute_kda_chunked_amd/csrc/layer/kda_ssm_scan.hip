@@ -42,6 +42,17 @@ struct Chunk {
   static constexpr int Q = sizeof(TI) == 4 ? 64 : 128;
 };
 
+// A value that the compiler takes for a new one each time: what is computed
+// from a lane's number is cheap, but kept in registers over a loop (some hundred
+// addresses) it would spill the accumulators.
+__device__ __forceinline__ int once(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// The wave's number in its block, known to be the same for its lanes.
+__device__ __forceinline__ int wave_number() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 __device__ __forceinline__ int64_t clamp_cu(const SsmArgs& a, int n) {
   if (!a.cu) return n == 0 ? 0 : a.T;
   const int64_t c = a.cu[n];
@@ -134,7 +145,7 @@ __global__ void __launch_bounds__(256) k_ssm_state(SsmArgs a) {
   const int n = blockIdx.x / per_seq, rest = blockIdx.x % per_seq;
   const int n0 = (rest % nsplit) * NB, hp = rest / nsplit, h = hp / halves, half = hp % halves;
   const int grp = h / (a.H / a.G);
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), i = lane & 15, g = lane >> 4;
   const int64_t s0 = clamp_cu(a, n), s1 = clamp_cu(a, n + 1), len = s1 > s0 ? s1 - s0 : 0;
   const int64_t nch = (len + Q - 1) / Q, first = s0 / Q + n;
   const TI* src = static_cast<const TI*>(REV ? a.dy : a.x) + static_cast<size_t>(h) * a.P + half * 64;
@@ -145,6 +156,8 @@ __global__ void __launch_bounds__(256) k_ssm_state(SsmArgs a) {
   float* to = REV ? a.dinit : a.final_state;
   const size_t state = ((static_cast<size_t>(n) * a.H + h) * N + n0 + i) * a.P + half * 64 + 16 * w + 4 * g;
 
+  const LaneAt<TI, 64> lx(lane);
+  const LaneAt<TI, NB> lb(lane);
   f32x4 acc[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t)
@@ -219,11 +232,11 @@ __global__ void __launch_bounds__(256) k_ssm_state(SsmArgs a) {
     }
 #pragma unroll
     for (int k0 = 0; k0 < Q; k0 += 32) {
-      const Frag<TI> ax = frag_col<64, false>(xs, k0, 16 * w, lane);
+      const Frag<TI> ax = frag_col<false>(xs, lx, k0, 16 * w);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        acc[t] = mma32(ax, frag_col<NB, false>(bh, k0, 16 * t, lane), acc[t]);
-        if constexpr (kPair) acc[t] = mma32(ax, frag_col<NB, false>(bl, k0, 16 * t, lane), acc[t]);
+        acc[t] = mma32(ax, frag_col<false>(bh, lb, k0, 16 * t), acc[t]);
+        if constexpr (kPair) acc[t] = mma32(ax, frag_col<false>(bl, lb, k0, 16 * t), acc[t]);
       }
     }
   }
@@ -247,16 +260,17 @@ __device__ __forceinline__ int own_tile(int w) {
 template <typename TI, int R, int COLS, int THREADS>
 __device__ __forceinline__ void load_tile(TI* tile, const TI* src, int64_t st, int rows) {
   constexpr int U = 16 / sizeof(TI), PER = R * COLS / U / THREADS;
+  const int tid = once(threadIdx.x);
   uint4 v[PER];
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
-    const int u = threadIdx.x + THREADS * m, r = u / (COLS / U);
+    const int u = tid + THREADS * m, r = u / (COLS / U);
     v[m] = make_uint4(0, 0, 0, 0);
     if (r < rows) v[m] = *reinterpret_cast<const uint4*>(src + r * st + (u % (COLS / U)) * U);
   }
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
-    const int u = threadIdx.x + THREADS * m;
+    const int u = tid + THREADS * m;
     *reinterpret_cast<uint4*>(tile + tile_at<TI, COLS>(u / (COLS / U), (u % (COLS / U)) * U)) = v[m];
   }
 }
@@ -288,24 +302,26 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_out(SsmArgs a) {
   const int64_t slot = blockIdx.x / (a.sets * a.G);
   const Place c = find_chunk<Q>(a, slot);
   if (c.rows <= 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), i = lane & 15, g = lane >> 4;
   const int it = own_tile<NW>(w), per = a.H / a.G, halves = a.P / 64;
   const int h0 = grp * per + set * a.hb, h1 = set * a.hb + a.hb < per ? h0 + a.hb : (grp + 1) * per;
 
+  const LaneAt<TI, N> ln(lane);
+  const LaneAt<TI, 64> lx(lane);
   TI *Bt = buf, *Ct = buf + Q * N;
   load_tile<TI, Q, N, TH>(Bt, static_cast<const TI*>(a.B) + c.t0 * a.Bs + static_cast<size_t>(grp) * N, a.Bs, c.rows);
   load_tile<TI, Q, N, TH>(Ct, static_cast<const TI*>(a.C) + c.t0 * a.Cs + static_cast<size_t>(grp) * N, a.Cs, c.rows);
   __syncthreads();
   Frag<TI> cf[N / 32];
 #pragma unroll
-  for (int k = 0; k < N / 32; ++k) cf[k] = frag_row<N>(Ct, 16 * it, 32 * k, lane);
+  for (int k = 0; k < N / 32; ++k) cf[k] = frag_row(Ct, ln, 16 * it, 32 * k);
   f32x4 G[NW];
 #pragma unroll
   for (int jt = 0; jt < NW; ++jt) {
     G[jt] = zero4();
     if (jt <= it) {
 #pragma unroll
-      for (int k = 0; k < N / 32; ++k) G[jt] = mma32(frag_row<N>(Bt, 16 * jt, 32 * k, lane), cf[k], G[jt]);
+      for (int k = 0; k < N / 32; ++k) G[jt] = mma32(frag_row(Bt, ln, 16 * jt, 32 * k), cf[k], G[jt]);
     }
   }
   TI *xs = buf, *Ss = buf + Q * 64;
@@ -328,7 +344,7 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_out(SsmArgs a) {
       for (int p = 0; p < 4; ++p) {
         y[p] = zero4();
 #pragma unroll
-        for (int k = 0; k < N / 32; ++k) y[p] = mma32(frag_col<64, false>(Ss, 32 * k, 16 * p, lane), cf[k], y[p]);
+        for (int k = 0; k < N / 32; ++k) y[p] = mma32(frag_col<false>(Ss, lx, 32 * k, 16 * p), cf[k], y[p]);
         y[p] *= ei;
       }
 #pragma unroll
@@ -346,13 +362,13 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_out(SsmArgs a) {
         }
         const Frag<TI> wf = pair_frag<TI>(W[0], W[1]);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) y[p] = mma32(frag_col<64, true>(xs, 32 * m, 16 * p, lane), wf, y[p]);
+        for (int p = 0; p < 4; ++p) y[p] = mma32(frag_col<true>(xs, lx, 32 * m, 16 * p), wf, y[p]);
       }
       const int row = 16 * it + i;
       if (row < c.rows) {
         TI* out = static_cast<TI*>(a.y) + ((c.t0 + row) * a.H + h) * a.P + half * 64 + 4 * g;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) store4<TI>(out + 16 * p, y[p] + D * tile_get4<TI, 64>(xs, row, 16 * p + 4 * g));
+        for (int p = 0; p < 4; ++p) store4<TI>(out + 16 * p, y[p] + D * tile_get4(xs, lx, 16 * it, 16 * p));
       }
     }
   }
@@ -405,7 +421,7 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   const int set = blockIdx.x % a.sets, grp = (blockIdx.x / a.sets) % a.G;
   const int64_t slot = blockIdx.x / (a.sets * a.G);
   const Place c = find_chunk<Q>(a, slot);
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, i = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), i = lane & 15, g = lane >> 4;
   const int jt = own_tile<NW>(w), per = a.H / a.G, halves = a.P / 64;
   const int h0 = grp * per + set * a.hb, h1 = set * a.hb + a.hb < per ? h0 + a.hb : (grp + 1) * per;
   if (c.rows <= 0) {  // its partial sums are added up all the same
@@ -420,15 +436,16 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   __syncthreads();
   // of the first role: rows of B, and C B^T
   Frag<TI> bf[N / 32];
-#pragma unroll
-  for (int k = 0; k < N / 32; ++k) bf[k] = frag_row<N>(Bt, 16 * jt, 32 * k, lane);
   f32x4 G[NW];
+  const LaneAt<TI, N> ln(lane);
+#pragma unroll
+  for (int k = 0; k < N / 32; ++k) bf[k] = frag_row(Bt, ln, 16 * jt, 32 * k);
 #pragma unroll
   for (int t = 0; t < NW; ++t) {
     G[t] = zero4();
     if (t >= jt) {
 #pragma unroll
-      for (int k = 0; k < N / 32; ++k) G[t] = mma32(frag_row<N>(Ct, 16 * t, 32 * k, lane), bf[k], G[t]);
+      for (int k = 0; k < N / 32; ++k) G[t] = mma32(frag_row(Ct, ln, 16 * t, 32 * k), bf[k], G[t]);
     }
   }
   // of the second: tokens t0 16 .., rows n0 .. of B^T and C^T
@@ -439,7 +456,6 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
 #pragma unroll
     for (int t = 0; t < TT; ++t) dC[u][t] = dB[u][t] = zero4();
 
-  float fa[2], fb[2], fc[2], fdl = 0.f, fxd = 0.f;  // wave 0: a head's sums over its halves
   int par = 0;
   for (int h = h0; h < h1; ++h) {
     const float D = a.D ? a.D[h] : 0.f;
@@ -455,6 +471,10 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
         clo[par][tid] = k[2];
       }
       __syncthreads();
+      const int fresh = once(lane);
+      const LaneAt<TI, N> ln(fresh);
+      const LaneAt<TI, 64> lx(fresh);
+      const LaneAt<TI, Q> lq(fresh);
       const float *hiv = chi[par], *lov = clo[par], *dtv = cdt[par];
       const float hQ = hiv[Q - 1], lQ = lov[Q - 1];
 
@@ -463,13 +483,13 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
         const float hj = hiv[row], lj = lov[row], dtj = dtv[row], rj = exp2_((hQ - hj) + (lQ - lj));
         Frag<TI> xf[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) xf[k] = frag_row<64>(xs, 16 * jt, 32 * k, lane);
+        for (int k = 0; k < 2; ++k) xf[k] = frag_row(xs, lx, 16 * jt, 32 * k);
         f32x4 dx[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           dx[p] = zero4();
 #pragma unroll
-          for (int k = 0; k < N / 32; ++k) dx[p] = mma32(frag_col<64, false>(Gs, 32 * k, 16 * p, lane), bf[k], dx[p]);
+          for (int k = 0; k < N / 32; ++k) dx[p] = mma32(frag_col<false>(Gs, lx, 32 * k, 16 * p), bf[k], dx[p]);
           dx[p] *= rj;
         }
         float cf = 0.f, diag = 0.f;
@@ -485,7 +505,7 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
             if (t >= jt) {
               f32x4 e = zero4(), f;
 #pragma unroll
-              for (int k = 0; k < 2; ++k) e = mma32(frag_row<64>(dys, 16 * t, 32 * k, lane), xf[k], e);
+              for (int k = 0; k < 2; ++k) e = mma32(frag_row(dys, lx, 16 * t, 32 * k), xf[k], e);
               const f32x4 h4 = *reinterpret_cast<const f32x4*>(hiv + i0), l4 = *reinterpret_cast<const f32x4*>(lov + i0);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
@@ -501,11 +521,12 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
               const float s = transpose_sum16<4>(v);  // lane i: of f[i % 4]
               if (i < 4) rowF[w][i0 + i] = s;
             }
-            store4<TI>(MT + tile_at<TI, Q>(row, i0), M);
+            store4<TI>(MT + shifted<LaneAt<TI, Q>>(lq.four, 16 * t) + 16 * jt * Q, M);
           }
           const Frag<TI> wf = pair_frag<TI>(W[0], W[1]);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) dx[p] = mma32(frag_col<64, true>(dys, 32 * m, 16 * p, lane), wf, dx[p]);
+          for (int p = 0; p < 4; ++p) dx[p] = mma32(frag_col<true>(dys, lx, 32 * m, 16 * p), wf, dx[p]);
+          __builtin_amdgcn_sched_barrier(0);
         }
         cf = sum_lane_groups(cf);
         if (g == 0) colF[row] = cf;
@@ -514,147 +535,143 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
         if (row < c.rows) {
           TI* out = static_cast<TI*>(a.dx) + ((c.t0 + row) * a.H + h) * a.P + half * 64 + 4 * g;
 #pragma unroll
-          for (int p = 0; p < 4; ++p) store4<TI>(out + 16 * p, dtj * dx[p] + D * tile_get4<TI, 64>(dys, row, 16 * p + 4 * g));
+          for (int p = 0; p < 4; ++p) store4<TI>(out + 16 * p, dtj * dx[p] + D * tile_get4(dys, lx, 16 * jt, 16 * p));
         }
       }
       __syncthreads();
 
       {  // second role
-        float ic[TT], ib[TT], dot = 0.f;
+        float dot = 0.f;
+        Frag<TI> sf[NT][2], sl[NT][2], gf[NT][2], gl[NT][2];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) ic[t] = ib[t] = 0.f;
-#pragma unroll
-        for (int u = 0; u < NT; ++u) {
-          const int nr = n0 + 16 * u;
-          Frag<TI> sf[2], sl[2], gf[2], gl[2];
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            sf[k] = frag_mem(static_cast<const TI*>(a.S) + sat, nr, 32 * k, 64, lane);
-            gf[k] = frag_mem(static_cast<const TI*>(a.dS) + sat, nr, 32 * k, 64, lane);
+            const int nr = n0 + 16 * u;
+            sf[u][k] = frag_mem(static_cast<const TI*>(a.S) + sat, nr, 32 * k, 64, fresh);
+            gf[u][k] = frag_mem(static_cast<const TI*>(a.dS) + sat, nr, 32 * k, 64, fresh);
             if constexpr (kPair) {
-              sl[k] = frag_mem(static_cast<const TI*>(a.S_lo) + sat, nr, 32 * k, 64, lane);
-              gl[k] = frag_mem(static_cast<const TI*>(a.dS_lo) + sat, nr, 32 * k, 64, lane);
+              sl[u][k] = frag_mem(static_cast<const TI*>(a.S_lo) + sat, nr, 32 * k, 64, fresh);
+              gl[u][k] = frag_mem(static_cast<const TI*>(a.dS_lo) + sat, nr, 32 * k, 64, fresh);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              if constexpr (kPair) dot += (to_f(sf[k][e]) + to_f(sl[k][e])) * (to_f(gf[k][e]) + to_f(gl[k][e]));
-              else dot += sf[k][e] * gf[k][e];
+              if constexpr (kPair) dot += (to_f(sf[u][k][e]) + to_f(sl[u][k][e])) * (to_f(gf[u][k][e]) + to_f(gl[u][k][e]));
+              else dot += sf[u][k][e] * gf[u][k][e];
             }
           }
 #pragma unroll
-          for (int t = 0; t < TT; ++t) {
-            const int tt = tt0 + t, row = 16 * tt + i;
-            const float ei = exp2_(hiv[row] + lov[row]), rj = exp2_((hQ - hiv[row]) + (lQ - lov[row]));
+        for (int t = 0; t < TT; ++t) {
+          const int tt = tt0 + t, row = 16 * tt + i;
+          const float ei = exp2_(hiv[row] + lov[row]), rj = exp2_((hQ - hiv[row]) + (lQ - lov[row])), dtj = dtv[row];
+          float ic = 0.f, ib = 0.f;
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            const int nr = n0 + 16 * u;
             f32x4 z = zero4(), v = zero4();
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const Frag<TI> yf = frag_row<64>(dys, 16 * tt, 32 * k, lane), xf = frag_row<64>(xs, 16 * tt, 32 * k, lane);
-              z = mma32(sf[k], yf, z);
-              v = mma32(gf[k], xf, v);
+              const Frag<TI> yf = frag_row(dys, lx, 16 * tt, 32 * k), xf = frag_row(xs, lx, 16 * tt, 32 * k);
+              z = mma32(sf[u][k], yf, z);
+              v = mma32(gf[u][k], xf, v);
               if constexpr (kPair) {
-                z = mma32(sl[k], yf, z);
-                v = mma32(gl[k], xf, v);
+                z = mma32(sl[u][k], yf, z);
+                v = mma32(gl[u][k], xf, v);
               }
             }
             z *= ei;
             v *= rj;
-            const f32x4 c4 = tile_get4<TI, N>(Ct, row, nr + 4 * g), b4 = tile_get4<TI, N>(Bt, row, nr + 4 * g);
+            const f32x4 c4 = tile_get4(Ct, ln, 16 * tt, nr), b4 = tile_get4(Bt, ln, 16 * tt, nr);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              ic[t] += c4[r] * z[r];
-              ib[t] += b4[r] * v[r];
+              ic += c4[r] * z[r];
+              ib += b4[r] * v[r];
             }
             dC[u][t] += z;
-            dB[u][t] += dtv[row] * v;
+            dB[u][t] += dtj * v;
 #pragma unroll
             for (int m = 0; m < NW / 2; ++m) {
-              if (2 * m <= tt) dC[u][t] = mma32(frag_col<N, false>(Bt, 32 * m, nr, lane), frag_col<Q, false>(MT, 32 * m, 16 * tt, lane), dC[u][t]);
-              if (2 * m + 1 >= tt) dB[u][t] = mma32(frag_col<N, false>(Ct, 32 * m, nr, lane), frag_row<Q>(MT, 16 * tt, 32 * m, lane), dB[u][t]);
+              if (2 * m <= tt) dC[u][t] = mma32(frag_col<false>(Bt, ln, 32 * m, nr), frag_col<false>(MT, lq, 32 * m, 16 * tt), dC[u][t]);
+              if (2 * m + 1 >= tt) dB[u][t] = mma32(frag_col<false>(Ct, ln, 32 * m, nr), frag_row(MT, lq, 16 * tt, 32 * m), dB[u][t]);
             }
           }
-        }
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const float s = sum_lane_groups(ic[t]), q = sum_lane_groups(ib[t]);
+          ic = sum_lane_groups(ic);
+          ib = sum_lane_groups(ib);
           if (g == 0) {
-            iC[ng][16 * (tt0 + t) + i] = s;
-            iB[ng][16 * (tt0 + t) + i] = q;
+            iC[ng][row] = ic;
+            iB[ng][row] = ib;
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
         dot = sum_wave(dot);
         if (lane == 0) sd[w] = tt0 == 0 ? dot : 0.f;  // waves of the same rows have the same
       }
       __syncthreads();
 
-      if (w == 0) {  // the scalars of the head
+      if (w == 0) {  // the scalars of the head, R tokens a lane
         constexpr int R = Q / 64;
-        float dots = 0.f, diag = 0.f;
+        const int t0 = R * once(lane);
+        float dots = 0.f, diag = 0.f, own[R], col[R], before[R], direct[R];
 #pragma unroll
+        for (int r = 0; r < R; ++r) own[r] = before[r] = 0.f;
+#pragma unroll 1
         for (int k = 0; k < NW; ++k) {
           dots += sd[k];
           diag += xd[k];
+          if (t0 / 16 >= own_tile<NW>(k))
+#pragma unroll
+            for (int r = 0; r < R; ++r) own[r] += rowF[k][t0 + r];
         }
-        float A[2] = {0.f, 0.f}, Bp[2] = {0.f, 0.f}, dir[2] = {0.f, 0.f};
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int t = R * lane + r;
-          float rf = 0.f, cc = 0.f, cb = 0.f;
-#pragma unroll
-          for (int k = 0; k < NW; ++k)
-            if (t / 16 >= own_tile<NW>(k)) rf += rowF[k][t];
-#pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            cc += iC[k][t];
-            cb += iB[k][t];
-          }
-          A[r] = rf - dtv[t] * colF[t] + cc;
-          Bp[r] = dtv[t] * cb;
-          dir[r] = colF[t] + cb;
-        }
-        if (half == 0) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) fa[r] = fb[r] = fc[r] = 0.f;
-          fdl = fxd = 0.f;
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          fa[r] += A[r];
-          fb[r] += Bp[r];
-          fc[r] += dir[r];
-        }
-        fdl += exp2_(hQ + lQ) * dots;
-        fxd += diag;
-        if (half == halves - 1) {
-          // sums of fa from the token on, of fb before it
-          float sa = fa[0] + (R > 1 ? fa[1] : 0.f), sb = fb[0] + (R > 1 ? fb[1] : 0.f);
-          const float la = sa, lb = sb;
-#pragma unroll
-          for (int o = 1; o < 64; o *= 2) {
-            const float da = __shfl_down(sa, o, 64), ub = __shfl_up(sb, o, 64);
-            if (lane + o < 64) sa += da;
-            if (lane >= o) sb += ub;
-          }
-          sa -= la;
-          sb -= lb;
-          const float Ah = expf(a.A_log[h]);
-          const f32x4* st = reinterpret_cast<const f32x4*>(a.steps) + (slot * a.H + h) * Q;
-          float dA = 0.f, db = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < NG; ++k)
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const int t = R * lane + r;
-            const float dl = sa + fa[r] + (r == 0 && R > 1 ? fa[1] : 0.f) + sb + (r > 0 ? fb[0] : 0.f) + fdl;
-            const float d = (fc[r] - Ah * dl) * st[t][3];
-            dA -= Ah * dtv[t] * dl;
-            db += d;
-            if (t < c.rows) static_cast<TI*>(a.ddt)[(c.t0 + t) * a.H + h] = from_f<TI>(d);
+            own[r] += iC[k][t0 + r];
+            before[r] += iB[k][t0 + r];
           }
-          dA = sum_wave(dA);
-          db = sum_wave(db);
-          if (lane == 0) {
-            a.part2[slot * 2 * a.H + h] = dA;
-            a.part2[slot * 2 * a.H + a.H + h] = db;
-            a.part1[slot * a.H + h] = fxd;
+        // dl_t: own over the tokens from t on, before over those before it
+        float sa = 0.f, sb = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          col[r] = colF[t0 + r];
+          direct[r] = col[r] + before[r];
+          own[r] -= dtv[t0 + r] * col[r];
+          before[r] *= dtv[t0 + r];
+          sa += own[r];
+          sb += before[r];
+        }
+        const float lb = sb;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+          const float da = __shfl_down(sa, o, 64), ub = __shfl_up(sb, o, 64);
+          if (lane + o < 64) sa += da;
+          if (lane >= o) sb += ub;
+        }
+        sb += exp2_(hQ + lQ) * dots - lb;
+        const float Ah = expf(a.A_log[h]);
+        const size_t at = (slot * a.H + h) * Q + t0;
+        float dA = 0.f, db = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float dl = sa + sb;
+          sa -= own[r];
+          sb += before[r];
+          float d = (direct[r] - Ah * dl) * a.steps[4 * (at + r) + 3];
+          dA -= Ah * dtv[t0 + r] * dl;
+          db += d;
+          if (halves > 1) {  // of two halves of a head the second adds to the first's
+            if (half) d += a.ddt_half[at + r];
+            else a.ddt_half[at + r] = d;
           }
+          if (t0 + r < c.rows && half == halves - 1) static_cast<TI*>(a.ddt)[(c.t0 + t0 + r) * a.H + h] = from_f<TI>(d);
+        }
+        dA = sum_wave(dA);
+        db = sum_wave(db);
+        if (lane == 0) {
+          float *p2 = a.part2 + slot * 2 * a.H + h, *p1 = a.part1 + slot * a.H + h;
+          *p2 = half ? *p2 + dA : dA;
+          p2[a.H] = half ? p2[a.H] + db : db;
+          *p1 = half ? *p1 + diag : diag;
         }
       }
     }

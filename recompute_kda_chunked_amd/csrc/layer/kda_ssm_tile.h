@@ -51,36 +51,64 @@ __device__ __forceinline__ s16x4 tr_read(const bf16* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
 }
 
+// Element offsets within a tile are a lane's part with some of its low bits
+// flipped by the tile's constant ones, plus constants: (row, col) lies at
+// row COLS + col with the bits of 8 units, col's low ones, flipped by row & 7.
+// The lane's parts, for rows and columns that start at multiples of 16:
+template <typename T, int COLS>
+struct LaneAt {
+  static constexpr int U = 16 / sizeof(T), WIN = COLS < 8 * U ? COLS : 8 * U;  // elements the flips stay in
+  int row, col, pair, four;
+  __device__ __forceinline__ explicit LaneAt(int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    row = tile_at<T, COLS>(i, 8 * g);
+    col = sizeof(T) == 2 ? tile_at<T, COLS>(8 * g + (i >> 2), 4 * (i & 3)) : tile_at<T, COLS>(8 * g, i);
+    pair = sizeof(T) == 2 ? tile_at<T, COLS>(4 * g + (i >> 2), 4 * (i & 3)) : tile_at<T, COLS>(4 * g, i);
+    four = tile_at<T, COLS>(i, 4 * g);
+  }
+};
+template <typename L>
+__device__ __forceinline__ int shifted(int at, int col) {
+  return (at ^ (col & (L::WIN - 1))) + (col & ~(L::WIN - 1));
+}
+
 // Rows r0 .. r0 + 15, reduction over columns k0 .. k0 + 31 (plain).
 template <int COLS>
-__device__ __forceinline__ bf16x8 frag_row(const bf16* t, int r0, int k0, int lane) {
-  return *reinterpret_cast<const bf16x8*>(t + tile_at<bf16, COLS>(r0 + (lane & 15), k0 + 8 * (lane >> 4)));
+__device__ __forceinline__ bf16x8 frag_row(const bf16* t, const LaneAt<bf16, COLS>& l, int r0, int k0) {
+  return *reinterpret_cast<const bf16x8*>(t + shifted<LaneAt<bf16, COLS>>(l.row, k0) + r0 * COLS);
 }
 template <int COLS>
-__device__ __forceinline__ f32x8 frag_row(const float* t, int r0, int k0, int lane) {
-  const int r = r0 + (lane & 15), k = k0 + 8 * (lane >> 4);
-  const f32x4 a = *reinterpret_cast<const f32x4*>(t + tile_at<float, COLS>(r, k));
-  const f32x4 b = *reinterpret_cast<const f32x4*>(t + tile_at<float, COLS>(r, k + 4));
+__device__ __forceinline__ f32x8 frag_row(const float* t, const LaneAt<float, COLS>& l, int r0, int k0) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(t + shifted<LaneAt<float, COLS>>(l.row, k0) + r0 * COLS);
+  const f32x4 b = *reinterpret_cast<const f32x4*>(t + shifted<LaneAt<float, COLS>>(l.row, k0 + 4) + r0 * COLS);
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 // Columns c0 .. c0 + 15, reduction over rows k0 .. k0 + 31, plain or paired.
-template <int COLS, bool PAIRED>
-__device__ __forceinline__ bf16x8 frag_col(const bf16* t, int k0, int c0, int lane) {
-  const int i = lane & 15, g = lane >> 4, r = k0 + (PAIRED ? 4 : 8) * g + (i >> 2), c = c0 + 4 * (i & 3);
-  const s16x4 a = tr_read(t + tile_at<bf16, COLS>(r, c)), b = tr_read(t + tile_at<bf16, COLS>(r + (PAIRED ? 16 : 4), c));
+template <bool PAIRED, int COLS>
+__device__ __forceinline__ bf16x8 frag_col(const bf16* t, const LaneAt<bf16, COLS>& l, int k0, int c0) {
+  constexpr int FLIP = PAIRED || COLS < 64 ? 0 : 32;  // four rows on: row & 7 differs in its bit 2
+  const int at = shifted<LaneAt<bf16, COLS>>(PAIRED ? l.pair : l.col, c0) + k0 * COLS;
+  const int on = shifted<LaneAt<bf16, COLS>>((PAIRED ? l.pair : l.col) ^ FLIP, c0) + (k0 + (PAIRED ? 16 : 4)) * COLS;
+  const s16x4 a = tr_read(t + at), b = tr_read(t + on);
   typedef __attribute__((ext_vector_type(8))) short s16x8;
   return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
 }
-template <int COLS, bool PAIRED>
-__device__ __forceinline__ f32x8 frag_col(const float* t, int k0, int c0, int lane) {
-  const int i = lane & 15, g = lane >> 4;
+template <bool PAIRED, int COLS>
+__device__ __forceinline__ f32x8 frag_col(const float* t, const LaneAt<float, COLS>& l, int k0, int c0) {
   f32x8 f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int k = PAIRED ? (e < 4 ? 4 * g + e : 12 + 4 * g + e) : 8 * g + e;
-    f[e] = t[tile_at<float, COLS>(k0 + k, c0 + i)];
+    const int r = PAIRED ? (e & 3) + 4 * (e & 4) : e;  // past the lane's own row
+    f[e] = t[shifted<LaneAt<float, COLS>>((PAIRED ? l.pair : l.col) ^ (4 * (r & 7)), c0) + (k0 + r) * COLS];
   }
   return f;
+}
+// Row r0 + i of the lane, columns c0 + 4 g .. + 3.
+template <typename T, int COLS>
+__device__ __forceinline__ f32x4 tile_get4(const T* t, const LaneAt<T, COLS>& l, int r0, int c0) {
+  uint32_t u[4];
+  load4_raw<T>(t + shifted<LaneAt<T, COLS>>(l.four, c0) + r0 * COLS, u);
+  return unpack4<T>(u);
 }
 // The same from a row-major matrix in memory, rows `ld` apart (plain).
 __device__ __forceinline__ bf16x8 frag_mem(const bf16* m, int r0, int k0, int ld, int lane) {
@@ -100,14 +128,6 @@ __device__ __forceinline__ Frag<T> pair_frag(const f32x4& a, const f32x4& b) {
     f[4 + e] = static_cast<T>(b[e]);
   }
   return f;
-}
-
-// Four consecutive elements of a tile as floats.
-template <typename T, int COLS>
-__device__ __forceinline__ f32x4 tile_get4(const T* t, int row, int col) {
-  uint32_t u[4];
-  load4_raw<T>(t + tile_at<T, COLS>(row, col), u);
-  return unpack4<T>(u);
 }
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
