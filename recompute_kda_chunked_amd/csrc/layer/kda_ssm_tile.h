@@ -1,8 +1,7 @@
 // Tiles and matrix products of the selective scan's kernels.
 //
-// A tile lies in LDS row by row in 16-byte units, unit u of row r at place
-// u ^ (r & 7), so that the reads below (16 rows at one column, or 4 rows of 32
-// bytes) spread over the banks. A fragment is one operand of a product over 32
+// A tile lies in LDS row by row, its 16-byte units in an order that goes by the
+// row. A fragment is one operand of a product over 32
 // values of the reduction index: 8 per lane, lane (i, g) = i + 16 g holding row
 // (or column) i and the 8 values that group g has; the products take any
 // assignment of the 32 values to (g, e) as long as both operands have the same:
@@ -38,11 +37,26 @@ __device__ __forceinline__ f32x4 mma32(f32x8 a, f32x8 b, f32x4 c) {
   return c;
 }
 
-// Place of element (row, col) in a tile of COLS columns.
+// Place of element (row, col) in a tile of COLS columns. The 16-byte units of a
+// row change places by row so that both kinds of reads below are free of bank
+// conflicts (64 banks of 4 bytes; a pass takes 16 bytes of the lanes i < 8 of
+// one g with the lanes i >= 8 of the next, or 8 bytes of two whole g): sixteen
+// rows at one unit with the next, and 4 + 4 rows, 8 rows on, at two units.
+template <typename T, int COLS>
+struct TileFlip {
+  static constexpr int U = 16 / sizeof(T), UNITS = COLS / U < 16 ? COLS / U : 16;  // units that change places
+  static constexpr int WIN = UNITS * U;
+  static __device__ __forceinline__ constexpr int units(int row) {
+    const int r = row & 7, far = (row >> 3) & 1;
+    if (UNITS == 4) return far << 1;
+    if (UNITS == 8) return r ^ (far << 2);
+    return sizeof(T) == 2 ? (r << 1) ^ (far << 3) : r ^ (far << 3);
+  }
+};
 template <typename T, int COLS>
 __device__ __forceinline__ int tile_at(int row, int col) {
-  constexpr int U = 16 / sizeof(T), M = (COLS / U < 8 ? COLS / U : 8) - 1;
-  return row * COLS + (((col / U) ^ (row & M)) * U) + col % U;
+  using F = TileFlip<T, COLS>;
+  return row * COLS + (col ^ (F::units(row) * F::U));
 }
 
 // A 4 x 16 block per group of 16 lanes, read transposed: lane i of
@@ -52,12 +66,11 @@ __device__ __forceinline__ s16x4 tr_read(const bf16* p) {
 }
 
 // Element offsets within a tile are a lane's part with some of its low bits
-// flipped by the tile's constant ones, plus constants: (row, col) lies at
-// row COLS + col with the bits of 8 units, col's low ones, flipped by row & 7.
-// The lane's parts, for rows and columns that start at multiples of 16:
+// flipped by the tile's constant ones, plus constants. The lane's parts, for rows
+// and columns that start at multiples of 16:
 template <typename T, int COLS>
 struct LaneAt {
-  static constexpr int U = 16 / sizeof(T), WIN = COLS < 8 * U ? COLS : 8 * U;  // elements the flips stay in
+  static constexpr int WIN = TileFlip<T, COLS>::WIN;
   int row, col, pair, four;
   __device__ __forceinline__ explicit LaneAt(int lane) {
     const int i = lane & 15, g = lane >> 4;
@@ -86,7 +99,7 @@ __device__ __forceinline__ f32x8 frag_row(const float* t, const LaneAt<float, CO
 // Columns c0 .. c0 + 15, reduction over rows k0 .. k0 + 31, plain or paired.
 template <bool PAIRED, int COLS>
 __device__ __forceinline__ bf16x8 frag_col(const bf16* t, const LaneAt<bf16, COLS>& l, int k0, int c0) {
-  constexpr int FLIP = PAIRED || COLS < 64 ? 0 : 32;  // four rows on: row & 7 differs in its bit 2
+  constexpr int FLIP = PAIRED ? 0 : (TileFlip<bf16, COLS>::units(4) ^ TileFlip<bf16, COLS>::units(0)) * 8;  // four rows on
   const int at = shifted<LaneAt<bf16, COLS>>(PAIRED ? l.pair : l.col, c0) + k0 * COLS;
   const int on = shifted<LaneAt<bf16, COLS>>((PAIRED ? l.pair : l.col) ^ FLIP, c0) + (k0 + (PAIRED ? 16 : 4)) * COLS;
   const s16x4 a = tr_read(t + at), b = tr_read(t + on);
