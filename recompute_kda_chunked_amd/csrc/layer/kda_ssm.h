@@ -38,22 +38,30 @@ struct SsmArgs {
   void *y, *dx, *ddt, *dB, *dC;
   float *final_state, *dA, *dD, *dbias, *dinit;
   // Workspace. steps [slots][H][Q]: {dt, high and low part of the chunk's
-  // running sum of log2 decays, d dt / d raw_dt}. S and dS: the states
-  // entering each chunk and the gradients of those leaving it, [slots][H]
-  // [P / 64][N][64] in the problem's dtype; for bf16 the second planes hold
-  // what the first ones' rounding left (null: not needed).
+  // running sum of log2 decays, d dt / d raw_dt}. S and dS: the states entering
+  // each chunk and the gradients of those leaving it, [slots][H][P / 64][N][64],
+  // fp32 with S_full, else in the problem's dtype.
   float* steps;
-  void *S, *S_lo, *dS, *dS_lo;
-  float *pB, *pC;  // partial dB and dC [sets][T][G][N] where sets > 1
+  void *S, *dS;
+  bool S_full;
+  // Segments of `seg` chunks (0: none) in seg_slots slots of their own: what each
+  // adds to its state, forward and back, and its log2 decay, [2][seg_slots][H]..
+  int seg;
+  int64_t seg_slots;
+  float *local, *seg_log;
+  // Of the gradients: per token {what dl adds up from it on, before it, the step
+  // size's own part} [slots][H][Q] of four, per chunk {states' part of dl, dD}.
+  float *sums, *ends;
+  float *pB, *pC;        // partial dB and dC [sets][T][G][N] where sets > 1
   float *part2, *part1;  // per slot {dA, ddt_bias} [2 H] and dD [H]
-  float* ddt_half;       // P = 128: draw_dt of a head's first half [slots][H][Q]
-  int hb, sets;    // heads of a group a block takes in turn, blocks a group
+  int hb, sets;          // heads of a group a block takes in turn, blocks a group
 };
 hipError_t launch_ssm_steps(int dtype, const SsmArgs& a, hipStream_t s);
-// States in sequence order (reverse: gradients, from the last chunk back).
-hipError_t launch_ssm_state(int dtype, int N, bool reverse, const SsmArgs& a, hipStream_t s);
+// `dirs` directions from dir0: 0 in sequence order, 1 (gradients) back.
+hipError_t launch_ssm_state(int dtype, int N, int dirs, int dir0, const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_out(int dtype, int N, const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_grad(int dtype, int N, const SsmArgs& a, hipStream_t s);
+hipError_t launch_ssm_scalars(int dtype, const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_reduce(int dtype, int N, const SsmArgs& a, hipStream_t s);
 
 // Group norm. Partial sums: group_norm_partials(...) rows of dweight [C] then

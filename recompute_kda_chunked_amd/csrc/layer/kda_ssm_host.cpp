@@ -26,36 +26,47 @@ int check_ssm(const kda_ssm_problem* p) {
   return KDA_OK;
 }
 
-// Workspace of the scan, in parts that start at multiples of 256 bytes.
+// The scan's launches and its workspace, in parts that start at multiples of 256
+// bytes.
 struct ScanPlan {
-  int Q, fwd_hb, fwd_sets, bwd_hb, bwd_sets;
-  int64_t slots;
-  size_t steps, state, partial, part2, part1, ddt_half;
-  explicit ScanPlan(const kda_ssm_problem* p) {
+  int Q, hb, sets, seg = 0;
+  int64_t slots, seg_slots = 0;
+  size_t steps, state, dstate = 0, local, seg_log, sums = 0, ends = 0, partial = 0, part2 = 0, part1 = 0;
+  ScanPlan(const kda_ssm_problem* p, bool bwd) {
     Q = ssm_chunk(p->dtype);
-    slots = p->total_tokens / Q + p->n_seqs;
-    const int per = p->H / p->G;
+    const int64_t T = p->total_tokens, HP = static_cast<int64_t>(p->H) * p->P;
+    slots = T / Q + p->n_seqs;
     // heads a block takes: as many of a group as leave the launch enough blocks
-    auto heads = [&](int64_t blocks) {
-      int hb = per;
-      while (hb > 1 && slots * p->G * ((per + hb - 1) / hb) < blocks) hb = (hb + 1) / 2;
-      return hb;
-    };
-    fwd_hb = heads(1024);
-    fwd_sets = (per + fwd_hb - 1) / fwd_hb;
-    bwd_hb = heads(512);
-    bwd_sets = (per + bwd_hb - 1) / bwd_hb;
+    const int per = p->H / p->G;
+    hb = per;
+    while (hb > 1 && slots * p->G * ((per + hb - 1) / hb) < (bwd ? 512 : 1024)) hb = (hb + 1) / 2;
+    sets = (per + hb - 1) / hb;
+    // a sequence's states in segments, where one sequence alone would leave most
+    // of the chip idle
+    const int dirs = bwd ? 2 : 1;
+    const int64_t chunks = (T + Q - 1) / Q, chain = dirs * (HP / 64) * (p->N / 32);
+    const int64_t want = 1024 / chain < 32 ? 1024 / chain : 32;
+    if (want > 1 && chunks >= 8) {
+      seg = static_cast<int>((chunks + want - 1) / want);
+      if (seg < 4) seg = 4;
+      seg_slots = T / (static_cast<int64_t>(seg) * Q) + p->n_seqs;
+    }
     auto part = [](int64_t n, size_t size) { return (static_cast<size_t>(n) * size + 255) / 256 * 256; };
     steps = part(slots * p->H * Q, 16);
-    state = part(slots * p->H * p->P * p->N, p->dtype == KDA_F32 ? 4 : 2);
-    partial = bwd_sets > 1 ? part(p->total_tokens * p->G * p->N * bwd_sets, 4) : 0;
-    part2 = part(slots * p->H * 2, 4);
-    part1 = part(slots * p->H, 4);
-    ddt_half = p->P > 64 ? part(slots * p->H * Q, 4) : 0;
+    state = part(slots * HP * p->N, bwd || p->dtype == KDA_F32 ? 4 : 2);
+    local = part(2 * seg_slots * HP * p->N, 4);
+    seg_log = part(2 * seg_slots * p->H, 4);
+    if (bwd) {
+      dstate = state;
+      sums = steps;
+      ends = part(slots * p->H * 2, 4);
+      partial = sets > 1 ? part(T * p->G * p->N * sets, 4) : 0;
+      part2 = part(slots * p->H * 2, 4);
+      part1 = part(slots * p->H, 4);
+    }
   }
-  size_t fwd() const { return steps + state; }
-  size_t bwd(int dtype) const {
-    return steps + (dtype == KDA_F32 ? 2 : 4) * state + 2 * partial + part2 + part1 + ddt_half;
+  size_t bytes() const {
+    return steps + state + dstate + local + seg_log + sums + ends + 2 * partial + part2 + part1;
   }
 };
 
@@ -70,7 +81,7 @@ int check_scan(const kda_ssm_problem* p, bool has_cu) {
   if (H > (1 << 20) || slots * H >= (int64_t{1} << 26) || slots * H * p->N * p->P >= (int64_t{1} << 40))
     return KDA_ERR_UNSUPPORTED;
   if (slots * H >= (1 << 23) - 1024 || slots * ((H + 3) / 4) >= (1 << 24) ||
-      p->n_seqs * H * (p->P / 64) * (p->N / 32) >= (1 << 24))
+      2 * (slots + 8) * H * (p->P / 64) * (p->N / 32) >= (1 << 26))
     return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
@@ -101,8 +112,27 @@ SsmArgs scan_args(const kda_ssm_problem* p, const ScanPlan& plan, const void* x,
   a.cu = cu;
   a.init = init;
   char* w = static_cast<char*>(workspace);
-  a.steps = reinterpret_cast<float*>(w);
-  a.S = w + plan.steps;
+  auto take = [&w](size_t bytes) {
+    char* at = w;
+    w += bytes;
+    return at;
+  };
+  a.steps = reinterpret_cast<float*>(take(plan.steps));
+  a.S = take(plan.state);
+  a.dS = take(plan.dstate);
+  a.S_full = plan.dstate > 0;
+  a.local = reinterpret_cast<float*>(take(plan.local));
+  a.seg_log = reinterpret_cast<float*>(take(plan.seg_log));
+  a.sums = reinterpret_cast<float*>(take(plan.sums));
+  a.ends = reinterpret_cast<float*>(take(plan.ends));
+  a.pB = reinterpret_cast<float*>(take(plan.partial));
+  a.pC = reinterpret_cast<float*>(take(plan.partial));
+  a.part2 = reinterpret_cast<float*>(take(plan.part2));
+  a.part1 = reinterpret_cast<float*>(take(plan.part1));
+  a.seg = plan.seg;
+  a.seg_slots = plan.seg_slots;
+  a.hb = plan.hb;
+  a.sets = plan.sets;
   return a;
 }
 
@@ -152,7 +182,7 @@ GroupNormArgs group_norm_args(const kda_group_norm_problem* p, const void* x, co
 extern "C" {
 
 size_t kda_ssm_fwd_workspace_bytes(const kda_ssm_problem* p) {
-  return check_scan(p, true) == KDA_OK ? ScanPlan(p).fwd() : 0;
+  return check_scan(p, true) == KDA_OK ? ScanPlan(p, false).bytes() : 0;
 }
 
 int kda_ssm_fwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, const float* A_log,
@@ -162,25 +192,23 @@ int kda_ssm_fwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, con
   const int st = check_scan(p, cu_seqlens != nullptr);
   if (st != KDA_OK) return st;
   if (p->total_tokens > 0 && (!x || !raw_dt || !A_log || !B || !C || !y)) return KDA_ERR_INVALID;
-  const ScanPlan plan(p);
-  if (plan.fwd() > 0 && !workspace) return KDA_ERR_INVALID;
-  if (workspace_bytes < plan.fwd()) return KDA_ERR_WORKSPACE;
+  const ScanPlan plan(p, false);
+  if (plan.bytes() > 0 && !workspace) return KDA_ERR_INVALID;
+  if (workspace_bytes < plan.bytes()) return KDA_ERR_WORKSPACE;
   SsmArgs a = scan_args(p, plan, x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, initial_state, workspace);
   a.y = y;
   a.final_state = final_state;
-  a.hb = plan.fwd_hb;
-  a.sets = plan.fwd_sets;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t units = a.T * a.H;
   if (a.T > 0 && a.n_seqs > 0) KDA_TRY(KDA_KERNEL_SSM_STEPS, units, launch_ssm_steps(p->dtype, a, s));
   if (a.n_seqs > 0 && (a.T > 0 || final_state))
-    KDA_TRY(KDA_KERNEL_SSM_STATE, units, launch_ssm_state(p->dtype, p->N, false, a, s));
+    KDA_TRY(KDA_KERNEL_SSM_STATE, units, launch_ssm_state(p->dtype, p->N, 1, 0, a, s));
   if (a.T > 0) KDA_TRY(KDA_KERNEL_SSM_OUT, units, launch_ssm_out(p->dtype, p->N, a, s));
   return KDA_OK;
 }
 
 size_t kda_ssm_bwd_workspace_bytes(const kda_ssm_problem* p) {
-  return check_scan(p, true) == KDA_OK ? ScanPlan(p).bwd(p->dtype) : 0;
+  return check_scan(p, true) == KDA_OK ? ScanPlan(p, true).bytes() : 0;
 }
 
 int kda_ssm_bwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, const float* A_log,
@@ -194,9 +222,9 @@ int kda_ssm_bwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, con
   if (!dA_log) return KDA_ERR_INVALID;
   if (p->total_tokens > 0 && (!x || !raw_dt || !A_log || !B || !C || !dy || !dx || !draw_dt || !dB || !dC))
     return KDA_ERR_INVALID;
-  const ScanPlan plan(p);
-  if (plan.bwd(p->dtype) > 0 && !workspace) return KDA_ERR_INVALID;
-  if (workspace_bytes < plan.bwd(p->dtype)) return KDA_ERR_WORKSPACE;
+  const ScanPlan plan(p, true);
+  if (plan.bytes() > 0 && !workspace) return KDA_ERR_INVALID;
+  if (workspace_bytes < plan.bytes()) return KDA_ERR_WORKSPACE;
   SsmArgs a = scan_args(p, plan, x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, initial_state, workspace);
   a.dy = dy;
   a.dfinal = d_final_state;
@@ -205,31 +233,19 @@ int kda_ssm_bwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, con
   a.dB = dB;
   a.dC = dC;
   a.dinit = d_initial_state;
-  a.hb = plan.bwd_hb;
-  a.sets = plan.bwd_sets;
-  char* w = static_cast<char*>(a.S) + plan.state;
-  a.dS = w;
-  w += plan.state;
-  if (p->dtype == KDA_BF16) {
-    a.S_lo = w;
-    a.dS_lo = w + plan.state;
-    w += 2 * plan.state;
-  }
-  a.pB = reinterpret_cast<float*>(w);
-  a.pC = reinterpret_cast<float*>(w + plan.partial);
-  a.part2 = reinterpret_cast<float*>(w + 2 * plan.partial);
-  a.part1 = reinterpret_cast<float*>(w + 2 * plan.partial + plan.part2);
-  a.ddt_half = reinterpret_cast<float*>(w + 2 * plan.partial + plan.part2 + plan.part1);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t units = a.T * a.H;
   if (a.T > 0 && a.n_seqs > 0) {
     KDA_TRY(KDA_KERNEL_SSM_STEPS, units, launch_ssm_steps(p->dtype, a, s));
-    KDA_TRY(KDA_KERNEL_SSM_STATE, units, launch_ssm_state(p->dtype, p->N, false, a, s));
+    KDA_TRY(KDA_KERNEL_SSM_STATE, units, launch_ssm_state(p->dtype, p->N, 2, 0, a, s));
+  } else if (a.n_seqs > 0 && d_initial_state) {  // empty sequences only
+    KDA_TRY(KDA_KERNEL_SSM_STATE, units, launch_ssm_state(p->dtype, p->N, 1, 1, a, s));
   }
-  if (a.n_seqs > 0 && (a.T > 0 || d_initial_state))
-    KDA_TRY(KDA_KERNEL_SSM_STATE, units, launch_ssm_state(p->dtype, p->N, true, a, s));
-  if (a.T > 0) KDA_TRY(KDA_KERNEL_SSM_GRAD, units, launch_ssm_grad(p->dtype, p->N, a, s));
-  if (a.T > 0 && a.sets > 1) KDA_TRY(KDA_KERNEL_SSM_REDUCE, a.T, launch_ssm_reduce(p->dtype, p->N, a, s));
+  if (a.T > 0) {
+    KDA_TRY(KDA_KERNEL_SSM_GRAD, units, launch_ssm_grad(p->dtype, p->N, a, s));
+    KDA_TRY(KDA_KERNEL_SSM_GRAD, units, launch_ssm_scalars(p->dtype, a, s));
+    if (a.sets > 1) KDA_TRY(KDA_KERNEL_SSM_REDUCE, a.T, launch_ssm_reduce(p->dtype, p->N, a, s));
+  }
   // without tokens the sums are empty
   const int64_t nb = a.T > 0 ? a.slots : 0;
   const ParamReduceArgs r2{a.part2, nb, p->H, p->H, dA_log, ddt_bias}, r1{a.part1, nb, p->H, 0, dD, nullptr};

@@ -59,24 +59,26 @@ __device__ __forceinline__ int64_t clamp_cu(const SsmArgs& a, int n) {
   return c < 0 ? 0 : (c > a.T ? a.T : c);
 }
 
-// The chunk of a slot: its first token and its tokens (<= 0: none).
+// The piece of L tokens of one sequence that a slot holds (see SsmArgs): the
+// sequence (-1: none), its first token and end, the piece's number in it, and its
+// tokens (<= 0: none).
 struct Place {
-  int64_t t0;
-  int rows;
+  int n, pos, rows;
+  int64_t s0, s1, t0;
 };
-template <int Q>
-__device__ __forceinline__ Place find_chunk(const SsmArgs& a, int64_t slot) {
-  if (a.n_seqs == 0) return {0, 0};
+__device__ __forceinline__ Place find_piece(const SsmArgs& a, int64_t slot, uint32_t L) {
+  if (a.n_seqs == 0) return {-1, 0, 0, 0, 0, 0};
+  auto first = [&](int n) { return static_cast<int64_t>(static_cast<uint32_t>(clamp_cu(a, n)) / L) + n; };
   int lo = 0, hi = a.n_seqs;  // the last sequence whose first slot is not behind
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (clamp_cu(a, mid) / Q + mid <= slot) lo = mid;
+    if (first(mid) <= slot) lo = mid;
     else hi = mid;
   }
-  const int64_t s = clamp_cu(a, lo), e = clamp_cu(a, lo + 1), pos = slot - (s / Q + lo);
-  if (pos < 0) return {0, 0};
-  const int64_t left = e - s - pos * Q;
-  return {s + pos * Q, static_cast<int>(left < Q ? (left < 0 ? 0 : left) : Q)};
+  const int64_t s = clamp_cu(a, lo), e = clamp_cu(a, lo + 1), pos = slot - first(lo);
+  if (pos < 0) return {-1, 0, 0, 0, 0, 0};
+  const int64_t left = e - s - pos * L;
+  return {lo, static_cast<int>(pos), static_cast<int>(left < L ? (left < 0 ? 0 : left) : L), s, e, s + pos * L};
 }
 
 // ------------------------------------------------------------ step sizes
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(256) k_ssm_steps(SsmArgs a) {
   const int nhb = (a.H + 3) / 4;
   const int64_t slot = blockIdx.x / nhb;
   const int h = (blockIdx.x % nhb) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const Place c = find_chunk<Q>(a, slot);
+  const Place c = find_piece(a, slot, Q);
   if (c.rows <= 0 || h >= a.H) return;
   const double l2 = -exp(static_cast<double>(a.A_log[h])) * 1.4426950408889634;
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
@@ -124,125 +126,206 @@ __global__ void __launch_bounds__(256) k_ssm_steps(SsmArgs a) {
 
 // ------------------------------------------------------------ states
 
-template <typename T>
-__device__ __forceinline__ float low_part(float x) {
-  return x - static_cast<float>(static_cast<T>(x));
+// Rows behind a chunk's last are read as its last and made zero at their use, and
+// what is loaded ahead at the end is loaded twice: a load under a condition would
+// be waited for where the condition ends.
+__device__ __forceinline__ uint4 kept(bool keep, uint4 v) {
+  return keep ? v : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ int row_or_last(int r, int rows) { return r < rows ? r : rows - 1; }
+
+// Blocks of consecutive numbers on one XCD (the hardware deals them out in turn
+// over eight), for those that read the same rows. `total` is a multiple of 8.
+__device__ __forceinline__ unsigned on_one_xcd(unsigned b, unsigned total) {
+  return (b & 7) * (total / 8) + b / 8;
 }
 
-// One block walks a sequence's chunks with 64 columns and 32 rows of one
-// head's state: S' = e^tot S + (w B)^T x, w_j = dt_j exp(cum_Q - cum_j); reverse,
-// dS = e^tot dS' + (w C)^T dy, w_i = exp(cum_i). The weighted rows are a pair of
-// bf16, x and dy are exact. Wave w holds columns 16 w .. of the transposed
-// state, a lane four of them in a row of it.
-template <typename TI, int N, bool REV, bool LO>
-__global__ void __launch_bounds__(256) k_ssm_state(SsmArgs a) {
+// A row of U values as kTerms vectors of TI that add up to them: fp32 itself, or
+// three bf16, which hold 24 bits.
+template <typename TI>
+struct Terms {
+  static constexpr int K = sizeof(TI) == 4 ? 1 : 3, U = 16 / sizeof(TI);
+  static __device__ __forceinline__ void split(float (&f)[U], RowVec<TI> (&v)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      v[k].set(f);
+      if (k + 1 < K) {
+        float h[U];
+        v[k].get(h);
+#pragma unroll
+        for (int e = 0; e < U; ++e) f[e] -= h[e];
+      }
+    }
+  }
+};
+
+// One block walks the chunks of a segment with 64 columns and 32 rows of one
+// head's state: S' = e^tot S + (w B)^T x, w_j = dt_j exp(cum_Q - cum_j); in
+// reverse dS = e^tot dS' + (w C)^T dy, w_i = exp(cum_i). The weighted rows are
+// three bf16 each, x and dy are exact, so that states are fp32 states. A wave
+// holds 32 columns by 16 rows of the transposed state, a lane four columns of a
+// row of each of its two tiles.
+//
+// A sequence is one segment where the launch has blocks enough; otherwise LOCAL
+// leaves what each segment adds to a state that enters it as zero, and the second
+// launch starts each segment from the states that the ones before it have left.
+enum { kLocal = 0, kStates = 1, kFullStates = 2 };  // leave what a segment adds; states in TI; in fp32
+template <typename TI, int N, int MODE>
+__global__ void __launch_bounds__(256) k_ssm_state(SsmArgs a, int dirs, int dir0, unsigned blocks) {
   constexpr int Q = Chunk<TI>::Q, U = 16 / sizeof(TI), NB = 32;
   constexpr int XU = Q * 64 / U / 256, BU = Q * NB / U / 256;  // 16-byte units a thread
-  constexpr bool kPair = sizeof(TI) == 2;
-  __shared__ __align__(16) TI xs[Q * 64], bh[Q * NB], bl[kPair ? Q * NB : 1];
-  const int halves = a.P / 64, nsplit = N / NB;
-  const int per_seq = a.H * halves * nsplit;
-  const int n = blockIdx.x / per_seq, rest = blockIdx.x % per_seq;
-  const int n0 = (rest % nsplit) * NB, hp = rest / nsplit, h = hp / halves, half = hp % halves;
+  constexpr int K = Terms<TI>::K;
+  constexpr bool LOCAL = MODE == kLocal;
+  __shared__ __align__(16) TI xs[Q * 64], bs[K][Q * NB];
+  const int halves = a.P / 64, nsplit = N / NB, seg = a.seg;
+  unsigned b = on_one_xcd(blockIdx.x, gridDim.x);
+  if (b >= blocks) return;
+  // heads vary slowest: each XCD has some of them, with all their segments,
+  // whose lengths differ
+  const unsigned per_head = blocks / (a.H * halves);
+  const int hp = b / per_head, h = hp / halves, half = hp % halves;
+  b %= per_head;
+  const int n0 = (b % nsplit) * NB;
+  b /= nsplit;
+  const int rev = dirs > 1 ? b % 2 : dir0;
+  const int64_t sslot = dirs > 1 ? b / 2 : b;
+  // without segments a slot is a sequence, also one without tokens
+  Place c;
+  if (seg) {
+    c = find_piece(a, sslot, seg * Q);
+  } else {
+    c = {static_cast<int>(sslot), 0, 0, clamp_cu(a, sslot), clamp_cu(a, sslot + 1), 0};
+    c.t0 = c.s0;
+    c.rows = static_cast<int>(c.s1 > c.s0 ? c.s1 - c.s0 : 0);
+  }
+  const int64_t len = c.s1 > c.s0 ? c.s1 - c.s0 : 0;
+  const int segs = seg && len ? static_cast<int>((len + seg * Q - 1) / (seg * Q)) : 1;  // of the sequence
+  const bool ends = rev ? c.pos == 0 : c.pos == segs - 1;  // its state leaves the sequence
+  if (seg && c.rows <= 0 && !(c.n >= 0 && len == 0 && c.pos == 0)) return;
+  if (LOCAL && ends) return;
   const int grp = h / (a.H / a.G);
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), i = lane & 15, g = lane >> 4;
-  const int64_t s0 = clamp_cu(a, n), s1 = clamp_cu(a, n + 1), len = s1 > s0 ? s1 - s0 : 0;
-  const int64_t nch = (len + Q - 1) / Q, first = s0 / Q + n;
-  const TI* src = static_cast<const TI*>(REV ? a.dy : a.x) + static_cast<size_t>(h) * a.P + half * 64;
-  const int64_t sst = REV ? static_cast<int64_t>(a.H) * a.P : a.xs;
-  const TI* rsrc = static_cast<const TI*>(REV ? a.C : a.B) + static_cast<size_t>(grp) * N + n0;
-  const int64_t rst = REV ? a.Cs : a.Bs;
-  const float* from = REV ? a.dfinal : a.init;
-  float* to = REV ? a.dinit : a.final_state;
-  const size_t state = ((static_cast<size_t>(n) * a.H + h) * N + n0 + i) * a.P + half * 64 + 16 * w + 4 * g;
+  const int p0 = 32 * (w & 1), nt = 16 * (w >> 1);
+  const int64_t t0 = c.t0;
+  const int nch = (c.rows + Q - 1) / Q;
+  const int64_t first = static_cast<uint32_t>(c.s0) / Q + c.n + (t0 - c.s0) / Q;  // slot of the first chunk
+  const TI* src = static_cast<const TI*>(rev ? a.dy : a.x) + static_cast<size_t>(h) * a.P + half * 64;
+  const int64_t sst = rev ? static_cast<int64_t>(a.H) * a.P : a.xs;
+  const TI* rsrc = static_cast<const TI*>(rev ? a.C : a.B) + static_cast<size_t>(grp) * N + n0;
+  const int64_t rst = rev ? a.Cs : a.Bs;
+  const float* from = rev ? a.dfinal : a.init;
+  float* to = rev ? a.dinit : a.final_state;
+  const size_t state = ((static_cast<size_t>(c.n) * a.H + h) * N + n0 + nt + i) * a.P + half * 64 + p0 + 4 * g;
+  // of a segment's own slot: [H][halves][N][64]
+  const int64_t sslots = a.seg_slots;
+  float* local = a.local + static_cast<size_t>(rev) * sslots * a.H * halves * N * 64 + (static_cast<size_t>(hp) * N + n0 + nt + i) * 64 + p0 + 4 * g;
+  const size_t lstep = static_cast<size_t>(a.H) * halves * N * 64;
 
   const LaneAt<TI, 64> lx(lane);
   const LaneAt<TI, NB> lb(lane);
   f32x4 acc[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t)
-    acc[t] = from ? *reinterpret_cast<const f32x4*>(from + state + static_cast<size_t>(16 * t) * a.P) : zero4();
+    acc[t] = from && !LOCAL ? *reinterpret_cast<const f32x4*>(from + state + 16 * t) : zero4();
+  if (!LOCAL && seg) {
+    for (int k = 0; k < (rev ? segs - 1 - c.pos : c.pos); ++k) {
+      const int64_t at = sslot - c.pos + (rev ? segs - 1 - k : k);
+      const float d = exp2_(a.seg_log[(rev * sslots + at) * a.H + h]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) acc[t] = d * acc[t] + *reinterpret_cast<const f32x4*>(local + at * lstep + 16 * t);
+    }
+  }
 
-  uint4 rx[XU], rb[BU];
-  float wt[BU], tot = 0.f;
-  auto load = [&](int64_t c) {
-    const int64_t t0 = s0 + c * Q;
-    const int rows = static_cast<int>(s1 - t0 < Q ? s1 - t0 : Q);
+  struct Stage {
+    uint4 x[XU], b[BU];
+    f32x4 k[BU], end;  // step sizes: nothing is computed from a load before its use
+  };
+  auto load = [&](int k, Stage& st) __attribute__((always_inline)) {
+    const int ch = rev ? nch - 1 - k : k;
+    const int64_t at = t0 + static_cast<int64_t>(ch) * Q;
+    const int rows = c.rows - ch * Q < Q ? c.rows - ch * Q : Q;
+    const f32x4* steps = reinterpret_cast<const f32x4*>(a.steps) + ((first + ch) * a.H + h) * Q;
+    st.end = steps[Q - 1];
 #pragma unroll
     for (int m = 0; m < XU; ++m) {
       const int u = tid + 256 * m, r = u / (64 / U);
-      rx[m] = make_uint4(0, 0, 0, 0);
-      if (r < rows) rx[m] = *reinterpret_cast<const uint4*>(src + (t0 + r) * sst + (u % (64 / U)) * U);
+      st.x[m] = *reinterpret_cast<const uint4*>(src + (at + row_or_last(r, rows)) * sst + (u % (64 / U)) * U);
     }
-    const f32x4* st = reinterpret_cast<const f32x4*>(a.steps) + ((first + c) * a.H + h) * Q;
-    const f32x4 end = st[Q - 1];
-    tot = exp2_(end[1] + end[2]);
 #pragma unroll
     for (int m = 0; m < BU; ++m) {
       const int u = tid + 256 * m, r = u / (NB / U);
-      rb[m] = make_uint4(0, 0, 0, 0);
-      if (r < rows) rb[m] = *reinterpret_cast<const uint4*>(rsrc + (t0 + r) * rst + (u % (NB / U)) * U);
-      const f32x4 k = st[r];
-      wt[m] = REV ? exp2_(k[1] + k[2]) : k[0] * exp2_((end[1] - k[1]) + (end[2] - k[2]));
+      st.b[m] = *reinterpret_cast<const uint4*>(rsrc + (at + row_or_last(r, rows)) * rst + (u % (NB / U)) * U);
+      st.k[m] = steps[r];
     }
   };
-  if (nch > 0) load(REV ? nch - 1 : 0);
-  for (int64_t k = 0; k < nch; ++k) {
-    const int64_t c = REV ? nch - 1 - k : k;
+  double total = 0.0;
+  auto step = [&](int k, Stage& st) __attribute__((always_inline)) {
+    const int ch = rev ? nch - 1 - k : k;
+    const int rows = c.rows - ch * Q;
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < XU; ++m) {
-      const int u = tid + 256 * m;
-      *reinterpret_cast<uint4*>(xs + tile_at<TI, 64>(u / (64 / U), (u % (64 / U)) * U)) = rx[m];
+      const int u = tid + 256 * m, r = u / (64 / U);
+      *reinterpret_cast<uint4*>(xs + tile_at<TI, 64>(r, (u % (64 / U)) * U)) = kept(r < rows, st.x[m]);
     }
 #pragma unroll
     for (int m = 0; m < BU; ++m) {
       const int u = tid + 256 * m, at = tile_at<TI, NB>(u / (NB / U), (u % (NB / U)) * U);
-      RowVec<TI> v, lo;
-      float f[U], l[U];
-      v.u = rb[m];
+      RowVec<TI> v, t[K];
+      float f[U];
+      v.u = kept(u / (NB / U) < rows, st.b[m]);
       v.get(f);
+      const f32x4 k4 = st.k[m];
+      const float wt = rev ? exp2_(k4[1] + k4[2]) : k4[0] * exp2_((st.end[1] - k4[1]) + (st.end[2] - k4[2]));
 #pragma unroll
-      for (int e = 0; e < U; ++e) {
-        f[e] *= wt[m];
-        l[e] = low_part<TI>(f[e]);
-      }
-      v.set(f);
-      *reinterpret_cast<uint4*>(bh + at) = v.u;
-      if constexpr (kPair) {
-        lo.set(l);
-        *reinterpret_cast<uint4*>(bl + at) = lo.u;
-      }
+      for (int e = 0; e < U; ++e) f[e] *= wt;
+      Terms<TI>::split(f, t);
+#pragma unroll
+      for (int q = 0; q < K; ++q) *reinterpret_cast<uint4*>(bs[q] + at) = t[q].u;
     }
-    const float decay = tot;
+    const float log = st.end[1] + st.end[2], decay = exp2_(log);
+    total += log;
     __syncthreads();
-    if (k + 1 < nch) load(REV ? c - 1 : c + 1);
-    TI* out = static_cast<TI*>(REV ? a.dS : a.S) + (((first + c) * a.H * halves + hp) * N + n0 + i) * 64 + 16 * w + 4 * g;
-    TI* out_lo = LO ? static_cast<TI*>(REV ? a.dS_lo : a.S_lo) + (((first + c) * a.H * halves + hp) * N + n0 + i) * 64 + 16 * w + 4 * g : nullptr;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      store4<TI>(out + 16 * t * 64, acc[t]);
-      if constexpr (LO) {
-        f32x4 l;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) l[r] = low_part<TI>(acc[t][r]);
-        store4<TI>(out_lo + 16 * t * 64, l);
-      }
-      acc[t] *= decay;
-    }
-#pragma unroll
-    for (int k0 = 0; k0 < Q; k0 += 32) {
-      const Frag<TI> ax = frag_col<false>(xs, lx, k0, 16 * w);
+    load(k + 2 < nch ? k + 2 : nch - 1, st);
+    if constexpr (!LOCAL) {
+      const size_t at = (((first + ch) * a.H * halves + hp) * N + n0 + nt + i) * 64 + p0 + 4 * g;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        acc[t] = mma32(ax, frag_col<false>(bh, lb, k0, 16 * t), acc[t]);
-        if constexpr (kPair) acc[t] = mma32(ax, frag_col<false>(bl, lb, k0, 16 * t), acc[t]);
+        if constexpr (MODE == kFullStates) store4<float>(static_cast<float*>(rev ? a.dS : a.S) + at + 16 * t, acc[t]);
+        else store4<TI>(static_cast<TI*>(a.S) + at + 16 * t, acc[t]);
       }
     }
-  }
-  if (to) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) *reinterpret_cast<f32x4*>(to + state + static_cast<size_t>(16 * t) * a.P) = acc[t];
+    for (int t = 0; t < 2; ++t) acc[t] *= decay;
+#pragma unroll
+    for (int k0 = 0; k0 < Q; k0 += 32) {
+      Frag<TI> bf[K];
+#pragma unroll
+      for (int q = 0; q < K; ++q) bf[q] = frag_col<false>(bs[q], lb, k0, nt);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const Frag<TI> ax = frag_col<false>(xs, lx, k0, p0 + 16 * t);
+#pragma unroll
+        for (int q = K - 1; q >= 0; --q) acc[t] = mma32(ax, bf[q], acc[t]);
+      }
+    }
+  };
+  Stage s0, s1;  // chunks are loaded two ahead
+  if (nch > 0) {
+    load(0, s0);
+    load(nch > 1 ? 1 : 0, s1);
+  }
+  for (int k = 0; k < nch; k += 2) {
+    step(k, s0);
+    if (k + 1 < nch) step(k + 1, s1);
+  }
+  if constexpr (LOCAL) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) *reinterpret_cast<f32x4*>(local + sslot * lstep + 16 * t) = acc[t];
+    if (tid == 0 && n0 == 0 && half == 0) a.seg_log[(rev * sslots + sslot) * a.H + h] = static_cast<float>(total);
+  } else if (to && ends) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) *reinterpret_cast<f32x4*>(to + state + 16 * t) = acc[t];
   }
 }
 
@@ -265,13 +348,12 @@ __device__ __forceinline__ void load_tile(TI* tile, const TI* src, int64_t st, i
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
     const int u = tid + THREADS * m, r = u / (COLS / U);
-    v[m] = make_uint4(0, 0, 0, 0);
-    if (r < rows) v[m] = *reinterpret_cast<const uint4*>(src + r * st + (u % (COLS / U)) * U);
+    v[m] = *reinterpret_cast<const uint4*>(src + row_or_last(r, rows) * st + (u % (COLS / U)) * U);
   }
 #pragma unroll
   for (int m = 0; m < PER; ++m) {
     const int u = tid + THREADS * m;
-    *reinterpret_cast<uint4*>(tile + tile_at<TI, COLS>(u / (COLS / U), (u % (COLS / U)) * U)) = v[m];
+    *reinterpret_cast<uint4*>(tile + tile_at<TI, COLS>(u / (COLS / U), (u % (COLS / U)) * U)) = kept(u / (COLS / U) < rows, v[m]);
   }
 }
 
@@ -300,17 +382,18 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_out(SsmArgs a) {
   }
   const int set = blockIdx.x % a.sets, grp = (blockIdx.x / a.sets) % a.G;
   const int64_t slot = blockIdx.x / (a.sets * a.G);
-  const Place c = find_chunk<Q>(a, slot);
-  if (c.rows <= 0) return;
+  const Place c = find_piece(a, slot, Q);
+  const int rows = c.rows;
+  const int64_t t0 = c.t0;
+  if (rows <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), i = lane & 15, g = lane >> 4;
   const int it = own_tile<NW>(w), per = a.H / a.G, halves = a.P / 64;
   const int h0 = grp * per + set * a.hb, h1 = set * a.hb + a.hb < per ? h0 + a.hb : (grp + 1) * per;
 
   const LaneAt<TI, N> ln(lane);
-  const LaneAt<TI, 64> lx(lane);
   TI *Bt = buf, *Ct = buf + Q * N;
-  load_tile<TI, Q, N, TH>(Bt, static_cast<const TI*>(a.B) + c.t0 * a.Bs + static_cast<size_t>(grp) * N, a.Bs, c.rows);
-  load_tile<TI, Q, N, TH>(Ct, static_cast<const TI*>(a.C) + c.t0 * a.Cs + static_cast<size_t>(grp) * N, a.Cs, c.rows);
+  load_tile<TI, Q, N, TH>(Bt, static_cast<const TI*>(a.B) + t0 * a.Bs + static_cast<size_t>(grp) * N, a.Bs, rows);
+  load_tile<TI, Q, N, TH>(Ct, static_cast<const TI*>(a.C) + t0 * a.Cs + static_cast<size_t>(grp) * N, a.Cs, rows);
   __syncthreads();
   Frag<TI> cf[N / 32];
 #pragma unroll
@@ -325,19 +408,48 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_out(SsmArgs a) {
     }
   }
   TI *xs = buf, *Ss = buf + Q * 64;
+  constexpr int U = 16 / sizeof(TI), XU = Q * 64 / U / TH, SU = N * 64 / U / TH;
+  uint4 nx[XU];  // the next head's x and state
+  f32x4 ns[SU];
+  f32x4 nsteps = zero4();
+  auto load = [&](int h, int half) __attribute__((always_inline)) {
+    const int ft = once(tid);
+    const TI* x = static_cast<const TI*>(a.x) + t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64;
+    const TI* S = static_cast<const TI*>(a.S) + ((slot * a.H + h) * halves + half) * static_cast<size_t>(N) * 64;
+#pragma unroll
+    for (int m = 0; m < XU; ++m) {
+      const int u = ft + TH * m, r = u / (64 / U);
+      nx[m] = *reinterpret_cast<const uint4*>(x + row_or_last(r, rows) * a.xs + (u % (64 / U)) * U);
+    }
+#pragma unroll
+    for (int m = 0; m < SU; ++m) ns[m] = *reinterpret_cast<const f32x4*>(S + (ft + TH * m) * U);
+    nsteps = reinterpret_cast<const f32x4*>(a.steps)[(slot * a.H + h) * Q + ft % Q];
+  };
+  load(h0, 0);
   for (int h = h0; h < h1; ++h) {
     const float D = a.D ? a.D[h] : 0.f;
     for (int half = 0; half < halves; ++half) {
       __syncthreads();
-      load_tile<TI, Q, 64, TH>(xs, static_cast<const TI*>(a.x) + c.t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64, a.xs, c.rows);
-      load_tile<TI, N, 64, TH>(Ss, static_cast<const TI*>(a.S) + ((slot * a.H + h) * halves + half) * N * 64, 64, N);
+      const int ft = once(tid);
+#pragma unroll
+      for (int m = 0; m < XU; ++m) {
+        const int u = ft + TH * m, r = u / (64 / U);
+        *reinterpret_cast<uint4*>(xs + tile_at<TI, 64>(r, (u % (64 / U)) * U)) = kept(r < rows, nx[m]);
+      }
+#pragma unroll
+      for (int m = 0; m < SU; ++m) {
+        const int u = ft + TH * m;
+        *reinterpret_cast<f32x4*>(Ss + tile_at<TI, 64>(u / (64 / U), (u % (64 / U)) * U)) = ns[m];
+      }
       if (tid < Q) {
-        const f32x4 k = reinterpret_cast<const f32x4*>(a.steps)[(slot * a.H + h) * Q + tid];
-        cdt[tid] = k[0];
-        chi[tid] = k[1];
-        clo[tid] = k[2];
+        cdt[ft] = nsteps[0];
+        chi[ft] = nsteps[1];
+        clo[ft] = nsteps[2];
       }
       __syncthreads();
+      const bool next = half + 1 == halves && h + 1 < h1;
+      load(next ? h + 1 : h, half + 1 < halves ? half + 1 : next ? 0 : half);
+      const LaneAt<TI, 64> lx(once(lane));
       const float hi = chi[16 * it + i], lo = clo[16 * it + i], ei = exp2_(hi + lo);
       f32x4 y[4];
 #pragma unroll
@@ -365,8 +477,8 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_out(SsmArgs a) {
         for (int p = 0; p < 4; ++p) y[p] = mma32(frag_col<true>(xs, lx, 32 * m, 16 * p), wf, y[p]);
       }
       const int row = 16 * it + i;
-      if (row < c.rows) {
-        TI* out = static_cast<TI*>(a.y) + ((c.t0 + row) * a.H + h) * a.P + half * 64 + 4 * g;
+      if (row < rows) {
+        TI* out = static_cast<TI*>(a.y) + ((t0 + row) * a.H + h) * a.P + half * 64 + 4 * g;
 #pragma unroll
         for (int p = 0; p < 4; ++p) store4<TI>(out + 16 * p, y[p] + D * tile_get4(xs, lx, 16 * it, 16 * p));
       }
@@ -387,6 +499,17 @@ __device__ __forceinline__ float sum_lane_groups(float x) {
   return __uint_as_float(h[0]) + __uint_as_float(h[1]);
 }
 
+// A value of an fp32 state as the operand's type and what its rounding leaves
+// (bf16: 16 bits together).
+template <typename TI>
+__device__ __forceinline__ void split2(const f32x8& x, Frag<TI>& hi, Frag<TI>& lo) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    hi[e] = static_cast<TI>(x[e]);
+    lo[e] = static_cast<TI>(x[e] - static_cast<float>(hi[e]));
+  }
+}
+
 // Two roles of a wave. First, 16 tokens j of the chunk: the scores of all i >= j
 // as [i][j] accumulators, dx_j, and L E dt to LDS. Then 16 rows of the state (or
 // several, or half the tokens; NT tiles of rows and TT of tokens), in which dB
@@ -399,13 +522,18 @@ struct GradShape {
   static constexpr int TT = NW / (NW / NG);                // token tiles a wave
 };
 
+// The next head's rows are loaded while a head's are worked on. The sums over a
+// row or column of scores that the step sizes' gradient needs are left to
+// k_ssm_scalars: what is added up over the chunk there costs a wave some
+// microseconds that the others would wait for here.
 template <typename TI, int N>
 __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   using SH = GradShape<TI, N>;
   constexpr int Q = SH::Q, NW = SH::NW, TH = 64 * NW, NT = SH::NT, NG = SH::NG, TT = SH::TT;
+  constexpr int U = 16 / sizeof(TI), XU = Q * 64 / U / TH;
   constexpr bool kPair = sizeof(TI) == 2;
   __shared__ __align__(16) TI Bt[Q * N], Ct[Q * N], xs[Q * 64], dys[Q * 64], MT[Q * Q], Gs[N * 64];
-  __shared__ __align__(16) float chi[2][Q], clo[2][Q], cdt[2][Q], rowF[NW][Q], iC[NG][Q], iB[NG][Q], colF[Q];
+  __shared__ __align__(16) float chi[Q], clo[Q], cdt[Q], rowF[NW][Q], iC[NG][Q], iB[NG][Q], colF[Q];
   __shared__ float sd[NW], xd[NW];
   const unsigned own = static_cast<unsigned>(a.slots) * a.G * a.sets;
   if (blockIdx.x >= own) {
@@ -420,78 +548,112 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   }
   const int set = blockIdx.x % a.sets, grp = (blockIdx.x / a.sets) % a.G;
   const int64_t slot = blockIdx.x / (a.sets * a.G);
-  const Place c = find_chunk<Q>(a, slot);
-  const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), i = lane & 15, g = lane >> 4;
+  const Place c = find_piece(a, slot, Q);
+  const int rows = c.rows;
+  const int64_t t0 = c.t0;
+  if (rows <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_number();
   const int jt = own_tile<NW>(w), per = a.H / a.G, halves = a.P / 64;
   const int h0 = grp * per + set * a.hb, h1 = set * a.hb + a.hb < per ? h0 + a.hb : (grp + 1) * per;
-  if (c.rows <= 0) {  // its partial sums are added up all the same
-    for (int h = h0 + tid; h < h1; h += TH) {
-      a.part2[slot * 2 * a.H + h] = a.part2[slot * 2 * a.H + a.H + h] = 0.f;
-      a.part1[slot * a.H + h] = 0.f;
+  const int ng = w % NG, tt0 = (w / NG) * TT, n0 = ng * NT * 16;  // of the second role
+
+  uint4 nx[XU], ny[XU];
+  f32x4 nsteps = zero4();
+  f32x8 G0[NT][2], S0[NT][2];  // dS and S, rows n0 .. as operands
+  auto load_rows = [&](int h, int half) __attribute__((always_inline)) {
+    const int fresh = once(tid);
+    const TI* x = static_cast<const TI*>(a.x) + t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64;
+    const TI* dy = static_cast<const TI*>(a.dy) + (t0 * a.H + h) * a.P + half * 64;
+#pragma unroll
+    for (int m = 0; m < XU; ++m) {
+      const int u = fresh + TH * m, r = u / (64 / U), col = (u % (64 / U)) * U;
+      nx[m] = *reinterpret_cast<const uint4*>(x + row_or_last(r, rows) * a.xs + col);
+      ny[m] = *reinterpret_cast<const uint4*>(dy + row_or_last(r, rows) * static_cast<int64_t>(a.H) * a.P + col);
     }
-    return;
-  }
-  load_tile<TI, Q, N, TH>(Bt, static_cast<const TI*>(a.B) + c.t0 * a.Bs + static_cast<size_t>(grp) * N, a.Bs, c.rows);
-  load_tile<TI, Q, N, TH>(Ct, static_cast<const TI*>(a.C) + c.t0 * a.Cs + static_cast<size_t>(grp) * N, a.Cs, c.rows);
+    nsteps = reinterpret_cast<const f32x4*>(a.steps)[(slot * a.H + h) * Q + fresh % Q];
+  };
+  auto load_state = [&](f32x8 (&f)[NT][2], const void* from, int h, int half) __attribute__((always_inline)) {
+    const float* m = static_cast<const float*>(from) + ((slot * a.H + h) * halves + half) * static_cast<size_t>(N) * 64;
+    const int fresh = once(lane);
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) f[u][k] = frag_mem(m, n0 + 16 * u, 32 * k, 64, fresh);
+  };
+  load_rows(h0, 0);
+  load_state(G0, a.dS, h0, 0);
+  load_tile<TI, Q, N, TH>(Bt, static_cast<const TI*>(a.B) + t0 * a.Bs + static_cast<size_t>(grp) * N, a.Bs, rows);
+  load_tile<TI, Q, N, TH>(Ct, static_cast<const TI*>(a.C) + t0 * a.Cs + static_cast<size_t>(grp) * N, a.Cs, rows);
   __syncthreads();
-  // of the first role: rows of B, and C B^T
-  Frag<TI> bf[N / 32];
-  f32x4 G[NW];
-  const LaneAt<TI, N> ln(lane);
-#pragma unroll
-  for (int k = 0; k < N / 32; ++k) bf[k] = frag_row(Bt, ln, 16 * jt, 32 * k);
-#pragma unroll
-  for (int t = 0; t < NW; ++t) {
-    G[t] = zero4();
-    if (t >= jt) {
-#pragma unroll
-      for (int k = 0; k < N / 32; ++k) G[t] = mma32(frag_row(Ct, ln, 16 * t, 32 * k), bf[k], G[t]);
-    }
-  }
-  // of the second: tokens t0 16 .., rows n0 .. of B^T and C^T
-  const int ng = w % NG, tt0 = (w / NG) * TT, n0 = ng * NT * 16;
   f32x4 dC[NT][TT], dB[NT][TT];
 #pragma unroll
   for (int u = 0; u < NT; ++u)
 #pragma unroll
     for (int t = 0; t < TT; ++t) dC[u][t] = dB[u][t] = zero4();
 
-  int par = 0;
   for (int h = h0; h < h1; ++h) {
     const float D = a.D ? a.D[h] : 0.f;
-    for (int half = 0; half < halves; ++half, par ^= 1) {
-      load_tile<TI, Q, 64, TH>(xs, static_cast<const TI*>(a.x) + c.t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64, a.xs, c.rows);
-      load_tile<TI, Q, 64, TH>(dys, static_cast<const TI*>(a.dy) + (c.t0 * a.H + h) * a.P + half * 64, static_cast<int64_t>(a.H) * a.P, c.rows);
-      const size_t sat = ((slot * a.H + h) * halves + half) * static_cast<size_t>(N) * 64;
-      load_tile<TI, N, 64, TH>(Gs, static_cast<const TI*>(a.dS) + sat, 64, N);
-      if (tid < Q) {
-        const f32x4 k = reinterpret_cast<const f32x4*>(a.steps)[(slot * a.H + h) * Q + tid];
-        cdt[par][tid] = k[0];
-        chi[par][tid] = k[1];
-        clo[par][tid] = k[2];
-      }
-      __syncthreads();
-      const int fresh = once(lane);
+    for (int half = 0; half < halves; ++half) {
+      const int fresh = once(lane), i = fresh & 15, g = fresh >> 4;
       const LaneAt<TI, N> ln(fresh);
       const LaneAt<TI, 64> lx(fresh);
       const LaneAt<TI, Q> lq(fresh);
-      const float *hiv = chi[par], *lov = clo[par], *dtv = cdt[par];
-      const float hQ = hiv[Q - 1], lQ = lov[Q - 1];
+      {
+        const int ft = once(tid);
+#pragma unroll
+        for (int m = 0; m < XU; ++m) {
+          const int u = ft + TH * m, r = u / (64 / U), at = tile_at<TI, 64>(r, (u % (64 / U)) * U);
+          *reinterpret_cast<uint4*>(xs + at) = kept(r < rows, nx[m]);
+          *reinterpret_cast<uint4*>(dys + at) = kept(r < rows, ny[m]);
+        }
+        if (tid < Q) {
+          cdt[ft] = nsteps[0];
+          chi[ft] = nsteps[1];
+          clo[ft] = nsteps[2];
+        }
+        if (tt0 == 0) {  // dS as the first role's operand
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+              for (int e = 0; e < 8; e += U) {
+                RowVec<TI> v;
+                float f[U];
+#pragma unroll
+                for (int q = 0; q < U; ++q) f[q] = G0[u][k][e + q];
+                v.set(f);
+                *reinterpret_cast<uint4*>(Gs + shifted<LaneAt<TI, 64>>(lx.row, 32 * k + e) + (n0 + 16 * u) * 64) = v.u;
+              }
+            }
+        }
+      }
+      __syncthreads();
+      const bool more = half + 1 < halves || h + 1 < h1;
+      const bool next = half + 1 == halves && more;
+      const int nh = next ? h + 1 : h, nhalf = half + 1 < halves ? half + 1 : next ? 0 : half;
+      load_state(S0, a.S, h, half);
+      load_rows(nh, nhalf);
+      const float hQ = chi[Q - 1], lQ = clo[Q - 1];
 
       {  // first role
         const int row = 16 * jt + i;
-        const float hj = hiv[row], lj = lov[row], dtj = dtv[row], rj = exp2_((hQ - hj) + (lQ - lj));
+        const float hj = chi[row], lj = clo[row], dtj = cdt[row], rj = exp2_((hQ - hj) + (lQ - lj));
         Frag<TI> xf[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) xf[k] = frag_row(xs, lx, 16 * jt, 32 * k);
         f32x4 dx[4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          dx[p] = zero4();
+        for (int p = 0; p < 4; ++p) dx[p] = zero4();
+        Frag<TI> bf[N / 32];
 #pragma unroll
-          for (int k = 0; k < N / 32; ++k) dx[p] = mma32(frag_col<false>(Gs, lx, 32 * k, 16 * p), bf[k], dx[p]);
-          dx[p] *= rj;
+        for (int k = 0; k < N / 32; ++k) {
+          bf[k] = frag_row(Bt, ln, 16 * jt, 32 * k);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) dx[p] = mma32(frag_col<false>(Gs, lx, 32 * k, 16 * p), bf[k], dx[p]);
         }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) dx[p] *= rj;
         float cf = 0.f, diag = 0.f;
 #pragma unroll
         for (int m = 0; m < NW / 2; ++m) {
@@ -503,15 +665,18 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
             W[q] = zero4();
             f32x4 M = zero4();
             if (t >= jt) {
-              f32x4 e = zero4(), f;
+              // C B^T is formed anew for each head: kept, it would spill
+              f32x4 e = zero4(), cb = zero4(), f;
 #pragma unroll
               for (int k = 0; k < 2; ++k) e = mma32(frag_row(dys, lx, 16 * t, 32 * k), xf[k], e);
-              const f32x4 h4 = *reinterpret_cast<const f32x4*>(hiv + i0), l4 = *reinterpret_cast<const f32x4*>(lov + i0);
+#pragma unroll
+              for (int k = 0; k < N / 32; ++k) cb = mma32(frag_row(Ct, ln, 16 * t, 32 * k), bf[k], cb);
+              const f32x4 h4 = *reinterpret_cast<const f32x4*>(chi + i0), l4 = *reinterpret_cast<const f32x4*>(clo + i0);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const float L = i0 + r >= row ? exp2_((h4[r] - hj) + (l4[r] - lj)) : 0.f;
                 if (i0 + r == row) diag += e[r];
-                W[q][r] = L * G[t][r];
+                W[q][r] = L * cb[r];
                 M[r] = L * e[r] * dtj;
                 const float F = W[q][r] * e[r];
                 cf += F;
@@ -532,156 +697,134 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
         if (g == 0) colF[row] = cf;
         diag = sum_wave(diag);
         if (lane == 0) xd[w] = diag;
-        if (row < c.rows) {
-          TI* out = static_cast<TI*>(a.dx) + ((c.t0 + row) * a.H + h) * a.P + half * 64 + 4 * g;
+        if (row < rows) {
+          TI* out = static_cast<TI*>(a.dx) + ((t0 + row) * a.H + h) * a.P + half * 64 + 4 * g;
 #pragma unroll
           for (int p = 0; p < 4; ++p) store4<TI>(out + 16 * p, dtj * dx[p] + D * tile_get4(dys, lx, 16 * jt, 16 * p));
         }
       }
       __syncthreads();
 
-      {  // second role
+      {  // second role: dC, then dB
         float dot = 0.f;
-        Frag<TI> sf[NT][2], sl[NT][2], gf[NT][2], gl[NT][2];
+        Frag<TI> sf[NT][2], sl[NT][2];
 #pragma unroll
         for (int u = 0; u < NT; ++u)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int nr = n0 + 16 * u;
-            sf[u][k] = frag_mem(static_cast<const TI*>(a.S) + sat, nr, 32 * k, 64, fresh);
-            gf[u][k] = frag_mem(static_cast<const TI*>(a.dS) + sat, nr, 32 * k, 64, fresh);
-            if constexpr (kPair) {
-              sl[u][k] = frag_mem(static_cast<const TI*>(a.S_lo) + sat, nr, 32 * k, 64, fresh);
-              gl[u][k] = frag_mem(static_cast<const TI*>(a.dS_lo) + sat, nr, 32 * k, 64, fresh);
-            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if constexpr (kPair) dot += (to_f(sf[u][k][e]) + to_f(sl[u][k][e])) * (to_f(gf[u][k][e]) + to_f(gl[u][k][e]));
-              else dot += sf[u][k][e] * gf[u][k][e];
-            }
+            for (int e = 0; e < 8; ++e) dot += S0[u][k][e] * G0[u][k][e];
+            split2<TI>(S0[u][k], sf[u][k], sl[u][k]);
           }
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           const int tt = tt0 + t, row = 16 * tt + i;
-          const float ei = exp2_(hiv[row] + lov[row]), rj = exp2_((hQ - hiv[row]) + (lQ - lov[row])), dtj = dtv[row];
-          float ic = 0.f, ib = 0.f;
+          const float ei = exp2_(chi[row] + clo[row]);
+          float ic = 0.f;
 #pragma unroll
           for (int u = 0; u < NT; ++u) {
             const int nr = n0 + 16 * u;
-            f32x4 z = zero4(), v = zero4();
+            f32x4 z = zero4();
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const Frag<TI> yf = frag_row(dys, lx, 16 * tt, 32 * k), xf = frag_row(xs, lx, 16 * tt, 32 * k);
+              const Frag<TI> yf = frag_row(dys, lx, 16 * tt, 32 * k);
               z = mma32(sf[u][k], yf, z);
-              v = mma32(gf[u][k], xf, v);
-              if constexpr (kPair) {
-                z = mma32(sl[u][k], yf, z);
-                v = mma32(gl[u][k], xf, v);
-              }
+              if constexpr (kPair) z = mma32(sl[u][k], yf, z);
             }
             z *= ei;
-            v *= rj;
-            const f32x4 c4 = tile_get4(Ct, ln, 16 * tt, nr), b4 = tile_get4(Bt, ln, 16 * tt, nr);
+            const f32x4 c4 = tile_get4(Ct, ln, 16 * tt, nr);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              ic += c4[r] * z[r];
-              ib += b4[r] * v[r];
-            }
+            for (int r = 0; r < 4; ++r) ic += c4[r] * z[r];
             dC[u][t] += z;
-            dB[u][t] += dtj * v;
 #pragma unroll
-            for (int m = 0; m < NW / 2; ++m) {
+            for (int m = 0; m < NW / 2; ++m)
               if (2 * m <= tt) dC[u][t] = mma32(frag_col<false>(Bt, ln, 32 * m, nr), frag_col<false>(MT, lq, 32 * m, 16 * tt), dC[u][t]);
-              if (2 * m + 1 >= tt) dB[u][t] = mma32(frag_col<false>(Ct, ln, 32 * m, nr), frag_row(MT, lq, 16 * tt, 32 * m), dB[u][t]);
-            }
           }
           ic = sum_lane_groups(ic);
-          ib = sum_lane_groups(ib);
-          if (g == 0) {
-            iC[ng][row] = ic;
-            iB[ng][row] = ib;
-          }
+          if (g == 0) iC[ng][row] = ic;
           __builtin_amdgcn_sched_barrier(0);
         }
         dot = sum_wave(dot);
         if (lane == 0) sd[w] = tt0 == 0 ? dot : 0.f;  // waves of the same rows have the same
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) split2<TI>(G0[u][k], sf[u][k], sl[u][k]);
+        load_state(G0, a.dS, nh, nhalf);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const int tt = tt0 + t, row = 16 * tt + i;
+          const float rj = exp2_((hQ - chi[row]) + (lQ - clo[row])), dtj = cdt[row];
+          float ib = 0.f;
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            const int nr = n0 + 16 * u;
+            f32x4 v = zero4();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const Frag<TI> xf = frag_row(xs, lx, 16 * tt, 32 * k);
+              v = mma32(sf[u][k], xf, v);
+              if constexpr (kPair) v = mma32(sl[u][k], xf, v);
+            }
+            v *= rj;
+            const f32x4 b4 = tile_get4(Bt, ln, 16 * tt, nr);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ib += b4[r] * v[r];
+            dB[u][t] += dtj * v;
+#pragma unroll
+            for (int m = 0; m < NW / 2; ++m)
+              if (2 * m + 1 >= tt) dB[u][t] = mma32(frag_col<false>(Ct, ln, 32 * m, nr), frag_row(MT, lq, 16 * tt, 32 * m), dB[u][t]);
+          }
+          ib = sum_lane_groups(ib);
+          if (g == 0) iB[ng][row] = ib;
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
       __syncthreads();
 
-      if (w == 0) {  // the scalars of the head, R tokens a lane
-        constexpr int R = Q / 64;
-        const int t0 = R * once(lane);
-        float dots = 0.f, diag = 0.f, own[R], col[R], before[R], direct[R];
+      {  // what k_ssm_scalars adds up: four lanes a token
+        const int ft = once(tid), t = ft >> 2, part = ft & 3;
+        float rf = 0.f, cc = 0.f, cb = 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) own[r] = before[r] = 0.f;
-#pragma unroll 1
-        for (int k = 0; k < NW; ++k) {
-          dots += sd[k];
-          diag += xd[k];
-          if (t0 / 16 >= own_tile<NW>(k))
+        for (int k = 0; k < NW / 4; ++k)
+          if (t / 16 >= own_tile<NW>(part * (NW / 4) + k)) rf += rowF[part * (NW / 4) + k][t];
 #pragma unroll
-            for (int r = 0; r < R; ++r) own[r] += rowF[k][t0 + r];
+        for (int k = 0; k < NG / 4; ++k) {
+          cc += iC[part * (NG / 4) + k][t];
+          cb += iB[part * (NG / 4) + k][t];
         }
-#pragma unroll 1
-        for (int k = 0; k < NG; ++k)
+        rf = group_sum<4>(rf + cc);
+        cb = group_sum<4>(cb);
+        if (part == 0) {
+          const float col = colF[t], d = cdt[t];
+          f32x4* out = reinterpret_cast<f32x4*>(a.sums) + (slot * a.H + h) * Q + t;
+          f32x4 v = f32x4{rf - d * col, d * cb, col + cb, 0.f};
+          if (half) v += *out;  // the head's first half, of this thread
+          *out = v;
+        }
+        if (tid == 0) {
+          float dots = 0.f, diag = 0.f;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            own[r] += iC[k][t0 + r];
-            before[r] += iB[k][t0 + r];
+          for (int k = 0; k < NW; ++k) {
+            dots += sd[k];
+            diag += xd[k];
           }
-        // dl_t: own over the tokens from t on, before over those before it
-        float sa = 0.f, sb = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          col[r] = colF[t0 + r];
-          direct[r] = col[r] + before[r];
-          own[r] -= dtv[t0 + r] * col[r];
-          before[r] *= dtv[t0 + r];
-          sa += own[r];
-          sb += before[r];
-        }
-        const float lb = sb;
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-          const float da = __shfl_down(sa, o, 64), ub = __shfl_up(sb, o, 64);
-          if (lane + o < 64) sa += da;
-          if (lane >= o) sb += ub;
-        }
-        sb += exp2_(hQ + lQ) * dots - lb;
-        const float Ah = expf(a.A_log[h]);
-        const size_t at = (slot * a.H + h) * Q + t0;
-        float dA = 0.f, db = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float dl = sa + sb;
-          sa -= own[r];
-          sb += before[r];
-          float d = (direct[r] - Ah * dl) * a.steps[4 * (at + r) + 3];
-          dA -= Ah * dtv[t0 + r] * dl;
-          db += d;
-          if (halves > 1) {  // of two halves of a head the second adds to the first's
-            if (half) d += a.ddt_half[at + r];
-            else a.ddt_half[at + r] = d;
-          }
-          if (t0 + r < c.rows && half == halves - 1) static_cast<TI*>(a.ddt)[(c.t0 + t0 + r) * a.H + h] = from_f<TI>(d);
-        }
-        dA = sum_wave(dA);
-        db = sum_wave(db);
-        if (lane == 0) {
-          float *p2 = a.part2 + slot * 2 * a.H + h, *p1 = a.part1 + slot * a.H + h;
-          *p2 = half ? *p2 + dA : dA;
-          p2[a.H] = half ? p2[a.H] + db : db;
-          *p1 = half ? *p1 + diag : diag;
+          float* out = a.ends + 2 * (slot * a.H + h);
+          dots *= exp2_(hQ + lQ);
+          out[0] = half ? out[0] + dots : dots;
+          out[1] = half ? out[1] + diag : diag;
         }
       }
+      if (more) __syncthreads();
     }
   }
   // dB and dC of the heads: to the outputs, or to this set's partial sums
+  const int i = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     const int row = 16 * (tt0 + t) + i;
-    if (row >= c.rows) continue;
-    const size_t at = ((c.t0 + row) * a.G + grp) * N + n0 + 4 * g;
+    if (row >= rows) continue;
+    const size_t at = ((t0 + row) * a.G + grp) * N + n0 + 4 * g;
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       if (a.sets == 1) {
@@ -693,6 +836,62 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
         store4<float>(a.pC + far + at + 16 * u, dC[u][t]);
       }
     }
+  }
+}
+
+// One wave per (chunk, head), Q / 64 tokens a lane: the gradient of each token's
+// log decay, of the step sizes, and the chunk's parts of the parameters'.
+template <typename TI>
+__global__ void __launch_bounds__(256) k_ssm_scalars(SsmArgs a) {
+  constexpr int Q = Chunk<TI>::Q, R = Q / 64;
+  const int nhb = (a.H + 3) / 4;
+  const int64_t slot = blockIdx.x / nhb;
+  const int h = (blockIdx.x % nhb) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (h >= a.H) return;
+  const Place c = find_piece(a, slot, Q);
+  float *p2 = a.part2 + slot * 2 * a.H + h, *p1 = a.part1 + slot * a.H + h;
+  if (c.rows <= 0) {  // its parts are added up all the same
+    if (lane == 0) p2[0] = p2[a.H] = p1[0] = 0.f;
+    return;
+  }
+  const int64_t at = (slot * a.H + h) * Q + R * lane;
+  f32x4 v[R], st[R];
+  float sa = 0.f, sb = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    v[r] = reinterpret_cast<const f32x4*>(a.sums)[at + r];
+    st[r] = reinterpret_cast<const f32x4*>(a.steps)[at + r];
+    sa += v[r][0];
+    sb += v[r][1];
+  }
+  const float q0 = a.ends[2 * (slot * a.H + h)], diag = a.ends[2 * (slot * a.H + h) + 1];
+  const float lb = sb;
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const float da = __shfl_down(sa, o, 64), ub = __shfl_up(sb, o, 64);
+    if (lane + o < 64) sa += da;
+    if (lane >= o) sb += ub;
+  }
+  sb += q0 - lb;
+  // dl_t: the first sums from t on, the second before t, and the states'
+  const float Ah = expf(a.A_log[h]);
+  float dA = 0.f, db = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float dl = sa + sb, d = (v[r][2] - Ah * dl) * st[r][3];
+    sa -= v[r][0];
+    sb += v[r][1];
+    dA -= Ah * st[r][0] * dl;
+    db += d;
+    const int t = R * lane + r;
+    if (t < c.rows) static_cast<TI*>(a.ddt)[(c.t0 + t) * a.H + h] = from_f<TI>(d);
+  }
+  dA = sum_wave(dA);
+  db = sum_wave(db);
+  if (lane == 0) {
+    p2[0] = dA;
+    p2[a.H] = db;
+    p1[0] = diag;
   }
 }
 
@@ -718,17 +917,14 @@ unsigned out_rest(const SsmArgs& a, int64_t bytes) {
   return a.cu ? rest_blocks(true, bytes, 1024) : 0;
 }
 
+// One or both directions; in segments two launches.
 template <typename TI, int N>
-hipError_t launch_state_n(bool reverse, const SsmArgs& a, hipStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.n_seqs) * a.H * (a.P / 64) * (N / 32);
-  const bool lo = sizeof(TI) == 2 && (reverse || a.S_lo);
-  if (reverse) {
-    if (lo) k_ssm_state<TI, N, true, true><<<grid, 256, 0, s>>>(a);
-    else k_ssm_state<TI, N, true, false><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (lo) k_ssm_state<TI, N, false, true><<<grid, 256, 0, s>>>(a);
-    else k_ssm_state<TI, N, false, false><<<grid, 256, 0, s>>>(a);
-  }
+hipError_t launch_state_n(int dirs, int dir0, const SsmArgs& a, hipStream_t s) {
+  const unsigned blocks = static_cast<unsigned>(a.seg ? a.seg_slots : a.n_seqs) * dirs * a.H * (a.P / 64) * (N / 32);
+  const unsigned grid = (blocks + 7) / 8 * 8;
+  if (a.seg) k_ssm_state<TI, N, kLocal><<<grid, 256, 0, s>>>(a, dirs, dir0, blocks);
+  if (a.S_full) k_ssm_state<TI, N, kFullStates><<<grid, 256, 0, s>>>(a, dirs, dir0, blocks);
+  else k_ssm_state<TI, N, kStates><<<grid, 256, 0, s>>>(a, dirs, dir0, blocks);
   return hipGetLastError();
 }
 template <typename TI, int N>
@@ -752,9 +948,15 @@ hipError_t launch_ssm_steps(int dtype, const SsmArgs& a, hipStream_t s) {
   else k_ssm_steps<bf16><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
-hipError_t launch_ssm_state(int dtype, int N, bool reverse, const SsmArgs& a, hipStream_t s) {
-  if (dtype == KDA_F32) return N == 64 ? launch_state_n<float, 64>(reverse, a, s) : launch_state_n<float, 128>(reverse, a, s);
-  return N == 64 ? launch_state_n<bf16, 64>(reverse, a, s) : launch_state_n<bf16, 128>(reverse, a, s);
+hipError_t launch_ssm_state(int dtype, int N, int dirs, int dir0, const SsmArgs& a, hipStream_t s) {
+  if (dtype == KDA_F32) return N == 64 ? launch_state_n<float, 64>(dirs, dir0, a, s) : launch_state_n<float, 128>(dirs, dir0, a, s);
+  return N == 64 ? launch_state_n<bf16, 64>(dirs, dir0, a, s) : launch_state_n<bf16, 128>(dirs, dir0, a, s);
+}
+hipError_t launch_ssm_scalars(int dtype, const SsmArgs& a, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>(a.slots) * ((a.H + 3) / 4);
+  if (dtype == KDA_F32) k_ssm_scalars<float><<<grid, 256, 0, s>>>(a);
+  else k_ssm_scalars<bf16><<<grid, 256, 0, s>>>(a);
+  return hipGetLastError();
 }
 hipError_t launch_ssm_out(int dtype, int N, const SsmArgs& a, hipStream_t s) {
   if (dtype == KDA_F32) return N == 64 ? launch_out_n<float, 64>(a, s) : launch_out_n<float, 128>(a, s);
