@@ -52,9 +52,12 @@ struct SsmArgs {
   // Of the gradients: per token {what dl adds up from it on, before it, the step
   // size's own part} [slots][H][Q] of four, per chunk {states' part of dl, dD}.
   float *sums, *ends;
-  float *pB, *pC;        // partial dB and dC [sets][T][G][N] where sets > 1
+  float *pB, *pC;        // partial dB and dC [blocks behind the whole ones][Q][N] where sets > 1
   float *part2, *part1;  // per slot {dA, ddt_bias} [2 H] and dD [H]
-  int hb, sets;          // heads of a group a block takes in turn, blocks a group
+  // Blocks that take all heads of a group in a chunk, and into how many the heads
+  // of each chunk and group behind those are divided.
+  unsigned whole;
+  int sets;
 };
 hipError_t launch_ssm_steps(int dtype, const SsmArgs& a, hipStream_t s);
 // `dirs` directions from dir0: 0 in sequence order, 1 (gradients) back.

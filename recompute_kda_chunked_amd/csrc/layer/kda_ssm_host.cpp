@@ -29,23 +29,35 @@ int check_ssm(const kda_ssm_problem* p) {
 // The scan's launches and its workspace, in parts that start at multiples of 256
 // bytes.
 struct ScanPlan {
-  int Q, hb, sets, seg = 0;
-  int64_t slots, seg_slots = 0;
+  int Q, sets = 1, seg = 0;
+  int64_t slots, whole, seg_slots = 0;
   size_t steps, state, dstate = 0, local, seg_log, sums = 0, ends = 0, partial = 0, part2 = 0, part1 = 0;
   ScanPlan(const kda_ssm_problem* p, bool bwd) {
     Q = ssm_chunk(p->dtype);
     const int64_t T = p->total_tokens, HP = static_cast<int64_t>(p->H) * p->P;
     slots = T / Q + p->n_seqs;
-    // heads a block takes: as many of a group as leave the launch enough blocks
+    // A block takes the heads of a group in turn, as many rounds of blocks as fill
+    // the chip; the chunks and groups left over are divided by heads, into as many
+    // blocks as cost least: rounds times a block's heads and a part of one for its
+    // start, and backward the partial sums of dB and dC.
     const int per = p->H / p->G;
-    hb = per;
-    while (hb > 1 && slots * p->G * ((per + hb - 1) / hb) < (bwd ? 512 : 1024)) hb = (hb + 1) / 2;
-    sets = (per + hb - 1) / hb;
+    const int64_t units = slots * p->G, round = bwd ? 256 : 512;
+    whole = units / round * round;
+    double best = 0.0;
+    for (int k = 1; k <= per; ++k) {
+      const int64_t blocks = (units - whole) * k;
+      const double cost = static_cast<double>((blocks + round - 1) / round) * ((per + k - 1) / k + 0.5) +
+                          (bwd && k > 1 ? 0.004 * blocks : 0.0);
+      if (k == 1 || cost < best) {
+        best = cost;
+        sets = k;
+      }
+    }
     // a sequence's states in segments, where one sequence alone would leave most
     // of the chip idle
     const int dirs = bwd ? 2 : 1;
-    const int64_t chunks = (T + Q - 1) / Q, chain = dirs * (HP / 64) * (p->N / 32);
-    const int64_t want = 1024 / chain < 32 ? 1024 / chain : 32;
+    const int64_t chunks = (T + Q - 1) / Q, chain = dirs * (HP / 64);
+    const int64_t want = 512 / chain < 32 ? 512 / chain : 32;
     if (want > 1 && chunks >= 8) {
       seg = static_cast<int>((chunks + want - 1) / want);
       if (seg < 4) seg = 4;
@@ -60,7 +72,7 @@ struct ScanPlan {
       dstate = state;
       sums = steps;
       ends = part(slots * p->H * 2, 4);
-      partial = sets > 1 ? part(T * p->G * p->N * sets, 4) : 0;
+      partial = sets > 1 ? part((units - whole) * sets * Q * p->N, 4) : 0;
       part2 = part(slots * p->H * 2, 4);
       part1 = part(slots * p->H, 4);
     }
@@ -78,6 +90,10 @@ int check_scan(const kda_ssm_problem* p, bool has_cu) {
   if (st != KDA_OK) return st;
   if (!has_cu && p->n_seqs != 1) return KDA_ERR_INVALID;
   const int64_t T = p->total_tokens, slots = T / 64 + p->n_seqs, H = p->H;
+  // rows of a chunk in 32 bits
+  constexpr int64_t most = 1 << 22;
+  if (H * p->P >= most || int64_t{p->G} * p->N >= most) return KDA_ERR_UNSUPPORTED;
+  if (T > 1 && (p->x_stride >= most || p->B_stride >= most || p->C_stride >= most)) return KDA_ERR_UNSUPPORTED;
   if (H > (1 << 20) || slots * H >= (int64_t{1} << 26) || slots * H * p->N * p->P >= (int64_t{1} << 40))
     return KDA_ERR_UNSUPPORTED;
   if (slots * H >= (1 << 23) - 1024 || slots * ((H + 3) / 4) >= (1 << 24) ||
@@ -131,7 +147,7 @@ SsmArgs scan_args(const kda_ssm_problem* p, const ScanPlan& plan, const void* x,
   a.part1 = reinterpret_cast<float*>(take(plan.part1));
   a.seg = plan.seg;
   a.seg_slots = plan.seg_slots;
-  a.hb = plan.hb;
+  a.whole = static_cast<unsigned>(plan.whole);
   a.sets = plan.sets;
   return a;
 }
@@ -244,7 +260,8 @@ int kda_ssm_bwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, con
   if (a.T > 0) {
     KDA_TRY(KDA_KERNEL_SSM_GRAD, units, launch_ssm_grad(p->dtype, p->N, a, s));
     KDA_TRY(KDA_KERNEL_SSM_GRAD, units, launch_ssm_scalars(p->dtype, a, s));
-    if (a.sets > 1) KDA_TRY(KDA_KERNEL_SSM_REDUCE, a.T, launch_ssm_reduce(p->dtype, p->N, a, s));
+    if (a.sets > 1 && plan.whole < a.slots * a.G)
+      KDA_TRY(KDA_KERNEL_SSM_REDUCE, a.T, launch_ssm_reduce(p->dtype, p->N, a, s));
   }
   // without tokens the sums are empty
   const int64_t nb = a.T > 0 ? a.slots : 0;

@@ -126,13 +126,47 @@ __global__ void __launch_bounds__(256) k_ssm_steps(SsmArgs a) {
 
 // ------------------------------------------------------------ states
 
-// Rows behind a chunk's last are read as its last and made zero at their use, and
-// what is loaded ahead at the end is loaded twice: a load under a condition would
-// be waited for where the condition ends.
-__device__ __forceinline__ uint4 kept(bool keep, uint4 v) {
-  return keep ? v : make_uint4(0, 0, 0, 0);
+// A chunk's R rows of COLS columns on their way to a tile: 16-byte units, thread
+// t's m-th unit number t + TH m. Addresses are a base that the block shares plus
+// 32 bits (token strides are below 2^22 elements). Rows behind the chunk's last
+// are read as its last and made zero when they are stored, and what is loaded
+// ahead at the end is loaded twice: a load under a condition would be waited for
+// where the condition ends. For the same reason nothing is computed from a load
+// before its use, and no part of one is left unused: its registers would be given
+// to other values, which wait for it.
+template <typename TI, int R, int COLS, int TH>
+struct Rows {
+  static constexpr int U = 16 / sizeof(TI), PER = R * COLS / U / TH, RPM = TH / (COLS / U);
+  static_assert(RPM % 8 == 0, "a thread's units lie whole periods of the tile's order apart, or half ones");
+  uint4 v[PER];
+  __device__ __forceinline__ void load(const TI* base, uint32_t stride, int rows, int tid) {
+    const uint32_t r0 = static_cast<uint32_t>(tid) / (COLS / U), col = 16 * (static_cast<uint32_t>(tid) % (COLS / U));
+    const uint32_t last = static_cast<uint32_t>(rows - 1);
+#pragma unroll
+    for (int m = 0; m < PER; ++m) {
+      const uint32_t r = r0 + RPM * m, at = r < last ? r : last;
+      v[m] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(base) + (__umul24(at, stride * static_cast<uint32_t>(sizeof(TI))) + col));
+    }
+  }
+  static __device__ __forceinline__ int place(int tid, int m) {
+    const int at = tile_at<TI, COLS>(tid / (COLS / U), (tid % (COLS / U)) * U);
+    return (at ^ (RPM * m & 8 ? TileFlip<TI, COLS>::units(8) * U : 0)) + m * RPM * COLS;
+  }
+  __device__ __forceinline__ uint4 kept(int rows, int tid, int m) const {
+    return tid / (COLS / U) + RPM * m < rows ? v[m] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void store(TI* tile, int rows, int tid) const {
+#pragma unroll
+    for (int m = 0; m < PER; ++m) *reinterpret_cast<uint4*>(tile + place(tid, m)) = kept(rows, tid, m);
+  }
+};
+// A token's step size and running sum.
+struct Step {
+  float dt, hi, lo;
+};
+__device__ __forceinline__ Step load_step(const float* steps, int64_t at) {
+  return *reinterpret_cast<const Step*>(steps + 4 * at);
 }
-__device__ __forceinline__ int row_or_last(int r, int rows) { return r < rows ? r : rows - 1; }
 
 // Blocks of consecutive numbers on one XCD (the hardware deals them out in turn
 // over eight), for those that read the same rows. `total` is a multiple of 8.
@@ -159,25 +193,24 @@ struct Terms {
   }
 };
 
-// One block walks the chunks of a segment with 64 columns and 32 rows of one
-// head's state: S' = e^tot S + (w B)^T x, w_j = dt_j exp(cum_Q - cum_j); in
-// reverse dS = e^tot dS' + (w C)^T dy, w_i = exp(cum_i). The weighted rows are
-// three bf16 each, x and dy are exact, so that states are fp32 states. A wave
-// holds 32 columns by 16 rows of the transposed state, a lane four columns of a
-// row of each of its two tiles.
+// One block walks the chunks of a segment with 64 columns of one head's state:
+// S' = e^tot S + B^T (w x), w_j = dt_j exp(cum_Q - cum_j); in reverse
+// dS = e^tot dS' + C^T (w dy), w_i = exp(cum_i). The weighted rows are three bf16
+// each, B and C are exact, so that states are fp32 states. A wave holds 32 columns
+// by half the rows of the transposed state, a lane four columns of a row of each
+// of its tiles.
 //
-// A sequence is one segment where the launch has blocks enough; otherwise LOCAL
+// A sequence is one segment where the launch has blocks enough; otherwise kLocal
 // leaves what each segment adds to a state that enters it as zero, and the second
 // launch starts each segment from the states that the ones before it have left.
 enum { kLocal = 0, kStates = 1, kFullStates = 2 };  // leave what a segment adds; states in TI; in fp32
 template <typename TI, int N, int MODE>
-__global__ void __launch_bounds__(256) k_ssm_state(SsmArgs a, int dirs, int dir0, unsigned blocks) {
-  constexpr int Q = Chunk<TI>::Q, U = 16 / sizeof(TI), NB = 32;
-  constexpr int XU = Q * 64 / U / 256, BU = Q * NB / U / 256;  // 16-byte units a thread
+__global__ void __launch_bounds__(256, 2) k_ssm_state(SsmArgs a, int dirs, int dir0, unsigned blocks) {
+  constexpr int Q = Chunk<TI>::Q, U = 16 / sizeof(TI), NT = N / 32;
   constexpr int K = Terms<TI>::K;
   constexpr bool LOCAL = MODE == kLocal;
-  __shared__ __align__(16) TI xs[Q * 64], bs[K][Q * NB];
-  const int halves = a.P / 64, nsplit = N / NB, seg = a.seg;
+  __shared__ __align__(16) TI bs[Q * N], xs[K][Q * 64];
+  const int halves = a.P / 64, seg = a.seg;
   unsigned b = on_one_xcd(blockIdx.x, gridDim.x);
   if (b >= blocks) return;
   // heads vary slowest: each XCD has some of them, with all their segments,
@@ -185,8 +218,6 @@ __global__ void __launch_bounds__(256) k_ssm_state(SsmArgs a, int dirs, int dir0
   const unsigned per_head = blocks / (a.H * halves);
   const int hp = b / per_head, h = hp / halves, half = hp % halves;
   b %= per_head;
-  const int n0 = (b % nsplit) * NB;
-  b /= nsplit;
   const int rev = dirs > 1 ? b % 2 : dir0;
   const int64_t sslot = dirs > 1 ? b / 2 : b;
   // without segments a slot is a sequence, also one without tokens
@@ -205,131 +236,161 @@ __global__ void __launch_bounds__(256) k_ssm_state(SsmArgs a, int dirs, int dir0
   if (LOCAL && ends) return;
   const int grp = h / (a.H / a.G);
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), i = lane & 15, g = lane >> 4;
-  const int p0 = 32 * (w & 1), nt = 16 * (w >> 1);
+  const int p0 = 32 * (w & 1), nt = (N / 2) * (w >> 1);
   const int64_t t0 = c.t0;
-  const int nch = (c.rows + Q - 1) / Q;
+  const int tokens = c.rows, nch = (tokens + Q - 1) / Q;
   const int64_t first = static_cast<uint32_t>(c.s0) / Q + c.n + (t0 - c.s0) / Q;  // slot of the first chunk
   const TI* src = static_cast<const TI*>(rev ? a.dy : a.x) + static_cast<size_t>(h) * a.P + half * 64;
   const int64_t sst = rev ? static_cast<int64_t>(a.H) * a.P : a.xs;
-  const TI* rsrc = static_cast<const TI*>(rev ? a.C : a.B) + static_cast<size_t>(grp) * N + n0;
+  const TI* rsrc = static_cast<const TI*>(rev ? a.C : a.B) + static_cast<size_t>(grp) * N;
   const int64_t rst = rev ? a.Cs : a.Bs;
   const float* from = rev ? a.dfinal : a.init;
   float* to = rev ? a.dinit : a.final_state;
-  const size_t state = ((static_cast<size_t>(c.n) * a.H + h) * N + n0 + nt + i) * a.P + half * 64 + p0 + 4 * g;
+  const size_t state = ((static_cast<size_t>(c.n) * a.H + h) * N + nt + i) * a.P + half * 64 + p0 + 4 * g;
   // of a segment's own slot: [H][halves][N][64]
-  const int64_t sslots = a.seg_slots;
-  float* local = a.local + static_cast<size_t>(rev) * sslots * a.H * halves * N * 64 + (static_cast<size_t>(hp) * N + n0 + nt + i) * 64 + p0 + 4 * g;
-  const size_t lstep = static_cast<size_t>(a.H) * halves * N * 64;
+  const size_t tile = (static_cast<size_t>(hp) * N + nt + i) * 64 + p0 + 4 * g, step = static_cast<size_t>(a.H) * halves * N * 64;
+  float* local = a.local + rev * a.seg_slots * step + tile;
 
   const LaneAt<TI, 64> lx(lane);
-  const LaneAt<TI, NB> lb(lane);
-  f32x4 acc[2];
+  const LaneAt<TI, N> lb(lane);
+  f32x4 acc[NT][2];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-    acc[t] = from && !LOCAL ? *reinterpret_cast<const f32x4*>(from + state + 16 * t) : zero4();
+  for (int u = 0; u < NT; ++u)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      acc[u][t] = from && !LOCAL ? *reinterpret_cast<const f32x4*>(from + state + static_cast<size_t>(16 * u) * a.P + 16 * t) : zero4();
   if (!LOCAL && seg) {
     for (int k = 0; k < (rev ? segs - 1 - c.pos : c.pos); ++k) {
       const int64_t at = sslot - c.pos + (rev ? segs - 1 - k : k);
-      const float d = exp2_(a.seg_log[(rev * sslots + at) * a.H + h]);
+      const float d = exp2_(a.seg_log[(rev * a.seg_slots + at) * a.H + h]);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) acc[t] = d * acc[t] + *reinterpret_cast<const f32x4*>(local + at * lstep + 16 * t);
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          acc[u][t] = d * acc[u][t] + *reinterpret_cast<const f32x4*>(local + at * step + 16 * u * 64 + 16 * t);
     }
   }
 
-  struct Stage {
-    uint4 x[XU], b[BU];
-    f32x4 k[BU], end;  // step sizes: nothing is computed from a load before its use
-  };
-  auto load = [&](int k, Stage& st) __attribute__((always_inline)) {
-    const int ch = rev ? nch - 1 - k : k;
+  using RX = Rows<TI, Q, 64, 256>;
+  RX rx;
+  Rows<TI, Q, N, 256> rb;
+  Step rk[RX::PER];
+  float end_hi, end_lo;
+  auto load = [&](int k) __attribute__((always_inline)) {
+    const int ch = rev ? nch - 1 - k : k, rows = tokens - ch * Q;
     const int64_t at = t0 + static_cast<int64_t>(ch) * Q;
-    const int rows = c.rows - ch * Q < Q ? c.rows - ch * Q : Q;
-    const f32x4* steps = reinterpret_cast<const f32x4*>(a.steps) + ((first + ch) * a.H + h) * Q;
-    st.end = steps[Q - 1];
+    const float* steps = a.steps + ((first + ch) * a.H + h) * (4 * Q);
+    end_hi = steps[4 * Q - 3];
+    end_lo = steps[4 * Q - 2];
+    rx.load(src + at * sst, static_cast<uint32_t>(sst), rows, tid);
 #pragma unroll
-    for (int m = 0; m < XU; ++m) {
-      const int u = tid + 256 * m, r = u / (64 / U);
-      st.x[m] = *reinterpret_cast<const uint4*>(src + (at + row_or_last(r, rows)) * sst + (u % (64 / U)) * U);
-    }
-#pragma unroll
-    for (int m = 0; m < BU; ++m) {
-      const int u = tid + 256 * m, r = u / (NB / U);
-      st.b[m] = *reinterpret_cast<const uint4*>(rsrc + (at + row_or_last(r, rows)) * rst + (u % (NB / U)) * U);
-      st.k[m] = steps[r];
-    }
+    for (int m = 0; m < RX::PER; ++m) rk[m] = load_step(steps, tid / (64 / U) + RX::RPM * m);
+    rb.load(rsrc + at * rst, static_cast<uint32_t>(rst), rows, tid);
   };
   double total = 0.0;
-  auto step = [&](int k, Stage& st) __attribute__((always_inline)) {
+  if (nch > 0) load(0);
+  for (int k = 0; k < nch; ++k) {
     const int ch = rev ? nch - 1 - k : k;
-    const int rows = c.rows - ch * Q;
+    const int rows = tokens - ch * Q;
     __syncthreads();
+    rb.store(bs, rows, tid);
 #pragma unroll
-    for (int m = 0; m < XU; ++m) {
-      const int u = tid + 256 * m, r = u / (64 / U);
-      *reinterpret_cast<uint4*>(xs + tile_at<TI, 64>(r, (u % (64 / U)) * U)) = kept(r < rows, st.x[m]);
-    }
-#pragma unroll
-    for (int m = 0; m < BU; ++m) {
-      const int u = tid + 256 * m, at = tile_at<TI, NB>(u / (NB / U), (u % (NB / U)) * U);
+    for (int m = 0; m < RX::PER; ++m) {
       RowVec<TI> v, t[K];
       float f[U];
-      v.u = kept(u / (NB / U) < rows, st.b[m]);
+      v.u = rx.kept(rows, tid, m);
       v.get(f);
-      const f32x4 k4 = st.k[m];
-      const float wt = rev ? exp2_(k4[1] + k4[2]) : k4[0] * exp2_((st.end[1] - k4[1]) + (st.end[2] - k4[2]));
+      const float wt = rev ? exp2_(rk[m].hi + rk[m].lo) : rk[m].dt * exp2_((end_hi - rk[m].hi) + (end_lo - rk[m].lo));
 #pragma unroll
       for (int e = 0; e < U; ++e) f[e] *= wt;
       Terms<TI>::split(f, t);
 #pragma unroll
-      for (int q = 0; q < K; ++q) *reinterpret_cast<uint4*>(bs[q] + at) = t[q].u;
+      for (int q = 0; q < K; ++q) *reinterpret_cast<uint4*>(xs[q] + RX::place(tid, m)) = t[q].u;
     }
-    const float log = st.end[1] + st.end[2], decay = exp2_(log);
+    const float log = end_hi + end_lo, decay = exp2_(log);
     total += log;
     __syncthreads();
-    load(k + 2 < nch ? k + 2 : nch - 1, st);
+    load(k + 1 < nch ? k + 1 : k);
     if constexpr (!LOCAL) {
-      const size_t at = (((first + ch) * a.H * halves + hp) * N + n0 + nt + i) * 64 + p0 + 4 * g;
+      const size_t at = (first + ch) * step + tile;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if constexpr (MODE == kFullStates) store4<float>(static_cast<float*>(rev ? a.dS : a.S) + at + 16 * t, acc[t]);
-        else store4<TI>(static_cast<TI*>(a.S) + at + 16 * t, acc[t]);
-      }
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if constexpr (MODE == kFullStates) store4<float>(static_cast<float*>(rev ? a.dS : a.S) + at + 16 * u * 64 + 16 * t, acc[u][t]);
+          else store4<TI>(static_cast<TI*>(a.S) + at + 16 * u * 64 + 16 * t, acc[u][t]);
+        }
     }
 #pragma unroll
-    for (int t = 0; t < 2; ++t) acc[t] *= decay;
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) acc[u][t] *= decay;
+    // operands a step ahead of their products: the wave waits for no read
+    struct Operands {
+      Frag<TI> x[2][K], b[NT];
+    } f[2];
+    auto read = [&](int k0, Operands& o) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int q = 0; q < K; ++q) o.x[t][q] = frag_col<false>(xs[q], lx, k0, p0 + 16 * t);
+#pragma unroll
+      for (int u = 0; u < NT; ++u) o.b[u] = frag_col<false>(bs, lb, k0, nt + 16 * u);
+    };
+    read(0, f[0]);
 #pragma unroll
     for (int k0 = 0; k0 < Q; k0 += 32) {
-      Frag<TI> bf[K];
+      Operands& o = f[(k0 / 32) % 2];
+      if (k0 + 32 < Q) read(k0 + 32, f[(k0 / 32 + 1) % 2]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int q = 0; q < K; ++q) bf[q] = frag_col<false>(bs[q], lb, k0, nt);
+      for (int q = K - 1; q >= 0; --q)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const Frag<TI> ax = frag_col<false>(xs, lx, k0, p0 + 16 * t);
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int q = K - 1; q >= 0; --q) acc[t] = mma32(ax, bf[q], acc[t]);
-      }
+          for (int t = 0; t < 2; ++t) acc[u][t] = mma32(o.x[t][q], o.b[u], acc[u][t]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-  };
-  Stage s0, s1;  // chunks are loaded two ahead
-  if (nch > 0) {
-    load(0, s0);
-    load(nch > 1 ? 1 : 0, s1);
-  }
-  for (int k = 0; k < nch; k += 2) {
-    step(k, s0);
-    if (k + 1 < nch) step(k + 1, s1);
   }
   if constexpr (LOCAL) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) *reinterpret_cast<f32x4*>(local + sslot * lstep + 16 * t) = acc[t];
-    if (tid == 0 && n0 == 0 && half == 0) a.seg_log[(rev * sslots + sslot) * a.H + h] = static_cast<float>(total);
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) *reinterpret_cast<f32x4*>(local + sslot * step + 16 * u * 64 + 16 * t) = acc[u][t];
+    if (tid == 0 && half == 0) a.seg_log[(rev * a.seg_slots + sslot) * a.H + h] = static_cast<float>(total);
   } else if (to && ends) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) *reinterpret_cast<f32x4*>(to + state + 16 * t) = acc[t];
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        *reinterpret_cast<f32x4*>(to + state + static_cast<size_t>(16 * u) * a.P + 16 * t) = acc[u][t];
   }
 }
 
 // ------------------------------------------------------------ shared by out and grad
+
+__host__ __device__ inline unsigned own_blocks(const SsmArgs& a) {
+  return a.whole + (static_cast<unsigned>(a.slots) * a.G - a.whole) * a.sets;
+}
+// What block b of k_ssm_out and k_ssm_grad does: the heads [h0, h1) of a group in
+// a chunk, all of them in the first a.whole blocks, a.sets blocks a chunk and
+// group behind those.
+struct Unit {
+  int64_t slot;
+  int grp, set, h0, h1;
+};
+__device__ __forceinline__ Unit unit_of(const SsmArgs& a, unsigned b) {
+  const int per = a.H / a.G;
+  const unsigned k = b < a.whole ? 0 : b - a.whole, unit = b < a.whole ? b : a.whole + k / a.sets;
+  Unit u;
+  u.set = k % a.sets;
+  u.grp = unit % a.G;
+  u.slot = unit / a.G;
+  const int hb = b < a.whole ? per : (per + a.sets - 1) / a.sets, last = (u.set + 1) * hb;
+  u.h0 = u.grp * per + (u.set * hb < per ? u.set * hb : per);
+  u.h1 = u.grp * per + (last < per ? last : per);
+  return u;
+}
 
 // A wave's tile of 16 tokens: those of wave w and w + NW / 2, which share a
 // SIMD, are as far from the diagonal's ends as each other, so that every SIMD
@@ -337,24 +398,6 @@ __global__ void __launch_bounds__(256) k_ssm_state(SsmArgs a, int dirs, int dir0
 template <int NW>
 __device__ __forceinline__ int own_tile(int w) {
   return w < NW / 2 ? w : NW - 1 - (w - NW / 2);
-}
-
-// COLS columns of `rows` rows `st` apart to a tile of Q rows (zeros behind).
-template <typename TI, int R, int COLS, int THREADS>
-__device__ __forceinline__ void load_tile(TI* tile, const TI* src, int64_t st, int rows) {
-  constexpr int U = 16 / sizeof(TI), PER = R * COLS / U / THREADS;
-  const int tid = once(threadIdx.x);
-  uint4 v[PER];
-#pragma unroll
-  for (int m = 0; m < PER; ++m) {
-    const int u = tid + THREADS * m, r = u / (COLS / U);
-    v[m] = *reinterpret_cast<const uint4*>(src + row_or_last(r, rows) * st + (u % (COLS / U)) * U);
-  }
-#pragma unroll
-  for (int m = 0; m < PER; ++m) {
-    const int u = tid + THREADS * m;
-    *reinterpret_cast<uint4*>(tile + tile_at<TI, COLS>(u / (COLS / U), (u % (COLS / U)) * U)) = kept(u / (COLS / U) < rows, v[m]);
-  }
 }
 
 // Zeroes `width` elements of each row that belongs to no sequence.
@@ -371,29 +414,34 @@ __device__ __forceinline__ void zero_rows(T* o, int64_t width, const SsmArgs& a,
 // Wave: 16 tokens i of the chunk. Scores are formed as [j][i] accumulators, an
 // operand as they stand of y^T[p][i] = sum_j x_j[p] (L G dt)_ij.
 template <typename TI, int N>
-__global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_out(SsmArgs a) {
+__global__ void __launch_bounds__(4 * Chunk<TI>::Q, sizeof(TI) == 2 ? 4 : 2) k_ssm_out(SsmArgs a) {
   constexpr int Q = Chunk<TI>::Q, NW = Q / 16, TH = 64 * NW;
   __shared__ __align__(16) TI buf[2 * Q * N];
   __shared__ float chi[Q], clo[Q], cdt[Q];
-  const unsigned own = static_cast<unsigned>(a.slots) * a.G * a.sets;
+  const unsigned own = own_blocks(a);
   if (blockIdx.x >= own) {
     zero_rows(static_cast<TI*>(a.y), static_cast<int64_t>(a.H) * a.P, a, blockIdx.x - own, gridDim.x - own);
     return;
   }
-  const int set = blockIdx.x % a.sets, grp = (blockIdx.x / a.sets) % a.G;
-  const int64_t slot = blockIdx.x / (a.sets * a.G);
+  const Unit unit = unit_of(a, blockIdx.x);
+  const int64_t slot = unit.slot;
+  const int grp = unit.grp, h0 = unit.h0, h1 = unit.h1;
   const Place c = find_piece(a, slot, Q);
   const int rows = c.rows;
   const int64_t t0 = c.t0;
-  if (rows <= 0) return;
+  if (rows <= 0 || h0 >= h1) return;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), i = lane & 15, g = lane >> 4;
-  const int it = own_tile<NW>(w), per = a.H / a.G, halves = a.P / 64;
-  const int h0 = grp * per + set * a.hb, h1 = set * a.hb + a.hb < per ? h0 + a.hb : (grp + 1) * per;
+  const int it = own_tile<NW>(w), halves = a.P / 64;
 
   const LaneAt<TI, N> ln(lane);
   TI *Bt = buf, *Ct = buf + Q * N;
-  load_tile<TI, Q, N, TH>(Bt, static_cast<const TI*>(a.B) + t0 * a.Bs + static_cast<size_t>(grp) * N, a.Bs, rows);
-  load_tile<TI, Q, N, TH>(Ct, static_cast<const TI*>(a.C) + t0 * a.Cs + static_cast<size_t>(grp) * N, a.Cs, rows);
+  {
+    Rows<TI, Q, N, TH> rb, rc;
+    rb.load(static_cast<const TI*>(a.B) + t0 * a.Bs + static_cast<size_t>(grp) * N, static_cast<uint32_t>(a.Bs), rows, tid);
+    rc.load(static_cast<const TI*>(a.C) + t0 * a.Cs + static_cast<size_t>(grp) * N, static_cast<uint32_t>(a.Cs), rows, tid);
+    rb.store(Bt, rows, tid);
+    rc.store(Ct, rows, tid);
+  }
   __syncthreads();
   Frag<TI> cf[N / 32];
 #pragma unroll
@@ -408,43 +456,25 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_out(SsmArgs a) {
     }
   }
   TI *xs = buf, *Ss = buf + Q * 64;
-  constexpr int U = 16 / sizeof(TI), XU = Q * 64 / U / TH, SU = N * 64 / U / TH;
-  uint4 nx[XU];  // the next head's x and state
-  f32x4 ns[SU];
-  f32x4 nsteps = zero4();
+  Rows<TI, Q, 64, TH> nx;  // the next head's x and state
+  Rows<TI, N, 64, TH> ns;
+  Step nstep;
   auto load = [&](int h, int half) __attribute__((always_inline)) {
-    const int ft = once(tid);
-    const TI* x = static_cast<const TI*>(a.x) + t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64;
-    const TI* S = static_cast<const TI*>(a.S) + ((slot * a.H + h) * halves + half) * static_cast<size_t>(N) * 64;
-#pragma unroll
-    for (int m = 0; m < XU; ++m) {
-      const int u = ft + TH * m, r = u / (64 / U);
-      nx[m] = *reinterpret_cast<const uint4*>(x + row_or_last(r, rows) * a.xs + (u % (64 / U)) * U);
-    }
-#pragma unroll
-    for (int m = 0; m < SU; ++m) ns[m] = *reinterpret_cast<const f32x4*>(S + (ft + TH * m) * U);
-    nsteps = reinterpret_cast<const f32x4*>(a.steps)[(slot * a.H + h) * Q + ft % Q];
+    nx.load(static_cast<const TI*>(a.x) + t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64, static_cast<uint32_t>(a.xs), rows, tid);
+    ns.load(static_cast<const TI*>(a.S) + ((slot * a.H + h) * halves + half) * static_cast<size_t>(N) * 64, 64, N, tid);
+    nstep = load_step(a.steps, (slot * a.H + h) * Q + tid % Q);
   };
   load(h0, 0);
   for (int h = h0; h < h1; ++h) {
     const float D = a.D ? a.D[h] : 0.f;
     for (int half = 0; half < halves; ++half) {
       __syncthreads();
-      const int ft = once(tid);
-#pragma unroll
-      for (int m = 0; m < XU; ++m) {
-        const int u = ft + TH * m, r = u / (64 / U);
-        *reinterpret_cast<uint4*>(xs + tile_at<TI, 64>(r, (u % (64 / U)) * U)) = kept(r < rows, nx[m]);
-      }
-#pragma unroll
-      for (int m = 0; m < SU; ++m) {
-        const int u = ft + TH * m;
-        *reinterpret_cast<f32x4*>(Ss + tile_at<TI, 64>(u / (64 / U), (u % (64 / U)) * U)) = ns[m];
-      }
+      nx.store(xs, rows, tid);
+      ns.store(Ss, N, tid);
       if (tid < Q) {
-        cdt[ft] = nsteps[0];
-        chi[ft] = nsteps[1];
-        clo[ft] = nsteps[2];
+        cdt[tid] = nstep.dt;
+        chi[tid] = nstep.hi;
+        clo[tid] = nstep.lo;
       }
       __syncthreads();
       const bool next = half + 1 == halves && h + 1 < h1;
@@ -530,47 +560,39 @@ template <typename TI, int N>
 __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   using SH = GradShape<TI, N>;
   constexpr int Q = SH::Q, NW = SH::NW, TH = 64 * NW, NT = SH::NT, NG = SH::NG, TT = SH::TT;
-  constexpr int U = 16 / sizeof(TI), XU = Q * 64 / U / TH;
+  constexpr int U = 16 / sizeof(TI);
   constexpr bool kPair = sizeof(TI) == 2;
   __shared__ __align__(16) TI Bt[Q * N], Ct[Q * N], xs[Q * 64], dys[Q * 64], MT[Q * Q], Gs[N * 64];
   __shared__ __align__(16) float chi[Q], clo[Q], cdt[Q], rowF[NW][Q], iC[NG][Q], iB[NG][Q], colF[Q];
   __shared__ float sd[NW], xd[NW];
-  const unsigned own = static_cast<unsigned>(a.slots) * a.G * a.sets;
+  const unsigned own = own_blocks(a);
   if (blockIdx.x >= own) {
     const unsigned b = blockIdx.x - own, nb = gridDim.x - own;
     zero_rows(static_cast<TI*>(a.dx), static_cast<int64_t>(a.H) * a.P, a, b, nb);
     zero_rows(static_cast<TI*>(a.ddt), a.H, a, b, nb);
-    if (a.sets == 1) {
-      zero_rows(static_cast<TI*>(a.dB), static_cast<int64_t>(a.G) * N, a, b, nb);
-      zero_rows(static_cast<TI*>(a.dC), static_cast<int64_t>(a.G) * N, a, b, nb);
-    }
+    zero_rows(static_cast<TI*>(a.dB), static_cast<int64_t>(a.G) * N, a, b, nb);
+    zero_rows(static_cast<TI*>(a.dC), static_cast<int64_t>(a.G) * N, a, b, nb);
     return;
   }
-  const int set = blockIdx.x % a.sets, grp = (blockIdx.x / a.sets) % a.G;
-  const int64_t slot = blockIdx.x / (a.sets * a.G);
+  const Unit unit = unit_of(a, blockIdx.x);
+  const int64_t slot = unit.slot;
+  const int grp = unit.grp, h0 = unit.h0, h1 = unit.h1;
   const Place c = find_piece(a, slot, Q);
   const int rows = c.rows;
   const int64_t t0 = c.t0;
-  if (rows <= 0) return;
+  if (rows <= 0 || h0 >= h1) return;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number();
-  const int jt = own_tile<NW>(w), per = a.H / a.G, halves = a.P / 64;
-  const int h0 = grp * per + set * a.hb, h1 = set * a.hb + a.hb < per ? h0 + a.hb : (grp + 1) * per;
+  const int jt = own_tile<NW>(w), halves = a.P / 64;
   const int ng = w % NG, tt0 = (w / NG) * TT, n0 = ng * NT * 16;  // of the second role
 
-  uint4 nx[XU], ny[XU];
-  f32x4 nsteps = zero4();
+  Rows<TI, Q, 64, TH> nx, ny;
+  Step nstep;
   f32x8 G0[NT][2], S0[NT][2];  // dS and S, rows n0 .. as operands
   auto load_rows = [&](int h, int half) __attribute__((always_inline)) {
-    const int fresh = once(tid);
-    const TI* x = static_cast<const TI*>(a.x) + t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64;
-    const TI* dy = static_cast<const TI*>(a.dy) + (t0 * a.H + h) * a.P + half * 64;
-#pragma unroll
-    for (int m = 0; m < XU; ++m) {
-      const int u = fresh + TH * m, r = u / (64 / U), col = (u % (64 / U)) * U;
-      nx[m] = *reinterpret_cast<const uint4*>(x + row_or_last(r, rows) * a.xs + col);
-      ny[m] = *reinterpret_cast<const uint4*>(dy + row_or_last(r, rows) * static_cast<int64_t>(a.H) * a.P + col);
-    }
-    nsteps = reinterpret_cast<const f32x4*>(a.steps)[(slot * a.H + h) * Q + fresh % Q];
+    const int64_t ds = static_cast<int64_t>(a.H) * a.P;
+    nx.load(static_cast<const TI*>(a.x) + t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64, static_cast<uint32_t>(a.xs), rows, tid);
+    ny.load(static_cast<const TI*>(a.dy) + t0 * ds + static_cast<size_t>(h) * a.P + half * 64, static_cast<uint32_t>(ds), rows, tid);
+    nstep = load_step(a.steps, (slot * a.H + h) * Q + tid % Q);
   };
   auto load_state = [&](f32x8 (&f)[NT][2], const void* from, int h, int half) __attribute__((always_inline)) {
     const float* m = static_cast<const float*>(from) + ((slot * a.H + h) * halves + half) * static_cast<size_t>(N) * 64;
@@ -582,8 +604,13 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   };
   load_rows(h0, 0);
   load_state(G0, a.dS, h0, 0);
-  load_tile<TI, Q, N, TH>(Bt, static_cast<const TI*>(a.B) + t0 * a.Bs + static_cast<size_t>(grp) * N, a.Bs, rows);
-  load_tile<TI, Q, N, TH>(Ct, static_cast<const TI*>(a.C) + t0 * a.Cs + static_cast<size_t>(grp) * N, a.Cs, rows);
+  {
+    Rows<TI, Q, N, TH> rb, rc;
+    rb.load(static_cast<const TI*>(a.B) + t0 * a.Bs + static_cast<size_t>(grp) * N, static_cast<uint32_t>(a.Bs), rows, tid);
+    rc.load(static_cast<const TI*>(a.C) + t0 * a.Cs + static_cast<size_t>(grp) * N, static_cast<uint32_t>(a.Cs), rows, tid);
+    rb.store(Bt, rows, tid);
+    rc.store(Ct, rows, tid);
+  }
   __syncthreads();
   f32x4 dC[NT][TT], dB[NT][TT];
 #pragma unroll
@@ -599,17 +626,12 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
       const LaneAt<TI, 64> lx(fresh);
       const LaneAt<TI, Q> lq(fresh);
       {
-        const int ft = once(tid);
-#pragma unroll
-        for (int m = 0; m < XU; ++m) {
-          const int u = ft + TH * m, r = u / (64 / U), at = tile_at<TI, 64>(r, (u % (64 / U)) * U);
-          *reinterpret_cast<uint4*>(xs + at) = kept(r < rows, nx[m]);
-          *reinterpret_cast<uint4*>(dys + at) = kept(r < rows, ny[m]);
-        }
+        nx.store(xs, rows, tid);
+        ny.store(dys, rows, tid);
         if (tid < Q) {
-          cdt[ft] = nsteps[0];
-          chi[ft] = nsteps[1];
-          clo[ft] = nsteps[2];
+          cdt[tid] = nstep.dt;
+          chi[tid] = nstep.hi;
+          clo[tid] = nstep.lo;
         }
         if (tt0 == 0) {  // dS as the first role's operand
 #pragma unroll
@@ -820,20 +842,21 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   }
   // dB and dC of the heads: to the outputs, or to this set's partial sums
   const int i = lane & 15, g = lane >> 4;
+  const bool whole = blockIdx.x < a.whole || a.sets == 1;
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     const int row = 16 * (tt0 + t) + i;
     if (row >= rows) continue;
     const size_t at = ((t0 + row) * a.G + grp) * N + n0 + 4 * g;
+    const size_t part = (static_cast<size_t>(blockIdx.x - a.whole) * Q + row) * N + n0 + 4 * g;
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-      if (a.sets == 1) {
+      if (whole) {
         store4<TI>(static_cast<TI*>(a.dB) + at + 16 * u, dB[u][t]);
         store4<TI>(static_cast<TI*>(a.dC) + at + 16 * u, dC[u][t]);
       } else {
-        const size_t far = static_cast<size_t>(set) * a.T * a.G * N;
-        store4<float>(a.pB + far + at + 16 * u, dB[u][t]);
-        store4<float>(a.pC + far + at + 16 * u, dC[u][t]);
+        store4<float>(a.pB + part + 16 * u, dB[u][t]);
+        store4<float>(a.pC + part + 16 * u, dC[u][t]);
       }
     }
   }
@@ -895,21 +918,26 @@ __global__ void __launch_bounds__(256) k_ssm_scalars(SsmArgs a) {
   }
 }
 
-// Sums of dB and dC over the sets of heads.
-template <typename TI>
-__global__ void __launch_bounds__(256) k_ssm_reduce(SsmArgs a, int64_t width) {
-  const int64_t before = clamp_cu(a, 0) * width, end = clamp_cu(a, a.n_seqs) * width, all = a.T * width;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 256 * 4;
-  for (int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; e < all; e += step) {
-    f32x4 b = zero4(), c = zero4();
-    if (e >= before && e < end) {
-      for (int s = 0; s < a.sets; ++s) {
-        b += *reinterpret_cast<const f32x4*>(a.pB + s * all + e);
-        c += *reinterpret_cast<const f32x4*>(a.pC + s * all + e);
-      }
+// Sums of dB and dC over the sets of heads of the chunks and groups behind the
+// whole ones.
+template <typename TI, int N>
+__global__ void __launch_bounds__(256) k_ssm_reduce(SsmArgs a) {
+  constexpr int Q = Chunk<TI>::Q;
+  const unsigned unit = a.whole + blockIdx.x;
+  const int grp = unit % a.G;
+  const Place c = find_piece(a, unit / a.G, Q);
+  // sets that have heads: the last ones may have none
+  const int per = a.H / a.G, hb = (per + a.sets - 1) / a.sets, sets = (per + hb - 1) / hb;
+  for (int e = 4 * (blockIdx.y * 256 + threadIdx.x); e < c.rows * N; e += 4 * 256 * gridDim.y) {
+    f32x4 b = zero4(), q = zero4();
+    for (int s = 0; s < sets; ++s) {
+      const size_t at = (static_cast<size_t>(blockIdx.x) * a.sets + s) * Q * N + e;
+      b += *reinterpret_cast<const f32x4*>(a.pB + at);
+      q += *reinterpret_cast<const f32x4*>(a.pC + at);
     }
-    store4<TI>(static_cast<TI*>(a.dB) + e, b);
-    store4<TI>(static_cast<TI*>(a.dC) + e, c);
+    const size_t to = ((c.t0 + e / N) * a.G + grp) * N + e % N;
+    store4<TI>(static_cast<TI*>(a.dB) + to, b);
+    store4<TI>(static_cast<TI*>(a.dC) + to, q);
   }
 }
 
@@ -920,7 +948,7 @@ unsigned out_rest(const SsmArgs& a, int64_t bytes) {
 // One or both directions; in segments two launches.
 template <typename TI, int N>
 hipError_t launch_state_n(int dirs, int dir0, const SsmArgs& a, hipStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(a.seg ? a.seg_slots : a.n_seqs) * dirs * a.H * (a.P / 64) * (N / 32);
+  const unsigned blocks = static_cast<unsigned>(a.seg ? a.seg_slots : a.n_seqs) * dirs * a.H * (a.P / 64);
   const unsigned grid = (blocks + 7) / 8 * 8;
   if (a.seg) k_ssm_state<TI, N, kLocal><<<grid, 256, 0, s>>>(a, dirs, dir0, blocks);
   if (a.S_full) k_ssm_state<TI, N, kFullStates><<<grid, 256, 0, s>>>(a, dirs, dir0, blocks);
@@ -929,13 +957,13 @@ hipError_t launch_state_n(int dirs, int dir0, const SsmArgs& a, hipStream_t s) {
 }
 template <typename TI, int N>
 hipError_t launch_out_n(const SsmArgs& a, hipStream_t s) {
-  const unsigned own = static_cast<unsigned>(a.slots) * a.G * a.sets;
+  const unsigned own = own_blocks(a);
   k_ssm_out<TI, N><<<own + out_rest(a, a.T * a.H * a.P * static_cast<int64_t>(sizeof(TI))), 4 * Chunk<TI>::Q, 0, s>>>(a);
   return hipGetLastError();
 }
 template <typename TI, int N>
 hipError_t launch_grad_n(const SsmArgs& a, hipStream_t s) {
-  const unsigned own = static_cast<unsigned>(a.slots) * a.G * a.sets;
+  const unsigned own = own_blocks(a);
   k_ssm_grad<TI, N><<<own + out_rest(a, a.T * a.H * a.P * static_cast<int64_t>(sizeof(TI))), 4 * Chunk<TI>::Q, 0, s>>>(a);
   return hipGetLastError();
 }
@@ -967,10 +995,14 @@ hipError_t launch_ssm_grad(int dtype, int N, const SsmArgs& a, hipStream_t s) {
   return N == 64 ? launch_grad_n<bf16, 64>(a, s) : launch_grad_n<bf16, 128>(a, s);
 }
 hipError_t launch_ssm_reduce(int dtype, int N, const SsmArgs& a, hipStream_t s) {
-  const int64_t width = static_cast<int64_t>(a.G) * N, want = (a.T * width + 1023) / 1024;
-  const unsigned grid = static_cast<unsigned>(want < 8192 ? want : 8192);
-  if (dtype == KDA_F32) k_ssm_reduce<float><<<grid, 256, 0, s>>>(a, width);
-  else k_ssm_reduce<bf16><<<grid, 256, 0, s>>>(a, width);
+  const dim3 grid(static_cast<unsigned>(a.slots) * a.G - a.whole, 8);
+  if (dtype == KDA_F32) {
+    if (N == 64) k_ssm_reduce<float, 64><<<grid, 256, 0, s>>>(a);
+    else k_ssm_reduce<float, 128><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (N == 64) k_ssm_reduce<bf16, 64><<<grid, 256, 0, s>>>(a);
+    else k_ssm_reduce<bf16, 128><<<grid, 256, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
