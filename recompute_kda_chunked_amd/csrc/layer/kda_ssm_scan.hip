@@ -518,8 +518,9 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q, sizeof(TI) == 2 ? 4 : 2) k_s
 
 // ------------------------------------------------------------ gradients
 
-// Sum over the four lane groups (lanes i, i + 16, i + 32, i + 48), every lane
-// receiving it.
+// Sums over the four lane groups (lanes i, i + 16, i + 32, i + 48), gfx950's swaps
+// of half and quarter waves: of one value, every lane receiving it, and of four at
+// once, group g receiving that of v[(g >> 1) | 2 (g & 1)].
 __device__ __forceinline__ float sum_lane_groups(float x) {
   const uint32_t b = __float_as_uint(x);
   const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
@@ -527,6 +528,16 @@ __device__ __forceinline__ float sum_lane_groups(float x) {
   const uint32_t c = __float_as_uint(x);
   const auto h = __builtin_amdgcn_permlane32_swap(c, c, false, false);
   return __uint_as_float(h[0]) + __uint_as_float(h[1]);
+}
+__device__ __forceinline__ float sum_lane_groups4(const float (&v)[4]) {
+  float s[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[2 * k]), __float_as_uint(v[2 * k + 1]), false, false);
+    s[k] = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+  }
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(s[0]), __float_as_uint(s[1]), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 // A value of an fp32 state as the operand's type and what its rounding leaves
@@ -563,8 +574,11 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   constexpr int U = 16 / sizeof(TI);
   constexpr bool kPair = sizeof(TI) == 2;
   __shared__ __align__(16) TI Bt[Q * N], Ct[Q * N], xs[Q * 64], dys[Q * 64], MT[Q * Q], Gs[N * 64];
-  __shared__ __align__(16) float chi[Q], clo[Q], cdt[Q], rowF[NW][Q], iC[NG][Q], iB[NG][Q], colF[Q];
-  __shared__ float sd[NW], xd[NW];
+  // per token: step size, decays from the chunk's start to it and from it to the
+  // end, log2 decay from the first token of its 16 to it, and of those first ones
+  // from the chunk's start
+  __shared__ __align__(16) float cdt[Q], cin[Q], cout[Q], crel[Q], rowF[NW][Q], iC[NG][Q], iB[NG][Q], colF[Q];
+  __shared__ float tile_hi[NW], tile_lo[NW], sd[NW], xd[NW];
   const unsigned own = own_blocks(a);
   if (blockIdx.x >= own) {
     const unsigned b = blockIdx.x - own, nb = gridDim.x - own;
@@ -587,12 +601,16 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
 
   Rows<TI, Q, 64, TH> nx, ny;
   Step nstep;
+  float end_hi, end_lo;
   f32x8 G0[NT][2], S0[NT][2];  // dS and S, rows n0 .. as operands
   auto load_rows = [&](int h, int half) __attribute__((always_inline)) {
     const int64_t ds = static_cast<int64_t>(a.H) * a.P;
     nx.load(static_cast<const TI*>(a.x) + t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64, static_cast<uint32_t>(a.xs), rows, tid);
     ny.load(static_cast<const TI*>(a.dy) + t0 * ds + static_cast<size_t>(h) * a.P + half * 64, static_cast<uint32_t>(ds), rows, tid);
-    nstep = load_step(a.steps, (slot * a.H + h) * Q + tid % Q);
+    const int64_t at = (slot * a.H + h) * Q;
+    nstep = load_step(a.steps, at + tid % Q);
+    end_hi = a.steps[4 * (at + Q) - 3];
+    end_lo = a.steps[4 * (at + Q) - 2];
   };
   auto load_state = [&](f32x8 (&f)[NT][2], const void* from, int h, int half) __attribute__((always_inline)) {
     const float* m = static_cast<const float*>(from) + ((slot * a.H + h) * halves + half) * static_cast<size_t>(N) * 64;
@@ -629,9 +647,15 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
         nx.store(xs, rows, tid);
         ny.store(dys, rows, tid);
         if (tid < Q) {
+          const float fh = __shfl(nstep.hi, lane & 48, 64), fl = __shfl(nstep.lo, lane & 48, 64);
           cdt[tid] = nstep.dt;
-          chi[tid] = nstep.hi;
-          clo[tid] = nstep.lo;
+          cin[tid] = exp2_(nstep.hi + nstep.lo);
+          cout[tid] = exp2_((end_hi - nstep.hi) + (end_lo - nstep.lo));
+          crel[tid] = (nstep.hi - fh) + (nstep.lo - fl);
+          if (tid % 16 == 0) {
+            tile_hi[tid / 16] = nstep.hi;
+            tile_lo[tid / 16] = nstep.lo;
+          }
         }
         if (tt0 == 0) {  // dS as the first role's operand
 #pragma unroll
@@ -656,11 +680,11 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
       const int nh = next ? h + 1 : h, nhalf = half + 1 < halves ? half + 1 : next ? 0 : half;
       load_state(S0, a.S, h, half);
       load_rows(nh, nhalf);
-      const float hQ = chi[Q - 1], lQ = clo[Q - 1];
+      const float all = cin[Q - 1];
 
       {  // first role
         const int row = 16 * jt + i;
-        const float hj = chi[row], lj = clo[row], dtj = cdt[row], rj = exp2_((hQ - hj) + (lQ - lj));
+        const float dtj = cdt[row], rj = cout[row], relj = crel[row], thj = tile_hi[jt], tlj = tile_lo[jt];
         Frag<TI> xf[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) xf[k] = frag_row(xs, lx, 16 * jt, 32 * k);
@@ -693,11 +717,16 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
               for (int k = 0; k < 2; ++k) e = mma32(frag_row(dys, lx, 16 * t, 32 * k), xf[k], e);
 #pragma unroll
               for (int k = 0; k < N / 32; ++k) cb = mma32(frag_row(Ct, ln, 16 * t, 32 * k), bf[k], cb);
-              const f32x4 h4 = *reinterpret_cast<const f32x4*>(chi + i0), l4 = *reinterpret_cast<const f32x4*>(clo + i0);
+              const f32x4 rel = *reinterpret_cast<const f32x4*>(crel + i0);
+              const float from = ((tile_hi[t] - thj) + (tile_lo[t] - tlj)) - relj;
+              const bool below = t > jt;
+              if (!below) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) diag += 4 * g + r == i ? e[r] : 0.f;
+              }
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                const float L = i0 + r >= row ? exp2_((h4[r] - hj) + (l4[r] - lj)) : 0.f;
-                if (i0 + r == row) diag += e[r];
+                const float L = below || 4 * g + r >= i ? exp2_(rel[r] + from) : 0.f;
                 W[q][r] = L * cb[r];
                 M[r] = L * e[r] * dtj;
                 const float F = W[q][r] * e[r];
@@ -728,7 +757,9 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
       __syncthreads();
 
       {  // second role: dC, then dB
-        float dot = 0.f;
+        static_assert(TT % 4 == 0, "sums of four token tiles at once");
+        const int order = (g >> 1) | 2 * (g & 1);
+        float dot = 0.f, four[4];
         Frag<TI> sf[NT][2], sl[NT][2];
 #pragma unroll
         for (int u = 0; u < NT; ++u)
@@ -741,7 +772,7 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           const int tt = tt0 + t, row = 16 * tt + i;
-          const float ei = exp2_(chi[row] + clo[row]);
+          const float ei = cin[row];
           float ic = 0.f;
 #pragma unroll
           for (int u = 0; u < NT; ++u) {
@@ -753,17 +784,18 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
               z = mma32(sf[u][k], yf, z);
               if constexpr (kPair) z = mma32(sl[u][k], yf, z);
             }
-            z *= ei;
             const f32x4 c4 = tile_get4(Ct, ln, 16 * tt, nr);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) ic += c4[r] * z[r];
-            dC[u][t] += z;
+            for (int r = 0; r < 4; ++r) {
+              ic += c4[r] * z[r];
+              dC[u][t][r] += ei * z[r];
+            }
 #pragma unroll
             for (int m = 0; m < NW / 2; ++m)
               if (2 * m <= tt) dC[u][t] = mma32(frag_col<false>(Bt, ln, 32 * m, nr), frag_col<false>(MT, lq, 32 * m, 16 * tt), dC[u][t]);
           }
-          ic = sum_lane_groups(ic);
-          if (g == 0) iC[ng][row] = ic;
+          four[t % 4] = ic * ei;
+          if (t % 4 == 3) iC[ng][16 * (tt - 3 + order) + i] = sum_lane_groups4(four);
           __builtin_amdgcn_sched_barrier(0);
         }
         dot = sum_wave(dot);
@@ -776,7 +808,7 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           const int tt = tt0 + t, row = 16 * tt + i;
-          const float rj = exp2_((hQ - chi[row]) + (lQ - clo[row])), dtj = cdt[row];
+          const float rj = cout[row], wj = rj * cdt[row];
           float ib = 0.f;
 #pragma unroll
           for (int u = 0; u < NT; ++u) {
@@ -788,17 +820,18 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
               v = mma32(sf[u][k], xf, v);
               if constexpr (kPair) v = mma32(sl[u][k], xf, v);
             }
-            v *= rj;
             const f32x4 b4 = tile_get4(Bt, ln, 16 * tt, nr);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) ib += b4[r] * v[r];
-            dB[u][t] += dtj * v;
+            for (int r = 0; r < 4; ++r) {
+              ib += b4[r] * v[r];
+              dB[u][t][r] += wj * v[r];
+            }
 #pragma unroll
             for (int m = 0; m < NW / 2; ++m)
               if (2 * m + 1 >= tt) dB[u][t] = mma32(frag_col<false>(Ct, ln, 32 * m, nr), frag_row(MT, lq, 16 * tt, 32 * m), dB[u][t]);
           }
-          ib = sum_lane_groups(ib);
-          if (g == 0) iB[ng][row] = ib;
+          four[t % 4] = ib * rj;
+          if (t % 4 == 3) iB[ng][16 * (tt - 3 + order) + i] = sum_lane_groups4(four);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -832,7 +865,7 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
             diag += xd[k];
           }
           float* out = a.ends + 2 * (slot * a.H + h);
-          dots *= exp2_(hQ + lQ);
+          dots *= all;
           out[0] = half ? out[0] + dots : dots;
           out[1] = half ? out[1] + diag : diag;
         }
