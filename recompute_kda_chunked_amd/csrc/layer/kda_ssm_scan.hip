@@ -540,16 +540,26 @@ __device__ __forceinline__ float sum_lane_groups4(const float (&v)[4]) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// A value of an fp32 state as the operand's type and what its rounding leaves
-// (bf16: 16 bits together).
+// Values of an fp32 state as operands that add up to them (three bf16 are 24 bits).
 template <typename TI>
-__device__ __forceinline__ void split2(const f32x8& x, Frag<TI>& hi, Frag<TI>& lo) {
+struct Split {
+  static constexpr int K = sizeof(TI) == 4 ? 1 : 3;
+  Frag<TI> f[K];
+  __device__ __forceinline__ void set(f32x8 x) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    hi[e] = static_cast<TI>(x[e]);
-    lo[e] = static_cast<TI>(x[e] - static_cast<float>(hi[e]));
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        f[k][e] = static_cast<TI>(x[e]);
+        if (k + 1 < K) x[e] -= static_cast<float>(f[k][e]);
+      }
   }
-}
+  __device__ __forceinline__ f32x4 mma(Frag<TI> b, f32x4 c) const {
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) c = mma32(f[k], b, c);
+    return c;
+  }
+};
 
 // Two roles of a wave. First, 16 tokens j of the chunk: the scores of all i >= j
 // as [i][j] accumulators, dx_j, and L E dt to LDS. Then 16 rows of the state (or
@@ -572,13 +582,12 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   using SH = GradShape<TI, N>;
   constexpr int Q = SH::Q, NW = SH::NW, TH = 64 * NW, NT = SH::NT, NG = SH::NG, TT = SH::TT;
   constexpr int U = 16 / sizeof(TI);
-  constexpr bool kPair = sizeof(TI) == 2;
   __shared__ __align__(16) TI Bt[Q * N], Ct[Q * N], xs[Q * 64], dys[Q * 64], MT[Q * Q], Gs[N * 64];
   // per token: step size, decays from the chunk's start to it and from it to the
-  // end, log2 decay from the first token of its 16 to it, and of those first ones
-  // from the chunk's start
-  __shared__ __align__(16) float cdt[Q], cin[Q], cout[Q], crel[Q], rowF[NW][Q], iC[NG][Q], iB[NG][Q], colF[Q];
-  __shared__ float tile_hi[NW], tile_lo[NW], sd[NW], xd[NW];
+  // end, and the running sum of log2 decays, whose differences lose their digits
+  // unless both parts are taken
+  __shared__ __align__(16) float cdt[Q], cin[Q], cout[Q], chi[Q], clo[Q], rowF[NW][Q], iC[NG][Q], iB[NG][Q], colF[Q], ownF[Q];
+  __shared__ float sd[NW], xd[NW];
   const unsigned own = own_blocks(a);
   if (blockIdx.x >= own) {
     const unsigned b = blockIdx.x - own, nb = gridDim.x - own;
@@ -597,7 +606,7 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   if (rows <= 0 || h0 >= h1) return;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number();
   const int jt = own_tile<NW>(w), halves = a.P / 64;
-  const int ng = w % NG, tt0 = (w / NG) * TT, n0 = ng * NT * 16;  // of the second role
+  const int ng = NG == NW ? w : w % NG, tt0 = NG == NW ? 0 : (w / NG) * TT, n0 = ng * NT * 16;  // of the second role
 
   Rows<TI, Q, 64, TH> nx, ny;
   Step nstep;
@@ -605,10 +614,11 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   f32x8 G0[NT][2], S0[NT][2];  // dS and S, rows n0 .. as operands
   auto load_rows = [&](int h, int half) __attribute__((always_inline)) {
     const int64_t ds = static_cast<int64_t>(a.H) * a.P;
-    nx.load(static_cast<const TI*>(a.x) + t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64, static_cast<uint32_t>(a.xs), rows, tid);
-    ny.load(static_cast<const TI*>(a.dy) + t0 * ds + static_cast<size_t>(h) * a.P + half * 64, static_cast<uint32_t>(ds), rows, tid);
+    const int ft = once(tid);
+    nx.load(static_cast<const TI*>(a.x) + t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64, static_cast<uint32_t>(a.xs), rows, ft);
+    ny.load(static_cast<const TI*>(a.dy) + t0 * ds + static_cast<size_t>(h) * a.P + half * 64, static_cast<uint32_t>(ds), rows, ft);
     const int64_t at = (slot * a.H + h) * Q;
-    nstep = load_step(a.steps, at + tid % Q);
+    nstep = load_step(a.steps, at + ft % Q);
     end_hi = a.steps[4 * (at + Q) - 3];
     end_lo = a.steps[4 * (at + Q) - 2];
   };
@@ -644,18 +654,15 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
       const LaneAt<TI, 64> lx(fresh);
       const LaneAt<TI, Q> lq(fresh);
       {
-        nx.store(xs, rows, tid);
-        ny.store(dys, rows, tid);
+        const int ft = once(tid);
+        nx.store(xs, rows, ft);
+        ny.store(dys, rows, ft);
         if (tid < Q) {
-          const float fh = __shfl(nstep.hi, lane & 48, 64), fl = __shfl(nstep.lo, lane & 48, 64);
-          cdt[tid] = nstep.dt;
-          cin[tid] = exp2_(nstep.hi + nstep.lo);
-          cout[tid] = exp2_((end_hi - nstep.hi) + (end_lo - nstep.lo));
-          crel[tid] = (nstep.hi - fh) + (nstep.lo - fl);
-          if (tid % 16 == 0) {
-            tile_hi[tid / 16] = nstep.hi;
-            tile_lo[tid / 16] = nstep.lo;
-          }
+          cdt[ft] = nstep.dt;
+          cin[ft] = exp2_(nstep.hi + nstep.lo);
+          cout[ft] = exp2_((end_hi - nstep.hi) + (end_lo - nstep.lo));
+          chi[ft] = nstep.hi;
+          clo[ft] = nstep.lo;
         }
         if (tt0 == 0) {  // dS as the first role's operand
 #pragma unroll
@@ -678,13 +685,11 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
       const bool more = half + 1 < halves || h + 1 < h1;
       const bool next = half + 1 == halves && more;
       const int nh = next ? h + 1 : h, nhalf = half + 1 < halves ? half + 1 : next ? 0 : half;
-      load_state(S0, a.S, h, half);
-      load_rows(nh, nhalf);
       const float all = cin[Q - 1];
 
       {  // first role
         const int row = 16 * jt + i;
-        const float dtj = cdt[row], rj = cout[row], relj = crel[row], thj = tile_hi[jt], tlj = tile_lo[jt];
+        const float dtj = cdt[row], rj = cout[row], hj = chi[row], lj = clo[row];
         Frag<TI> xf[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) xf[k] = frag_row(xs, lx, 16 * jt, 32 * k);
@@ -692,11 +697,22 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) dx[p] = zero4();
         Frag<TI> bf[N / 32];
+        {
+          Frag<TI> gf[2][4];
+          auto read = [&](int k) __attribute__((always_inline)) {
+            bf[k] = frag_row(Bt, ln, 16 * jt, 32 * k);
 #pragma unroll
-        for (int k = 0; k < N / 32; ++k) {
-          bf[k] = frag_row(Bt, ln, 16 * jt, 32 * k);
+            for (int p = 0; p < 4; ++p) gf[k % 2][p] = frag_col<false>(Gs, lx, 32 * k, 16 * p);
+          };
+          read(0);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) dx[p] = mma32(frag_col<false>(Gs, lx, 32 * k, 16 * p), bf[k], dx[p]);
+          for (int k = 0; k < N / 32; ++k) {
+            if (k + 1 < N / 32) read(k + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) dx[p] = mma32(gf[k % 2][p], bf[k], dx[p]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
 #pragma unroll
         for (int p = 0; p < 4; ++p) dx[p] *= rj;
@@ -704,44 +720,66 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
 #pragma unroll
         for (int m = 0; m < NW / 2; ++m) {
           if (2 * m + 1 < jt) continue;
+          // a tile's operands are read at once; those of one above the diagonal for
+          // nothing
+          Frag<TI> yc[4];
           f32x4 W[2];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int t = 2 * m + q, i0 = 16 * t + 4 * g;
+            Frag<TI> yf[2], qf[N / 32];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) yf[k] = frag_row(dys, lx, 16 * t, 32 * k);
+            // C B^T is formed anew for each head: kept, it would spill
+#pragma unroll
+            for (int k = 0; k < N / 32; ++k) qf[k] = frag_row(Ct, ln, 16 * t, 32 * k);
+            const f32x4 h4 = *reinterpret_cast<const f32x4*>(chi + i0), l4 = *reinterpret_cast<const f32x4*>(clo + i0);
+            if (q == 1) {
+#pragma unroll
+              for (int p = 0; p < 4; ++p) yc[p] = frag_col<true>(dys, lx, 32 * m, 16 * p);
+            }
+            __builtin_amdgcn_sched_barrier(0);
             W[q] = zero4();
             f32x4 M = zero4();
             if (t >= jt) {
-              // C B^T is formed anew for each head: kept, it would spill
               f32x4 e = zero4(), cb = zero4(), f;
 #pragma unroll
-              for (int k = 0; k < 2; ++k) e = mma32(frag_row(dys, lx, 16 * t, 32 * k), xf[k], e);
-#pragma unroll
-              for (int k = 0; k < N / 32; ++k) cb = mma32(frag_row(Ct, ln, 16 * t, 32 * k), bf[k], cb);
-              const f32x4 rel = *reinterpret_cast<const f32x4*>(crel + i0);
-              const float from = ((tile_hi[t] - thj) + (tile_lo[t] - tlj)) - relj;
+              for (int k = 0; k < N / 32; ++k) {
+                if (k < 2) e = mma32(yf[k], xf[k], e);
+                cb = mma32(qf[k], bf[k], cb);
+              }
               const bool below = t > jt;
-              if (!below) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) diag += 4 * g + r == i ? e[r] : 0.f;
+              for (int r = 0; r < 4; ++r) {
+                const float L = below || 4 * g + r >= i ? exp2_((h4[r] - hj) + (l4[r] - lj)) : 0.f;
+                W[q][r] = L * cb[r];
+                M[r] = L * e[r] * dtj;
+                f[r] = W[q][r] * e[r];
+              }
+              if (!below) {  // a token's own score, which decays nowhere, apart
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  if (4 * g + r == i) {
+                    diag += e[r];
+                    ownF[row] = f[r];
+                    f[r] = 0.f;
+                  }
               }
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                const float L = below || 4 * g + r >= i ? exp2_(rel[r] + from) : 0.f;
-                W[q][r] = L * cb[r];
-                M[r] = L * e[r] * dtj;
-                const float F = W[q][r] * e[r];
-                cf += F;
-                f[r] = F * dtj;
+                cf += f[r];
+                f[r] *= dtj;
               }
               const float v[4] = {f[0], f[1], f[2], f[3]};
               const float s = transpose_sum16<4>(v);  // lane i: of f[i % 4]
               if (i < 4) rowF[w][i0 + i] = s;
             }
             store4<TI>(MT + shifted<LaneAt<TI, Q>>(lq.four, 16 * t) + 16 * jt * Q, M);
+            __builtin_amdgcn_sched_barrier(0);
           }
           const Frag<TI> wf = pair_frag<TI>(W[0], W[1]);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) dx[p] = mma32(frag_col<true>(dys, lx, 32 * m, 16 * p), wf, dx[p]);
+          for (int p = 0; p < 4; ++p) dx[p] = mma32(yc[p], wf, dx[p]);
           __builtin_amdgcn_sched_barrier(0);
         }
         cf = sum_lane_groups(cf);
@@ -754,47 +792,72 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
           for (int p = 0; p < 4; ++p) store4<TI>(out + 16 * p, dtj * dx[p] + D * tile_get4(dys, lx, 16 * jt, 16 * p));
         }
       }
+      load_state(S0, a.S, h, half);
       __syncthreads();
 
       {  // second role: dC, then dB
         static_assert(TT % 4 == 0, "sums of four token tiles at once");
         const int order = (g >> 1) | 2 * (g & 1);
         float dot = 0.f, four[4];
-        Frag<TI> sf[NT][2], sl[NT][2];
+        Split<TI> sf[NT][2];
 #pragma unroll
         for (int u = 0; u < NT; ++u)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) dot += S0[u][k][e] * G0[u][k][e];
-            split2<TI>(S0[u][k], sf[u][k], sl[u][k]);
+            sf[u][k].set(S0[u][k]);
           }
+        // a token tile's operands are read while the one before it is worked on
+        struct Tile {
+          Frag<TI> v[2], m[NW / 2];
+          uint32_t c4[NT][4];
+          float in, wt;
+        } tile[2];
+        Frag<TI> rows_t[NT][NW / 2];  // this wave's columns of B, then of C, by tokens
+        auto read_rows = [&](const TI* from) __attribute__((always_inline)) {
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int m = 0; m < NW / 2; ++m) rows_t[u][m] = frag_col<false>(from, ln, 32 * m, n0 + 16 * u);
+        };
+        auto read_c = [&](int t) __attribute__((always_inline)) {
+          Tile& o = tile[t % 2];
+          const int tt = tt0 + t;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) o.v[k] = frag_row(dys, lx, 16 * tt, 32 * k);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) load4_raw<TI>(Ct + shifted<LaneAt<TI, N>>(ln.four, n0 + 16 * u) + 16 * tt * N, o.c4[u]);
+          o.in = cin[16 * tt + i];
+#pragma unroll
+          for (int m = 0; m < NW / 2; ++m)
+            if (2 * m <= tt) o.m[m] = frag_col<false>(MT, lq, 32 * m, 16 * tt);
+        };
+        read_rows(Bt);
+        read_c(0);
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const int tt = tt0 + t, row = 16 * tt + i;
-          const float ei = cin[row];
+          const int tt = tt0 + t;
+          Tile& o = tile[t % 2];
+          if (t) read_c(t);
+          __builtin_amdgcn_sched_barrier(0);
           float ic = 0.f;
 #pragma unroll
           for (int u = 0; u < NT; ++u) {
-            const int nr = n0 + 16 * u;
             f32x4 z = zero4();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const Frag<TI> yf = frag_row(dys, lx, 16 * tt, 32 * k);
-              z = mma32(sf[u][k], yf, z);
-              if constexpr (kPair) z = mma32(sl[u][k], yf, z);
-            }
-            const f32x4 c4 = tile_get4(Ct, ln, 16 * tt, nr);
+            for (int k = 0; k < 2; ++k) z = sf[u][k].mma(o.v[k], z);
+#pragma unroll
+            for (int m = 0; m < NW / 2; ++m)
+              if (2 * m <= tt) dC[u][t] = mma32(rows_t[u][m], o.m[m], dC[u][t]);
+            const f32x4 c4 = unpack4<TI>(o.c4[u]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               ic += c4[r] * z[r];
-              dC[u][t][r] += ei * z[r];
+              dC[u][t][r] += o.in * z[r];
             }
-#pragma unroll
-            for (int m = 0; m < NW / 2; ++m)
-              if (2 * m <= tt) dC[u][t] = mma32(frag_col<false>(Bt, ln, 32 * m, nr), frag_col<false>(MT, lq, 32 * m, 16 * tt), dC[u][t]);
           }
-          four[t % 4] = ic * ei;
+          four[t % 4] = ic * o.in;
           if (t % 4 == 3) iC[ng][16 * (tt - 3 + order) + i] = sum_lane_groups4(four);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -803,34 +866,48 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
 #pragma unroll
         for (int u = 0; u < NT; ++u)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) split2<TI>(G0[u][k], sf[u][k], sl[u][k]);
-        load_state(G0, a.dS, nh, nhalf);
+          for (int k = 0; k < 2; ++k) sf[u][k].set(G0[u][k]);
+        load_rows(nh, nhalf);
+        auto read_b = [&](int t) __attribute__((always_inline)) {
+          Tile& o = tile[t % 2];
+          const int tt = tt0 + t;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) o.v[k] = frag_row(xs, lx, 16 * tt, 32 * k);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) load4_raw<TI>(Bt + shifted<LaneAt<TI, N>>(ln.four, n0 + 16 * u) + 16 * tt * N, o.c4[u]);
+          o.in = cout[16 * tt + i];
+          o.wt = cdt[16 * tt + i];
+#pragma unroll
+          for (int m = 0; m < NW / 2; ++m)
+            if (2 * m + 1 >= tt) o.m[m] = frag_row(MT, lq, 16 * tt, 32 * m);
+        };
+        read_rows(Ct);
+        read_b(0);
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const int tt = tt0 + t, row = 16 * tt + i;
-          const float rj = cout[row], wj = rj * cdt[row];
+          const int tt = tt0 + t;
+          Tile& o = tile[t % 2];
+          if (t) read_b(t);
+          __builtin_amdgcn_sched_barrier(0);
           float ib = 0.f;
+          if (t == TT / 2) load_state(G0, a.dS, nh, nhalf);
 #pragma unroll
           for (int u = 0; u < NT; ++u) {
-            const int nr = n0 + 16 * u;
             f32x4 v = zero4();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const Frag<TI> xf = frag_row(xs, lx, 16 * tt, 32 * k);
-              v = mma32(sf[u][k], xf, v);
-              if constexpr (kPair) v = mma32(sl[u][k], xf, v);
-            }
-            const f32x4 b4 = tile_get4(Bt, ln, 16 * tt, nr);
+            for (int k = 0; k < 2; ++k) v = sf[u][k].mma(o.v[k], v);
+#pragma unroll
+            for (int m = 0; m < NW / 2; ++m)
+              if (2 * m + 1 >= tt) dB[u][t] = mma32(rows_t[u][m], o.m[m], dB[u][t]);
+            const f32x4 b4 = unpack4<TI>(o.c4[u]);
+            const float wj = o.in * o.wt;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               ib += b4[r] * v[r];
               dB[u][t][r] += wj * v[r];
             }
-#pragma unroll
-            for (int m = 0; m < NW / 2; ++m)
-              if (2 * m + 1 >= tt) dB[u][t] = mma32(frag_col<false>(Ct, ln, 32 * m, nr), frag_row(MT, lq, 16 * tt, 32 * m), dB[u][t]);
           }
-          four[t % 4] = ib * rj;
+          four[t % 4] = ib * o.in;
           if (t % 4 == 3) iB[ng][16 * (tt - 3 + order) + i] = sum_lane_groups4(four);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -853,7 +930,7 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
         if (part == 0) {
           const float col = colF[t], d = cdt[t];
           f32x4* out = reinterpret_cast<f32x4*>(a.sums) + (slot * a.H + h) * Q + t;
-          f32x4 v = f32x4{rf - d * col, d * cb, col + cb, 0.f};
+          f32x4 v = f32x4{rf - d * col, d * cb, (col + ownF[t]) + cb, 0.f};
           if (half) v += *out;  // the head's first half, of this thread
           *out = v;
         }
