@@ -42,14 +42,16 @@ hipError_t launch_recurrent(int dtype, int D, bool gdn2, const RecurrentArgs& a,
 // 147 / 143.
 inline bool streams_past_caches(int64_t bytes) { return bytes >= (int64_t{288} << 20); }
 
-// Sums of `nb` partial rows of M = n0 + n1 floats, in a fixed order: the
-// first n0 columns to out0, the rest to out1 unless it is null (nb = 0:
-// zeros).
+// Sums of `nb` partial rows of M = n0 + n1 + n2 floats, in a fixed order: the
+// first n0 columns to out0, the next to out1 and out2 unless they are null
+// (nb = 0: zeros).
 struct ParamReduceArgs {
   const float* partials;
   int64_t nb;
   int n0, n1;
   float *out0, *out1;
+  int n2 = 0;
+  float* out2 = nullptr;
 };
 hipError_t launch_param_reduce(const ParamReduceArgs& a, hipStream_t s);
 

@@ -26,7 +26,7 @@ template <int CL>
 __global__ void __launch_bounds__(1024) k_param_reduce(ParamReduceArgs a) {
   constexpr int RL = 1024 / CL;
   __shared__ float sm[RL][CL + 1];
-  const int M = a.n0 + a.n1, cl = threadIdx.x % CL, rl = threadIdx.x / CL;
+  const int M = a.n0 + a.n1 + a.n2, cl = threadIdx.x % CL, rl = threadIdx.x / CL;
   const int c = blockIdx.x * CL + cl;
   float s = 0.f;
   if (c < M) {
@@ -48,7 +48,11 @@ __global__ void __launch_bounds__(1024) k_param_reduce(ParamReduceArgs a) {
 #pragma unroll
     for (int r = 0; r < RL / 16; ++r) s += sm[r][cl];
     if (c < a.n0) a.out0[c] = s;
-    else if (a.out1) a.out1[c - a.n0] = s;
+    else if (c >= a.n0 + a.n1) {
+      if (a.out2) a.out2[c - a.n0 - a.n1] = s;
+    } else if (a.out1) {
+      a.out1[c - a.n0] = s;
+    }
   }
 }
 
@@ -485,7 +489,7 @@ int64_t gated_groups(int dtype, int V, int64_t rows) {
 }  // namespace
 
 hipError_t launch_param_reduce(const ParamReduceArgs& a, hipStream_t s) {
-  const int M = a.n0 + a.n1;
+  const int M = a.n0 + a.n1 + a.n2;
   if (M <= 1024) k_param_reduce<4><<<(M + 3) / 4, 1024, 0, s>>>(a);
   else if (M <= 16384) k_param_reduce<32><<<(M + 31) / 32, 1024, 0, s>>>(a);
   else k_param_reduce<64><<<(M + 63) / 64, 1024, 0, s>>>(a);

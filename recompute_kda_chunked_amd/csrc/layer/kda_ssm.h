@@ -44,16 +44,17 @@ struct SsmArgs {
   float* steps;
   void *S, *dS;
   bool S_full;
-  // Segments of `seg` chunks (0: none) in seg_slots slots of their own: what each
-  // adds to its state, forward and back, and its log2 decay, [2][seg_slots][H]..
+  // Segments of `seg` chunks (0: none) of sequences of more than long_from tokens,
+  // in seg_slots slots of their own: what each adds to its state, and its log2
+  // decay, [directions][seg_slots][H]..
   int seg;
-  int64_t seg_slots;
+  int64_t seg_slots, long_from;
   float *local, *seg_log;
   // Of the gradients: per token {what dl adds up from it on, before it, the step
   // size's own part} [slots][H][Q] of four, per chunk {states' part of dl, dD}.
   float *sums, *ends;
   float *pB, *pC;        // partial dB and dC [blocks behind the whole ones][Q][N] where sets > 1
-  float *part2, *part1;  // per slot {dA, ddt_bias} [2 H] and dD [H]
+  float *param;          // per slot {dA, ddt_bias, dD} [3 H]
   // Blocks that take all heads of a group in a chunk, and into how many the heads
   // of each chunk and group behind those are divided.
   unsigned whole;

@@ -30,8 +30,8 @@ int check_ssm(const kda_ssm_problem* p) {
 // bytes.
 struct ScanPlan {
   int Q, sets = 1, seg = 0;
-  int64_t slots, whole, seg_slots = 0;
-  size_t steps, state, dstate = 0, local, seg_log, sums = 0, ends = 0, partial = 0, part2 = 0, part1 = 0;
+  int64_t slots, whole, seg_slots = 0, long_from;
+  size_t steps, state, dstate = 0, local, seg_log, sums = 0, ends = 0, partial = 0, param = 0;
   ScanPlan(const kda_ssm_problem* p, bool bwd) {
     Q = ssm_chunk(p->dtype);
     const int64_t T = p->total_tokens, HP = static_cast<int64_t>(p->H) * p->P;
@@ -53,12 +53,18 @@ struct ScanPlan {
         sets = k;
       }
     }
-    // a sequence's states in segments, where one sequence alone would leave most
-    // of the chip idle
+    // The states of a long sequence in segments, which costs them twice over: where
+    // its chunks in turn take longer than that work of the whole launch, 512 blocks
+    // at a time, and a launch's start (7 chunks). Measured with N 128, P 64, bf16,
+    // forward, one sequence or 4 alike, without and with segments: 8192 tokens x 64
+    // heads 293 / 166 us and 142 / 182, x 8 heads 230 / 67 and 78 / 59. The lengths
+    // are known on the device, which decides; with many sequences for their chunks
+    // none is long, and a slot of each would take more room than the states.
     const int dirs = bwd ? 2 : 1;
     const int64_t chunks = (T + Q - 1) / Q, chain = dirs * (HP / 64);
     const int64_t want = 512 / chain < 32 ? 512 / chain : 32;
-    if (want > 1 && chunks >= 8) {
+    long_from = chain > 512 ? T : (2 * chunks * chain / 512 + 7) * Q;
+    if (T > long_from && 4 * int64_t{p->n_seqs} <= chunks) {
       seg = static_cast<int>((chunks + want - 1) / want);
       if (seg < 4) seg = 4;
       seg_slots = T / (static_cast<int64_t>(seg) * Q) + p->n_seqs;
@@ -66,19 +72,18 @@ struct ScanPlan {
     auto part = [](int64_t n, size_t size) { return (static_cast<size_t>(n) * size + 255) / 256 * 256; };
     steps = part(slots * p->H * Q, 16);
     state = part(slots * HP * p->N, bwd || p->dtype == KDA_F32 ? 4 : 2);
-    local = part(2 * seg_slots * HP * p->N, 4);
-    seg_log = part(2 * seg_slots * p->H, 4);
+    local = part(dirs * seg_slots * HP * p->N, 4);
+    seg_log = part(dirs * seg_slots * p->H, 4);
     if (bwd) {
       dstate = state;
       sums = steps;
       ends = part(slots * p->H * 2, 4);
       partial = sets > 1 ? part((units - whole) * sets * Q * p->N, 4) : 0;
-      part2 = part(slots * p->H * 2, 4);
-      part1 = part(slots * p->H, 4);
+      param = part(slots * p->H * 3, 4);
     }
   }
   size_t bytes() const {
-    return steps + state + dstate + local + seg_log + sums + ends + 2 * partial + part2 + part1;
+    return steps + state + dstate + local + seg_log + sums + ends + 2 * partial + param;
   }
 };
 
@@ -97,7 +102,7 @@ int check_scan(const kda_ssm_problem* p, bool has_cu) {
   if (H > (1 << 20) || slots * H >= (int64_t{1} << 26) || slots * H * p->N * p->P >= (int64_t{1} << 40))
     return KDA_ERR_UNSUPPORTED;
   if (slots * H >= (1 << 23) - 1024 || slots * ((H + 3) / 4) >= (1 << 24) ||
-      2 * (slots + 8) * H * (p->P / 64) * (p->N / 32) >= (1 << 26))
+      2 * (slots + 8) * H * (p->P / 64) >= (1 << 24))
     return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
@@ -143,9 +148,9 @@ SsmArgs scan_args(const kda_ssm_problem* p, const ScanPlan& plan, const void* x,
   a.ends = reinterpret_cast<float*>(take(plan.ends));
   a.pB = reinterpret_cast<float*>(take(plan.partial));
   a.pC = reinterpret_cast<float*>(take(plan.partial));
-  a.part2 = reinterpret_cast<float*>(take(plan.part2));
-  a.part1 = reinterpret_cast<float*>(take(plan.part1));
+  a.param = reinterpret_cast<float*>(take(plan.param));
   a.seg = plan.seg;
+  a.long_from = plan.long_from;
   a.seg_slots = plan.seg_slots;
   a.whole = static_cast<unsigned>(plan.whole);
   a.sets = plan.sets;
@@ -265,9 +270,8 @@ int kda_ssm_bwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, con
   }
   // without tokens the sums are empty
   const int64_t nb = a.T > 0 ? a.slots : 0;
-  const ParamReduceArgs r2{a.part2, nb, p->H, p->H, dA_log, ddt_bias}, r1{a.part1, nb, p->H, 0, dD, nullptr};
-  KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r2, s));
-  if (dD) KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r1, s));
+  const ParamReduceArgs r{a.param, nb, p->H, p->H, dA_log, ddt_bias, p->H, dD};
+  KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r, s));
   return KDA_OK;
 }
 

@@ -105,7 +105,9 @@ __global__ void __launch_bounds__(256) k_ssm_steps(SsmArgs a) {
       dt[r] = ssm_step(z, a.dt_min, a.dt_max);
       if (!(dt[r] <= a.dt_min || dt[r] >= a.dt_max) || z != z) slope[r] = 1.f / (1.f + expf(-z));
     }
-    cum[r] = l2 * dt[r] + (r ? cum[r - 1] : 0.0);
+    // a decay below 2^-1024 is zero in fp32 already; sums stay finite (NaN stays)
+    const double log = l2 * dt[r];
+    cum[r] = (log < -1024.0 ? -1024.0 : log) + (r ? cum[r - 1] : 0.0);
   }
   double tot = cum[R - 1];
 #pragma unroll
@@ -200,9 +202,10 @@ struct Terms {
 // by half the rows of the transposed state, a lane four columns of a row of each
 // of its tiles.
 //
-// A sequence is one segment where the launch has blocks enough; otherwise kLocal
-// leaves what each segment adds to a state that enters it as zero, and the second
-// launch starts each segment from the states that the ones before it have left.
+// A sequence is one segment unless it is long (see SsmArgs::long_from); of those,
+// kLocal leaves what each segment adds to a state that enters it as zero, and the
+// second launch starts each segment from the states that the ones before it have
+// left.
 enum { kLocal = 0, kStates = 1, kFullStates = 2 };  // leave what a segment adds; states in TI; in fp32
 template <typename TI, int N, int MODE>
 __global__ void __launch_bounds__(256, 2) k_ssm_state(SsmArgs a, int dirs, int dir0, unsigned blocks) {
@@ -230,9 +233,14 @@ __global__ void __launch_bounds__(256, 2) k_ssm_state(SsmArgs a, int dirs, int d
     c.rows = static_cast<int>(c.s1 > c.s0 ? c.s1 - c.s0 : 0);
   }
   const int64_t len = c.s1 > c.s0 ? c.s1 - c.s0 : 0;
-  const int segs = seg && len ? static_cast<int>((len + seg * Q - 1) / (seg * Q)) : 1;  // of the sequence
+  int segs = 1;  // of the sequence
+  if (seg) {
+    if (c.n < 0) return;
+    if (len > a.long_from) segs = static_cast<int>((len + seg * Q - 1) / (seg * Q));
+    else c.rows = static_cast<int>(len);
+    if (c.pos >= segs) return;
+  }
   const bool ends = rev ? c.pos == 0 : c.pos == segs - 1;  // its state leaves the sequence
-  if (seg && c.rows <= 0 && !(c.n >= 0 && len == 0 && c.pos == 0)) return;
   if (LOCAL && ends) return;
   const int grp = h / (a.H / a.G);
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), i = lane & 15, g = lane >> 4;
@@ -982,9 +990,9 @@ __global__ void __launch_bounds__(256) k_ssm_scalars(SsmArgs a) {
   const int h = (blockIdx.x % nhb) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (h >= a.H) return;
   const Place c = find_piece(a, slot, Q);
-  float *p2 = a.part2 + slot * 2 * a.H + h, *p1 = a.part1 + slot * a.H + h;
+  float* out = a.param + slot * 3 * a.H + h;
   if (c.rows <= 0) {  // its parts are added up all the same
-    if (lane == 0) p2[0] = p2[a.H] = p1[0] = 0.f;
+    if (lane == 0) out[0] = out[a.H] = out[2 * a.H] = 0.f;
     return;
   }
   const int64_t at = (slot * a.H + h) * Q + R * lane;
@@ -1011,20 +1019,20 @@ __global__ void __launch_bounds__(256) k_ssm_scalars(SsmArgs a) {
   float dA = 0.f, db = 0.f;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const float dl = sa + sb, d = (v[r][2] - Ah * dl) * st[r][3];
+    const int t = R * lane + r;
+    const float dl = t < c.rows ? sa + sb : 0.f, d = (v[r][2] - Ah * dl) * st[r][3];
     sa -= v[r][0];
     sb += v[r][1];
     dA -= Ah * st[r][0] * dl;
     db += d;
-    const int t = R * lane + r;
     if (t < c.rows) static_cast<TI*>(a.ddt)[(c.t0 + t) * a.H + h] = from_f<TI>(d);
   }
   dA = sum_wave(dA);
   db = sum_wave(db);
   if (lane == 0) {
-    p2[0] = dA;
-    p2[a.H] = db;
-    p1[0] = diag;
+    out[0] = dA;
+    out[a.H] = db;
+    out[2 * a.H] = diag;
   }
 }
 

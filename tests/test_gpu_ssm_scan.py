@@ -9,13 +9,11 @@ output, and each element is held to its own:
                   fp32's roundings (sums of at most 128 + 128 terms in serial
                   runs of 32, the scores, decays and step sizes: below 100
                   roundings of 2^-24 = 6e-6); in fp32 1e-5
-  draw_dt         half a step, plus of the terms of its chunk, over which the
-                  decay's gradient is summed up and differs: 1e-5, and in
-                  bf16 2^-16 for the pairs of bf16 that states are (what a
-                  second rounding leaves, twice: 2 * 2^-17)
-  states and their gradients  (fp32) 2^-16 of their terms in bf16, 1e-5 in fp32
-  dA_log, ddt_bias, dD  fp32 sums of the above before their rounding: the same
-                  parts of their terms' sizes
+  draw_dt         half a step, plus 1e-5 of the terms of its chunk, over which
+                  the decay's gradient is summed up and differs
+  states and their gradients, dA_log, ddt_bias, dD  (fp32) 1e-5 of their terms
+In bf16 the fp32 outputs come from exact products too: a weighted row or state is
+three bf16, of 8 bits each, which leaves 2^-25 of it.
 """
 import numpy as np
 import pytest
@@ -81,8 +79,8 @@ def chunk_sums(t, cu, Q):
 def parity(x):
     dtype = x["x"].dtype
     half, Q = HALF_STEP[dtype], 128 if dtype is BF16 else 64
-    one, two = (1e-5, 1e-5) if dtype is F32 else (2.0 ** -8 + 1e-5, 2.0 ** -16 + 1e-5)
-    state = 1e-5 if dtype is F32 else 2.0 ** -16
+    one, two = 1e-5 if dtype is F32 else 2.0 ** -8 + 1e-5, 1e-5
+    state = 1e-5
     y_ref, s_ref, g = reference(x)
     y_abs, s_abs, t = reference(x, absolute=True)
     y, final = forward(x)
@@ -140,6 +138,81 @@ def test_scan_of_large_and_vanishing_steps(dtype):
     x["raw_dt"][:, 0], x["raw_dt"][:, 1] = -70.0, 90.0  # nothing written; only the own token seen
     x["raw_dt"][::9, 2], x["raw_dt"][4::9, 3] = 60.0, -60.0
     parity(x)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scan_of_decays_that_leave_nothing(dtype):
+    announce("scan with exp(A_log) up to fp32's largest %s" % dtype)
+    x = make([150, 3], 4, 1, 64, 64, dtype, 17)
+    x["A_log"].copy_(torch.tensor([87.5, 30.0, 8.0, -80.0]))  # nothing, nothing, little and all of a state is left
+    parity(x)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lens,H,G,P", [([1500, 0, 1, 1100, 399], 2, 1, 64), ([2111], 3, 3, 128), ([40, 2500, 60], 1, 1, 64)])
+def test_long_sequences_in_segments(dtype, lens, H, G, P):
+    announce("long sequences %s %s H%d P%d" % (lens, dtype, H, P))
+    x = make(lens, H, G, 128, P, dtype, 18)
+    x["A_log"][0] = -6.0  # a state that lasts over segments
+    parity(x)
+    parity(dict(x, init=None, dfinal=None))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_short_sequences(dtype):
+    announce("600 short sequences, heads of a group together and apart %s" % dtype)
+    lens = [1 + (7 * n) % 4 for n in range(600)]
+    parity(make(lens, 6, 1, 64, 64, dtype, 19))
+
+
+def test_segments_of_ragged_batches_replayed():
+    announce("long sequences: rows of no sequence, other lengths in a captured call")
+    x = make([1500, 0, 1, 1100, 399], 2, 1, 128, 64, BF16, 20)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = (*forward(x), *backward(x))
+    for cu in ([0, 1500, 1500, 1501, 2601, 3000], [700, 2900, 2900, 2900, 2901, 2950], [0, 600, 1200, 1800, 2400, 3000],
+               [5, 5, 5, 5, 5, 3000], [0, 0, 0, 0, 0, 0], [0, 3000, 3000, 3000, 3000, 3000]):
+        x["cu"].copy_(torch.tensor(cu, dtype=torch.int32))
+        leave_nan(x["x"].shape, BF16)
+        ref = (*forward(x), *backward(x))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(s, t) for s, t in zip(out, ref))
+        for n, (a, b) in enumerate(zip(cu, cu[1:])):  # each sequence by itself
+            part = dict(x, **{k: x[k][a:b].contiguous() for k in ("x", "raw_dt", "B", "C", "dy")}, cu=None,
+                        init=x["init"][n:n + 1].contiguous(), dfinal=x["dfinal"][n:n + 1].contiguous())
+            if b - a == 0:
+                assert torch.equal(ref[1][n], x["init"][n]) and torch.equal(ref[-1][n], x["dfinal"][n])
+                continue
+            one = (*forward(part), *backward(part))
+            for i in (0, 1, 2, 3, 5, 6, 9):  # states differ by the roundings of their segments
+                got = ref[i][n:n + 1] if i in (1, 9) else ref[i][a:b]
+                assert rel(to_np(got), to_np(one[i])) <= (1e-5 if i in (1, 9) else 2.0 ** -8), (cu, n, i)
+        for i in (0, 2, 3, 5, 6):
+            assert bool((ref[i][:cu[0]] == 0).all()) and bool((ref[i][cu[-1]:] == 0).all())
+
+
+def test_offsets_past_32_bits():
+    announce("scan: offsets past 2^31 elements")
+    H, G, N, P, T = 64, 1, 64, 128, 262144 + 300
+    x = make([70], H, G, N, P, BF16, 21)
+    far = dict(x, init=torch.zeros((2, H, N, P), device="cuda"), dfinal=torch.zeros((2, H, N, P), device="cuda"),
+               cu=torch.tensor([0, T - 70, T], dtype=torch.int32, device="cuda"))
+    for k in ("x", "raw_dt", "B", "C", "dy"):
+        far[k] = torch.zeros((T, *x[k].shape[1:]), dtype=BF16, device="cuda")
+        far[k][T - 70:] = x[k]
+    for k in ("init", "dfinal"):
+        far[k][1] = x[k][0]
+    a, b = (*forward(x), *backward(x)), (*forward(far), *backward(far))
+    assert b[0].numel() > 2 ** 31
+    for i in (0, 2, 3):
+        assert torch.equal(a[i], b[i][T - 70:]), i
+    for i in (1, 9):
+        assert torch.equal(a[i][0], b[i][1]), i
+    for i in (5, 6):  # the heads add up in another division
+        assert rel(to_np(b[i][T - 70:]), to_np(a[i])) <= 2.0 ** -8
+    assert not bool(b[0][:1000].any()) and not bool(b[2][-1000 - 70:-70].any())
 
 
 def make_single(dtype):
@@ -232,7 +305,7 @@ def test_pieces_of_a_sequence_and_decoding_continue_it(dtype):
     # rounding points move with the pieces' chunks: each is held to the reference
     y_ref, s_ref, _ = reference(x)
     y_abs, s_abs, _ = reference(x, absolute=True)
-    one, state = (1e-5, 1e-5) if dtype is F32 else (2.0 ** -8 + 1e-5, 2.0 ** -16 + 1e-5)
+    one, state = 1e-5 if dtype is F32 else 2.0 ** -8 + 1e-5, 1e-5
     lens, at, pool, rows = [300, 41], [0, 300], x["init"], []
     got = np.zeros_like(y_ref)
     for cut in ([100, 20], [97, 19]):

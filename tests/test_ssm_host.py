@@ -8,7 +8,7 @@ import pytest
 import torch
 from torch.autograd import forward_ad
 
-from recompute_kda_chunked_amd import KdaError, _lib, group_norm, ssm, ssm_recurrent
+from recompute_kda_chunked_amd import KdaError, _lib, group_norm, ssm, ssm_recurrent, ssm_scan, ssm_scan_backward
 from test_abi import lib  # noqa: F401  (fixture)
 
 FAKE, NUL = ctypes.c_void_p(0x1000), ctypes.c_void_p(0)
@@ -71,6 +71,70 @@ def test_recurrent_null_pointers_and_empty_calls(lib):  # noqa: F811
     assert call_rec(lib, problem(n_seqs=0, total_tokens=5), cu=FAKE) == _lib.KDA_OK
 
 
+FWD = ("x", "raw_dt", "A_log", "B", "C", "D", "dt_bias", "cu", "init", "y", "final")
+BWD = FWD[:9] + ("dy", "dfinal", "dx", "draw_dt", "dA_log", "dB", "dC", "dD", "ddt_bias", "dinit")
+
+
+def call_scan(lib, p, bwd, ws=1 << 44, workspace=FAKE, **null):  # noqa: F811
+    fn = lib.kda_ssm_bwd if bwd else lib.kda_ssm_fwd
+    return fn(ctypes.byref(p) if p is not None else None, *[NUL if n in null else FAKE for n in (BWD if bwd else FWD)],
+              workspace, ws, NUL)
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+@pytest.mark.parametrize("kw,code", BAD + [
+    (dict(total_tokens=1 << 31), _lib.KDA_ERR_INVALID),
+    (dict(x_stride=1 << 22), _lib.KDA_ERR_UNSUPPORTED),     # a chunk's rows in 32 bits
+    (dict(B_stride=1 << 22), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(C_stride=(1 << 22) + 8), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(H=1 << 16, G=1), _lib.KDA_ERR_UNSUPPORTED),       # H * P
+    (dict(H=1 << 15, G=1 << 15), _lib.KDA_ERR_UNSUPPORTED),  # G * N
+    (dict(total_tokens=(1 << 31) - 1), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(n_seqs=1 << 21), _lib.KDA_ERR_UNSUPPORTED),       # 2^23 (chunk, head)
+    (dict(P=128, n_seqs=1 << 20), _lib.KDA_ERR_UNSUPPORTED),  # 2^24 blocks of both state passes
+])
+def test_scan_rejects(lib, bwd, kw, code):  # noqa: F811
+    p = problem(**kw)
+    assert call_scan(lib, p, bwd) == code
+    assert (lib.kda_ssm_bwd_workspace_bytes if bwd else lib.kda_ssm_fwd_workspace_bytes)(ctypes.byref(p)) == 0
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_scan_null_pointers_and_workspace(lib, bwd):  # noqa: F811
+    size = lib.kda_ssm_bwd_workspace_bytes if bwd else lib.kda_ssm_fwd_workspace_bytes
+    assert call_scan(lib, None, bwd) == _lib.KDA_ERR_INVALID and size(None) == 0
+    p = problem(total_tokens=300)
+    need = size(ctypes.byref(p))
+    assert need > 0
+    assert call_scan(lib, p, bwd, ws=need - 1) == _lib.KDA_ERR_WORKSPACE
+    assert call_scan(lib, p, bwd, workspace=NUL) == _lib.KDA_ERR_INVALID
+    assert call_scan(lib, p, bwd, cu=1) == _lib.KDA_ERR_INVALID  # three sequences without cu_seqlens
+    for n in ("dy", "dx", "draw_dt", "dA_log", "dB", "dC") if bwd else ("y",):
+        assert call_scan(lib, p, bwd, ws=need, **{n: 1}) == _lib.KDA_ERR_INVALID
+    for n in ("x", "raw_dt", "A_log", "B", "C"):
+        assert call_scan(lib, p, bwd, ws=need, **{n: 1}) == _lib.KDA_ERR_INVALID
+    if bwd:  # the sums are written whatever there is
+        assert call_scan(lib, problem(n_seqs=0, total_tokens=0), bwd, dA_log=1) == _lib.KDA_ERR_INVALID
+    else:  # nothing to do: no launch, whatever the pointers
+        none = {n: 1 for n in FWD if n != "cu"}
+        assert call_scan(lib, problem(n_seqs=0, total_tokens=0), bwd, **none) == _lib.KDA_OK
+        assert call_scan(lib, problem(total_tokens=0), bwd, **none) == _lib.KDA_OK
+
+
+def test_scan_workspace_follows_the_tokens(lib):  # noqa: F811
+    """Short sequences need no segments, long ones few: the room stays near the
+    states' (fp32, two of them backward), a slot a chunk or sequence."""
+    for dtype, Q, kept in ((_lib.KDA_BF16, 128, 2), (_lib.KDA_F32, 64, 4)):
+        for n, T in ((1, 100), (1, 1 << 15), (1, 1 << 18), (8, 1 << 15), (1000, 1 << 12), (4000, 1 << 15)):
+            p = problem(n_seqs=n, total_tokens=T, dtype=dtype, H=64, G=1)
+            slots = T // Q + n
+            states = slots * 64 * 64 * 128
+            steps = slots * 64 * Q * 16
+            fwd, bwd = (f(ctypes.byref(p)) for f in (lib.kda_ssm_fwd_workspace_bytes, lib.kda_ssm_bwd_workspace_bytes))
+            assert states * kept <= fwd <= 2 * states * 4 + steps + (1 << 20)
+            assert states * 8 <= bwd <= 3 * states * 4 + 2 * steps + 4 * slots * 64 * 5 + 256 * 64 * Q * 128 * 8 + (1 << 20)
+
+
 def norm_problem(**kw):
     d = dict(rows=5, C=512, groups=8, dtype=_lib.KDA_BF16, gate=0, activation=_lib.KDA_ACT_SILU, center=1, eps=1e-6)
     d.update(kw)
@@ -130,6 +194,12 @@ def rec_inputs(T=3, H=4, G=2, N=64, P=128, dtype=torch.float32):
                 dt_bias=torch.zeros(H), state=torch.zeros(T, H, N, P))
 
 
+def scan_inputs():
+    x = rec_inputs()
+    x["initial_state"] = x.pop("state")[:1].contiguous()
+    return x
+
+
 def norm_inputs():
     return dict(x=torch.zeros(4, 96), weight=torch.zeros(96), bias=torch.zeros(96), gate=torch.zeros(4, 96))
 
@@ -138,7 +208,7 @@ def norm(**x):
     return group_norm(**x, groups=3)
 
 
-DIFFERENTIABLE = [(norm, norm_inputs)]
+DIFFERENTIABLE = [(norm, norm_inputs), (ssm_scan, scan_inputs)]
 IN_PLACE = [(ssm_recurrent, rec_inputs)]
 
 
@@ -185,6 +255,46 @@ def test_recurrent_binding_refuses(no_launch, change, match):
     with pytest.raises(KdaError, match=match):
         ssm_recurrent(**dict(rec_inputs(), **change))
     assert not no_launch
+
+
+@pytest.mark.parametrize("change,match", [
+    (dict(x=torch.zeros(3, 512)), "expected \\[T,H,P\\]"),
+    (dict(x=torch.zeros(3, 4, 128, dtype=torch.float16)), "float32 or bfloat16"),
+    (dict(raw_dt=torch.zeros(3, 4).bfloat16()), "raw_dt: expected"),
+    (dict(B=torch.zeros(3, 3, 64), C=torch.zeros(3, 3, 64)), "must divide the heads"),
+    (dict(C=torch.zeros(4, 2, 64)), "C: expected"),
+    (dict(x=torch.zeros(3, 4, 32)), "not built"),
+    (dict(dt_limit=(INF, INF)), "dt_limit"),
+    (dict(initial_state=torch.zeros(3, 4, 64, 128)), "initial_state: expected"),
+    (dict(initial_state=torch.zeros(1, 4, 64, 128).bfloat16()), "initial_state: expected"),
+    (dict(initial_state=torch.zeros(1, 4, 128, 64).transpose(2, 3)), "contiguous"),
+    (dict(cu_seqlens=torch.zeros(2)), "cu_seqlens: expected"),
+    (dict(cu_seqlens=torch.zeros(0, dtype=torch.int32)), "cu_seqlens: expected"),
+    (dict(cu_seqlens=torch.zeros(2, 1, dtype=torch.int32)), "cu_seqlens: expected"),
+    (dict(x=torch.zeros(3, 4, 130)[..., :128]), "elements of a token must be contiguous"),
+    (dict(C=torch.zeros(3, 129)[:, :128].view(3, 2, 64)), "multiples of 16 bytes"),
+])
+def test_scan_binding_refuses(no_launch, change, match):
+    x = dict(scan_inputs(), **change)
+    with pytest.raises(KdaError, match=match):
+        ssm_scan(**x)
+    args = [x[k] for k in ("x", "raw_dt", "A_log", "B", "C", "D", "dt_bias")]
+    with pytest.raises(KdaError, match=match):
+        ssm_scan_backward(*args, torch.zeros_like(x["x"]), x.get("cu_seqlens"), initial_state=x["initial_state"],
+                          **{k: x[k] for k in ("dt_limit",) if k in x})
+    assert not no_launch
+
+
+def test_scan_gradients_must_match(no_launch):
+    x = scan_inputs()
+    args = [x[k] for k in ("x", "raw_dt", "A_log", "B", "C", "D", "dt_bias")]
+    ssm_scan_backward(*args, torch.zeros(3, 4, 128), d_final_state=torch.zeros(1, 4, 64, 128))
+    for dy, dfinal, match in ((torch.zeros(3, 512), None, "dy: expected"),
+                              (torch.zeros(3, 4, 128).bfloat16(), None, "dy: expected"),
+                              (torch.zeros(3, 4, 129)[..., :128], None, "dy must be contiguous"),
+                              (torch.zeros(3, 4, 128), torch.zeros(2, 4, 64, 128), "d_final_state: expected")):
+        with pytest.raises(KdaError, match=match):
+            ssm_scan_backward(*args, dy, d_final_state=dfinal)
 
 
 def test_recurrent_out_must_be_apart(no_launch):
