@@ -50,9 +50,11 @@ struct SsmArgs {
   int seg;
   int64_t seg_slots, long_from;
   float *local, *seg_log;
-  // Of the gradients: per token {what dl adds up from it on, before it, the step
-  // size's own part} [slots][H][Q] of four, per chunk {states' part of dl, dD}.
-  float *sums, *ends;
+  // Of the gradients (see k_ssm_scalars): per token {what dl adds up from it on in
+  // the chunk, before it, the step size's own part, from it on in its tile of 16
+  // tokens} [slots][H][Q] of four, and before it in its tile; per chunk {states'
+  // part of dl, dD} and the sums over pairs of tiles [slots][H][Q / 16][Q / 16].
+  float *sums, *before, *ends, *cross;
   float *pB, *pC;        // partial dB and dC [blocks behind the whole ones][Q][N] where sets > 1
   float *param;          // per slot {dA, ddt_bias, dD} [3 H]
   // Blocks that take all heads of a group in a chunk, and into how many the heads

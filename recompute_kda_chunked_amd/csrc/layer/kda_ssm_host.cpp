@@ -31,7 +31,7 @@ int check_ssm(const kda_ssm_problem* p) {
 struct ScanPlan {
   int Q, sets = 1, seg = 0;
   int64_t slots, whole, seg_slots = 0, long_from;
-  size_t steps, state, dstate = 0, local, seg_log, sums = 0, ends = 0, partial = 0, param = 0;
+  size_t steps, state, dstate = 0, local, seg_log, sums = 0, before = 0, ends = 0, cross = 0, partial = 0, param = 0;
   ScanPlan(const kda_ssm_problem* p, bool bwd) {
     Q = ssm_chunk(p->dtype);
     const int64_t T = p->total_tokens, HP = static_cast<int64_t>(p->H) * p->P;
@@ -77,13 +77,15 @@ struct ScanPlan {
     if (bwd) {
       dstate = state;
       sums = steps;
+      before = part(slots * p->H * Q, 4);
       ends = part(slots * p->H * 2, 4);
+      cross = part(slots * p->H * (Q / 16) * (Q / 16), 4);
       partial = sets > 1 ? part((units - whole) * sets * Q * p->N, 4) : 0;
       param = part(slots * p->H * 3, 4);
     }
   }
   size_t bytes() const {
-    return steps + state + dstate + local + seg_log + sums + ends + 2 * partial + param;
+    return steps + state + dstate + local + seg_log + sums + before + ends + cross + 2 * partial + param;
   }
 };
 
@@ -145,7 +147,9 @@ SsmArgs scan_args(const kda_ssm_problem* p, const ScanPlan& plan, const void* x,
   a.local = reinterpret_cast<float*>(take(plan.local));
   a.seg_log = reinterpret_cast<float*>(take(plan.seg_log));
   a.sums = reinterpret_cast<float*>(take(plan.sums));
+  a.before = reinterpret_cast<float*>(take(plan.before));
   a.ends = reinterpret_cast<float*>(take(plan.ends));
+  a.cross = reinterpret_cast<float*>(take(plan.cross));
   a.pB = reinterpret_cast<float*>(take(plan.partial));
   a.pC = reinterpret_cast<float*>(take(plan.partial));
   a.param = reinterpret_cast<float*>(take(plan.param));

@@ -614,6 +614,9 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
   if (rows <= 0 || h0 >= h1) return;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number();
   const int jt = own_tile<NW>(w), halves = a.P / 64;
+  // the sums over a diagonal tile's columns lie where the waves of the last tiles
+  // have no rows
+  auto tile_cols = [&](int t) __attribute__((always_inline)) { return t + 1 < NW ? rowF[NW / 2] + 16 * t : rowF[NW / 2 + 1]; };
   const int ng = NG == NW ? w : w % NG, tt0 = NG == NW ? 0 : (w / NG) * TT, n0 = ng * NT * 16;  // of the second role
 
   Rows<TI, Q, 64, TH> nx, ny;
@@ -724,7 +727,8 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
         }
 #pragma unroll
         for (int p = 0; p < 4; ++p) dx[p] *= rj;
-        float cf = 0.f, diag = 0.f;
+        // what follows j: behind its own tile of 16 tokens, and in it
+        float cf = 0.f, cd = 0.f, diag = 0.f;
 #pragma unroll
         for (int m = 0; m < NW / 2; ++m) {
           if (2 * m + 1 < jt) continue;
@@ -773,11 +777,11 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
                     f[r] = 0.f;
                   }
               }
+              const float sum = (f[0] + f[1]) + (f[2] + f[3]);
+              if (below) cf += sum;
+              else cd = sum;
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                cf += f[r];
-                f[r] *= dtj;
-              }
+              for (int r = 0; r < 4; ++r) f[r] *= dtj;
               const float v[4] = {f[0], f[1], f[2], f[3]};
               const float s = transpose_sum16<4>(v);  // lane i: of f[i % 4]
               if (i < 4) rowF[w][i0 + i] = s;
@@ -791,7 +795,11 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
           __builtin_amdgcn_sched_barrier(0);
         }
         cf = sum_lane_groups(cf);
-        if (g == 0) colF[row] = cf;
+        cd = sum_lane_groups(cd);
+        if (g == 0) {
+          colF[row] = cf;
+          tile_cols(jt)[i] = cd;
+        }
         diag = sum_wave(diag);
         if (lane == 0) xd[w] = diag;
         if (row < rows) {
@@ -933,14 +941,29 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
           cc += iC[part * (NG / 4) + k][t];
           cb += iB[part * (NG / 4) + k][t];
         }
-        rf = group_sum<4>(rf + cc);
+        rf = group_sum<4>(rf);
+        cc = group_sum<4>(cc);
         cb = group_sum<4>(cb);
         if (part == 0) {
-          const float col = colF[t], d = cdt[t];
-          f32x4* out = reinterpret_cast<f32x4*>(a.sums) + (slot * a.H + h) * Q + t;
-          f32x4 v = f32x4{rf - d * col, d * cb, (col + ownF[t]) + cb, 0.f};
-          if (half) v += *out;  // the head's first half, of this thread
+          const float col = colF[t], in = tile_cols(t / 16)[t % 16], d = cdt[t];
+          const int64_t at = (slot * a.H + h) * Q + t;
+          f32x4* out = reinterpret_cast<f32x4*>(a.sums) + at;
+          f32x4 v = f32x4{cc, d * cb, ((col + in) + ownF[t]) + cb, rf - d * in};
+          float b = d * col;
+          if (half) {  // the head's first half, of this thread
+            v += *out;
+            b += a.before[at];
+          }
           *out = v;
+          a.before[at] = b;
+        }
+        // this wave's columns by the tiles of the rows behind theirs
+#pragma unroll
+        for (int k = 0; k < Q / 64; ++k) {
+          const int l = ft & 63, tile = 4 * k + (l >> 4);
+          float x = group_sum<16>(tile > jt ? rowF[w][64 * k + l] : 0.f);
+          float* out = a.cross + (slot * a.H + h) * (NW * NW) + jt * NW + tile;
+          if (l % 16 == 0) *out = half ? *out + x : x;
         }
         if (tid == 0) {
           float dots = 0.f, diag = 0.f;
@@ -982,9 +1005,16 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
 
 // One wave per (chunk, head), Q / 64 tokens a lane: the gradient of each token's
 // log decay, of the step sizes, and the chunk's parts of the parameters'.
+//
+// Of dl_t's first sum, over i >= t > j, pairs of different tiles of 16 tokens are
+// added up as they are, by where t lies: in i's tile (a sum over rows from t on),
+// in j's (over columns before t) or between them (`cross`, sums over a pair of
+// tiles). Those of one tile are differences of what rows and columns from t on add
+// up to. Taken over the whole chunk, those differences are short but their roundings
+// reach every t before them: dA_log was off by 1e-5 where steps are long, 1e-6 so.
 template <typename TI>
 __global__ void __launch_bounds__(256) k_ssm_scalars(SsmArgs a) {
-  constexpr int Q = Chunk<TI>::Q, R = Q / 64;
+  constexpr int Q = Chunk<TI>::Q, R = Q / 64, NW = Q / 16, LT = 16 / R;  // LT: lanes of a tile
   const int nhb = (a.H + 3) / 4;
   const int64_t slot = blockIdx.x / nhb;
   const int h = (blockIdx.x % nhb) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -995,34 +1025,54 @@ __global__ void __launch_bounds__(256) k_ssm_scalars(SsmArgs a) {
     if (lane == 0) out[0] = out[a.H] = out[2 * a.H] = 0.f;
     return;
   }
-  const int64_t at = (slot * a.H + h) * Q + R * lane;
+  const int64_t head = slot * a.H + h, at = head * Q + R * lane;
   f32x4 v[R], st[R];
-  float sa = 0.f, sb = 0.f;
+  float bf[R];
+  float sa = 0.f, sb = 0.f, ta = 0.f, tb = 0.f;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     v[r] = reinterpret_cast<const f32x4*>(a.sums)[at + r];
     st[r] = reinterpret_cast<const f32x4*>(a.steps)[at + r];
+    bf[r] = a.before[at + r];
     sa += v[r][0];
     sb += v[r][1];
+    ta += v[r][3];
+    tb += bf[r];
   }
-  const float q0 = a.ends[2 * (slot * a.H + h)], diag = a.ends[2 * (slot * a.H + h) + 1];
-  const float lb = sb;
+  const float pair = lane < NW * NW ? a.cross[head * (NW * NW) + lane] : 0.f;
+  const float q0 = a.ends[2 * head], diag = a.ends[2 * head + 1];
+  // from the lane on, and up to it
 #pragma unroll
   for (int o = 1; o < 64; o *= 2) {
     const float da = __shfl_down(sa, o, 64), ub = __shfl_up(sb, o, 64);
     if (lane + o < 64) sa += da;
     if (lane >= o) sb += ub;
+    if (o < LT) {
+      const float dt = __shfl_down(ta, o, 64), ut = __shfl_up(tb, o, 64);
+      if (lane % LT + o < LT) ta += dt;
+      if (lane % LT >= o) tb += ut;
+    }
   }
-  sb += q0 - lb;
-  // dl_t: the first sums from t on, the second before t, and the states'
+  const float ub = __shfl_up(sb, 1, 64), ut = __shfl_up(tb, 1, 64);
+  sb = lane ? ub : 0.f;
+  tb = lane % LT ? ut : 0.f;
+  float over = 0.f;
+#pragma unroll
+  for (int k = 1; k + 1 < NW; ++k) {
+    const float s = sum_wave(lane % NW > k && lane / NW < k ? pair : 0.f);
+    if (lane / LT == k) over = s;
+  }
+  over += q0;
   const float Ah = expf(a.A_log[h]);
   float dA = 0.f, db = 0.f;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int t = R * lane + r;
-    const float dl = t < c.rows ? sa + sb : 0.f, d = (v[r][2] - Ah * dl) * st[r][3];
+    const float dl = t < c.rows ? ((sa + sb) + (ta + tb)) + over : 0.f, d = (v[r][2] - Ah * dl) * st[r][3];
     sa -= v[r][0];
     sb += v[r][1];
+    ta -= v[r][3];
+    tb += bf[r];
     dA -= Ah * st[r][0] * dl;
     db += d;
     if (t < c.rows) static_cast<TI*>(a.ddt)[(c.t0 + t) * a.H + h] = from_f<TI>(d);

@@ -11,7 +11,9 @@ output, and each element is held to its own:
                   roundings of 2^-24 = 6e-6); in fp32 1e-5
   draw_dt         half a step, plus 1e-5 of the terms of its chunk, over which
                   the decay's gradient is summed up and differs
-  states and their gradients, dA_log, ddt_bias, dD  (fp32) 1e-5 of their terms
+  dA_log          (fp32) 1e-5 of its terms, and 1e-6 (16 roundings of 2^-24) of
+                  those of a tile of 16 tokens, of which it takes differences
+  states and their gradients, ddt_bias, dD  (fp32) 1e-5 of their terms
 In bf16 the fp32 outputs come from exact products too: a weighted row or state is
 three bf16, of 8 bits each, which leaves 2^-25 of it.
 """
@@ -94,7 +96,7 @@ def parity(x):
     dt, slope = ssm_ref.step_sizes(to_np(x["raw_dt"]), None if x["dt_bias"] is None else to_np(x["dt_bias"]), x["limit"])
     terms = chunk_sums(t["tall"], x["cu_host"], Q) * slope
     held("draw_dt", ddt, g["draw_dt"], half * np.abs(g["draw_dt"]) + two * terms)
-    held("dA_log", dA, g["dA_log"], two * np.sum(dt * chunk_sums(t["tall"], x["cu_host"], Q), 0))
+    held("dA_log", dA, g["dA_log"], 1e-5 * np.abs(t["dA_log"]) + 1e-6 * np.sum(dt * chunk_sums(t["tall"], x["cu_host"], 16), 0))
     if x["D"] is not None:
         held("dD", dD, g["dD"], 1e-5 * t["dD"])
     if x["dt_bias"] is not None:
@@ -145,6 +147,15 @@ def test_scan_of_decays_that_leave_nothing(dtype):
     announce("scan with exp(A_log) up to fp32's largest %s" % dtype)
     x = make([150, 3], 4, 1, 64, 64, dtype, 17)
     x["A_log"].copy_(torch.tensor([87.5, 30.0, 8.0, -80.0]))  # nothing, nothing, little and all of a state is left
+    parity(x)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scan_of_long_steps(dtype):
+    announce("scan whose decays forget within a few tokens %s" % dtype)
+    x = make([400, 128, 37], 4, 1, 128, 64, dtype, 22)
+    x["A_log"].add_(1.5)
+    x["dt_bias"].zero_()
     parity(x)
 
 
