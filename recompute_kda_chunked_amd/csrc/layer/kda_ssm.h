@@ -36,17 +36,18 @@ struct SsmArgs {
   const float *A_log, *D, *dt_bias, *init, *dfinal;
   const int32_t* cu;
   void *y, *dx, *ddt, *dB, *dC;
-  float *final_state, *dA, *dD, *dbias, *dinit;
+  float *final_state, *dinit;
   // Workspace. steps [slots][H][Q]: {dt, high and low part of the chunk's
   // running sum of log2 decays, d dt / d raw_dt}. S and dS: the states entering
-  // each chunk and the gradients of those leaving it, [slots][H][P / 64][N][64],
-  // fp32 with S_full, else in the problem's dtype.
+  // each chunk and the gradients of those leaving it, [slots][H][P / 64][N][64] in
+  // the problem's dtype, or with S_full in fp32 and in the order of accumulators,
+  // [slots][H][P / 64][N / 16][64 / 16][lane][4].
   float* steps;
   void *S, *dS;
   bool S_full;
   // Segments of `seg` chunks (0: none) of sequences of more than long_from tokens,
   // in seg_slots slots of their own: what each adds to its state, and its log2
-  // decay, [directions][seg_slots][H]..
+  // decay, [directions][seg_slots][H].., the former in the order of accumulators.
   int seg;
   int64_t seg_slots, long_from;
   float *local, *seg_log;

@@ -255,9 +255,10 @@ __global__ void __launch_bounds__(256, 2) k_ssm_state(SsmArgs a, int dirs, int d
   const float* from = rev ? a.dfinal : a.init;
   float* to = rev ? a.dinit : a.final_state;
   const size_t state = ((static_cast<size_t>(c.n) * a.H + h) * N + nt + i) * a.P + half * 64 + p0 + 4 * g;
-  // of a segment's own slot: [H][halves][N][64]
+  // of a slot: [H][halves][N][64], or as in SsmArgs::local
   const size_t tile = (static_cast<size_t>(hp) * N + nt + i) * 64 + p0 + 4 * g, step = static_cast<size_t>(a.H) * halves * N * 64;
-  float* local = a.local + rev * a.seg_slots * step + tile;
+  const size_t order = static_cast<size_t>(hp) * N * 64 + (nt / 16 * 4 + p0 / 16) * 256 + 4 * lane;
+  float* local = a.local + rev * a.seg_slots * step + order;
 
   const LaneAt<TI, 64> lx(lane);
   const LaneAt<TI, N> lb(lane);
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(256, 2) k_ssm_state(SsmArgs a, int dirs, int d
       for (int u = 0; u < NT; ++u)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          acc[u][t] = d * acc[u][t] + *reinterpret_cast<const f32x4*>(local + at * step + 16 * u * 64 + 16 * t);
+          acc[u][t] = d * acc[u][t] + *reinterpret_cast<const f32x4*>(local + at * step + (4 * u + t) * 256);
     }
   }
 
@@ -320,13 +321,14 @@ __global__ void __launch_bounds__(256, 2) k_ssm_state(SsmArgs a, int dirs, int d
     __syncthreads();
     load(k + 1 < nch ? k + 1 : k);
     if constexpr (!LOCAL) {
-      const size_t at = (first + ch) * step + tile;
+      const size_t at = (first + ch) * step;
 #pragma unroll
       for (int u = 0; u < NT; ++u)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if constexpr (MODE == kFullStates) store4<float>(static_cast<float*>(rev ? a.dS : a.S) + at + 16 * u * 64 + 16 * t, acc[u][t]);
-          else store4<TI>(static_cast<TI*>(a.S) + at + 16 * u * 64 + 16 * t, acc[u][t]);
+          // whole lines at once, and past the caches
+          if constexpr (MODE == kFullStates) store4<float, true>(static_cast<float*>(rev ? a.dS : a.S) + at + order + (4 * u + t) * 256, acc[u][t]);
+          else store4<TI>(static_cast<TI*>(a.S) + at + tile + 16 * u * 64 + 16 * t, acc[u][t]);
         }
     }
 #pragma unroll
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(256, 2) k_ssm_state(SsmArgs a, int dirs, int d
 #pragma unroll
     for (int u = 0; u < NT; ++u)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) *reinterpret_cast<f32x4*>(local + sslot * step + 16 * u * 64 + 16 * t) = acc[u][t];
+      for (int t = 0; t < 2; ++t) *reinterpret_cast<f32x4*>(local + sslot * step + (4 * u + t) * 256) = acc[u][t];
     if (tid == 0 && half == 0) a.seg_log[(rev * a.seg_slots + sslot) * a.H + h] = static_cast<float>(total);
   } else if (to && ends) {
 #pragma unroll
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q) k_ssm_grad(SsmArgs a) {
 #pragma unroll
     for (int u = 0; u < NT; ++u)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) f[u][k] = frag_mem(m, n0 + 16 * u, 32 * k, 64, fresh);
+      for (int k = 0; k < 2; ++k) f[u][k] = frag_state(m, n0 + 16 * u, 32 * k, fresh);
   };
   load_rows(h0, 0);
   load_state(G0, a.dS, h0, 0);

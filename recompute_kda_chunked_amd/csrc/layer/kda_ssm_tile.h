@@ -123,12 +123,14 @@ __device__ __forceinline__ f32x4 tile_get4(const T* t, const LaneAt<T, COLS>& l,
   load4_raw<T>(t + shifted<LaneAt<T, COLS>>(l.four, c0) + r0 * COLS, u);
   return unpack4<T>(u);
 }
-// The same from a row-major matrix in memory, rows `ld` apart (plain).
-__device__ __forceinline__ bf16x8 frag_mem(const bf16* m, int r0, int k0, int ld, int lane) {
-  return *reinterpret_cast<const bf16x8*>(m + (r0 + (lane & 15)) * ld + k0 + 8 * (lane >> 4));
-}
-__device__ __forceinline__ f32x8 frag_mem(const float* m, int r0, int k0, int ld, int lane) {
-  return *reinterpret_cast<const f32x8*>(m + (r0 + (lane & 15)) * ld + k0 + 8 * (lane >> 4));
+// Rows r0 .. r0 + 15, reduction over columns k0 .. k0 + 31 (plain), of a state of
+// 64 columns in memory in the order of accumulators: tiles of 16 x 16, by lane,
+// lane i + 16 g with columns 4 g .. 4 g + 3 of row i.
+__device__ __forceinline__ f32x8 frag_state(const float* m, int r0, int k0, int lane) {
+  const int i = lane & 15, g = lane >> 4;
+  const float* p = m + (r0 / 4 + k0 / 16 + (g >> 1)) * 256 + 4 * (i + 32 * (g & 1));
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 64);
+  return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
 // Two accumulator tiles as one operand (paired).
