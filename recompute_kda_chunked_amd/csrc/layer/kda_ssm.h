@@ -39,9 +39,9 @@ struct SsmArgs {
   float *final_state, *dinit;
   // Workspace. steps [slots][H][Q]: {dt, high and low part of the chunk's
   // running sum of log2 decays, d dt / d raw_dt}. S and dS: the states entering
-  // each chunk and the gradients of those leaving it, [slots][H][P / 64][N][64] in
-  // the problem's dtype, or with S_full in fp32 and in the order of accumulators,
-  // [slots][H][P / 64][N / 16][64 / 16][lane][4].
+  // each chunk and the gradients of those leaving it, [slots][H][P / 64] and then in
+  // the order of accumulators, in the problem's dtype [N / 16][64 / 32][lane][2][4],
+  // or with S_full in fp32 [N / 16][64 / 16][lane][4].
   float* steps;
   void *S, *dS;
   bool S_full;

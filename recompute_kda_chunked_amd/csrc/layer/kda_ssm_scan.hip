@@ -162,6 +162,43 @@ struct Rows {
     for (int m = 0; m < PER; ++m) *reinterpret_cast<uint4*>(tile + place(tid, m)) = kept(rows, tid, m);
   }
 };
+// A state of 64 columns on its way from accumulators to k_ssm_out's tile, in TI:
+// [N / 16][64 / 32][lane][2][4], lane i + 16 g with columns 4 g .. 4 g + 3 and 16
+// on of row i.
+template <typename TI, int N>
+struct StateRows {
+  static constexpr int TH = 4 * Chunk<TI>::Q, U = 16 / sizeof(TI), PER = N * 64 / U / TH;
+  f32x4 v[PER];
+  static __device__ __forceinline__ void put(TI* at, int u, const f32x4& a, const f32x4& b) {
+    if constexpr (U == 8) {
+      bf16x8 f = pair_frag<TI>(a, b);
+      *reinterpret_cast<bf16x8*>(at + u * 1024) = f;
+    } else {
+      *reinterpret_cast<f32x4*>(at + u * 1024) = a;
+      *reinterpret_cast<f32x4*>(at + u * 1024 + 4) = b;
+    }
+  }
+  __device__ __forceinline__ void load(const TI* s, int tid) {
+#pragma unroll
+    for (int m = 0; m < PER; ++m) v[m] = *reinterpret_cast<const f32x4*>(s + (tid + TH * m) * U);
+  }
+  __device__ __forceinline__ void store(TI* tile, int tid) const {
+    constexpr int PARTS = 8 / U, RPM = TH / (128 * PARTS) * 16;  // units a lane, rows a step of TH units
+    const int l = tid / PARTS % 64, i = l & 15, g = l >> 4, c = tid / (64 * PARTS) % 2, r = tid / (128 * PARTS) * 16 + i;
+#pragma unroll
+    for (int m = 0; m < PER; ++m) {
+      if constexpr (U == 8) {
+        const f32x4 x = v[m];
+        typedef __attribute__((ext_vector_type(2))) float f32x2;
+        *reinterpret_cast<f32x2*>(tile + tile_at<TI, 64>(r, 32 * c + 4 * g) + m * RPM * 64) = f32x2{x[0], x[1]};
+        *reinterpret_cast<f32x2*>(tile + tile_at<TI, 64>(r, 32 * c + 16 + 4 * g) + m * RPM * 64) = f32x2{x[2], x[3]};
+      } else {
+        *reinterpret_cast<f32x4*>(tile + tile_at<TI, 64>(r, 32 * c + 16 * (tid % 2) + 4 * g) + m * RPM * 64) = v[m];
+      }
+    }
+  }
+};
+
 // A token's step size and running sum.
 struct Step {
   float dt, hi, lo;
@@ -255,8 +292,8 @@ __global__ void __launch_bounds__(256, 2) k_ssm_state(SsmArgs a, int dirs, int d
   const float* from = rev ? a.dfinal : a.init;
   float* to = rev ? a.dinit : a.final_state;
   const size_t state = ((static_cast<size_t>(c.n) * a.H + h) * N + nt + i) * a.P + half * 64 + p0 + 4 * g;
-  // of a slot: [H][halves][N][64], or as in SsmArgs::local
-  const size_t tile = (static_cast<size_t>(hp) * N + nt + i) * 64 + p0 + 4 * g, step = static_cast<size_t>(a.H) * halves * N * 64;
+  // of a slot, as in SsmArgs::S without and with S_full
+  const size_t tile = static_cast<size_t>(hp) * N * 64 + (nt / 16 * 2 + p0 / 32) * 512 + 8 * lane, step = static_cast<size_t>(a.H) * halves * N * 64;
   const size_t order = static_cast<size_t>(hp) * N * 64 + (nt / 16 * 4 + p0 / 16) * 256 + 4 * lane;
   float* local = a.local + rev * a.seg_slots * step + order;
 
@@ -323,13 +360,15 @@ __global__ void __launch_bounds__(256, 2) k_ssm_state(SsmArgs a, int dirs, int d
     if constexpr (!LOCAL) {
       const size_t at = (first + ch) * step;
 #pragma unroll
-      for (int u = 0; u < NT; ++u)
+      for (int u = 0; u < NT; ++u) {
+        // whole lines at once, fp32 past the caches
+        if constexpr (MODE == kFullStates) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          // whole lines at once, and past the caches
-          if constexpr (MODE == kFullStates) store4<float, true>(static_cast<float*>(rev ? a.dS : a.S) + at + order + (4 * u + t) * 256, acc[u][t]);
-          else store4<TI>(static_cast<TI*>(a.S) + at + tile + 16 * u * 64 + 16 * t, acc[u][t]);
+          for (int t = 0; t < 2; ++t) store4<float, true>(static_cast<float*>(rev ? a.dS : a.S) + at + order + (4 * u + t) * 256, acc[u][t]);
+        } else {
+          StateRows<TI, N>::put(static_cast<TI*>(a.S) + at + tile, u, acc[u][0], acc[u][1]);
         }
+      }
     }
 #pragma unroll
     for (int u = 0; u < NT; ++u)
@@ -467,11 +506,11 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q, sizeof(TI) == 2 ? 4 : 2) k_s
   }
   TI *xs = buf, *Ss = buf + Q * 64;
   Rows<TI, Q, 64, TH> nx;  // the next head's x and state
-  Rows<TI, N, 64, TH> ns;
+  StateRows<TI, N> ns;
   Step nstep;
   auto load = [&](int h, int half) __attribute__((always_inline)) {
     nx.load(static_cast<const TI*>(a.x) + t0 * a.xs + static_cast<size_t>(h) * a.P + half * 64, static_cast<uint32_t>(a.xs), rows, tid);
-    ns.load(static_cast<const TI*>(a.S) + ((slot * a.H + h) * halves + half) * static_cast<size_t>(N) * 64, 64, N, tid);
+    ns.load(static_cast<const TI*>(a.S) + ((slot * a.H + h) * halves + half) * static_cast<size_t>(N) * 64, tid);
     nstep = load_step(a.steps, (slot * a.H + h) * Q + tid % Q);
   };
   load(h0, 0);
@@ -480,7 +519,7 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q, sizeof(TI) == 2 ? 4 : 2) k_s
     for (int half = 0; half < halves; ++half) {
       __syncthreads();
       nx.store(xs, rows, tid);
-      ns.store(Ss, N, tid);
+      ns.store(Ss, once(tid));
       if (tid < Q) {
         cdt[tid] = nstep.dt;
         chi[tid] = nstep.hi;
