@@ -451,9 +451,15 @@ int kda_short_conv_update(const kda_short_conv_problem *p, const void *x, const 
    (the *_stride fields, 0: adjacent), as slices of the convolution's output
    have; strides of x, B and C are multiples of 16 bytes. Pointers other than
    raw_dt's and cu_seqlens are 16-byte aligned; outputs must not overlap inputs.
-   T = 0 is allowed. States, decays and sums are fp32; a bf16 problem rounds
-   what the matrix cores multiply (once, or to a pair of bf16 where an fp32
-   output depends on it). The backward recomputes what it needs from the
+   T = 0 is allowed. Token strides of x, B and C, H * P and G * N are below 2^22
+   elements; the blocks of a launch bound the tokens and sequences
+   (KDA_ERR_UNSUPPORTED, from about 2^22 / H chunks of 64 tokens and sequences).
+   States, decays and sums are fp32; a bf16 problem rounds what the matrix cores
+   multiply (once, or to three bf16, which hold it, where an fp32 output depends
+   on it). NaN and infinities spread over their sequence as the formulas have
+   them. The workspace holds the states every 128 tokens (64 for fp32) and at
+   sequence starts, in the problem's type, backward in fp32 and twice, and up to
+   as much again where long sequences are divided. The backward recomputes what it needs from the
    inputs, takes dy and d_final_state (NULL: zero) and writes dx [T, H, P],
    draw_dt [T, H], dB, dC [T, G, N] (dtype, rows adjacent), dA_log, dD and
    ddt_bias [H] (fp32, summed in a fixed order; dD and ddt_bias may be NULL:

@@ -6,7 +6,10 @@
 // `lp` lanes (a power of two up to a wave, or the whole block), NV 16-byte
 // vectors a lane; slots keep their group over all their rows, so weights and
 // their gradients stay in registers. Means are taken off before the squares
-// are added up. Sums are fp32, every output is rounded once.
+// are added up. Sums are fp32, every output is rounded once. Measured at 8192 rows
+// of 4096 bf16 channels, groups of 512 with a gate: forward 34 us (5.9 TB/s),
+// backward 56 (6.0), the rows past the caches; 4097 x 2560 without a gate, in the
+// caches, 15 (2.8).
 #include "../kda_internal.h"
 #include "kda.h"
 #include "kda_layer.h"
@@ -18,7 +21,8 @@ namespace kda {
 namespace {
 
 // How a launch lies over a row: lp lanes a group, gpb groups and rb rows of
-// them a block.
+// them a block. A group of 65 to 128 vectors takes a wave with two each, as fast as
+// a block of its own (8192 x 4096 in 4 groups: 32 us and 31 forward, 70 and 86 back).
 struct GroupShape {
   int nv, lp, gpb, rb, threads, gx;
   bool block;
@@ -262,7 +266,9 @@ __global__ void __launch_bounds__(512) k_group_norm(GroupNormArgs a, int lp, int
 }
 
 // Blocks along the rows: forward all of them up to 65535 and 2^22 blocks in
-// all, backward, where each leaves a partial row, enough to fill the chip.
+// all, backward, where each leaves a partial row, enough to fill the chip: 512, 1024
+// or 2048 take 70, 65 and 67 us at 8192 rows of 4096 channels in 8 groups, 113, 71
+// and 83 in 2, 102, 108 and 120 at 4096 rows of one group of 8192.
 unsigned group_norm_rows(const GroupShape& g, int64_t rows, bool bwd) {
   const int64_t want = (rows + g.rb - 1) / g.rb, fill = (1 << 22) / g.gx;
   const int64_t most = bwd ? (1024 + g.gx - 1) / g.gx : (fill < 65535 ? fill : 65535);

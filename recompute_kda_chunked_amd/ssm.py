@@ -139,8 +139,10 @@ def ssm_scan(x, raw_dt, A_log, B, C, D=None, dt_bias=None, cu_seqlens=None, *, i
     be captured into a graph). initial_state fp32 [n,H,N,P] (None: zero). With
     output_final_state returns (y, final_state), from which the next call or
     ssm_recurrent goes on. Rows of y that belong to no sequence are zero. No
-    gradient reaches raw_dt where a limit holds. The workspace is about the
-    states' size every 128 tokens (64 for fp32), four times that backward."""
+    gradient reaches raw_dt where a limit holds. The workspace is the states'
+    size every 128 tokens (64 for fp32) and for each sequence, of x's type
+    forward, fp32 and twice backward; up to as much again where long sequences
+    are divided."""
     if _through_autograd(x, raw_dt, A_log, B, C, D, dt_bias, initial_state):
         return SsmScanFunction.apply(x, raw_dt, A_log, B, C, D, dt_bias, cu_seqlens, initial_state,
                                      output_final_state, dt_limit)
