@@ -204,6 +204,25 @@ def test_segments_of_ragged_batches_replayed():
             assert bool((ref[i][:cu[0]] == 0).all()) and bool((ref[i][cu[-1]:] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_what_is_not_a_number_stays_in_its_sequence_and_behind_its_token(dtype, value):
+    announce("scan with %s in one sequence %s" % (value, dtype))
+    x = make([130, 1500, 70, 1300], 2, 2, 64, 64, dtype, 23)
+    want = (*forward(x), *backward(x))
+    bad = dict(x, x=x["x"].clone(), B=x["B"].clone())
+    bad["x"][130 + 700, 0] = value
+    bad["B"][130 + 700, 1] = value
+    got = (*forward(bad), *backward(bad))
+    for i in (0, 2, 3, 5, 6):  # rows: the others' as they were
+        assert torch.equal(got[i][:130], want[i][:130]) and torch.equal(got[i][1630:], want[i][1630:])
+    for i in (1, 9):
+        assert torch.equal(got[i][[0, 2, 3]], want[i][[0, 2, 3]]) and not bool(torch.isfinite(got[i][1]).all() and i == 1)
+    # chunks before the token's (128 or 64 tokens) are untouched, outputs from it on are not finite
+    assert torch.equal(got[0][130:130 + 640], want[0][130:130 + 640])
+    assert not bool(torch.isfinite(got[0][130 + 700]).any())
+
+
 def test_offsets_past_32_bits():
     announce("scan: offsets past 2^31 elements")
     H, G, N, P, T = 64, 1, 64, 128, 262144 + 300
