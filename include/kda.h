@@ -515,7 +515,7 @@ int kda_ssm_recurrent(const kda_ssm_problem *p, const void *x, const void *raw_d
    KDA_ACT_SIGMOID, KDA_ACT_SILU or, without a gate, KDA_ACT_NONE. The backward
    recomputes the norm from x and gate and writes dx, dgate [rows, C] (dtype,
    rows adjacent) and dweight, dbias [C] (fp32, summed in a fixed order; dbias
-   NULL: not written). Pointers are 16-byte aligned; outputs must not overlap
+   NULL: not written; also without a bias it is the gradient at zero). Pointers are 16-byte aligned; outputs must not overlap
    inputs. rows = 0: nothing but dweight and dbias (zero) is written. Errors as
    for the gated norm. */
 enum { KDA_GROUP_GATE_NONE = 0, KDA_GROUP_GATE_AFTER = 1, KDA_GROUP_GATE_FIRST = 2 };

@@ -254,12 +254,12 @@ __global__ void __launch_bounds__(512) k_group_norm(GroupNormArgs a, int lp, int
     }
   }
   if constexpr (BWD) {
-    float* p = a.partials + (static_cast<size_t>(blockIdx.y) * rb + rsub) * (a.bias ? 2 : 1) * a.C;
+    float* p = a.partials + (static_cast<size_t>(blockIdx.y) * rb + rsub) * (a.dbias ? 2 : 1) * a.C;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (have[j]) {
         store_params<N>(p + c[j], dw[j]);
-        if (a.bias) store_params<N>(p + a.C + c[j], db[j]);
+        if (a.dbias) store_params<N>(p + a.C + c[j], db[j]);
       }
     }
   }

@@ -72,10 +72,11 @@ hipError_t launch_ssm_scalars(int dtype, const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_reduce(int dtype, int N, const SsmArgs& a, hipStream_t s);
 
 // Group norm. Partial sums: group_norm_partials(...) rows of dweight [C] then
-// (with a bias) dbias [C].
+// (with `dbias`, wanted with or without a bias) dbias [C].
 struct GroupNormArgs {
   int64_t rows, xs, gs;  // strides of x and gate in elements
   int C, groups, W, act, center;
+  bool dbias;
   float eps;
   const void *x, *gate, *dy;
   const float *weight, *bias;

@@ -181,7 +181,7 @@ int check_group_norm(const kda_group_norm_problem* p) {
   return KDA_OK;
 }
 
-// Room for both parameters' partial sums, whether or not there is a bias.
+// Room for both parameters' partial sums, whether or not the bias's are wanted.
 size_t group_norm_ws(const kda_group_norm_problem* p) {
   return static_cast<size_t>(group_norm_partials(p->dtype, p->C, p->groups, p->rows)) * 2 * p->C * sizeof(float);
 }
@@ -372,13 +372,13 @@ int kda_group_norm_bwd(const kda_group_norm_problem* p, const void* x, const voi
   a.dy = dy;
   a.dx = dx;
   a.dgate = dgate;
+  a.dbias = dbias != nullptr;
   a.partials = static_cast<float*>(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (p->rows > 0)
     KDA_TRY(KDA_KERNEL_GROUP_NORM_BWD, p->rows, launch_group_norm_bwd(p->dtype, p->gate, a, s));
   const int64_t nb = group_norm_partials(p->dtype, p->C, p->groups, p->rows);
-  const bool two = bias != nullptr || (p->rows == 0 && dbias);  // no rows: zeros for both
-  const ParamReduceArgs r{a.partials, nb, p->C, two ? p->C : 0, dweight, dbias};
+  const ParamReduceArgs r{a.partials, nb, p->C, dbias ? p->C : 0, dweight, dbias};
   KDA_TRY(KDA_KERNEL_PARAM_REDUCE, 0, launch_param_reduce(r, s));
   return KDA_OK;
 }

@@ -15,7 +15,7 @@ import pytest
 import torch
 
 from oracle import ssm_ref
-from recompute_kda_chunked_amd import group_norm, group_norm_backward, group_norm_forward
+from recompute_kda_chunked_amd import group_norm, group_norm_backward, group_norm_forward, ssm
 from test_gpu_norms import check, randn
 from test_gpu_states import announce, rel, to_np
 
@@ -160,3 +160,27 @@ def test_group_norm_past_32_bits():
     y = group_norm_forward(x, w, groups=4, activation="none")
     assert torch.equal(y[-1000:], group_norm_forward(x[-1000:].clone(), w, groups=4, activation="none"))
     assert torch.equal(y[:1000], y[-1000:])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", ["none", "after", "first"])
+@pytest.mark.parametrize("T", [0, 1, 300])
+def test_gradients_of_parameters_that_are_not_given(dtype, gate, T):
+    announce("dbias without a bias, a bias without dbias %s %s T%d" % (dtype, gate, T))
+    x, dy = randn(81, dtype, T, 144), randn(82, dtype, T, 144)
+    g, w, zero = None if gate == "none" else randn(83, dtype, T, 144), randn(84, F32, 144), torch.zeros(144, device="cuda")
+    kw = options(gate, "silu", 2, True)
+
+    def call(bias, dbias):
+        dev, p = ssm._group_norm_problem(x, w, bias, g, 2, 1e-6, "silu", True, gate == "first", dy)
+        out = [torch.full_like(t, float("nan")) for t in (x, x if g is None else g, w)]
+        ssm._call(dev, "kda_group_norm_bwd", p, x, g, w, bias, dy, out[0], None if g is None else out[1], out[2], dbias,
+                  workspace=ssm._workspace(dev, "kda_group_norm_bwd", p))
+        return [out[0], out[2]] + ([] if g is None else [out[1]])
+
+    dx, dw, db, dg = group_norm_backward(x, w, zero, g, dy, **kw)
+    want = [dx, dw] + ([] if g is None else [dg])
+    got = torch.full_like(w, float("nan"))
+    for bias, dbias in ((None, got), (zero, None), (None, None)):
+        assert all(torch.equal(a, b) for a, b in zip(call(bias, dbias), want))
+    assert torch.equal(got, db)
