@@ -456,8 +456,8 @@ int kda_short_conv_update(const kda_short_conv_problem *p, const void *x, const 
    (KDA_ERR_UNSUPPORTED, from about 2^22 / H chunks of 64 tokens and sequences).
    States, decays and sums are fp32; a bf16 problem rounds what the matrix cores
    multiply (once, or to three bf16, which hold it, where an fp32 output depends
-   on it). NaN and infinities spread over their sequence as the formulas have
-   them. The workspace holds the states every 128 tokens (64 for fp32) and at
+   on it). What the formulas derive from NaN or an infinity is NaN or an
+   infinity in y and final_state, and nothing else there changes. The workspace holds the states every 128 tokens (64 for fp32) and at
    sequence starts, in the problem's type, backward in fp32 and twice, and up to
    as much again where long sequences are divided. The backward recomputes what it needs from the
    inputs, takes dy and d_final_state (NULL: zero) and writes dx [T, H, P],

@@ -140,6 +140,28 @@ __global__ void __launch_bounds__(256) k_ssm_steps(SsmArgs a) {
 
 // ------------------------------------------------------------ states
 
+// Of units of a row, the largest bits without signs: whether a value is NaN or
+// infinite.
+template <typename TI>
+struct Largest {
+  typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
+  uint32_t top = 0;
+  __device__ __forceinline__ void add(const uint4& u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(TI) == 2)
+        top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, top), __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu)));
+      else
+        top = max(top, w[i] & 0x7fffffffu);
+    }
+  }
+  __device__ __forceinline__ bool finite() const {
+    if constexpr (sizeof(TI) == 2) return !((top + 0x00800080u) & 0x80008000u);
+    else return top < 0x7f800000u;
+  }
+};
+
 // A chunk's R rows of COLS columns on their way to a tile: 16-byte units, thread
 // t's m-th unit number t + TH m. Addresses are a base that the block shares plus
 // 32 bits (token strides are below 2^22 elements). Rows behind the chunk's last
@@ -172,6 +194,35 @@ struct Rows {
   __device__ __forceinline__ void store(TI* tile, int rows, int tid) const {
 #pragma unroll
     for (int m = 0; m < PER; ++m) *reinterpret_cast<uint4*>(tile + place(tid, m)) = kept(rows, tid, m);
+  }
+  __device__ __forceinline__ bool finite() const {
+    Largest<TI> l;
+#pragma unroll
+    for (int m = 0; m < PER; ++m) l.add(v[m]);
+    return l.finite();
+  }
+  // Stores zeros for what is no finite number, and in `first` (of each column) the
+  // first row that has one.
+  __device__ __forceinline__ void store_finite(TI* tile, int rows, int tid, int* first) const {
+#pragma unroll 1
+    for (int m = 0; m < PER; ++m) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+        if (k == m) u = kept(rows, tid, k);
+      RowVec<TI> r;
+      float f[U];
+      r.u = u;
+      r.get(f);
+#pragma unroll
+      for (int e = 0; e < U; ++e)
+        if (!(fabsf(f[e]) <= FLT_MAX)) {
+          f[e] = 0.f;
+          atomicMin(first + (tid % (COLS / U)) * U + e, tid / (COLS / U) + RPM * m);
+        }
+      r.set(f);
+      *reinterpret_cast<uint4*>(tile + place(tid, m)) = r.u;
+    }
   }
 };
 // A state of 64 columns on its way from accumulators to k_ssm_out's tile, in TI:
@@ -482,6 +533,8 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q, sizeof(TI) == 2 ? 4 : 2) k_s
   constexpr int Q = Chunk<TI>::Q, NW = Q / 16, TH = 64 * NW;
   __shared__ __align__(16) TI buf[2 * Q * N];
   __shared__ float chi[Q], clo[Q], cdt[Q];
+  __shared__ __align__(16) int first[2][64];  // by turns: of each column of x, the first row that is not finite
+  __shared__ int odd[2];                      // whether there is one
   const unsigned own = own_blocks(a);
   if (blockIdx.x >= own) {
     zero_rows(static_cast<TI*>(a.y), static_cast<int64_t>(a.H) * a.P, a, blockIdx.x - own, gridDim.x - own);
@@ -506,6 +559,8 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q, sizeof(TI) == 2 ? 4 : 2) k_s
     rb.store(Bt, rows, tid);
     rc.store(Ct, rows, tid);
   }
+  if (tid < 64) first[0][tid] = Q;
+  if (tid == 0) odd[0] = 0;
   __syncthreads();
   Frag<TI> cf[N / 32];
 #pragma unroll
@@ -529,11 +584,24 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q, sizeof(TI) == 2 ? 4 : 2) k_s
     nstep = load_step(a.steps, (slot * a.H + h) * Q + tid % Q);
   };
   load(h0, 0);
+  int turn = 0;
   for (int h = h0; h < h1; ++h) {
     const float D = a.D ? a.D[h] : 0.f;
-    for (int half = 0; half < halves; ++half) {
+    for (int half = 0; half < halves; ++half, turn ^= 1) {
       __syncthreads();
-      nx.store(xs, rows, tid);
+      if (tid < 64) first[turn ^ 1][tid] = Q;
+      if (tid == 0) odd[turn ^ 1] = 0;
+      // The products take whole pairs of tiles, and the zero scores of the tokens
+      // behind i times NaN or an infinity would be NaN: x is stored without them, and
+      // what they belong to is made NaN below (which token by token it is too, an
+      // infinity by C S of rows of both signs). Looking for them costs 2.5 of 120 to
+      // 250 us of a forward at 8192 x 64 heads.
+      if (__builtin_expect(__any(!nx.finite()), 0)) {
+        nx.store_finite(xs, rows, once(tid), first[turn]);
+        odd[turn] = 1;
+      } else {
+        nx.store(xs, rows, tid);
+      }
       ns.store(Ss, once(tid));
       if (tid < Q) {
         cdt[tid] = nstep.dt;
@@ -571,6 +639,13 @@ __global__ void __launch_bounds__(4 * Chunk<TI>::Q, sizeof(TI) == 2 ? 4 : 2) k_s
         for (int p = 0; p < 4; ++p) y[p] = mma32(frag_col<true>(xs, lx, 32 * m, 16 * p), wf, y[p]);
       }
       const int row = 16 * it + i;
+      if (__builtin_expect(odd[turn], 0)) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (row >= first[turn][16 * p + 4 * g + r]) y[p][r] = nan_value();
+      }
       if (row < rows) {
         TI* out = static_cast<TI*>(a.y) + ((t0 + row) * a.H + h) * a.P + half * 64 + 4 * g;
 #pragma unroll

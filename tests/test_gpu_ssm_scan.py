@@ -447,3 +447,30 @@ def test_a_layer_in_training_and_decoding():
             assert rel(to_np(got), to_np(want[0][[90 + j, 95 + j, 249 + j]])) <= 1e-5
         assert rel(to_np(pools[1]), to_np(want[2])) <= 1e-5
         assert rel(to_np(pools[0]), to_np(want[1])) <= 1e-6
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("N,P", [(64, 128), (128, 64)])
+def test_what_is_not_a_number_reaches_no_output_before_its_token(dtype, value, N, P):
+    announce("scan with %s: outputs that the formulas keep free of it %s N%d P%d" % (value, dtype, N, P))
+    x = make([40, 300, 20], 4, 2, N, P, dtype, 25)
+    want_y, want_s = forward(x)
+    for at in (0, 15, 16, 47, 62, 130, 255, 299):
+        t, rest = 40 + at, slice(40 + at, 340)
+        # one channel of a head from the token on; a group's heads from it on, by a row of their
+        # states; a group's heads at the token alone; a head from it on
+        cases = [("x", (t, 1, 5), (rest, 1, 5), (1, 1, slice(None), 5)), ("B", (t, 1, 7), (rest, slice(2, 4)), (1, slice(2, 4), 7)),
+                 ("C", (t, 0, 3), (t, slice(0, 2)), None)]
+        if value != value:
+            cases.append(("raw_dt", (t, 2), (rest, 2), (1, 2)))
+        for name, index, rows, states in cases:
+            bad = dict(x, **{name: x[name].clone()})
+            bad[name][index] = value
+            y, s = forward(bad)
+            hit, hit_s = torch.zeros_like(y, dtype=torch.bool), torch.zeros_like(s, dtype=torch.bool)
+            hit[rows] = True
+            if states is not None:
+                hit_s[states] = True
+            assert torch.equal(y[~hit], want_y[~hit]) and torch.equal(s[~hit_s], want_s[~hit_s]), (name, at)
+            assert not bool(torch.isfinite(y[hit]).any()) and not bool(torch.isfinite(s[hit_s]).any()), (name, at)
