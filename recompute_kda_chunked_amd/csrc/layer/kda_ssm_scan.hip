@@ -276,8 +276,10 @@ __device__ __forceinline__ unsigned on_one_xcd(unsigned b, unsigned total) {
   return (b & 7) * (total / 8) + b / 8;
 }
 
-// A row of U values as kTerms vectors of TI that add up to them: fp32 itself, or
-// three bf16, which hold 24 bits.
+// A row of U values as K vectors of TI that add up to them: fp32 itself, or
+// three bf16, which hold 24 bits. What is left of an infinity, NaN, is made a
+// finite number, at most 2^119 as what is left of those is (1 of 158 us of a
+// forward at 8192 x 64 heads; a comparison and a choice 3.5).
 template <typename TI>
 struct Terms {
   static constexpr int K = sizeof(TI) == 4 ? 1 : 3, U = 16 / sizeof(TI);
@@ -289,7 +291,7 @@ struct Terms {
         float h[U];
         v[k].get(h);
 #pragma unroll
-        for (int e = 0; e < U; ++e) f[e] -= h[e];
+        for (int e = 0; e < U; ++e) f[e] = k > 0 ? f[e] - h[e] : __builtin_amdgcn_fmed3f(f[e] - h[e], -0x1p119f, 0x1p119f);
       }
     }
   }

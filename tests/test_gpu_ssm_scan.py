@@ -474,3 +474,20 @@ def test_what_is_not_a_number_reaches_no_output_before_its_token(dtype, value, N
                 hit_s[states] = True
             assert torch.equal(y[~hit], want_y[~hit]) and torch.equal(s[~hit_s], want_s[~hit_s]), (name, at)
             assert not bool(torch.isfinite(y[hit]).any()) and not bool(torch.isfinite(s[hit_s]).any()), (name, at)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lens,H", [([40, 300], 2), ([2000], 1)])  # the last in segments
+def test_an_infinity_stays_one_in_the_states(dtype, lens, H):
+    announce("infinities in states %s %s" % (dtype, lens))
+    x = make(lens, H, 1, 64, 64, dtype, 26)
+    x["A_log"].fill_(-9.0)  # nothing decays away
+    for at, value in ((150, float("inf")), (170, float("-inf"))):
+        x["x"][at, 0, at % 64] = value
+    pool = x["init"].clone()
+    y = ssm_recurrent(*[x[k] for k in NAMES], pool, x["cu"])
+    got, final = forward(x)
+    there = torch.isinf(pool)
+    assert int(there.sum()) == 128 and torch.equal(final[there], pool[there])
+    assert bool(torch.isfinite(final[~there]).all())
+    assert torch.equal(torch.isfinite(got), torch.isfinite(y))
