@@ -104,7 +104,9 @@ __global__ void __launch_bounds__(256) k_ssm_steps(SsmArgs a) {
   const int h = (blockIdx.x % nhb) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   const Place c = find_piece(a, slot, Q);
   if (c.rows <= 0 || h >= a.H) return;
-  const double l2 = -exp(static_cast<double>(a.A_log[h])) * 1.4426950408889634;
+  // finite, so that no step (also a token behind the chunk's last) decays nothing
+  double l2 = -exp(static_cast<double>(a.A_log[h])) * 1.4426950408889634;
+  l2 = l2 < -1e300 ? -1e300 : l2;
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   float dt[R], slope[R];
   double cum[R];
@@ -1196,17 +1198,18 @@ __global__ void __launch_bounds__(256) k_ssm_scalars(SsmArgs a) {
     if (lane / LT == k) over = s;
   }
   over += q0;
-  const float Ah = expf(a.A_log[h]);
+  float Ah = expf(a.A_log[h]);  // finite: what decays at once has a dl of zero
+  Ah = Ah > FLT_MAX ? FLT_MAX : Ah;
   float dA = 0.f, db = 0.f;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int t = R * lane + r;
-    const float dl = t < c.rows ? ((sa + sb) + (ta + tb)) + over : 0.f, d = (v[r][2] - Ah * dl) * st[r][3];
+    const float dl = t < c.rows ? ((sa + sb) + (ta + tb)) + over : 0.f, d = st[r][3] != 0.f ? (v[r][2] - Ah * dl) * st[r][3] : 0.f;
     sa -= v[r][0];
     sb += v[r][1];
     ta -= v[r][3];
     tb += bf[r];
-    dA -= Ah * st[r][0] * dl;
+    dA -= Ah * (st[r][0] * dl);
     db += d;
     if (t < c.rows) static_cast<TI*>(a.ddt)[(c.t0 + t) * a.H + h] = from_f<TI>(d);
   }

@@ -51,7 +51,9 @@ __global__ void __launch_bounds__(2 * P) k_ssm_recurrent(SsmStepArgs a) {
       for (int64_t t = t0; t < t1; ++t) store4<TI>(y + t * os + col, f32x4{f, f, f, f});
     return;
   }
-  const float A = -expf(a.A_log[h]), D = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  float A = -expf(a.A_log[h]);  // finite: a step of zero decays nothing
+  A = A < -FLT_MAX ? -FLT_MAX : A;
+  const float D = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   const int g = h / (a.H / a.G);
 
   struct Token {

@@ -220,3 +220,12 @@ def test_a_pool_over_an_input_is_refused():
     x["x"] = x["state"].view(-1)[-256:].view(2, 2, 64)
     with pytest.raises(KdaError, match="kda_ssm_recurrent failed"):
         run(x)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_decays_past_fp32(dtype):
+    announce("exp(A_log) past fp32's largest, steps of zero %s" % dtype)
+    x = ssm_inputs([6, 1], 4, 1, 64, 64, dtype, 14)
+    x["A_log"].copy_(torch.tensor([89.0, 100.0, 700.0, 1.0]))
+    x["raw_dt"][2] = x["raw_dt"][6] = -float("inf")
+    compare(x)

@@ -491,3 +491,20 @@ def test_an_infinity_stays_one_in_the_states(dtype, lens, H):
     assert int(there.sum()) == 128 and torch.equal(final[there], pool[there])
     assert bool(torch.isfinite(final[~there]).all())
     assert torch.equal(torch.isfinite(got), torch.isfinite(y))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scan_of_decays_past_fp32(dtype):
+    announce("scan with exp(A_log) past fp32's and fp64's largest %s" % dtype)
+    x = make([150, 3, 128, 64], 4, 1, 64, 64, dtype, 28)
+    x["A_log"].copy_(torch.tensor([89.0, 100.0, 700.0, 1.0]))
+    x["raw_dt"][5] = x["raw_dt"][149] = -float("inf")  # steps of zero
+    parity(x)
+    x["A_log"][0] = 1000.0
+    x["raw_dt"][5] = x["raw_dt"][149] = 0.0  # the reference's exp(1000) times zero is NaN
+    y_ref, s_ref = ssm_ref.scan(*[to_np(x[k]) for k in NAMES], x["cu_host"], to_np(x["init"]))
+    y_abs, s_abs = reference(dict(x, A_log=x["A_log"].clamp(max=700.0)), absolute=True)[:2]
+    y, final = forward(x)
+    one = 1e-5 if dtype is F32 else 2.0 ** -8 + 1e-5
+    held("y", y, y_ref, HALF_STEP[dtype] * np.abs(y_ref) + one * y_abs)
+    held("final", final, s_ref, 1e-5 * s_abs)
