@@ -271,7 +271,8 @@ int kda_ssm_bwd(const kda_ssm_problem* p, const void* x, const void* raw_dt, con
   }
   if (a.T > 0) {
     KDA_TRY(KDA_KERNEL_SSM_GRAD, units, launch_ssm_grad(p->dtype, p->N, a, s));
-    KDA_TRY(KDA_KERNEL_SSM_GRAD, units, launch_ssm_scalars(p->dtype, a, s));
+    // no sequences and less than a chunk of tokens: no slot
+    if (a.slots > 0) KDA_TRY(KDA_KERNEL_SSM_GRAD, units, launch_ssm_scalars(p->dtype, a, s));
     if (a.sets > 1 && plan.whole < a.slots * a.G)
       KDA_TRY(KDA_KERNEL_SSM_REDUCE, a.T, launch_ssm_reduce(p->dtype, p->N, a, s));
   }

@@ -508,3 +508,17 @@ def test_scan_of_decays_past_fp32(dtype):
     one = 1e-5 if dtype is F32 else 2.0 ** -8 + 1e-5
     held("y", y, y_ref, HALF_STEP[dtype] * np.abs(y_ref) + one * y_abs)
     held("final", final, s_ref, 1e-5 * s_abs)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [1, 37, 63, 64, 127, 128])
+def test_no_sequences_over_few_tokens(dtype, T):
+    announce("scan of %d tokens in no sequence %s" % (T, dtype))
+    x = make([T], 6, 1, 64, 64, dtype, 29)
+    x.update(cu=torch.zeros(1, dtype=torch.int32, device="cuda"), init=None, dfinal=None)
+    leave_nan(x["x"].shape, dtype)
+    y, final = forward(x)
+    got = backward(x)
+    assert final.shape == (0, 6, 64, 64)
+    for t in (y, *got[:7]):
+        assert bool((t == 0).all())
