@@ -457,10 +457,13 @@ int kda_short_conv_update(const kda_short_conv_problem *p, const void *x, const 
    States, decays and sums are fp32; a bf16 problem rounds what the matrix cores
    multiply (once, or to three bf16, which hold it, where an fp32 output depends
    on it). What the formulas derive from NaN or an infinity is NaN or an
-   infinity in y and final_state, and nothing else there changes. The workspace holds the states every 128 tokens (64 for fp32) and at
-   sequence starts, in the problem's type, backward in fp32 and twice, and up to
-   as much again where long sequences are divided. The backward recomputes what it needs from the
-   inputs, takes dy and d_final_state (NULL: zero) and writes dx [T, H, P],
+   infinity in y and final_state, and nothing else there changes; of the gradients
+   they may also reach others in their chunk (128 tokens counted from their
+   sequence's first, 64 for fp32), and their heads' dA_log, dD and ddt_bias. The
+   workspace holds the states every 128 tokens (64 for fp32) and at sequence
+   starts, in the problem's type, backward in fp32 and twice, and up to as much
+   again where long sequences are divided. The backward recomputes what it needs
+   from the inputs, takes dy and d_final_state (NULL: zero) and writes dx [T, H, P],
    draw_dt [T, H], dB, dC [T, G, N] (dtype, rows adjacent), dA_log, dD and
    ddt_bias [H] (fp32, summed in a fixed order; dD and ddt_bias may be NULL:
    not written) and d_initial_state (NULL: not written). No gradient reaches

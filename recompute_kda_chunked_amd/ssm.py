@@ -139,7 +139,10 @@ def ssm_scan(x, raw_dt, A_log, B, C, D=None, dt_bias=None, cu_seqlens=None, *, i
     be captured into a graph). initial_state fp32 [n,H,N,P] (None: zero). With
     output_final_state returns (y, final_state), from which the next call or
     ssm_recurrent goes on. Rows of y that belong to no sequence are zero. No
-    gradient reaches raw_dt where a limit holds. The workspace is the states'
+    gradient reaches raw_dt where a limit holds. NaN and infinities reach y and
+    the final state only where the formulas have them; of the gradients they may
+    reach others of their chunk (128 tokens from the sequence's first, 64 for
+    fp32). The workspace is the states'
     size every 128 tokens (64 for fp32) and for each sequence, of x's type
     forward, fp32 and twice backward; up to as much again where long sequences
     are divided."""

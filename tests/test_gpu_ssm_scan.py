@@ -522,3 +522,32 @@ def test_no_sequences_over_few_tokens(dtype, T):
     assert final.shape == (0, 6, 64, 64)
     for t in (y, *got[:7]):
         assert bool((t == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_gradients_of_what_is_not_a_number(dtype, value):
+    announce("gradients with %s in a chunk %s" % (value, dtype))
+    x = make([40, 700, 20], 4, 2, 64, 128, dtype, 27)
+    want = backward(x)
+    t, Q = 40 + 300, 128 if dtype is BF16 else 64
+    before, behind = 40 + 300 // Q * Q, 40 + (300 // Q + 1) * Q  # its chunk
+    for name, index, kept in (("x", (t, 1, 5), "before"), ("B", (t, 1, 7), "before"), ("C", (t, 1, 7), "behind"),
+                              ("dy", (t, 1, 5), "behind")):
+        bad = dict(x, **{name: x[name].clone()})
+        bad[name][index] = value
+        got = backward(bad)
+        for i in (0, 1, 3, 4):  # chunks that the formulas keep free of it, and the other sequences
+            a, b = (0, before) if kept == "before" else (behind, 760)
+            assert torch.equal(got[i][a:b], want[i][a:b]), (name, i)
+            assert torch.equal(got[i][:40], want[i][:40]) and torch.equal(got[i][740:], want[i][740:]), (name, i)
+        if name == "x":  # dx and the gradients of states do not depend on x
+            assert torch.equal(got[0], want[0]) and torch.equal(got[7], want[7])
+        if name == "dy":  # one column of a head's states
+            assert not bool(torch.isfinite(got[7][1, 1, :, 5]).any())
+            got[7][1, 1, :, 5] = want[7][1, 1, :, 5]
+            assert torch.equal(got[7], want[7])
+        for i in (0, 1):  # the other heads: of the group in x and dy, of the other one in B and C
+            others = [0, 2, 3] if name in ("x", "dy") else [0, 1]
+            assert torch.equal(got[i][:, others], want[i][:, others]), (name, i)
+        assert not bool(torch.isfinite(got[2]).all())
