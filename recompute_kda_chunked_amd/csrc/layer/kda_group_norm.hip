@@ -7,9 +7,11 @@
 // vectors a lane; slots keep their group over all their rows, so weights and
 // their gradients stay in registers. Means are taken off before the squares
 // are added up. Sums are fp32, every output is rounded once. Measured at 8192 rows
-// of 4096 bf16 channels, groups of 512 with a gate: forward 34 us (5.9 TB/s),
-// backward 56 (6.0), the rows past the caches; 4097 x 2560 without a gate, in the
-// caches, 15 (2.8).
+// of 4096 bf16 channels, groups of 512 with a gate: forward 35 us (5.8 TB/s),
+// backward 58 (5.8), the rows past the caches; 4097 x 2560 in groups of
+// 64 without a gate, in the caches, 15 (2.8): of the two blocks of a row the second
+// has 8 of its 32 places in use, and forward each row reads its parameters, 64
+// bytes for 16 of x.
 #include "../kda_internal.h"
 #include "kda.h"
 #include "kda_layer.h"

@@ -39,10 +39,15 @@ struct ScanPlan {
     // A block takes the heads of a group in turn, as many rounds of blocks as fill
     // the chip; the chunks and groups left over are divided by heads, into as many
     // blocks as cost least: rounds times a block's heads and a part of one for its
-    // start, and backward the partial sums of dB and dC. A call of 8192 tokens x 48
-    // heads of one group (64 units) takes 119 us forward and 313 backward, with a
-    // block a unit 239 and 582; 64 heads of 8 groups (520 units) 150 and 388, with a
-    // block a unit 141 and 368, within what two runs differ by.
+    // start, and backward the partial sums of dB and dC. Microseconds forward and
+    // backward, bf16, N 128, P 64, against a block a unit (both sides in turn, within
+    // 1%):
+    //   8192 tokens in 1, 48 heads of 1 group   (65 units)   126 / 256   337 / 608
+    //   8192 tokens in 3, 48 heads of 1 group   (67 units)   174 / 304   331 / 602
+    //   8192 tokens in 1, 64 heads of 8 groups  (520 units)  141 / 141   380 / 376
+    //   8192 tokens in 3, 64 heads of 8 groups  (536 units)  154 / 176   364 / 418
+    //   4099 tokens in 9, 48 heads of 1 group   (41 units)    64 / 213   168 / 517
+    //   1531 tokens in 6, 12 heads of 2 groups  (34 units)    31 / 48     58 / 94
     const int per = p->H / p->G;
     const int64_t units = slots * p->G, round = bwd ? 256 : 512;
     whole = units / round * round;
@@ -61,8 +66,12 @@ struct ScanPlan {
     // at a time, and a launch's start (7 chunks). Measured with N 128, P 64, bf16,
     // forward, one sequence or 4 alike, without and with segments: 8192 tokens x 64
     // heads 293 / 166 us and 142 / 182, x 8 heads 230 / 67 and 78 / 59. The lengths
-    // are known on the device, which decides; with many sequences for their chunks
-    // none is long, and a slot of each would take more room than the states.
+    // are known on the device, which decides, and every sequence has a slot for a
+    // segment: with more than a sequence for four chunks their room would come near
+    // the states', and no sequence is divided, also not a long one among short ones,
+    // which then takes its chunks in turn. Forward and backward, 8 heads: one of 7500
+    // tokens with 15 others (692 tokens) 63 and 103 us, with 16 208 and 250; one of
+    // 30000 with 63 others (2768) 125 and 255, with 64 770 and 911.
     const int dirs = bwd ? 2 : 1;
     const int64_t chunks = (T + Q - 1) / Q, chain = dirs * (HP / 64);
     const int64_t want = 512 / chain < 32 ? 512 / chain : 32;

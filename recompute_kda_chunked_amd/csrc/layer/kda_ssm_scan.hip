@@ -28,16 +28,16 @@
 // (the states themselves, dA_log, ddt_bias) a value is three bf16, its 24 bits.
 // Running sums of log decays are fp64, kept as pairs of fp32.
 //
-// What bounds it, at 8192 tokens in three sequences, 64 heads of one group, N 128,
+// What bounds it, at 8192 tokens in three sequences, 64 heads of 8 groups, N 128,
 // P 64, bf16, forward and backward: nothing at its full rate (350 MB at the least
-// are 68 us, the products' 52 GFLOP 46 us at the rate of a large product). Of 590
-// us the state passes take 64 + 45 forward (as segments, see k_ssm_state) and 183
+// are 68 us, the products' 52 GFLOP 46 us at the rate of a large product). Of 584
+// us the state passes take 64 + 45 forward (as segments, see k_ssm_state) and 180
 // backward, a chunk's step a chain of loads, LDS writes, LDS reads and products
-// that 1.4 waves a SIMD cannot hide (3.3 us alone), and 270 MB of states go to HBM.
-// The gradient kernel takes 223: one block of 8 waves a CU by its LDS, vector
+// that 1.4 waves a SIMD cannot hide (3.3 us alone), and 270 MB of states go to HBM
+// and come back. The gradient kernel takes 222: one block of 8 waves a CU by its LDS, vector
 // instructions issued about half of the time (counters), the LDS in use a third and
 // the matrix cores a fifth, one after another between barriers. The output
-// takes 60, two blocks a CU. Chunks of 128 and not 64 tokens halve the states'
+// takes 64, two blocks a CU. Chunks of 128 and not 64 tokens halve the states'
 // bytes and the steps of the chain; fp32 tiles of 128 would not fit the LDS.
 #include "../kda_internal.h"
 #include "kda.h"
@@ -527,9 +527,9 @@ __device__ __forceinline__ void zero_rows(T* o, int64_t width, const SsmArgs& a,
 
 // ------------------------------------------------------------ output
 
-// One group's chunk a block, the heads in turn: 59 us at 8192 x 64 heads. C B^T
-// stays in registers over the heads (at 128 registers, two blocks a CU; operands
-// read further ahead spill), the next head's rows and state are loaded during a
+// One group's chunk a block, the heads in turn: 64 us at 8192 x 64 heads. C B^T
+// stays in registers over the heads (at 128 registers, two blocks a CU, with 9 of
+// them spilled at N = 128; operands read further ahead spill more), the next head's rows and state are loaded during a
 // head's products. Wave: 16 tokens i of the chunk. Scores are formed as [j][i] accumulators, an
 // operand as they stand of y^T[p][i] = sum_j x_j[p] (L G dt)_ij.
 template <typename TI, int N>

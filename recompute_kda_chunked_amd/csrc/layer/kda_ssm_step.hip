@@ -11,8 +11,8 @@
 // another. A lane reads the B and C of its own rows, which the heads of a group
 // and the waves of a head find in the caches; the next token's rows are loaded
 // during a token's step. States go past the caches as in the recurrent form of
-// the delta rule: 193 sequences of one token, 64 heads, N 128, P 64, take 150 us
-// (5.4 TB/s), 33 of up to 8 tokens with 48 heads 19. Sums and the state are fp32 for either dtype; only y is
+// the delta rule: 193 sequences of one token, 64 heads, N 128, P 64, take 151 us
+// (5.4 TB/s), 33 of up to 6 tokens with 48 heads 19.5. Sums and the state are fp32 for either dtype; only y is
 // rounded, once.
 #include "../kda_device.h"
 #include "kda_rows.h"
